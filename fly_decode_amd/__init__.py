@@ -1,7 +1,8 @@
 """fly_decode_amd -- lossless codebook-compressed BF16 weights decoded on MI355X (gfx950).
 
-A thin ctypes binding over ``libcbk.so`` (C ABI declared in ``include/cbk.h`` and, for the
-exponent entropy-coded format, ``include/cbk_ec.h``).  Every step of the
+A thin ctypes binding over ``libcbk.so`` (C ABI declared in ``include/cbk.h``, for the exponent
+entropy-coded format in ``include/cbk_ec.h``, and for the operators on any number of tokens and
+their gradients in ``include/cbk_nn.h``).  Every step of the
 hot path runs in the library's HIP kernels; this module only marshals arguments.  PyTorch is used
 for device memory and streams: inputs and outputs are torch tensors whose ``data_ptr()`` is handed
 to the library, and GPU calls are enqueued on ``torch.cuda.current_stream()``.
@@ -20,7 +21,8 @@ __all__ = ["CBK_OK", "CbkError", "bits_for", "words_for", "compressed_bytes", "e
            "Compressed", "decode_bf16", "decode_group", "gemv", "gemv_group", "gemm_small", "library_path",
            "load_library", "ECTensor", "ec_encode", "ec_decode_bf16", "ec_gemv", "ec_build_index",
            "ec_decode_group", "ec_gemv_group", "cap_patterns",
-           "GemvChain"]
+           "GemvChain", "linear", "linear_dx", "ffn_gated", "ffn_gated_bwd", "xent", "xent_bwd",
+           "linear_workspace_bytes", "ffn_workspace_bytes", "xent_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # CBK_LIBRARY names another build of the same library (for side-by-side comparisons)
@@ -165,6 +167,20 @@ def load_library():
         lib.cbk_ec_gemv_group.argtypes = [ctypes.POINTER(_ECTensor), ctypes.POINTER(ctypes.c_void_p), ctypes.c_uint32,
                                           ctypes.POINTER(ctypes.c_uint64), ctypes.c_uint64, ctypes.c_void_p,
                                           ctypes.POINTER(ctypes.c_void_p), ctypes.c_void_p]
+        vp, u64, sz = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_size_t
+        for name, types in (("cbk_linear_workspace_bytes", [tp, u64]), ("cbk_ffn_workspace_bytes", [tp, tp, u64]),
+                            ("cbk_xent_workspace_bytes", [tp, u64])):
+            getattr(lib, name).restype = sz
+            getattr(lib, name).argtypes = types
+        for name, types in (
+                ("cbk_linear", [tp, vp, u64, u64, vp, u64]),
+                ("cbk_linear_dx", [tp, vp, u64, u64, vp, u64]),
+                ("cbk_ffn_gated", [tp, tp, ctypes.c_int, vp, u64, u64, vp, u64]),
+                ("cbk_ffn_gated_bwd", [tp, tp, ctypes.c_int, vp, u64, vp, u64, u64, vp, u64, vp, vp, u64]),
+                ("cbk_xent", [tp, vp, u64, vp, u64, ctypes.c_int64, vp, vp]),
+                ("cbk_xent_bwd", [tp, vp, u64, vp, vp, vp, u64, ctypes.c_int64, vp, u64])):
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = types + [vp, sz, vp]
         _lib = lib
     return _lib
 
@@ -622,3 +638,207 @@ def ec_gemv_group(ts, x, ys=None, stream=None, indexes=None):
     _check(load_library().cbk_ec_gemv_group(arr, ix, len(ts), rows, ts[0].cols if ts else 0, xp, _ptrs(ys),
                                             _stream(stream)), "cbk_ec_gemv_group")
     return ys
+
+
+# ---- operators on any number of tokens, and their gradients (include/cbk_nn.h)
+
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def linear_workspace_bytes(t: Compressed, tokens: int) -> int:
+    """Workspace of ``linear`` and ``linear_dx`` for that many tokens (0: none)."""
+    return int(load_library().cbk_linear_workspace_bytes(ctypes.byref(t._struct()), tokens))
+
+
+def ffn_workspace_bytes(gate: Compressed, up: Compressed, tokens: int) -> int:
+    """Workspace of ``ffn_gated`` and ``ffn_gated_bwd``."""
+    return int(load_library().cbk_ffn_workspace_bytes(ctypes.byref(gate._struct()), ctypes.byref(up._struct()), tokens))
+
+
+def xent_workspace_bytes(head: Compressed, tokens: int) -> int:
+    """Workspace of ``xent`` and ``xent_bwd``."""
+    return int(load_library().cbk_xent_workspace_bytes(ctypes.byref(head._struct()), tokens))
+
+
+def _tokens(x, cols, name):
+    """Checks a [tokens][cols] bfloat16 matrix with unit column stride; returns (pointer, row stride)."""
+    import torch
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != cols or (cols > 1 and x.shape[0] > 0 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a [tokens][{cols}] bfloat16 matrix with unit column stride")
+    rows, ld = x.shape[0], x.stride(0)
+    if rows <= 1:  # a single row's stride means nothing
+        ld = max(ld, cols)
+    elif ld < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return x.data_ptr() or None, ld
+
+
+def _vector(x, n, dtype, name):
+    if x.dtype != dtype or x.dim() != 1 or x.numel() != n or (n > 1 and x.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n}")
+    return x.data_ptr() or None
+
+
+def _one_device(first, *others):
+    for x in others:
+        if x is not None and x.device != first.device:
+            raise ValueError(f"the arguments are on {first.device} and {x.device}")
+
+
+class _Call:
+    """Device, stream, outputs and workspace of one call on the device of ``x``: allocations come
+    from torch's allocator and, where the caller names a stream of its own, are recorded on it."""
+
+    def __init__(self, x, stream):
+        import torch
+        if x.device.type != "cuda":
+            raise ValueError("the operators run on GPU tensors")
+        self.torch, self.device = torch, x.device
+        self.given = stream is not None
+        self.stream = stream if self.given else torch.cuda.current_stream(x.device)
+
+    def empty(self, shape, dtype):
+        out = self.torch.empty(shape, dtype=dtype, device=self.device)
+        if self.given:
+            out.record_stream(self.stream)
+        return out
+
+    def run(self, name, need, workspace, *args):
+        if workspace is None:
+            # at least one element, so that there is an address; torch's blocks are 512-byte aligned
+            workspace = self.empty((max(need, 1),), self.torch.uint8)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
+        nbytes = workspace.numel() * workspace.element_size()
+        tail = (ctypes.c_void_p(workspace.data_ptr() or None), nbytes, ctypes.c_void_p(self.stream.cuda_stream))
+        fn = getattr(load_library(), name)
+        if self.torch.cuda.current_device() == self.device.index:
+            st = fn(*args, *tail)
+        else:
+            with self.torch.cuda.device(self.device):
+                st = fn(*args, *tail)
+        _check(st, name)
+
+
+def linear(t: Compressed, X, out=None, workspace=None, stream=None):
+    """out[tokens][rows] (bfloat16) = X . W^T for a bfloat16 X[tokens][cols], any number of tokens
+    (row strides may exceed the widths).  ``workspace``: a uint8 device tensor of at least
+    ``linear_workspace_bytes(t, tokens)`` bytes; allocated when not given."""
+    xp, ldx = _tokens(X, t.cols, "X")
+    _one_device(X, t.words, t.codebook, out)
+    call, T = _Call(X, stream), X.shape[0]
+    if out is None:
+        out = call.empty((T, t.rows), X.dtype)
+    op, ldo = _tokens(out, t.rows, "out")
+    if out.shape[0] != T:
+        raise ValueError("out and X differ in tokens")
+    ts = ctypes.byref(t._struct())
+    call.run("cbk_linear", int(load_library().cbk_linear_workspace_bytes(ts, T)) if workspace is None else 0, workspace,
+             ts, xp, ldx, T, op, ldo)
+    return out
+
+
+def linear_dx(t: Compressed, dY, out=None, workspace=None, stream=None):
+    """The gradient of ``linear``'s X: out[tokens][cols] (bfloat16) = dY . W for a bfloat16
+    dY[tokens][rows]."""
+    gp, ldg = _tokens(dY, t.rows, "dY")
+    _one_device(dY, t.words, t.codebook, out)
+    call, T = _Call(dY, stream), dY.shape[0]
+    if out is None:
+        out = call.empty((T, t.cols), dY.dtype)
+    op, ldo = _tokens(out, t.cols, "out")
+    if out.shape[0] != T:
+        raise ValueError("out and dY differ in tokens")
+    ts = ctypes.byref(t._struct())
+    call.run("cbk_linear_dx", int(load_library().cbk_linear_workspace_bytes(ts, T)) if workspace is None else 0, workspace,
+             ts, gp, ldg, T, op, ldo)
+    return out
+
+
+def ffn_gated(gate: Compressed, up: Compressed, X, act: str = "silu", out=None, workspace=None, stream=None):
+    """out[tokens][rows] (bfloat16) = act(X . Wg^T) * (X . Wu^T); act is "silu", "gelu" or
+    "gelu_tanh".  The products stay in fp32 until the result is rounded."""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    if (gate.rows, gate.cols) != (up.rows, up.cols):
+        raise ValueError("gate and up must have the same shape")
+    xp, ldx = _tokens(X, gate.cols, "X")
+    _one_device(X, gate.words, gate.codebook, up.words, up.codebook, out)
+    call, T = _Call(X, stream), X.shape[0]
+    if out is None:
+        out = call.empty((T, gate.rows), X.dtype)
+    op, ldo = _tokens(out, gate.rows, "out")
+    if out.shape[0] != T:
+        raise ValueError("out and X differ in tokens")
+    gs, us = ctypes.byref(gate._struct()), ctypes.byref(up._struct())
+    call.run("cbk_ffn_gated", int(load_library().cbk_ffn_workspace_bytes(gs, us, T)) if workspace is None else 0, workspace,
+             gs, us, _ACTS[act], xp, ldx, T, op, ldo)
+    return out
+
+
+def ffn_gated_bwd(gate: Compressed, up: Compressed, X, dH, act: str = "silu", dX=None, projections: bool = True,
+                  workspace=None, stream=None):
+    """The gradient of ``ffn_gated`` for the same X and the gradient dH[tokens][rows] of its output:
+    (dX[tokens][cols], dG[tokens][rows], dU[tokens][rows]), all bfloat16; dG and dU, the gradients
+    at the outputs of the gate and up projections, are None when ``projections`` is false."""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    if (gate.rows, gate.cols) != (up.rows, up.cols):
+        raise ValueError("gate and up must have the same shape")
+    xp, ldx = _tokens(X, gate.cols, "X")
+    hp, ldh = _tokens(dH, gate.rows, "dH")
+    T = X.shape[0]
+    if dH.shape[0] != T or (dX is not None and dX.shape[0] != T):
+        raise ValueError("X, dH and dX differ in tokens")
+    _one_device(X, dH, gate.words, gate.codebook, up.words, up.codebook, dX)
+    call = _Call(X, stream)
+    if dX is None:
+        dX = call.empty((T, gate.cols), X.dtype)
+    dp, ldd = _tokens(dX, gate.cols, "dX")
+    dG = dU = None
+    if projections:
+        dG, dU = call.empty((T, gate.rows), X.dtype), call.empty((T, gate.rows), X.dtype)
+    gs, us = ctypes.byref(gate._struct()), ctypes.byref(up._struct())
+    call.run("cbk_ffn_gated_bwd", int(load_library().cbk_ffn_workspace_bytes(gs, us, T)) if workspace is None else 0,
+             workspace, gs, us, _ACTS[act], xp, ldx, hp, ldh, T, dp, ldd, (dG.data_ptr() or None) if projections else None,
+             (dU.data_ptr() or None) if projections else None, gate.rows)
+    return dX, dG, dU
+
+
+def xent(head: Compressed, X, labels, ignore_index: int = -100, workspace=None, stream=None):
+    """Softmax cross entropy of the logits X . W^T over the head's rows, without keeping them:
+    (loss[tokens], lse[tokens]) in float32 for int64 labels; the loss of a token whose label is
+    ignore_index is 0.  No reduction over tokens."""
+    import torch
+    xp, ldx = _tokens(X, head.cols, "X")
+    T = X.shape[0]
+    lp = _vector(labels, T, torch.int64, "labels")
+    _one_device(X, labels, head.words, head.codebook)
+    call = _Call(X, stream)
+    loss, lse = call.empty((T,), torch.float32), call.empty((T,), torch.float32)
+    hs = ctypes.byref(head._struct())
+    call.run("cbk_xent", int(load_library().cbk_xent_workspace_bytes(hs, T)) if workspace is None else 0, workspace,
+             hs, xp, ldx, lp, T, ignore_index, loss.data_ptr() or None, lse.data_ptr() or None)
+    return loss, lse
+
+
+def xent_bwd(head: Compressed, X, labels, lse, dloss, ignore_index: int = -100, out=None, workspace=None, stream=None):
+    """The gradient of ``xent``'s X, out[tokens][cols] (bfloat16), for the lse it returned and the
+    gradient dloss[tokens] (float32) of its loss."""
+    import torch
+    xp, ldx = _tokens(X, head.cols, "X")
+    T = X.shape[0]
+    lp = _vector(labels, T, torch.int64, "labels")
+    sp = _vector(lse, T, torch.float32, "lse")
+    dp = _vector(dloss, T, torch.float32, "dloss")
+    _one_device(X, labels, lse, dloss, head.words, head.codebook, out)
+    call = _Call(X, stream)
+    if out is None:
+        out = call.empty((T, head.cols), X.dtype)
+    op, ldo = _tokens(out, head.cols, "out")
+    if out.shape[0] != T:
+        raise ValueError("out and X differ in tokens")
+    hs = ctypes.byref(head._struct())
+    call.run("cbk_xent_bwd", int(load_library().cbk_xent_workspace_bytes(hs, T)) if workspace is None else 0, workspace,
+             hs, xp, ldx, lp, sp, dp, T, ignore_index, op, ldo)
+    return out

@@ -23,7 +23,8 @@ DEVICE_FLAGS = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "include")]
 
 SOURCES = [("cbk_api.cpp", False), ("cbk_kernels.hip", True), ("cbk_encode.hip", True),
-           ("cbk_ec_host.cpp", False), ("cbk_ec.hip", True)]
+           ("cbk_ec_host.cpp", False), ("cbk_ec.hip", True),
+           ("cbk_nn_host.cpp", False), ("cbk_nn.hip", True)]
 
 
 def _run(cmd):

@@ -43,7 +43,10 @@ unsigned worker_count(uint64_t n) {
     return std::max(1u, std::min(hw ? hw : 1u, 16u));
 }
 
-cbk_status check_tensor(const cbk_tensor *t) {
+}  // namespace
+
+// The checks of a tensor that every GPU call makes.
+cbk_status cbk::check_tensor(const cbk_tensor *t) {
     if (!t) return CBK_E_INVALID;
     if (t->rows && t->cols > UINT64_MAX / t->rows) return CBK_E_INVALID;
     const uint64_t n = t->rows * t->cols;
@@ -60,7 +63,7 @@ cbk_status check_tensor(const cbk_tensor *t) {
     return CBK_OK;
 }
 
-}  // namespace
+using cbk::check_tensor;
 
 extern "C" {
 

@@ -1,5 +1,5 @@
-// Internal interface between the host API (cbk_api.cpp, cbk_ec_host.cpp) and the HIP launchers
-// (cbk_kernels.hip, cbk_encode.hip, cbk_ec.hip).
+// Internal interface between the host API (cbk_api.cpp, cbk_ec_host.cpp, cbk_nn_host.cpp) and the HIP
+// launchers (cbk_kernels.hip, cbk_encode.hip, cbk_ec.hip, cbk_nn.hip).
 // Arguments reaching these launchers are already validated.
 #pragma once
 #include <hip/hip_runtime.h>
@@ -7,8 +7,11 @@
 
 #include "../../include/cbk.h"
 #include "../../include/cbk_ec.h"
+#include "../../include/cbk_nn.h"
 
 namespace cbk {
+
+cbk_status check_tensor(const cbk_tensor *t);  // cbk_api.cpp
 
 cbk_status launch_decode(const cbk_tensor &t, uint16_t *out, hipStream_t s);
 cbk_status launch_decode_group(const cbk_tensor *ts, uint32_t count, uint16_t *const *outs, hipStream_t s);
@@ -42,5 +45,35 @@ cbk_status launch_ec_decode(const cbk_ec_tensor *ts, const uint8_t *const *index
 cbk_status launch_ec_gemv(const cbk_ec_tensor *ts, const uint8_t *const *indexes, uint32_t count,
                           const uint64_t *rows, uint64_t cols, const uint16_t *x, float *const *ys, hipStream_t s);
 cbk_status launch_ec_index(const cbk_ec_tensor *t, uint8_t *index, hipStream_t s);
+
+// Operators on any number of tokens (cbk_nn.hip).  A plan says how a call is cut up and where its
+// scratch lies in the workspace; it depends on the sizes alone, so that the workspace's size is
+// known without a GPU.  Tokens are taken Tc at a time, the rows of the tensors in pieces.
+struct NnPlan {
+    uint64_t Kp;      // columns of a decoded row in the workspace: cols rounded up to 64, at least 64
+    uint64_t Tc;      // tokens of a chunk
+    uint64_t Rp;      // decoded rows of a piece (of both tensors, for the feed-forward block), a multiple of 256
+    uint64_t rows;    // rows of one tensor in a piece
+    uint64_t pieces;
+    uint64_t pack, w, g, acc, stat, top;  // offsets in bytes
+    uint64_t bytes;
+};
+enum class NnOp { linear, ffn, xent };
+NnPlan nn_plan(NnOp op, uint64_t rows, uint64_t cols, uint64_t tokens);
+
+cbk_status launch_linear(const cbk_tensor &t, const uint16_t *X, uint64_t ldx, uint64_t T, uint16_t *Y, uint64_t ldy,
+                         void *ws, hipStream_t s);
+cbk_status launch_linear_dx(const cbk_tensor &t, const uint16_t *dY, uint64_t lddy, uint64_t T, uint16_t *dX,
+                            uint64_t lddx, void *ws, hipStream_t s);
+cbk_status launch_ffn(const cbk_tensor &gate, const cbk_tensor &up, int act, const uint16_t *X, uint64_t ldx, uint64_t T,
+                      uint16_t *H, uint64_t ldh, void *ws, hipStream_t s);
+cbk_status launch_ffn_bwd(const cbk_tensor &gate, const cbk_tensor &up, int act, const uint16_t *X, uint64_t ldx,
+                          const uint16_t *dH, uint64_t lddh, uint64_t T, uint16_t *dX, uint64_t lddx, uint16_t *dG,
+                          uint16_t *dU, uint64_t ldg, void *ws, hipStream_t s);
+cbk_status launch_xent(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, const int64_t *labels, uint64_t T,
+                       int64_t ignore, float *loss, float *lse, void *ws, hipStream_t s);
+cbk_status launch_xent_bwd(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, const int64_t *labels,
+                           const float *lse, const float *dloss, uint64_t T, int64_t ignore, uint16_t *dX,
+                           uint64_t lddx, void *ws, hipStream_t s);
 
 }  // namespace cbk

@@ -1,0 +1,766 @@
+// HIP kernels for gfx950 (CDNA4) of the operators in cbk_nn.h: products of any number of tokens
+// with codebook-compressed weights, the gated feed-forward block, the softmax cross entropy of a
+// compressed head, and their gradients.
+//
+// All are products with a tensor W [N][K] that is stored as b-bit indices into a codebook:
+//   forward   Y = X W^T   (reduction over W's columns)
+//   gradient  dX = G W    (reduction over W's rows)
+// A piece of W is decoded into the workspace once ([rows][Kp] BF16, Kp = K rounded up to 64, zero
+// padded), and one matrix-core kernel, k_mm, multiplies it in either orientation; what differs
+// between the operators is the work it does on its accumulators (the epilogue).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "cbk_device.h"
+
+namespace cbk {
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+#define CBK_LDS __attribute__((address_space(3)))
+
+inline uint32_t ceil_div(uint64_t n, uint64_t m) { return static_cast<uint32_t>((n + m - 1) / m); }
+inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// ------------------------------------------------------------------------------- small pieces
+
+// Copies 16 bytes a lane from the resource (at the lane's voff plus the wave's soff) straight into
+// LDS, lane l to dst + 16 l; dst is the same in every lane.  The wave's vmcnt counts it.  The
+// host's pass over this file does not know this chip's wide copies and transposing reads, so it
+// gets empty bodies.
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, unsigned char *dst, uint32_t voff, uint32_t soff) {
+#ifdef __HIP_DEVICE_COMPILE__
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (CBK_LDS void *)(dst), 16, static_cast<int>(voff), static_cast<int>(soff), 0, 0);
+#endif
+}
+
+// The transposing 64-bit LDS read: the 16 lanes of a group read 4 rows of 16 BF16 (lane s the 4
+// values at row s / 4, columns 4 (s % 4)..), and lane i gets column i of the 4 rows.
+__device__ __forceinline__ s16x4 read_transposed(const unsigned char *src) {
+#ifdef __HIP_DEVICE_COMPILE__
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((CBK_LDS s16x4 *)(src));
+#else
+    return s16x4{};
+#endif
+}
+
+// fp32 to BF16, to nearest even (NaN stays NaN).
+__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return static_cast<uint32_t>(to_bf16(a)) | (static_cast<uint32_t>(to_bf16(b)) << 16);
+}
+
+// act(z) and, where D is not null, act'(z), in fp32.  The tails are formed without subtractions
+// of nearly equal numbers: 1 - tanh and 1 - erf come from a logistic function and from erfc.
+__device__ __forceinline__ float activation(int act, float z, float *D) {
+    if (act == CBK_ACT_SILU) {
+        const float s = 1.f / (1.f + __expf(-z));
+        if (D) *D = s * (1.f + z * (1.f - s));
+        return z * s;
+    }
+    if (act == CBK_ACT_GELU) {
+        const float p = 0.5f * erfcf(z * -0.70710678118654752f);
+        if (D) *D = p + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+        return z * p;
+    }
+    // (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y)); past |z| = 16 it is 0 or 1 to every bit and z^3 might overflow
+    const float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+    const float w = fminf(fmaxf(z, -16.f), 16.f);
+    const float s = 1.f / (1.f + __expf(-c * (w + 0.044715f * w * w * w)));
+    if (D) *D = s + w * s * (1.f - s) * c * (1.f + 3.f * 0.044715f * w * w);
+    return z * s;
+}
+
+// X [T][K] with leading dimension ld into P [T][Kp], columns past K zero.
+__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t *__restrict__ X, uint64_t ld, uint64_t T, uint32_t K,
+                                                  uint32_t Kp, uint16_t *__restrict__ P) {
+    const uint64_t n = T * (Kp / 4), stride = static_cast<uint64_t>(gridDim.x) * blockDim.x;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+        const uint64_t t = i / (Kp / 4);
+        const uint32_t k = static_cast<uint32_t>(i - t * (Kp / 4)) * 4;
+        const uint16_t *x = X + t * ld + k;
+        uint16_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = k + j < K ? x[j] : static_cast<uint16_t>(0);
+        *reinterpret_cast<u32x2 *>(P + t * Kp + k) = (u32x2){static_cast<uint32_t>(v[0]) | (static_cast<uint32_t>(v[1]) << 16),
+                                                             static_cast<uint32_t>(v[2]) | (static_cast<uint32_t>(v[3]) << 16)};
+    }
+}
+
+// out[t][0 .. n) = 0
+__global__ __launch_bounds__(256) void k_zero_rows(uint16_t *__restrict__ out, uint64_t ld, uint64_t T, uint32_t n) {
+    const uint64_t all = T * n, stride = static_cast<uint64_t>(gridDim.x) * blockDim.x;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += stride)
+        out[i / n * ld + i % n] = 0;
+}
+
+// ------------------------------------------------------------------------- decoding a piece
+// Rows [row0, row0 + nrows) of a tensor into out [rows_out][Kp]; columns past cols and rows past
+// nrows are zero.  `pair` 0: row f goes to row f.  1 and 2: the gate and up tensors share the
+// piece, 16 rows of each in turn (row f to 32 (f / 16) + 16 (pair - 1) + f % 16), so that a wave
+// of k_mm has a column's gate and up sums in the same lanes.
+struct UnpackArgs {
+    const uint32_t *words;
+    const uint16_t *cb;
+    uint32_t b, U, cols, Kp;
+    uint64_t row0;
+    uint32_t nrows, rows_out, pair;
+    uint16_t *out;
+};
+
+__device__ __forceinline__ uint32_t piece_row(uint32_t f, uint32_t pair) {
+    return pair == 0 ? f : (f >> 4) * 32 + (pair - 1) * 16 + (f & 15);
+}
+
+// Any width, any number of columns: a thread per 4 columns.
+__global__ __launch_bounds__(256) void k_unpack_generic(const UnpackArgs a) {
+    const uint64_t n = static_cast<uint64_t>(a.rows_out) * (a.Kp / 4), stride = static_cast<uint64_t>(gridDim.x) * blockDim.x;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+        const uint32_t f = static_cast<uint32_t>(i / (a.Kp / 4)), k = static_cast<uint32_t>(i - static_cast<uint64_t>(f) * (a.Kp / 4)) * 4;
+        uint32_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = 0;
+            if (f < a.nrows && k + j < a.cols) {
+                const uint32_t idx = stream_field(a.words, a.b, (a.row0 + f) * a.cols + k + j);
+                v[j] = idx < a.U ? a.cb[idx] : kCorrupt;
+            }
+        }
+        *reinterpret_cast<u32x2 *>(a.out + static_cast<uint64_t>(piece_row(f, a.pair)) * a.Kp + k) = (u32x2){v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
+    }
+}
+
+// ------------------------------------------------------------------------- the matrix product
+// C[m][n] = sum_r A[m][r] B(r, n) over R = 64 ktiles, A [M][lda] the tokens' side, B a decoded
+// piece: NN false, B(r, n) = B[n][r] (forward); NN true, B(r, n) = B[r][n] (gradient).
+//
+// A workgroup of WM x WN waves owns a BM x BN tile, a wave (BM / WM) x (BN / WN) of it in 16 x 16
+// fragments of v_mfma_f32_16x16x32_bf16.  The weights are the instruction's A operand and the
+// tokens its B operand, so lane l holds columns n = 4 (l / 16) + 0..3 of token m = l % 16 of a
+// fragment: four neighbours in the output's rows.  Slices of 64 of the reduction are copied
+// straight into LDS (16 bytes a lane), the next one while the current one is multiplied.
+//
+// LDS layout.  A copy fills 1024 consecutive bytes, so what is permuted is which 16-byte chunk a
+// lane fetches.  Rows of 64 reduction elements (A, and B when NN is false) are 8 chunks, chunk c
+// of row r in slot c ^ (r & 7): the 8 lanes that read 8 rows' chunks at once hit 8 different
+// slots.  When NN is true B's slice is 64 reduction rows of BN columns, read with the transposing
+// 64-bit LDS read (a group of 16 lanes reads 4 rows x 16 columns, and lane i gets column i); chunk
+// c of row r sits in slot c ^ (2 (r & 3) + 8 ((r / 8) & 1..3)), so the 4 rows of a group and
+// neighbouring groups hit different banks.
+enum Epi { kOut, kGated, kGatedBwd, kStats, kProb };
+
+struct MmArgs {
+    const uint16_t *A;
+    const uint16_t *B;
+    uint64_t lda;   // elements
+    uint32_t ldb;
+    uint32_t M, N;  // tokens; columns of C that exist
+    uint32_t ktiles, tm, tn;
+
+    uint16_t *out;  // kOut, kGated: [M][ldo] BF16
+    uint64_t ldo;
+    uint32_t vec;   // out (and dH, dG, dU) can be accessed 8 bytes at a time
+    float *acc;     // kOut over several pieces: fp32 sums [M][N]
+    uint32_t acc_in, last;
+    const int64_t *labels;
+    int64_t ignore;
+    const float *scale;  // kOut: factor of each token (with labels), or null
+    uint64_t V;          // rows of the head
+
+    int act;
+    uint32_t f0, F;  // first row of the tensors in this piece, and all of them
+    const uint16_t *dH;
+    uint16_t *dG, *dU, *G;  // G: the piece's gradients at the projections [M][ldG], columns as the piece's rows
+    uint64_t lddh, ldg;
+    uint32_t ldG;
+
+    f32x2 *stat;  // kStats: (max, sum exp(z - max)) of each token and column tile, [M][ldstat]
+    uint32_t ldstat, stat0;
+    float *top;   // the label's logit
+    const float *lse;
+};
+
+// The four values of a fragment row to out[0..3], of which `n` exist.
+__device__ __forceinline__ void store4(uint16_t *out, const float (&v)[4], uint32_t n, bool vec) {
+    if (n >= 4 && vec) {
+        *reinterpret_cast<u32x2 *>(out) = (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    } else {
+#pragma unroll
+        for (uint32_t r = 0; r < 4; ++r)
+            if (r < n) out[r] = to_bf16(v[r]);
+    }
+}
+__device__ __forceinline__ void load4(const uint16_t *in, float (&v)[4], uint32_t n, bool vec) {
+    if (n >= 4 && vec) {
+        const u32x2 t = *reinterpret_cast<const u32x2 *>(in);
+        v[0] = bf16_value(static_cast<uint16_t>(t.x));
+        v[1] = bf16_value(static_cast<uint16_t>(t.x >> 16));
+        v[2] = bf16_value(static_cast<uint16_t>(t.y));
+        v[3] = bf16_value(static_cast<uint16_t>(t.y >> 16));
+    } else {
+#pragma unroll
+        for (uint32_t r = 0; r < 4; ++r) v[r] = r < n ? bf16_value(in[r]) : 0.f;
+    }
+}
+__device__ __forceinline__ uint32_t left(uint32_t n, uint32_t at) { return at < n ? n - at : 0u; }
+
+// Reference point of a sum of exponentials whose largest argument is m: 0 where m is infinite.
+__device__ __forceinline__ float exp_base(float m) { return fabsf(m) == __builtin_inff() ? 0.f : m; }
+
+template <int BM, int BN, int WM, int WN, bool NN, int EPI>
+__global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
+    constexpr int NW = WM * WN;
+    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr uint32_t ABYTES = BM * 128, BBYTES = BN * 128;  // one slice
+    constexpr int IA = ABYTES / 1024 / NW, IB = BBYTES / 1024 / NW;
+    static_assert(IA * NW * 1024 == ABYTES && IB * NW * 1024 == BBYTES, "whole copies");
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const uint32_t li = lane & 15, lg = lane >> 4;
+
+    // Workgroups go to the 8 XCDs in turn; give each XCD a run of consecutive tiles, and order the
+    // tiles in groups of GM token tiles, so that an XCD's workgroups share rows and columns in its L2.
+    const uint32_t all = p.tm * p.tn, q = all >> 3, rem = all & 7, xcd = blockIdx.x & 7;
+    const uint32_t lin = xcd * q + min(xcd, rem) + (blockIdx.x >> 3);
+    constexpr uint32_t GM = 8;
+    const uint32_t per = GM * p.tn, grp = lin / per, g0 = grp * GM, gm = min(GM, p.tm - g0);
+    const uint32_t in = lin - grp * per;
+    const uint32_t m0 = (g0 + in % gm) * BM, n0 = (in / gm) * BN;
+
+    // copies: this lane's byte offsets within A's and B's resources
+    const auto ra = wave_rsrc(p.A + static_cast<uint64_t>(m0) * p.lda, 0x7FFFFFF0u);
+    const auto rb = wave_rsrc(NN ? p.B : p.B + static_cast<uint64_t>(n0) * p.ldb, 0x7FFFFFF0u);
+    uint32_t va[IA], vb[IB];
+#pragma unroll
+    for (int i = 0; i < IA; ++i) {
+        const uint32_t r = (wave + NW * i) * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+        va[i] = min(r, p.M - 1 - m0) * static_cast<uint32_t>(p.lda) * 2u + c * 16u;  // rows past M repeat the last one
+    }
+#pragma unroll
+    for (int i = 0; i < IB; ++i) {
+        if constexpr (NN) {
+            constexpr uint32_t CH = BN / 8, RPI = 64 / CH;  // chunks of a row, rows of a copy
+            const uint32_t r = (wave + NW * i) * RPI + lane / CH;
+            const uint32_t c = (lane % CH) ^ (2 * (r & 3) + 8 * ((r >> 3) & (CH / 8 - 1)));
+            vb[i] = (r * p.ldb + min(n0 + c * 8, p.ldb - 8)) * 2u;  // columns past the piece repeat its last chunk
+        } else {
+            const uint32_t r = (wave + NW * i) * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+            vb[i] = r * p.ldb * 2u + c * 16u;
+        }
+    }
+    auto fetch = [&](uint32_t kt, uint32_t buf) {
+        unsigned char *da = smem + buf * ABYTES, *db = smem + 2 * ABYTES + buf * BBYTES;
+#pragma unroll
+        for (int i = 0; i < IA; ++i)
+            copy_to_lds(ra, da + (wave + NW * i) * 1024, va[i], kt * 128);
+        const uint32_t sb = NN ? kt * 128 * p.ldb : kt * 128;
+#pragma unroll
+        for (int i = 0; i < IB; ++i)
+            copy_to_lds(rb, db + (wave + NW * i) * 1024, vb[i], sb);
+    };
+
+    // fragment reads: byte offsets of this lane
+    const uint32_t fa = (wm * (BM / WM) + li) * 128 + ((lg ^ (li & 7)) * 16);
+    const uint32_t fb = (wn * (BN / WN) + li) * 128 + ((lg ^ (li & 7)) * 16);
+    uint32_t ft[FN];
+    if constexpr (NN) {
+        constexpr uint32_t CH = BN / 8;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t r = 8 * lg + (li >> 2);
+            const uint32_t c = (wn * (BN / WN) + 16 * j) / 8 + ((li & 3) >> 1);
+            ft[j] = r * (BN * 2) + (c ^ (2 * (r & 3) + 8 * (lg & (CH / 8 - 1)))) * 16 + (li & 1) * 8;
+        }
+    }
+
+    f32x4_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+
+    fetch(0, 0);
+    for (uint32_t kt = 0; kt < p.ktiles; ++kt) {
+        const uint32_t buf = kt & 1;
+        // this slice has arrived, and no wave still reads the buffer that the next one goes to
+        __builtin_amdgcn_s_waitcnt(0x0070);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (kt + 1 < p.ktiles) fetch(kt + 1, buf ^ 1);
+        const unsigned char *sa = smem + buf * ABYTES, *sb = smem + 2 * ABYTES + buf * BBYTES;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8_t xa[FM], xb[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                if constexpr (NN) {
+                    const unsigned char *at = sb + ft[j] + ks * 32 * BN * 2;
+                    const s16x4 lo = read_transposed(at);
+                    const s16x4 hi = read_transposed(at + 4 * BN * 2);
+                    xb[j] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                } else {
+                    xb[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sb + (fb ^ (ks * 64)) + j * 2048));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                xa[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sa + (fa ^ (ks * 64)) + i * 2048));
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[j], xa[i], acc[i][j], 0, 0, 0);
+        }
+    }
+
+    const uint32_t mw = m0 + wm * (BM / WM) + li, nw = n0 + wn * (BN / WN) + 4 * lg;  // of fragment (0, 0)
+    if constexpr (EPI == kOut) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const uint32_t m = mw + 16 * i;
+            if (m >= p.M) continue;
+            float s = 1.f;
+            bool skip = false;
+            if (p.last && p.scale) {
+                const int64_t lab = p.labels[m];
+                skip = lab == p.ignore;
+                s = lab >= 0 && static_cast<uint64_t>(lab) < p.V ? p.scale[m] : __builtin_nanf("");
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const uint32_t n = nw + 16 * j, have = left(p.N, n);
+                if (have == 0) continue;
+                float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                f32x4_t *sum = reinterpret_cast<f32x4_t *>(p.acc + static_cast<uint64_t>(m) * p.ldb + n);
+                if (p.acc_in) {
+                    const f32x4_t t = *sum;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] += t[r];
+                }
+                if (!p.last) {
+                    *sum = (f32x4_t){v[0], v[1], v[2], v[3]};
+                    continue;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = skip ? 0.f : v[r] * s;
+                store4(p.out + m * p.ldo + n, v, have, p.vec);
+            }
+        }
+    } else if constexpr (EPI == kGated || EPI == kGatedBwd) {
+        static_assert(FN % 2 == 0, "a wave holds whole pairs of gate and up fragments");
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const uint32_t m = mw + 16 * i;
+            if (m >= p.M) continue;
+#pragma unroll
+            for (int j = 0; j < FN; j += 2) {
+                const uint32_t n = nw + 16 * j;                    // gate's row of the piece; up's is n + 16
+                const uint32_t f = p.f0 + (n >> 5) * 16 + (n & 15);  // their row in the tensors
+                const uint32_t have = left(p.F, f);
+                if constexpr (EPI == kGated) {
+                    if (have == 0) continue;
+                    float h[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) h[r] = activation(p.act, acc[i][j][r], nullptr) * acc[i][j + 1][r];
+                    store4(p.out + m * p.ldo + f, h, have, p.vec);
+                } else {
+                    float dh[4] = {0.f, 0.f, 0.f, 0.f}, dg[4], du[4];
+                    if (have) load4(p.dH + m * p.lddh + f, dh, have, p.vec);
+#pragma unroll
+                    for (uint32_t r = 0; r < 4; ++r) {
+                        float d;
+                        const float a = activation(p.act, acc[i][j][r], &d);
+                        // rows past the tensors' end are part of the next product's reduction: zeros
+                        dg[r] = r < have ? dh[r] * acc[i][j + 1][r] * d : 0.f;
+                        du[r] = r < have ? dh[r] * a : 0.f;
+                    }
+                    if (n < p.ldG) {
+                        uint16_t *G = p.G + static_cast<uint64_t>(m) * p.ldG + n;
+                        store4(G, dg, 4, true);
+                        store4(G + 16, du, 4, true);
+                    }
+                    if (have && p.dG) store4(p.dG + m * p.ldg + f, dg, have, p.vec);
+                    if (have && p.dU) store4(p.dU + m * p.ldg + f, du, have, p.vec);
+                }
+            }
+        }
+    } else if constexpr (EPI == kStats) {
+        // each wave's part of a token's columns, then the workgroup's, in a fixed order
+        f32x2 *part = reinterpret_cast<f32x2 *>(smem);  // [BM][WN]
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const uint32_t m = mw + 16 * i;
+            int64_t lab = -1;
+            if (m < p.M) lab = p.labels[m] - p.f0;  // the label's column in this piece, if it is one
+            float mx = -__builtin_inff();
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (uint32_t r = 0; r < 4; ++r)
+                    if (nw + 16 * j + r < p.N) mx = fmaxf(mx, acc[i][j][r]);
+            mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            const float base = exp_base(mx);
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (uint32_t r = 0; r < 4; ++r) {
+                    const uint32_t n = nw + 16 * j + r;
+                    if (n < p.N) {
+                        s += __expf(acc[i][j][r] - base);
+                        if (static_cast<int64_t>(n) == lab) p.top[m] = acc[i][j][r];
+                    }
+                }
+            s += __shfl_xor(s, 16, 64);
+            s += __shfl_xor(s, 32, 64);
+            if (lg == 0) part[(wm * (BM / WM) + 16 * i + li) * WN + wn] = (f32x2){mx, s};
+        }
+        __syncthreads();
+        if (tid < BM && m0 + tid < p.M) {
+            float mx = -__builtin_inff(), s = 0.f;
+#pragma unroll
+            for (int w = 0; w < WN; ++w) mx = fmaxf(mx, part[tid * WN + w][0]);
+            const float base = exp_base(mx);
+#pragma unroll
+            for (int w = 0; w < WN; ++w) {
+                const f32x2 t = part[tid * WN + w];
+                if (t[1] != 0.f) s += t[1] * __expf(exp_base(t[0]) - base);
+            }
+            p.stat[static_cast<uint64_t>(m0 + tid) * p.ldstat + p.stat0 + n0 / BN] = (f32x2){mx, s};
+        }
+    } else if constexpr (EPI == kProb) {
+        // exp(z - lse) - [label], BF16, the columns of the next product's reduction (zeros past V)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const uint32_t m = mw + 16 * i;
+            if (m >= p.M) continue;
+            const int64_t lab = p.labels[m] - p.f0;
+            const float lse = p.lse[m];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const uint32_t n = nw + 16 * j;
+                float v[4];
+#pragma unroll
+                for (uint32_t r = 0; r < 4; ++r)
+                    v[r] = n + r < p.N ? __expf(acc[i][j][r] - lse) - (static_cast<int64_t>(n + r) == lab ? 1.f : 0.f) : 0.f;
+                store4(p.G + static_cast<uint64_t>(m) * p.ldG + n, v, 4, true);
+            }
+        }
+    }
+}
+
+// The parts of a token's softmax statistics joined in order, one wave a token: lse, and the loss.
+__global__ __launch_bounds__(256) void k_xent_join(const f32x2 *__restrict__ stat, uint32_t parts, uint32_t M,
+                                                   const int64_t *__restrict__ labels, int64_t ignore, uint64_t V,
+                                                   const float *__restrict__ top, float *__restrict__ loss,
+                                                   float *__restrict__ lse) {
+    const uint32_t m = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (m >= M) return;
+    const f32x2 *row = stat + static_cast<uint64_t>(m) * parts;
+    float mx = -__builtin_inff();
+    for (uint32_t i = lane; i < parts; i += 64) mx = fmaxf(mx, row[i][0]);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+    const float base = exp_base(mx);
+    float s = 0.f;
+    for (uint32_t i = lane; i < parts; i += 64) {
+        const f32x2 t = row[i];
+        if (t[1] != 0.f) s += t[1] * __expf(exp_base(t[0]) - base);
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+    if (lane == 0) {
+        const float l = base + logf(s);
+        const int64_t lab = labels[m];
+        lse[m] = l;
+        loss[m] = lab == ignore ? 0.f
+                  : lab >= 0 && static_cast<uint64_t>(lab) < V ? l - top[m]
+                                                               : __builtin_nanf("");
+    }
+}
+
+// ------------------------------------------------------------------------------- host side
+
+uint32_t grid_for(uint64_t items, uint32_t per) {
+    return static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>((items + per - 1) / per, 65536)));
+}
+
+cbk_status unpack(const cbk_tensor &t, uint64_t row0, uint64_t nrows, uint64_t rows_out, uint32_t pair, uint64_t Kp,
+                  uint16_t *out, hipStream_t s) {
+    const UnpackArgs a{t.words, t.codebook, t.b, t.U, static_cast<uint32_t>(t.cols), static_cast<uint32_t>(Kp), row0,
+                       static_cast<uint32_t>(nrows), static_cast<uint32_t>(rows_out), pair, out};
+    hipLaunchKernelGGL(k_unpack_generic, dim3(grid_for(rows_out * (Kp / 4), 256)), dim3(256), 0, s, a);
+    return launched();
+}
+
+template <int BM, int BN, int WM, int WN, bool NN, int EPI>
+cbk_status mm_tile(MmArgs &p, uint32_t columns, hipStream_t s) {
+    constexpr uint32_t lds = 2 * (BM + BN) * 128;
+    if (!allow_lds(k_mm<BM, BN, WM, WN, NN, EPI>, lds)) return CBK_E_HIP;
+    p.tm = ceil_div(p.M, BM);
+    p.tn = ceil_div(columns, BN);
+    hipLaunchKernelGGL((k_mm<BM, BN, WM, WN, NN, EPI>), dim3(p.tm * p.tn), dim3(64 * WM * WN), lds, s, p);
+    return launched();
+}
+
+// `columns`: the columns of C to cover.
+template <bool NN, int EPI>
+cbk_status mm(MmArgs &p, uint32_t columns, hipStream_t s) {
+    return mm_tile<128, 128, 2, 2, NN, EPI>(p, columns, s);
+}
+
+// The tokens' side of a product: used as it is if the copies to LDS can read whole 64-wide slices
+// of it (16-byte aligned rows, no ragged end, and 256 rows within 31 bits), else padded into P.
+cbk_status token_side(MmArgs &p, const uint16_t *X, uint64_t ld, uint64_t T, uint64_t K, uint64_t Kp, uint16_t *P,
+                      hipStream_t s) {
+    if (K == Kp && aligned_to(X, 16) && ld % 8 == 0 && ld <= (uint64_t(1) << 21)) {
+        p.A = X;
+        p.lda = ld;
+        return CBK_OK;
+    }
+    p.A = P;
+    p.lda = Kp;
+    hipLaunchKernelGGL(k_pad_rows, dim3(grid_for(T * (Kp / 4), 256)), dim3(256), 0, s, X, ld, T, static_cast<uint32_t>(K),
+                       static_cast<uint32_t>(Kp), P);
+    return launched();
+}
+
+bool vec8(const void *p, uint64_t ld) { return aligned_to(p, 8) && ld % 4 == 0; }
+
+uint64_t up64(uint64_t n) { return (n + 63) / 64 * 64; }
+
+#define CBK_TRY(x)                          \
+    do {                                    \
+        const cbk_status st_ = (x);         \
+        if (st_ != CBK_OK) return st_;      \
+    } while (0)
+
+template <typename T>
+T *at(void *ws, uint64_t offset) { return reinterpret_cast<T *>(static_cast<unsigned char *>(ws) + offset); }
+
+cbk_status zero_rows(uint16_t *out, uint64_t ld, uint64_t T, uint64_t n, hipStream_t s) {
+    hipLaunchKernelGGL(k_zero_rows, dim3(grid_for(T * n, 256)), dim3(256), 0, s, out, ld, T, static_cast<uint32_t>(n));
+    return launched();
+}
+
+// Decoded rows of a piece that holds `nrows` rows of each of its tensors, rounded up to what a
+// reduction over them takes.
+uint64_t piece_rows(uint64_t nrows, bool pair) { return pair ? up64(2 * ((nrows + 15) / 16 * 16)) : up64(nrows); }
+
+cbk_status unpack_piece(const cbk_tensor *const *ts, int count, uint64_t row0, uint64_t nrows, uint64_t Kp, uint16_t *W,
+                        hipStream_t s) {
+    const uint64_t rows = piece_rows(nrows, count == 2);
+    for (int i = 0; i < count; ++i)
+        CBK_TRY(unpack(*ts[i], row0, nrows, count == 2 ? rows / 2 : rows, count == 2 ? i + 1 : 0, Kp, W, s));
+    return CBK_OK;
+}
+
+}  // namespace
+
+cbk_status launch_linear(const cbk_tensor &t, const uint16_t *X, uint64_t ldx, uint64_t T, uint16_t *Y, uint64_t ldy,
+                         void *ws, hipStream_t s) {
+    const NnPlan pl = nn_plan(NnOp::linear, t.rows, t.cols, T);
+    const cbk_tensor *ts[1] = {&t};
+    for (uint64_t c = 0; c < T; c += pl.Tc) {
+        MmArgs p{};
+        p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
+        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, t.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        for (uint64_t r = 0; r < t.rows; r += pl.rows) {
+            const uint64_t n = std::min(pl.rows, t.rows - r);
+            CBK_TRY(unpack_piece(ts, 1, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
+            p.B = at<uint16_t>(ws, pl.w);
+            p.ldb = static_cast<uint32_t>(pl.Kp);
+            p.N = static_cast<uint32_t>(n);
+            p.ktiles = static_cast<uint32_t>(pl.Kp / 64);
+            p.out = Y + c * ldy + r;
+            p.ldo = ldy;
+            p.vec = vec8(p.out, ldy);
+            p.last = 1;
+            CBK_TRY((mm<false, kOut>(p, p.N, s)));
+        }
+    }
+    return CBK_OK;
+}
+
+namespace {
+
+// One piece's part of dX: the reduction over the piece's rows, summed over the pieces in fp32.
+cbk_status gradient_piece(MmArgs &p, const NnPlan &pl, uint64_t rows, uint64_t cols, bool first, bool last, uint16_t *dX,
+                          uint64_t lddx, void *ws, hipStream_t s) {
+    p.B = at<uint16_t>(ws, pl.w);
+    p.ldb = static_cast<uint32_t>(pl.Kp);
+    p.N = static_cast<uint32_t>(cols);
+    p.ktiles = static_cast<uint32_t>(rows / 64);
+    p.acc = at<float>(ws, pl.acc);
+    p.acc_in = !first;
+    p.last = last;
+    p.out = dX;
+    p.ldo = lddx;
+    p.vec = vec8(dX, lddx);
+    return mm<true, kOut>(p, p.N, s);
+}
+
+}  // namespace
+
+cbk_status launch_linear_dx(const cbk_tensor &t, const uint16_t *dY, uint64_t lddy, uint64_t T, uint16_t *dX,
+                            uint64_t lddx, void *ws, hipStream_t s) {
+    if (t.rows == 0) return zero_rows(dX, lddx, T, t.cols, s);
+    const NnPlan pl = nn_plan(NnOp::linear, t.rows, t.cols, T);
+    const cbk_tensor *ts[1] = {&t};
+    for (uint64_t c = 0; c < T; c += pl.Tc) {
+        MmArgs p{};
+        p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
+        for (uint64_t r = 0; r < t.rows; r += pl.rows) {
+            const uint64_t n = std::min(pl.rows, t.rows - r);
+            CBK_TRY(token_side(p, dY + c * lddy + r, lddy, p.M, n, up64(n), at<uint16_t>(ws, pl.pack), s));
+            CBK_TRY(unpack_piece(ts, 1, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
+            CBK_TRY(gradient_piece(p, pl, piece_rows(n, false), t.cols, r == 0, r + n == t.rows, dX + c * lddx, lddx, ws, s));
+        }
+    }
+    return CBK_OK;
+}
+
+cbk_status launch_ffn(const cbk_tensor &gate, const cbk_tensor &up, int act, const uint16_t *X, uint64_t ldx, uint64_t T,
+                      uint16_t *H, uint64_t ldh, void *ws, hipStream_t s) {
+    const NnPlan pl = nn_plan(NnOp::ffn, gate.rows, gate.cols, T);
+    const cbk_tensor *ts[2] = {&gate, &up};
+    for (uint64_t c = 0; c < T; c += pl.Tc) {
+        MmArgs p{};
+        p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
+        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, gate.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        for (uint64_t r = 0; r < gate.rows; r += pl.rows) {
+            const uint64_t n = std::min(pl.rows, gate.rows - r);
+            CBK_TRY(unpack_piece(ts, 2, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
+            p.B = at<uint16_t>(ws, pl.w);
+            p.ldb = static_cast<uint32_t>(pl.Kp);
+            p.N = static_cast<uint32_t>(piece_rows(n, true));
+            p.ktiles = static_cast<uint32_t>(pl.Kp / 64);
+            p.act = act;
+            p.f0 = static_cast<uint32_t>(r);
+            p.F = static_cast<uint32_t>(gate.rows);
+            p.out = H + c * ldh;
+            p.ldo = ldh;
+            p.vec = vec8(p.out, ldh);
+            CBK_TRY((mm<false, kGated>(p, p.N, s)));
+        }
+    }
+    return CBK_OK;
+}
+
+cbk_status launch_ffn_bwd(const cbk_tensor &gate, const cbk_tensor &up, int act, const uint16_t *X, uint64_t ldx,
+                          const uint16_t *dH, uint64_t lddh, uint64_t T, uint16_t *dX, uint64_t lddx, uint16_t *dG,
+                          uint16_t *dU, uint64_t ldg, void *ws, hipStream_t s) {
+    if (gate.rows == 0) return gate.cols == 0 ? CBK_OK : zero_rows(dX, lddx, T, gate.cols, s);
+    const NnPlan pl = nn_plan(NnOp::ffn, gate.rows, gate.cols, T);
+    const cbk_tensor *ts[2] = {&gate, &up};
+    for (uint64_t c = 0; c < T; c += pl.Tc) {
+        MmArgs p{};
+        p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
+        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, gate.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        for (uint64_t r = 0; r < gate.rows; r += pl.rows) {
+            const uint64_t n = std::min(pl.rows, gate.rows - r), rows = piece_rows(n, true);
+            CBK_TRY(unpack_piece(ts, 2, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
+            MmArgs a = p;
+            a.B = at<uint16_t>(ws, pl.w);
+            a.ldb = static_cast<uint32_t>(pl.Kp);
+            a.N = static_cast<uint32_t>(rows);
+            a.ktiles = static_cast<uint32_t>(pl.Kp / 64);
+            a.act = act;
+            a.f0 = static_cast<uint32_t>(r);
+            a.F = static_cast<uint32_t>(gate.rows);
+            a.dH = dH + c * lddh;
+            a.lddh = lddh;
+            a.dG = dG ? dG + c * ldg : nullptr;
+            a.dU = dU ? dU + c * ldg : nullptr;
+            a.ldg = ldg;
+            a.vec = vec8(a.dH, lddh) && (!dG || vec8(a.dG, ldg)) && (!dU || vec8(a.dU, ldg));
+            a.G = at<uint16_t>(ws, pl.g);
+            a.ldG = static_cast<uint32_t>(rows);
+            CBK_TRY((mm<false, kGatedBwd>(a, a.N, s)));
+            if (gate.cols == 0) continue;
+            MmArgs d{};
+            d.M = p.M;
+            d.A = a.G;
+            d.lda = a.ldG;
+            CBK_TRY(gradient_piece(d, pl, rows, gate.cols, r == 0, r + n == gate.rows, dX + c * lddx, lddx, ws, s));
+        }
+    }
+    return CBK_OK;
+}
+
+cbk_status launch_xent(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, const int64_t *labels, uint64_t T,
+                       int64_t ignore, float *loss, float *lse, void *ws, hipStream_t s) {
+    const NnPlan pl = nn_plan(NnOp::xent, head.rows, head.cols, T);
+    const cbk_tensor *ts[1] = {&head};
+    for (uint64_t c = 0; c < T; c += pl.Tc) {
+        MmArgs p{};
+        p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
+        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, head.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        p.stat = at<f32x2>(ws, pl.stat);
+        p.top = at<float>(ws, pl.top);
+        p.labels = labels + c;
+        constexpr uint32_t kTile = 128;
+        p.ldstat = 0;
+        for (uint64_t r = 0; r < head.rows; r += pl.rows) p.ldstat += ceil_div(std::min(pl.rows, head.rows - r), kTile);
+        for (uint64_t r = 0; r < head.rows; r += pl.rows) {
+            const uint64_t n = std::min(pl.rows, head.rows - r);
+            CBK_TRY(unpack_piece(ts, 1, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
+            p.B = at<uint16_t>(ws, pl.w);
+            p.ldb = static_cast<uint32_t>(pl.Kp);
+            p.N = static_cast<uint32_t>(n);
+            p.ktiles = static_cast<uint32_t>(pl.Kp / 64);
+            p.f0 = static_cast<uint32_t>(r);
+            CBK_TRY((mm<false, kStats>(p, p.N, s)));
+            p.stat0 += ceil_div(n, kTile);
+        }
+        hipLaunchKernelGGL(k_xent_join, dim3((p.M + 3) / 4), dim3(256), 0, s, p.stat, p.ldstat, p.M, p.labels, ignore,
+                           head.rows, p.top, loss + c, lse + c);
+        CBK_TRY(launched());
+    }
+    return CBK_OK;
+}
+
+cbk_status launch_xent_bwd(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, const int64_t *labels,
+                           const float *lse, const float *dloss, uint64_t T, int64_t ignore, uint16_t *dX,
+                           uint64_t lddx, void *ws, hipStream_t s) {
+    const NnPlan pl = nn_plan(NnOp::xent, head.rows, head.cols, T);
+    const cbk_tensor *ts[1] = {&head};
+    for (uint64_t c = 0; c < T; c += pl.Tc) {
+        MmArgs p{};
+        p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
+        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, head.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        p.labels = labels + c;
+        for (uint64_t r = 0; r < head.rows; r += pl.rows) {
+            const uint64_t n = std::min(pl.rows, head.rows - r), rows = piece_rows(n, false);
+            CBK_TRY(unpack_piece(ts, 1, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
+            MmArgs a = p;
+            a.B = at<uint16_t>(ws, pl.w);
+            a.ldb = static_cast<uint32_t>(pl.Kp);
+            a.N = static_cast<uint32_t>(n);
+            a.ktiles = static_cast<uint32_t>(pl.Kp / 64);
+            a.f0 = static_cast<uint32_t>(r);
+            a.lse = lse + c;
+            a.G = at<uint16_t>(ws, pl.g);
+            a.ldG = static_cast<uint32_t>(pl.Rp);
+            CBK_TRY((mm<false, kProb>(a, static_cast<uint32_t>(rows), s)));
+            MmArgs d{};
+            d.M = p.M;
+            d.A = a.G;
+            d.lda = a.ldG;
+            d.labels = p.labels;
+            d.ignore = ignore;
+            d.scale = dloss + c;
+            d.V = head.rows;
+            CBK_TRY(gradient_piece(d, pl, rows, head.cols, r == 0, r + n == head.rows, dX + c * lddx, lddx, ws, s));
+        }
+    }
+    return CBK_OK;
+}
+
+}  // namespace cbk
