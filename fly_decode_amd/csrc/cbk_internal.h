@@ -47,19 +47,23 @@ cbk_status launch_ec_gemv(const cbk_ec_tensor *ts, const uint8_t *const *indexes
 cbk_status launch_ec_index(const cbk_ec_tensor *t, uint8_t *index, hipStream_t s);
 
 // Operators on any number of tokens (cbk_nn.hip).  A plan says how a call is cut up and where its
-// scratch lies in the workspace; it depends on the sizes alone, so that the workspace's size is
-// known without a GPU.  Tokens are taken Tc at a time, the rows of the tensors in pieces.
+// scratch lies in the workspace; it depends on the tensors and the number of tokens alone, so that
+// the workspace's size is known without a GPU.  Tokens are taken Tc at a time, the rows of the
+// tensors in pieces.
 struct NnPlan {
     uint64_t Kp;      // columns of a decoded row in the workspace: cols rounded up to 64, at least 64
     uint64_t Tc;      // tokens of a chunk
-    uint64_t Rp;      // decoded rows of a piece (of both tensors, for the feed-forward block), a multiple of 256
     uint64_t rows;    // rows of one tensor in a piece
+    uint64_t Rp;      // columns of a piece's gradients (those of both tensors, for the feed-forward block)
     uint64_t pieces;
-    uint64_t pack, w, g, acc, stat, top;  // offsets in bytes
+    uint32_t fused;   // 0: pieces are decoded into memory; else the token tile of k_fused: 16, 64, 128 or 256
+    uint32_t grid;    // k_fused: most workgroups
+    uint64_t pack, w, part, g, acc, stat, top;  // offsets in bytes
     uint64_t bytes;
 };
 enum class NnOp { linear, ffn, xent };
-NnPlan nn_plan(NnOp op, uint64_t rows, uint64_t cols, uint64_t tokens);
+NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens);
+uint32_t nn_fused_lds(uint32_t b, uint32_t bm, uint32_t count);
 
 cbk_status launch_linear(const cbk_tensor &t, const uint16_t *X, uint64_t ldx, uint64_t T, uint16_t *Y, uint64_t ldy,
                          void *ws, hipStream_t s);

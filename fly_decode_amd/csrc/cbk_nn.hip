@@ -13,39 +13,23 @@
 
 #include <algorithm>
 
-#include "cbk_device.h"
+#include "cbk_nn_device.h"
 
 namespace cbk {
 namespace {
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-#define CBK_LDS __attribute__((address_space(3)))
+
+#define CBK_TRY(x)                          \
+    do {                                    \
+        const cbk_status st_ = (x);         \
+        if (st_ != CBK_OK) return st_;      \
+    } while (0)
 
 inline uint32_t ceil_div(uint64_t n, uint64_t m) { return static_cast<uint32_t>((n + m - 1) / m); }
 inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // ------------------------------------------------------------------------------- small pieces
-
-// Copies 16 bytes a lane from the resource (at the lane's voff plus the wave's soff) straight into
-// LDS, lane l to dst + 16 l; dst is the same in every lane.  The wave's vmcnt counts it.  The
-// host's pass over this file does not know this chip's wide copies and transposing reads, so it
-// gets empty bodies.
-__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, unsigned char *dst, uint32_t voff, uint32_t soff) {
-#ifdef __HIP_DEVICE_COMPILE__
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (CBK_LDS void *)(dst), 16, static_cast<int>(voff), static_cast<int>(soff), 0, 0);
-#endif
-}
-
-// The transposing 64-bit LDS read: the 16 lanes of a group read 4 rows of 16 BF16 (lane s the 4
-// values at row s / 4, columns 4 (s % 4)..), and lane i gets column i of the 4 rows.
-__device__ __forceinline__ s16x4 read_transposed(const unsigned char *src) {
-#ifdef __HIP_DEVICE_COMPILE__
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((CBK_LDS s16x4 *)(src));
-#else
-    return s16x4{};
-#endif
-}
 
 // fp32 to BF16, to nearest even (NaN stays NaN).
 __device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
@@ -102,13 +86,19 @@ __global__ __launch_bounds__(256) void k_zero_rows(uint16_t *__restrict__ out, u
 // nrows are zero.  `pair` 0: row f goes to row f.  1 and 2: the gate and up tensors share the
 // piece, 16 rows of each in turn (row f to 32 (f / 16) + 16 (pair - 1) + f % 16), so that a wave
 // of k_mm has a column's gate and up sums in the same lanes.
-struct UnpackArgs {
+struct UnpackTensor {
     const uint32_t *words;
     const uint16_t *cb;
-    uint32_t b, U, cols, Kp;
+    uint32_t U, nchunks;
+};
+struct UnpackArgs {
+    UnpackTensor t[2];
+    uint32_t b, cols, Kp;
     uint64_t row0;
     uint32_t nrows, rows_out, pair;
     uint16_t *out;
+    float inv_cols;
+    uint32_t steps;
 };
 
 __device__ __forceinline__ uint32_t piece_row(uint32_t f, uint32_t pair) {
@@ -117,6 +107,7 @@ __device__ __forceinline__ uint32_t piece_row(uint32_t f, uint32_t pair) {
 
 // Any width, any number of columns: a thread per 4 columns.
 __global__ __launch_bounds__(256) void k_unpack_generic(const UnpackArgs a) {
+    const UnpackTensor &T = a.t[0];
     const uint64_t n = static_cast<uint64_t>(a.rows_out) * (a.Kp / 4), stride = static_cast<uint64_t>(gridDim.x) * blockDim.x;
     for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
         const uint32_t f = static_cast<uint32_t>(i / (a.Kp / 4)), k = static_cast<uint32_t>(i - static_cast<uint64_t>(f) * (a.Kp / 4)) * 4;
@@ -125,11 +116,105 @@ __global__ __launch_bounds__(256) void k_unpack_generic(const UnpackArgs a) {
         for (int j = 0; j < 4; ++j) {
             v[j] = 0;
             if (f < a.nrows && k + j < a.cols) {
-                const uint32_t idx = stream_field(a.words, a.b, (a.row0 + f) * a.cols + k + j);
-                v[j] = idx < a.U ? a.cb[idx] : kCorrupt;
+                const uint32_t idx = stream_field(T.words, a.b, (a.row0 + f) * a.cols + k + j);
+                v[j] = idx < T.U ? T.cb[idx] : kCorrupt;
             }
         }
         *reinterpret_cast<u32x2 *>(a.out + static_cast<uint64_t>(piece_row(f, a.pair)) * a.Kp + k) = (u32x2){v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
+    }
+}
+
+// The zeros of a piece: columns [cols, Kp) of its rows, and its rows past nrows.
+__global__ __launch_bounds__(256) void k_unpack_pad(const UnpackArgs a) {
+    for (uint32_t f = blockIdx.x; f < a.rows_out; f += gridDim.x)
+        for (uint32_t pr = a.pair ? 1 : 0; pr <= a.pair; ++pr) {
+            uint16_t *row = a.out + static_cast<uint64_t>(piece_row(f, pr)) * a.Kp;
+            for (uint32_t k = (f < a.nrows ? a.cols : 0) + threadIdx.x; k < a.Kp; k += blockDim.x) row[k] = 0;
+        }
+}
+
+// Widths 1 to 15: the stream is decoded in its own order, as by k_decode_fast (a wave takes steps
+// of 64 units of 64 fields: coalesced loads, transposition through its LDS stage, gathers from the
+// codebook in LDS), and each run of 8 fields, or each field where a row's length is no multiple of
+// 8, goes to its row's place in the piece.  Both tensors of a pair go in one launch (blockIdx.y).
+// row0 * cols is a multiple of 128, so a piece starts on a 16-byte chunk of the stream.  The stores keep the ordinary cache
+// policy: the matrix product reads the piece next.
+constexpr int kUnpackWaves = 4;
+
+template <int B, bool RUNS>
+__global__ __launch_bounds__(64 * kUnpackWaves) void k_unpack(const UnpackArgs a) {
+    using G = U64<B>;
+    constexpr int NT = 64 * kUnpackWaves;
+    constexpr uint32_t kUnit = 2 * 64 + 16;  // LDS bytes per decoded unit (16 bytes of padding)
+    __shared__ __attribute__((aligned(16))) uint16_t cbl[Table<B>::SIZE];
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    const UnpackTensor &T = a.t[blockIdx.y];
+    const uint32_t pair = a.pair ? blockIdx.y + 1 : 0;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr uint32_t kStage = G::STAGE_CHUNKS * 16 > 64 * kUnit ? G::STAGE_CHUNKS * 16 : 64 * kUnit;
+    unsigned char *stb = smem + wave * kStage;
+    u32x4 *stage = reinterpret_cast<u32x4 *>(stb);
+    const uint64_t unit0 = a.row0 * a.cols / 64;
+    const u32x4 *w4 = reinterpret_cast<const u32x4 *>(T.words) + unit0 * G::UD / 4;
+    const uint64_t nchunks = T.nchunks - unit0 * G::UD / 4;
+    const uint32_t NW = gridDim.x * kUnpackWaves, gw = blockIdx.x * kUnpackWaves + wave;
+    const uint32_t fields = a.nrows * a.cols;
+
+    CbStage<B, NT> cs;
+    cs.issue(T.cb, T.U, w4, tid);
+    issue_barrier();
+    u32x4 nxt[G::LPL];
+    load_step<B>(nxt, w4, gw * 64, 64, nchunks, gw < a.steps, lane);
+    cs.store(cbl, T.U, tid);
+    lds_barrier();
+
+    for (uint32_t st = gw; st < a.steps; st += NW) {
+        const uint32_t us = st * 64;
+        uint32_t d[G::UD];
+        transpose_step<B>(d, nxt, stage, us, lane);
+        if (st + NW < a.steps) load_step<B>(nxt, w4, (st + NW) * 64, 64, nchunks, true, lane);
+        uint32_t wv[2][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wv[0][i] = unit_gather<B>(cbl, d, i);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            if (g + 1 < 8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) wv[(g + 1) & 1][i] = unit_gather<B>(cbl, d, 8 * (g + 1) + i);
+            }
+            const uint32_t *w = wv[g & 1];
+            *reinterpret_cast<u32x4 *>(stb + lane * kUnit + 16 * g) =
+                (u32x4){w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16)};
+        }
+        asm volatile("" ::: "memory");
+        // Row and column of field i of the piece: with at most 2^15 rows the product with the
+        // rounded reciprocal is off by less than 2^15 * 2^-22, so one step mends the row.
+        auto place = [&](uint32_t i) {
+            uint32_t r = static_cast<uint32_t>(static_cast<float>(i) * a.inv_cols);
+            int32_t k = static_cast<int32_t>(i - r * a.cols);
+            if (k < 0) {
+                --r;
+                k += a.cols;
+            } else if (k >= static_cast<int32_t>(a.cols)) {
+                ++r;
+                k -= a.cols;
+            }
+            return a.out + static_cast<uint64_t>(piece_row(r, pair)) * a.Kp + k;
+        };
+        if constexpr (RUNS) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t q = j * 64 + lane, i = us * 64 + q * 8;
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(stb + (q >> 3) * kUnit + (q & 7) * 16);
+                if (i < fields) *reinterpret_cast<u32x4 *>(place(i)) = v;
+            }
+        } else {
+            for (int j = 0; j < 64; ++j) {
+                const uint32_t i = (us + j) * 64 + lane;
+                if (i < fields) *place(i) = *reinterpret_cast<const uint16_t *>(stb + j * kUnit + lane * 2);
+            }
+        }
+        asm volatile("" ::: "memory");
     }
 }
 
@@ -163,8 +248,8 @@ struct MmArgs {
     uint16_t *out;  // kOut, kGated: [M][ldo] BF16
     uint64_t ldo;
     uint32_t vec;   // out (and dH, dG, dU) can be accessed 8 bytes at a time
-    float *acc;     // kOut over several pieces: fp32 sums [M][N]
-    uint32_t acc_in, last;
+    float *acc;     // kOut over several pieces: fp32 sums [M][ldacc]
+    uint32_t ldacc, acc_in, last;
     const int64_t *labels;
     int64_t ignore;
     const float *scale;  // kOut: factor of each token (with labels), or null
@@ -209,6 +294,65 @@ __device__ __forceinline__ uint32_t left(uint32_t n, uint32_t at) { return at < 
 
 // Reference point of a sum of exponentials whose largest argument is m: 0 where m is infinite.
 __device__ __forceinline__ float exp_base(float m) { return fabsf(m) == __builtin_inff() ? 0.f : m; }
+
+// What the operators do with four neighbouring sums (columns n..n + 3) of token m.
+__device__ __forceinline__ void emit_out(const MmArgs &p, uint32_t m, uint32_t n, float (&v)[4]) {
+    const uint32_t have = left(p.N, n);
+    if (have == 0) return;
+    f32x4_t *sum = reinterpret_cast<f32x4_t *>(p.acc + static_cast<uint64_t>(m) * p.ldacc + n);
+    if (p.acc_in) {
+        const f32x4_t t = *sum;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += t[r];
+    }
+    if (!p.last) {
+        *sum = (f32x4_t){v[0], v[1], v[2], v[3]};
+        return;
+    }
+    if (p.scale) {
+        const int64_t lab = p.labels[m];
+        const float f = lab >= 0 && static_cast<uint64_t>(lab) < p.V ? p.scale[m] : __builtin_nanf("");
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = lab == p.ignore ? 0.f : v[r] * f;
+    }
+    store4(p.out + m * p.ldo + n, v, have, p.vec);
+}
+__device__ __forceinline__ void emit_gated(const MmArgs &p, uint32_t m, uint32_t f, const float (&g)[4], const float (&u)[4]) {
+    const uint32_t have = left(p.F, f);
+    if (have == 0) return;
+    float h[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) h[r] = activation(p.act, g[r], nullptr) * u[r];
+    store4(p.out + m * p.ldo + f, h, have, p.vec);
+}
+// G: where the piece's dG and dU go (gcol, ucol).  Rows past the tensors' end are part of the next
+// product's reduction: zeros.
+__device__ __forceinline__ void emit_gated_bwd(const MmArgs &p, uint32_t m, uint32_t f, uint32_t gcol, uint32_t ucol,
+                                               const float (&g)[4], const float (&u)[4]) {
+    const uint32_t have = left(p.F, f);
+    float dh[4] = {0.f, 0.f, 0.f, 0.f}, dg[4], du[4];
+    if (have) load4(p.dH + m * p.lddh + f, dh, have, p.vec);
+#pragma unroll
+    for (uint32_t r = 0; r < 4; ++r) {
+        float d;
+        const float a = activation(p.act, g[r], &d);
+        dg[r] = r < have ? dh[r] * u[r] * d : 0.f;
+        du[r] = r < have ? dh[r] * a : 0.f;
+    }
+    uint16_t *G = p.G + static_cast<uint64_t>(m) * p.ldG;
+    store4(G + gcol, dg, 4, true);
+    store4(G + ucol, du, 4, true);
+    if (have && p.dG) store4(p.dG + m * p.ldg + f, dg, have, p.vec);
+    if (have && p.dU) store4(p.dU + m * p.ldg + f, du, have, p.vec);
+}
+// exp(z - lse) - [label], the columns of the next product's reduction (zeros past the piece).
+__device__ __forceinline__ void emit_prob(const MmArgs &p, uint32_t m, uint32_t n, int64_t lab, float lse, const float (&z)[4]) {
+    float v[4];
+#pragma unroll
+    for (uint32_t r = 0; r < 4; ++r)
+        v[r] = n + r < p.N ? __expf(z[r] - lse) - (static_cast<int64_t>(n + r) == lab ? 1.f : 0.f) : 0.f;
+    store4(p.G + static_cast<uint64_t>(m) * p.ldG + n, v, 4, true);
+}
 
 template <int BM, int BN, int WM, int WN, bool NN, int EPI>
 __global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
@@ -317,36 +461,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
     }
 
     const uint32_t mw = m0 + wm * (BM / WM) + li, nw = n0 + wn * (BN / WN) + 4 * lg;  // of fragment (0, 0)
-    if constexpr (EPI == kOut) {
+    if constexpr (EPI == kOut || EPI == kProb) {
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const uint32_t m = mw + 16 * i;
             if (m >= p.M) continue;
-            float s = 1.f;
-            bool skip = false;
-            if (p.last && p.scale) {
-                const int64_t lab = p.labels[m];
-                skip = lab == p.ignore;
-                s = lab >= 0 && static_cast<uint64_t>(lab) < p.V ? p.scale[m] : __builtin_nanf("");
-            }
+            const int64_t lab = EPI == kProb ? p.labels[m] - p.f0 : 0;
+            const float lse = EPI == kProb ? p.lse[m] : 0.f;
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                const uint32_t n = nw + 16 * j, have = left(p.N, n);
-                if (have == 0) continue;
                 float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                f32x4_t *sum = reinterpret_cast<f32x4_t *>(p.acc + static_cast<uint64_t>(m) * p.ldb + n);
-                if (p.acc_in) {
-                    const f32x4_t t = *sum;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] += t[r];
-                }
-                if (!p.last) {
-                    *sum = (f32x4_t){v[0], v[1], v[2], v[3]};
-                    continue;
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = skip ? 0.f : v[r] * s;
-                store4(p.out + m * p.ldo + n, v, have, p.vec);
+                if constexpr (EPI == kProb)
+                    emit_prob(p, m, nw + 16 * j, lab, lse, v);
+                else
+                    emit_out(p, m, nw + 16 * j, v);
             }
         }
     } else if constexpr (EPI == kGated || EPI == kGatedBwd) {
@@ -359,32 +487,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
             for (int j = 0; j < FN; j += 2) {
                 const uint32_t n = nw + 16 * j;                    // gate's row of the piece; up's is n + 16
                 const uint32_t f = p.f0 + (n >> 5) * 16 + (n & 15);  // their row in the tensors
-                const uint32_t have = left(p.F, f);
-                if constexpr (EPI == kGated) {
-                    if (have == 0) continue;
-                    float h[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) h[r] = activation(p.act, acc[i][j][r], nullptr) * acc[i][j + 1][r];
-                    store4(p.out + m * p.ldo + f, h, have, p.vec);
-                } else {
-                    float dh[4] = {0.f, 0.f, 0.f, 0.f}, dg[4], du[4];
-                    if (have) load4(p.dH + m * p.lddh + f, dh, have, p.vec);
-#pragma unroll
-                    for (uint32_t r = 0; r < 4; ++r) {
-                        float d;
-                        const float a = activation(p.act, acc[i][j][r], &d);
-                        // rows past the tensors' end are part of the next product's reduction: zeros
-                        dg[r] = r < have ? dh[r] * acc[i][j + 1][r] * d : 0.f;
-                        du[r] = r < have ? dh[r] * a : 0.f;
-                    }
-                    if (n < p.ldG) {
-                        uint16_t *G = p.G + static_cast<uint64_t>(m) * p.ldG + n;
-                        store4(G, dg, 4, true);
-                        store4(G + 16, du, 4, true);
-                    }
-                    if (have && p.dG) store4(p.dG + m * p.ldg + f, dg, have, p.vec);
-                    if (have && p.dU) store4(p.dU + m * p.ldg + f, du, have, p.vec);
-                }
+                const float g[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                const float u[4] = {acc[i][j + 1][0], acc[i][j + 1][1], acc[i][j + 1][2], acc[i][j + 1][3]};
+                if constexpr (EPI == kGated)
+                    emit_gated(p, m, f, g, u);
+                else if (n < p.ldG)
+                    emit_gated_bwd(p, m, f, n, n + 16, g, u);
             }
         }
     } else if constexpr (EPI == kStats) {
@@ -433,24 +541,67 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
             }
             p.stat[static_cast<uint64_t>(m0 + tid) * p.ldstat + p.stat0 + n0 / BN] = (f32x2){mx, s};
         }
-    } else if constexpr (EPI == kProb) {
-        // exp(z - lse) - [label], BF16, the columns of the next product's reduction (zeros past V)
+    }
+}
+
+// The parts of a tile that k_fused left, added in order, and the operator's work on the sums.  A
+// workgroup takes 8 tokens of a tile, 32 lanes of 4 columns each (16 lanes with a column's gate and
+// up sums for a pair).
+struct JoinArgs {
+    const float *part;
+    uint32_t tiles, slices, grid, up_col;  // up_col: where dU starts in G
+};
+
+template <int EPI>
+__global__ __launch_bounds__(256) void k_join(const MmArgs p, const JoinArgs q) {
+    constexpr bool pair = EPI == kGated || EPI == kGatedBwd;
+    constexpr uint32_t QUADS = pair ? 16 : 32, ROWS = 256 / QUADS;
+    const uint32_t tile = blockIdx.x, m = blockIdx.y * ROWS + threadIdx.x / QUADS, c = threadIdx.x % QUADS * 4;
+    if (m >= p.M) return;
+    // The workgroups whose runs hold the tile's first and last slice: run g starts at
+    // floor(g * total / grid).
+    const uint64_t total = static_cast<uint64_t>(q.tiles) * q.slices, at = static_cast<uint64_t>(tile) * q.slices;
+    const uint32_t g0 = static_cast<uint32_t>(((at + 1) * q.grid - 1) / total);
+    const uint32_t g1 = static_cast<uint32_t>(((at + q.slices) * q.grid - 1) / total);
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t g = g0; g <= g1; ++g) {
+        const float *src = q.part + (static_cast<uint64_t>(g + tile) * p.M + m) * kFusedTile + c;
+        const f32x4_t t = *reinterpret_cast<const f32x4_t *>(src);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const uint32_t m = mw + 16 * i;
-            if (m >= p.M) continue;
-            const int64_t lab = p.labels[m] - p.f0;
-            const float lse = p.lse[m];
+        for (int r = 0; r < 4; ++r) v[r] += t[r];
+        if constexpr (pair) {
+            const f32x4_t w = *reinterpret_cast<const f32x4_t *>(src + 64);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const uint32_t n = nw + 16 * j;
-                float v[4];
-#pragma unroll
-                for (uint32_t r = 0; r < 4; ++r)
-                    v[r] = n + r < p.N ? __expf(acc[i][j][r] - lse) - (static_cast<int64_t>(n + r) == lab ? 1.f : 0.f) : 0.f;
-                store4(p.G + static_cast<uint64_t>(m) * p.ldG + n, v, 4, true);
-            }
+            for (int r = 0; r < 4; ++r) u[r] += w[r];
         }
+    }
+    const uint32_t n = tile * kFusedTile + c;
+    if constexpr (EPI == kOut) {
+        emit_out(p, m, n, v);
+    } else if constexpr (EPI == kGated) {
+        emit_gated(p, m, p.f0 + tile * 64 + c, v, u);
+    } else if constexpr (EPI == kGatedBwd) {
+        emit_gated_bwd(p, m, p.f0 + tile * 64 + c, tile * 64 + c, q.up_col + tile * 64 + c, v, u);
+    } else if constexpr (EPI == kProb) {
+        emit_prob(p, m, n, p.labels[m] - p.f0, p.lse[m], v);
+    } else {
+        const int64_t lab = p.labels[m] - p.f0;
+        float mx = -__builtin_inff(), s = 0.f;
+#pragma unroll
+        for (uint32_t r = 0; r < 4; ++r)
+            if (n + r < p.N) mx = fmaxf(mx, v[r]);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+        const float base = exp_base(mx);
+#pragma unroll
+        for (uint32_t r = 0; r < 4; ++r)
+            if (n + r < p.N) {
+                s += __expf(v[r] - base);
+                if (static_cast<int64_t>(n + r) == lab) p.top[m] = v[r];
+            }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+        if (c == 0) p.stat[static_cast<uint64_t>(m) * p.ldstat + p.stat0 + tile] = (f32x2){mx, s};
     }
 }
 
@@ -491,12 +642,84 @@ uint32_t grid_for(uint64_t items, uint32_t per) {
     return static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>((items + per - 1) / per, 65536)));
 }
 
-cbk_status unpack(const cbk_tensor &t, uint64_t row0, uint64_t nrows, uint64_t rows_out, uint32_t pair, uint64_t Kp,
-                  uint16_t *out, hipStream_t s) {
-    const UnpackArgs a{t.words, t.codebook, t.b, t.U, static_cast<uint32_t>(t.cols), static_cast<uint32_t>(Kp), row0,
-                       static_cast<uint32_t>(nrows), static_cast<uint32_t>(rows_out), pair, out};
-    hipLaunchKernelGGL(k_unpack_generic, dim3(grid_for(rows_out * (Kp / 4), 256)), dim3(256), 0, s, a);
-    return launched();
+struct UnpackRunArgs {
+    UnpackArgs a;
+    uint32_t count;
+    hipStream_t s;
+    cbk_status st;
+};
+
+template <int B>
+struct UnpackRun {
+    static bool run(UnpackRunArgs &r) {
+        using G = U64<B>;
+        constexpr uint32_t stage = G::STAGE_CHUNKS * 16 > 64 * 144 ? G::STAGE_CHUNKS * 16 : 64 * 144;
+        constexpr uint32_t lds = kUnpackWaves * stage;
+        r.a.steps = ceil_div(static_cast<uint64_t>(r.a.nrows) * r.a.cols, 4096);
+        // two workgroups per CU, whose waves take every so-manieth step
+        const dim3 grid(std::min(ceil_div(r.a.steps, kUnpackWaves), std::max(1u, 2 * static_cast<uint32_t>(cu_count()) / r.count)), r.count);
+        if (r.a.cols % 8 == 0) {
+            if (!allow_lds(k_unpack<B, true>, lds)) return false;
+            hipLaunchKernelGGL((k_unpack<B, true>), grid, dim3(64 * kUnpackWaves), lds, r.s, r.a);
+        } else {
+            if (!allow_lds(k_unpack<B, false>, lds)) return false;
+            hipLaunchKernelGGL((k_unpack<B, false>), grid, dim3(64 * kUnpackWaves), lds, r.s, r.a);
+        }
+        r.st = launched();
+        return true;
+    }
+};
+using UnpackB = std::integer_sequence<int, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15>;
+
+// Rows [row0, row0 + nrows) of one tensor, or of a pair, into rows_out rows each of the piece.
+cbk_status unpack(const cbk_tensor *const *ts, uint32_t count, uint64_t row0, uint64_t nrows, uint64_t rows_out,
+                  uint64_t Kp, uint16_t *out, hipStream_t s) {
+    UnpackRunArgs r{};
+    r.s = s;
+    r.a.cols = static_cast<uint32_t>(ts[0]->cols);
+    r.a.Kp = static_cast<uint32_t>(Kp);
+    r.a.row0 = row0;
+    r.a.nrows = static_cast<uint32_t>(nrows);
+    r.a.rows_out = static_cast<uint32_t>(rows_out);
+    r.a.pair = count == 2 ? 2 : 0;
+    r.a.out = out;
+    r.a.inv_cols = 1.f / static_cast<float>(std::max(1u, r.a.cols));
+    bool fast = r.a.cols > 0 && row0 * r.a.cols % 128 == 0 && nrows <= 32768 && nrows * r.a.cols < (uint64_t(1) << 27);
+    for (uint32_t i = 0; i < count; ++i) {
+        const cbk_tensor &t = *ts[i];
+        const uint64_t chunks = cbk_words_for(t.rows * t.cols, t.b) / 4;
+        r.a.t[i] = UnpackTensor{t.words, t.codebook, t.U, static_cast<uint32_t>(chunks)};
+        fast = fast && t.b >= 1 && t.b <= 15 && aligned_to(t.codebook, 16) && chunks < (uint64_t(1) << 32);
+    }
+    if (fast) {
+        const bool together = count == 1 || ts[0]->b == ts[1]->b;
+        for (uint32_t i = 0; i < count && fast; i += together ? count : 1) {
+            UnpackRunArgs one = r;
+            one.count = together ? count : 1;
+            one.a.b = ts[i]->b;
+            if (!together) {
+                // a tensor of the pair by itself: as the pair's first, written where it belongs
+                one.a.t[0] = r.a.t[i];
+                one.a.out = out + i * 16 * Kp;
+            }
+            fast = dispatch_b<UnpackRun>(static_cast<int>(one.a.b), one, UnpackB{});
+            if (fast && one.st != CBK_OK) return one.st;
+        }
+        if (fast) {
+            if (r.a.cols == Kp && nrows == rows_out) return CBK_OK;
+            hipLaunchKernelGGL(k_unpack_pad, dim3(std::min<uint32_t>(r.a.rows_out, 4096)), dim3(256), 0, s, r.a);
+            return launched();
+        }
+    }
+    for (uint32_t i = 0; i < count; ++i) {
+        UnpackArgs a = r.a;
+        a.t[0] = r.a.t[i];
+        a.b = ts[i]->b;
+        a.pair = count == 2 ? i + 1 : 0;
+        hipLaunchKernelGGL(k_unpack_generic, dim3(grid_for(rows_out * (Kp / 4), 256)), dim3(256), 0, s, a);
+        CBK_TRY(launched());
+    }
+    return CBK_OK;
 }
 
 template <int BM, int BN, int WM, int WN, bool NN, int EPI>
@@ -535,12 +758,6 @@ bool vec8(const void *p, uint64_t ld) { return aligned_to(p, 8) && ld % 4 == 0; 
 
 uint64_t up64(uint64_t n) { return (n + 63) / 64 * 64; }
 
-#define CBK_TRY(x)                          \
-    do {                                    \
-        const cbk_status st_ = (x);         \
-        if (st_ != CBK_OK) return st_;      \
-    } while (0)
-
 template <typename T>
 T *at(void *ws, uint64_t offset) { return reinterpret_cast<T *>(static_cast<unsigned char *>(ws) + offset); }
 
@@ -555,72 +772,177 @@ uint64_t piece_rows(uint64_t nrows, bool pair) { return pair ? up64(2 * ((nrows 
 
 cbk_status unpack_piece(const cbk_tensor *const *ts, int count, uint64_t row0, uint64_t nrows, uint64_t Kp, uint16_t *W,
                         hipStream_t s) {
-    const uint64_t rows = piece_rows(nrows, count == 2);
-    for (int i = 0; i < count; ++i)
-        CBK_TRY(unpack(*ts[i], row0, nrows, count == 2 ? rows / 2 : rows, count == 2 ? i + 1 : 0, Kp, W, s));
-    return CBK_OK;
+    return unpack(ts, count, row0, nrows, piece_rows(nrows, count == 2) / count, Kp, W, s);
+}
+
+}  // namespace
+
+namespace {
+
+struct FusedRunArgs {
+    FusedArgs a;
+    uint32_t bm;
+    bool nn;
+    hipStream_t s;
+    cbk_status st;
+};
+template <int B>
+struct FusedRun {
+    static bool run(FusedRunArgs &r) {
+        r.st = launch_fused<B>(r.a, r.bm, r.nn, r.s);
+        return true;
+    }
+};
+using FusedB = std::integer_sequence<int, 8, 9, 10, 11, 12, 13, 14>;
+
+// The weights of a call, decoded on the way (k_fused) or a piece at a time into the workspace, and
+// the products with a piece of them.
+struct Weights {
+    const cbk_tensor *ts[2];
+    uint32_t count;
+    NnPlan pl;
+    void *ws;
+    hipStream_t s;
+    uint64_t row0, nrows;  // the piece
+
+    // Rows of the piece's reduction: as the decoded rows lie (both tensors' rows in turns of 16), or,
+    // for k_fused, each tensor's rows rounded up to a slice.
+    uint64_t reduction() const {
+        if (pl.fused) return count * up64(nrows);
+        return piece_rows(nrows, count == 2);
+    }
+
+    cbk_status piece(uint64_t r) {
+        row0 = r;
+        nrows = std::min(pl.rows, ts[0]->rows - r);
+        return pl.fused ? CBK_OK : unpack_piece(ts, count, row0, nrows, pl.Kp, at<uint16_t>(ws, pl.w), s);
+    }
+    bool last() const { return row0 + nrows == ts[0]->rows; }
+
+    cbk_status fused(MmArgs &p, bool nn, JoinArgs &q) const {
+        FusedRunArgs r{};
+        FusedArgs &a = r.a;
+        for (uint32_t i = 0; i < count; ++i)
+            a.t[i] = FusedTensor{ts[i]->words, ts[i]->codebook, cbk_words_for(ts[i]->rows * ts[i]->cols, ts[i]->b) * 4, ts[i]->U, 0};
+        a.count = count;
+        a.A = p.A;
+        a.lda = p.lda;
+        a.M = p.M;
+        a.row0 = row0;
+        a.nrows = static_cast<uint32_t>(nrows);
+        a.groups = static_cast<uint32_t>(pl.Kp / 32);
+        a.slices_of_first = ~0u;
+        if (nn) {
+            a.tiles = ceil_div(pl.Kp, kFusedTile);
+            a.slices = static_cast<uint32_t>(reduction() / 64);
+            if (count == 2) a.slices_of_first = a.slices / 2;
+        } else {
+            a.tiles = ceil_div(nrows, kFusedTile / count);
+            a.slices = static_cast<uint32_t>(pl.Kp / 64);
+        }
+        // at least four slices a workgroup, so that the start of its pipeline is paid for
+        const uint64_t total = static_cast<uint64_t>(a.tiles) * a.slices;
+        a.grid = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(pl.grid, total / 4)));
+        a.part = at<float>(ws, pl.part);
+        r.bm = pl.fused;
+        r.nn = nn;
+        r.s = s;
+        if (!dispatch_b<FusedRun>(static_cast<int>(ts[0]->b), r, FusedB{})) return CBK_E_UNSUPPORTED;
+        q = JoinArgs{a.part, a.tiles, a.slices, a.grid, static_cast<uint32_t>(up64(nrows))};
+        return r.st;
+    }
+
+    template <int EPI>
+    cbk_status join(MmArgs &p, const JoinArgs &q) const {
+        constexpr uint32_t rows = EPI == kGated || EPI == kGatedBwd ? 16 : 8;
+        hipLaunchKernelGGL((k_join<EPI>), dim3(q.tiles, ceil_div(p.M, rows)), dim3(256), 0, s, p, q);
+        return launched();
+    }
+
+    // C = A . (piece)^T with the epilogue EPI.
+    template <int EPI>
+    cbk_status forward(MmArgs &p) const {
+        if (pl.fused) {
+            JoinArgs q;
+            CBK_TRY(fused(p, false, q));
+            return join<EPI>(p, q);
+        }
+        p.B = at<uint16_t>(ws, pl.w);
+        p.ldb = static_cast<uint32_t>(pl.Kp);
+        p.ktiles = static_cast<uint32_t>(pl.Kp / 64);
+        const uint64_t rows = piece_rows(nrows, count == 2);
+        if (EPI == kGated || EPI == kGatedBwd) p.N = static_cast<uint32_t>(rows);
+        return mm<false, EPI>(p, EPI == kProb ? static_cast<uint32_t>(rows) : p.N, s);
+    }
+
+    // The piece's part of dX = A . (piece), summed over the pieces in fp32; rounded with the last.
+    cbk_status gradient(MmArgs &p, uint16_t *dX, uint64_t lddx) const {
+        p.N = static_cast<uint32_t>(ts[0]->cols);
+        p.acc = at<float>(ws, pl.acc);
+        p.ldacc = static_cast<uint32_t>(pl.Kp);
+        p.acc_in = row0 != 0;
+        p.last = last();
+        p.out = dX;
+        p.ldo = lddx;
+        p.vec = vec8(dX, lddx);
+        if (pl.fused) {
+            JoinArgs q;
+            CBK_TRY(fused(p, true, q));
+            return join<kOut>(p, q);
+        }
+        p.B = at<uint16_t>(ws, pl.w);
+        p.ldb = static_cast<uint32_t>(pl.Kp);
+        p.ktiles = static_cast<uint32_t>(reduction() / 64);
+        return mm<true, kOut>(p, p.N, s);
+    }
+};
+
+Weights weights_of(NnOp op, const cbk_tensor *a, const cbk_tensor *b, uint64_t T, void *ws, hipStream_t s) {
+    Weights w{};
+    w.ts[0] = a;
+    w.ts[1] = b;
+    w.count = b ? 2 : 1;
+    w.pl = nn_plan(op, w.ts, T);
+    w.ws = ws;
+    w.s = s;
+    return w;
 }
 
 }  // namespace
 
 cbk_status launch_linear(const cbk_tensor &t, const uint16_t *X, uint64_t ldx, uint64_t T, uint16_t *Y, uint64_t ldy,
                          void *ws, hipStream_t s) {
-    const NnPlan pl = nn_plan(NnOp::linear, t.rows, t.cols, T);
-    const cbk_tensor *ts[1] = {&t};
+    Weights w = weights_of(NnOp::linear, &t, nullptr, T, ws, s);
+    const NnPlan &pl = w.pl;
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
         CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, t.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
         for (uint64_t r = 0; r < t.rows; r += pl.rows) {
-            const uint64_t n = std::min(pl.rows, t.rows - r);
-            CBK_TRY(unpack_piece(ts, 1, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
-            p.B = at<uint16_t>(ws, pl.w);
-            p.ldb = static_cast<uint32_t>(pl.Kp);
-            p.N = static_cast<uint32_t>(n);
-            p.ktiles = static_cast<uint32_t>(pl.Kp / 64);
+            CBK_TRY(w.piece(r));
+            p.N = static_cast<uint32_t>(w.nrows);
             p.out = Y + c * ldy + r;
             p.ldo = ldy;
             p.vec = vec8(p.out, ldy);
             p.last = 1;
-            CBK_TRY((mm<false, kOut>(p, p.N, s)));
+            CBK_TRY(w.forward<kOut>(p));
         }
     }
     return CBK_OK;
 }
 
-namespace {
-
-// One piece's part of dX: the reduction over the piece's rows, summed over the pieces in fp32.
-cbk_status gradient_piece(MmArgs &p, const NnPlan &pl, uint64_t rows, uint64_t cols, bool first, bool last, uint16_t *dX,
-                          uint64_t lddx, void *ws, hipStream_t s) {
-    p.B = at<uint16_t>(ws, pl.w);
-    p.ldb = static_cast<uint32_t>(pl.Kp);
-    p.N = static_cast<uint32_t>(cols);
-    p.ktiles = static_cast<uint32_t>(rows / 64);
-    p.acc = at<float>(ws, pl.acc);
-    p.acc_in = !first;
-    p.last = last;
-    p.out = dX;
-    p.ldo = lddx;
-    p.vec = vec8(dX, lddx);
-    return mm<true, kOut>(p, p.N, s);
-}
-
-}  // namespace
-
 cbk_status launch_linear_dx(const cbk_tensor &t, const uint16_t *dY, uint64_t lddy, uint64_t T, uint16_t *dX,
                             uint64_t lddx, void *ws, hipStream_t s) {
     if (t.rows == 0) return zero_rows(dX, lddx, T, t.cols, s);
-    const NnPlan pl = nn_plan(NnOp::linear, t.rows, t.cols, T);
-    const cbk_tensor *ts[1] = {&t};
+    Weights w = weights_of(NnOp::linear, &t, nullptr, T, ws, s);
+    const NnPlan &pl = w.pl;
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
         for (uint64_t r = 0; r < t.rows; r += pl.rows) {
-            const uint64_t n = std::min(pl.rows, t.rows - r);
-            CBK_TRY(token_side(p, dY + c * lddy + r, lddy, p.M, n, up64(n), at<uint16_t>(ws, pl.pack), s));
-            CBK_TRY(unpack_piece(ts, 1, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
-            CBK_TRY(gradient_piece(p, pl, piece_rows(n, false), t.cols, r == 0, r + n == t.rows, dX + c * lddx, lddx, ws, s));
+            CBK_TRY(w.piece(r));
+            CBK_TRY(token_side(p, dY + c * lddy + r, lddy, p.M, w.nrows, up64(w.nrows), at<uint16_t>(ws, pl.pack), s));
+            CBK_TRY(w.gradient(p, dX + c * lddx, lddx));
         }
     }
     return CBK_OK;
@@ -628,26 +950,21 @@ cbk_status launch_linear_dx(const cbk_tensor &t, const uint16_t *dY, uint64_t ld
 
 cbk_status launch_ffn(const cbk_tensor &gate, const cbk_tensor &up, int act, const uint16_t *X, uint64_t ldx, uint64_t T,
                       uint16_t *H, uint64_t ldh, void *ws, hipStream_t s) {
-    const NnPlan pl = nn_plan(NnOp::ffn, gate.rows, gate.cols, T);
-    const cbk_tensor *ts[2] = {&gate, &up};
+    Weights w = weights_of(NnOp::ffn, &gate, &up, T, ws, s);
+    const NnPlan &pl = w.pl;
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
         CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, gate.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        p.act = act;
+        p.F = static_cast<uint32_t>(gate.rows);
+        p.out = H + c * ldh;
+        p.ldo = ldh;
+        p.vec = vec8(p.out, ldh);
         for (uint64_t r = 0; r < gate.rows; r += pl.rows) {
-            const uint64_t n = std::min(pl.rows, gate.rows - r);
-            CBK_TRY(unpack_piece(ts, 2, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
-            p.B = at<uint16_t>(ws, pl.w);
-            p.ldb = static_cast<uint32_t>(pl.Kp);
-            p.N = static_cast<uint32_t>(piece_rows(n, true));
-            p.ktiles = static_cast<uint32_t>(pl.Kp / 64);
-            p.act = act;
+            CBK_TRY(w.piece(r));
             p.f0 = static_cast<uint32_t>(r);
-            p.F = static_cast<uint32_t>(gate.rows);
-            p.out = H + c * ldh;
-            p.ldo = ldh;
-            p.vec = vec8(p.out, ldh);
-            CBK_TRY((mm<false, kGated>(p, p.N, s)));
+            CBK_TRY(w.forward<kGated>(p));
         }
     }
     return CBK_OK;
@@ -657,38 +974,32 @@ cbk_status launch_ffn_bwd(const cbk_tensor &gate, const cbk_tensor &up, int act,
                           const uint16_t *dH, uint64_t lddh, uint64_t T, uint16_t *dX, uint64_t lddx, uint16_t *dG,
                           uint16_t *dU, uint64_t ldg, void *ws, hipStream_t s) {
     if (gate.rows == 0) return gate.cols == 0 ? CBK_OK : zero_rows(dX, lddx, T, gate.cols, s);
-    const NnPlan pl = nn_plan(NnOp::ffn, gate.rows, gate.cols, T);
-    const cbk_tensor *ts[2] = {&gate, &up};
+    Weights w = weights_of(NnOp::ffn, &gate, &up, T, ws, s);
+    const NnPlan &pl = w.pl;
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
         CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, gate.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        p.act = act;
+        p.F = static_cast<uint32_t>(gate.rows);
+        p.dH = dH + c * lddh;
+        p.lddh = lddh;
+        p.dG = dG ? dG + c * ldg : nullptr;
+        p.dU = dU ? dU + c * ldg : nullptr;
+        p.ldg = ldg;
+        p.vec = vec8(p.dH, lddh) && (!dG || vec8(p.dG, ldg)) && (!dU || vec8(p.dU, ldg));
+        p.G = at<uint16_t>(ws, pl.g);
         for (uint64_t r = 0; r < gate.rows; r += pl.rows) {
-            const uint64_t n = std::min(pl.rows, gate.rows - r), rows = piece_rows(n, true);
-            CBK_TRY(unpack_piece(ts, 2, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
-            MmArgs a = p;
-            a.B = at<uint16_t>(ws, pl.w);
-            a.ldb = static_cast<uint32_t>(pl.Kp);
-            a.N = static_cast<uint32_t>(rows);
-            a.ktiles = static_cast<uint32_t>(pl.Kp / 64);
-            a.act = act;
-            a.f0 = static_cast<uint32_t>(r);
-            a.F = static_cast<uint32_t>(gate.rows);
-            a.dH = dH + c * lddh;
-            a.lddh = lddh;
-            a.dG = dG ? dG + c * ldg : nullptr;
-            a.dU = dU ? dU + c * ldg : nullptr;
-            a.ldg = ldg;
-            a.vec = vec8(a.dH, lddh) && (!dG || vec8(a.dG, ldg)) && (!dU || vec8(a.dU, ldg));
-            a.G = at<uint16_t>(ws, pl.g);
-            a.ldG = static_cast<uint32_t>(rows);
-            CBK_TRY((mm<false, kGatedBwd>(a, a.N, s)));
+            CBK_TRY(w.piece(r));
+            p.f0 = static_cast<uint32_t>(r);
+            p.ldG = static_cast<uint32_t>(w.reduction());
+            CBK_TRY(w.forward<kGatedBwd>(p));
             if (gate.cols == 0) continue;
             MmArgs d{};
             d.M = p.M;
-            d.A = a.G;
-            d.lda = a.ldG;
-            CBK_TRY(gradient_piece(d, pl, rows, gate.cols, r == 0, r + n == gate.rows, dX + c * lddx, lddx, ws, s));
+            d.A = p.G;
+            d.lda = p.ldG;
+            CBK_TRY(w.gradient(d, dX + c * lddx, lddx));
         }
     }
     return CBK_OK;
@@ -696,8 +1007,8 @@ cbk_status launch_ffn_bwd(const cbk_tensor &gate, const cbk_tensor &up, int act,
 
 cbk_status launch_xent(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, const int64_t *labels, uint64_t T,
                        int64_t ignore, float *loss, float *lse, void *ws, hipStream_t s) {
-    const NnPlan pl = nn_plan(NnOp::xent, head.rows, head.cols, T);
-    const cbk_tensor *ts[1] = {&head};
+    Weights w = weights_of(NnOp::xent, &head, nullptr, T, ws, s);
+    const NnPlan &pl = w.pl;
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
@@ -705,19 +1016,15 @@ cbk_status launch_xent(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, 
         p.stat = at<f32x2>(ws, pl.stat);
         p.top = at<float>(ws, pl.top);
         p.labels = labels + c;
-        constexpr uint32_t kTile = 128;
+        constexpr uint32_t kTile = 128;  // columns of a part of the statistics
         p.ldstat = 0;
         for (uint64_t r = 0; r < head.rows; r += pl.rows) p.ldstat += ceil_div(std::min(pl.rows, head.rows - r), kTile);
         for (uint64_t r = 0; r < head.rows; r += pl.rows) {
-            const uint64_t n = std::min(pl.rows, head.rows - r);
-            CBK_TRY(unpack_piece(ts, 1, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
-            p.B = at<uint16_t>(ws, pl.w);
-            p.ldb = static_cast<uint32_t>(pl.Kp);
-            p.N = static_cast<uint32_t>(n);
-            p.ktiles = static_cast<uint32_t>(pl.Kp / 64);
+            CBK_TRY(w.piece(r));
+            p.N = static_cast<uint32_t>(w.nrows);
             p.f0 = static_cast<uint32_t>(r);
-            CBK_TRY((mm<false, kStats>(p, p.N, s)));
-            p.stat0 += ceil_div(n, kTile);
+            CBK_TRY(w.forward<kStats>(p));
+            p.stat0 += ceil_div(w.nrows, kTile);
         }
         hipLaunchKernelGGL(k_xent_join, dim3((p.M + 3) / 4), dim3(256), 0, s, p.stat, p.ldstat, p.M, p.labels, ignore,
                            head.rows, p.top, loss + c, lse + c);
@@ -729,35 +1036,30 @@ cbk_status launch_xent(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, 
 cbk_status launch_xent_bwd(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, const int64_t *labels,
                            const float *lse, const float *dloss, uint64_t T, int64_t ignore, uint16_t *dX,
                            uint64_t lddx, void *ws, hipStream_t s) {
-    const NnPlan pl = nn_plan(NnOp::xent, head.rows, head.cols, T);
-    const cbk_tensor *ts[1] = {&head};
+    Weights w = weights_of(NnOp::xent, &head, nullptr, T, ws, s);
+    const NnPlan &pl = w.pl;
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
         CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, head.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
         p.labels = labels + c;
+        p.lse = lse + c;
+        p.G = at<uint16_t>(ws, pl.g);
+        p.ldG = static_cast<uint32_t>(pl.Rp);
         for (uint64_t r = 0; r < head.rows; r += pl.rows) {
-            const uint64_t n = std::min(pl.rows, head.rows - r), rows = piece_rows(n, false);
-            CBK_TRY(unpack_piece(ts, 1, r, n, pl.Kp, at<uint16_t>(ws, pl.w), s));
-            MmArgs a = p;
-            a.B = at<uint16_t>(ws, pl.w);
-            a.ldb = static_cast<uint32_t>(pl.Kp);
-            a.N = static_cast<uint32_t>(n);
-            a.ktiles = static_cast<uint32_t>(pl.Kp / 64);
-            a.f0 = static_cast<uint32_t>(r);
-            a.lse = lse + c;
-            a.G = at<uint16_t>(ws, pl.g);
-            a.ldG = static_cast<uint32_t>(pl.Rp);
-            CBK_TRY((mm<false, kProb>(a, static_cast<uint32_t>(rows), s)));
+            CBK_TRY(w.piece(r));
+            p.N = static_cast<uint32_t>(w.nrows);
+            p.f0 = static_cast<uint32_t>(r);
+            CBK_TRY(w.forward<kProb>(p));
             MmArgs d{};
             d.M = p.M;
-            d.A = a.G;
-            d.lda = a.ldG;
+            d.A = p.G;
+            d.lda = p.ldG;
             d.labels = p.labels;
             d.ignore = ignore;
             d.scale = dloss + c;
             d.V = head.rows;
-            CBK_TRY(gradient_piece(d, pl, rows, head.cols, r == 0, r + n == head.rows, dX + c * lddx, lddx, ws, s));
+            CBK_TRY(w.gradient(d, dX + c * lddx, lddx));
         }
     }
     return CBK_OK;

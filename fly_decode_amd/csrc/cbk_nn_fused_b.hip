@@ -1,0 +1,7 @@
+// cbk_nn_fused.h for index widths: 10 11.
+#include "cbk_nn_fused.h"
+
+namespace cbk {
+template cbk_status launch_fused<10>(const FusedArgs &, uint32_t, bool, hipStream_t);
+template cbk_status launch_fused<11>(const FusedArgs &, uint32_t, bool, hipStream_t);
+}  // namespace cbk

@@ -49,9 +49,11 @@ cbk_status check_pair(const cbk_tensor *gate, const cbk_tensor *up, int act) {
     return CBK_OK;
 }
 
-uint64_t bytes_of(cbk::NnOp op, const cbk_tensor *t, uint64_t tokens) {
+// Workspace of a call on one tensor, or on a gate and up pair.
+uint64_t bytes_of(cbk::NnOp op, const cbk_tensor *t, const cbk_tensor *up, uint64_t tokens) {
     if (check_weights(t) != CBK_OK || tokens >= kMaxTokens) return 0;
-    return cbk::nn_plan(op, t->rows, t->cols, tokens).bytes;
+    const cbk_tensor *ts[2] = {t, up};
+    return cbk::nn_plan(op, ts, tokens).bytes;
 }
 
 // First failure of a list of checks, in order.
@@ -66,19 +68,41 @@ cbk_status first(S... st) {
 
 namespace cbk {
 
+namespace {
+
+// The token tile of k_fused, or 0 where the tensors or the number of tokens are not its kind: widths
+// 8 to 14 (equal, for a pair), rows of whole 64-field units, up to 256 tokens, and a workgroup's
+// tables and slices within the LDS.
+uint32_t fused_tile(const cbk_tensor *const *ts, uint64_t count, uint64_t tokens) {
+    if (tokens > 256) return 0;
+    for (uint64_t i = 0; i < count; ++i) {
+        const cbk_tensor &t = *ts[i];
+        if (t.b < 8 || t.b > 14 || t.b != ts[0]->b || t.cols == 0 || t.cols % 64 != 0 || !aligned(t.codebook, 16)) return 0;
+    }
+    const uint32_t bm = tokens <= 16 ? 16 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256;
+    return nn_fused_lds(ts[0]->b, bm, static_cast<uint32_t>(count)) <= 160 * 1024 ? bm : 0;
+}
+
+}  // namespace
+
+// LDS of a workgroup of k_fused: the tables, and two slices of the tokens and of the weights.
+uint32_t nn_fused_lds(uint32_t b, uint32_t bm, uint32_t count) { return count * (2u << b) + 2 * 128 * bm + 2 * 128 * 128; }
+
 // A decoded piece takes up to kPieceBytes and kPieceRows, so that a call's scratch stays far below
 // the tensor's uncompressed size; chunks of kChunk tokens bound what is kept per token.
-NnPlan nn_plan(NnOp op, uint64_t rows, uint64_t cols, uint64_t tokens) {
+NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
     constexpr uint64_t kPieceBytes = uint64_t(128) << 20;
     constexpr uint64_t kPieceRows = 32768;
     constexpr uint64_t kChunk = 8192;
+    const uint64_t rows = ts[0]->rows, cols = ts[0]->cols;
     NnPlan p{};
     if (tokens == 0 || rows == 0) return p;
     const uint64_t pair = op == NnOp::ffn ? 2 : 1;  // decoded rows per row of a tensor
     p.Kp = std::max<uint64_t>(64, up_to(cols, 64));
     p.Tc = std::min(tokens, kChunk);
+    p.fused = fused_tile(ts, pair, tokens);
     const uint64_t total = up_to(pair * up_to(rows, 16), 256);
-    const uint64_t most = std::min(kPieceRows, std::max<uint64_t>(256, kPieceBytes / (2 * p.Kp) / 256 * 256));
+    const uint64_t most = p.fused ? kPieceRows : std::min(kPieceRows, std::max<uint64_t>(256, kPieceBytes / (2 * p.Kp) / 256 * 256));
     p.pieces = (total + most - 1) / most;
     p.Rp = up_to((total + p.pieces - 1) / p.pieces, 256);
     p.rows = p.Rp / pair;
@@ -91,7 +115,13 @@ NnPlan nn_plan(NnOp op, uint64_t rows, uint64_t cols, uint64_t tokens) {
     };
     // a padded copy of the chunk's X (or of a piece's columns of dY)
     p.pack = take(p.Tc * std::max(p.Kp, op == NnOp::linear ? p.Rp : 0) * 2);
-    p.w = take(p.Rp * p.Kp * 2);
+    if (p.fused) {
+        // as many workgroups as the LDS lets run at once on 256 CUs, and their parts of the tiles
+        p.grid = nn_fused_lds(ts[0]->b, p.fused, static_cast<uint32_t>(pair)) <= 80 * 1024 ? 512 : 256;
+        p.part = take((p.grid + std::max(p.Rp, p.Kp + 64) / 128) * p.Tc * 128 * 4);
+    } else {
+        p.w = take(p.Rp * p.Kp * 2);
+    }
     p.g = op == NnOp::linear ? at : take(p.Tc * p.Rp * 2);
     p.acc = p.pieces > 1 ? take(p.Tc * p.Kp * 4) : at;
     p.stat = op == NnOp::xent ? take(p.Tc * p.pieces * (p.Rp / 128) * 8) : at;
@@ -106,7 +136,7 @@ using cbk::NnOp;
 
 extern "C" {
 
-size_t cbk_linear_workspace_bytes(const cbk_tensor *t, uint64_t tokens) { return bytes_of(NnOp::linear, t, tokens); }
+size_t cbk_linear_workspace_bytes(const cbk_tensor *t, uint64_t tokens) { return bytes_of(NnOp::linear, t, nullptr, tokens); }
 
 cbk_status cbk_linear(const cbk_tensor *t, const uint16_t *X, uint64_t ldx, uint64_t tokens, uint16_t *Y, uint64_t ldy,
                       void *workspace, size_t workspace_bytes, void *stream) {
@@ -115,7 +145,7 @@ cbk_status cbk_linear(const cbk_tensor *t, const uint16_t *X, uint64_t ldx, uint
     if (tokens >= kMaxTokens) return CBK_E_UNSUPPORTED;
     if (tokens == 0 || t->rows == 0) return CBK_OK;
     st = first(check_matrix(X, ldx, t->cols), check_matrix(Y, ldy, t->rows),
-               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::linear, t, tokens)));
+               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::linear, t, nullptr, tokens)));
     if (st != CBK_OK) return st;
     return cbk::launch_linear(*t, X, ldx, tokens, Y, ldy, workspace, static_cast<hipStream_t>(stream));
 }
@@ -127,14 +157,14 @@ cbk_status cbk_linear_dx(const cbk_tensor *t, const uint16_t *dY, uint64_t lddy,
     if (tokens >= kMaxTokens) return CBK_E_UNSUPPORTED;
     if (tokens == 0 || t->cols == 0) return CBK_OK;
     st = first(check_matrix(dY, lddy, t->rows), check_matrix(dX, lddx, t->cols),
-               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::linear, t, tokens)));
+               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::linear, t, nullptr, tokens)));
     if (st != CBK_OK) return st;
     return cbk::launch_linear_dx(*t, dY, lddy, tokens, dX, lddx, workspace, static_cast<hipStream_t>(stream));
 }
 
 size_t cbk_ffn_workspace_bytes(const cbk_tensor *gate, const cbk_tensor *up, uint64_t tokens) {
     if (check_pair(gate, up, CBK_ACT_SILU) != CBK_OK) return 0;
-    return bytes_of(NnOp::ffn, gate, tokens);
+    return bytes_of(NnOp::ffn, gate, up, tokens);
 }
 
 cbk_status cbk_ffn_gated(const cbk_tensor *gate, const cbk_tensor *up, int act, const uint16_t *X, uint64_t ldx,
@@ -145,7 +175,7 @@ cbk_status cbk_ffn_gated(const cbk_tensor *gate, const cbk_tensor *up, int act, 
     if (tokens >= kMaxTokens) return CBK_E_UNSUPPORTED;
     if (tokens == 0 || gate->rows == 0) return CBK_OK;
     st = first(check_matrix(X, ldx, gate->cols), check_matrix(H, ldh, gate->rows),
-               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::ffn, gate, tokens)));
+               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::ffn, gate, up, tokens)));
     if (st != CBK_OK) return st;
     return cbk::launch_ffn(*gate, *up, act, X, ldx, tokens, H, ldh, workspace, static_cast<hipStream_t>(stream));
 }
@@ -161,13 +191,13 @@ cbk_status cbk_ffn_gated_bwd(const cbk_tensor *gate, const cbk_tensor *up, int a
     st = first(check_matrix(X, ldx, gate->cols), check_matrix(dH, lddh, gate->rows),
                check_matrix(dX, lddx, gate->cols), dG ? check_matrix(dG, ldg, gate->rows) : CBK_OK,
                dU ? check_matrix(dU, ldg, gate->rows) : CBK_OK,
-               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::ffn, gate, tokens)));
+               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::ffn, gate, up, tokens)));
     if (st != CBK_OK) return st;
     return cbk::launch_ffn_bwd(*gate, *up, act, X, ldx, dH, lddh, tokens, dX, lddx, dG, dU, ldg, workspace,
                                static_cast<hipStream_t>(stream));
 }
 
-size_t cbk_xent_workspace_bytes(const cbk_tensor *head, uint64_t tokens) { return bytes_of(NnOp::xent, head, tokens); }
+size_t cbk_xent_workspace_bytes(const cbk_tensor *head, uint64_t tokens) { return bytes_of(NnOp::xent, head, nullptr, tokens); }
 
 cbk_status cbk_xent(const cbk_tensor *head, const uint16_t *X, uint64_t ldx, const int64_t *labels, uint64_t tokens,
                     int64_t ignore_index, float *loss, float *lse, void *workspace, size_t workspace_bytes,
@@ -180,7 +210,7 @@ cbk_status cbk_xent(const cbk_tensor *head, const uint16_t *X, uint64_t ldx, con
     if (!labels || !loss || !lse) return CBK_E_INVALID;
     if (!aligned(labels, 8) || !aligned(loss, 4) || !aligned(lse, 4)) return CBK_E_ALIGN;
     st = first(check_matrix(X, ldx, head->cols),
-               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::xent, head, tokens)));
+               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::xent, head, nullptr, tokens)));
     if (st != CBK_OK) return st;
     return cbk::launch_xent(*head, X, ldx, labels, tokens, ignore_index, loss, lse, workspace,
                             static_cast<hipStream_t>(stream));
@@ -197,7 +227,7 @@ cbk_status cbk_xent_bwd(const cbk_tensor *head, const uint16_t *X, uint64_t ldx,
     if (!labels || !lse || !dloss) return CBK_E_INVALID;
     if (!aligned(labels, 8) || !aligned(lse, 4) || !aligned(dloss, 4)) return CBK_E_ALIGN;
     st = first(check_matrix(X, ldx, head->cols), check_matrix(dX, lddx, head->cols),
-               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::xent, head, tokens)));
+               check_workspace(workspace, workspace_bytes, bytes_of(NnOp::xent, head, nullptr, tokens)));
     if (st != CBK_OK) return st;
     if (head->cols == 0) return CBK_OK;
     return cbk::launch_xent_bwd(*head, X, ldx, labels, lse, dloss, tokens, ignore_index, dX, lddx, workspace,

@@ -14,6 +14,12 @@ SHAPES = [
     (33, 129, 100, 1000), (64, 256, 256, 5000), (65, 255, 321, 9000), (128, 128, 64, 1), (129, 100, 640, 300),
     (200, 515, 1000, 3000), (257, 384, 320, 40000), (31, 2000, 72, 30), (5, 700, 448, 20000),
 ]
+# up to 256 tokens, rows of whole 64-field units and widths 8 to 14 (here 8, 9, 10, 11, 12, 13, 14): decoded on the way
+FUSED = [
+    (1, 128, 64, 250), (2, 1000, 1024, 500), (13, 515, 448, 1000), (16, 64, 4096, 2000), (17, 2113, 192, 4000),
+    (63, 640, 1088, 8000), (64, 130, 64, 5000), (65, 384, 512, 16000), (128, 900, 320, 3000), (129, 1000, 576, 260),
+    (200, 1291, 704, 16000), (256, 257, 2048, 7000),
+]
 
 
 @pytest.fixture(scope="module")
@@ -45,7 +51,7 @@ def acts(torch, T, n, seed, scale=1.0):
     return (torch.randn(T, n, generator=torch.Generator().manual_seed(seed)) * scale).bfloat16()
 
 
-@pytest.mark.parametrize("T,rows,cols,U", SHAPES)
+@pytest.mark.parametrize("T,rows,cols,U", SHAPES + FUSED)
 def test_linear(env, T, rows, cols, U):
     torch, cbk = env
     w, x = weights(torch, rows, cols, U, 1), acts(torch, T, cols, 2)
@@ -53,7 +59,7 @@ def test_linear(env, T, rows, cols, U):
     ref.assert_within(y, *ref.linear(x, w), "linear")
 
 
-@pytest.mark.parametrize("T,rows,cols,U", SHAPES)
+@pytest.mark.parametrize("T,rows,cols,U", SHAPES + FUSED)
 def test_linear_dx(env, T, rows, cols, U):
     torch, cbk = env
     w, dy = weights(torch, rows, cols, U, 3), acts(torch, T, rows, 4)
@@ -81,7 +87,23 @@ def test_ffn_gated_bwd(env, T, rows, cols, U, act):
         ref.assert_within(g, *want, name)
 
 
-@pytest.mark.parametrize("T,rows,cols,U", SHAPES)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T,rows,cols,U", FUSED)
+def test_ffn_pair_of_one_width(env, T, rows, cols, U, act):
+    """Forward and gradient where gate and up have the same width (one launch decodes both)."""
+    torch, cbk = env
+    wg, x = weights(torch, rows, cols, U, 20, 0.2), acts(torch, T, cols, 22)
+    wu = -wg.flip(0, 1)  # as many distinct patterns
+    dh = acts(torch, T, rows, 23, 0.1)
+    g, u = compress(cbk, wg), compress(cbk, wu)
+    assert g.b == u.b
+    ref.assert_within(cbk.ffn_gated(g, u, x.cuda(), act=act), *ref.ffn(act, x, wg, wu), "ffn_gated")
+    got = cbk.ffn_gated_bwd(g, u, x.cuda(), dh.cuda(), act=act)
+    for name, v, want in zip(("dX", "dG", "dU"), got, ref.ffn_bwd(act, x, wg, wu, dh)):
+        ref.assert_within(v, *want, name)
+
+
+@pytest.mark.parametrize("T,rows,cols,U", SHAPES + FUSED)
 def test_xent_and_gradient(env, T, rows, cols, U):
     torch, cbk = env
     w, x = weights(torch, rows, cols, U, 12, 0.1), acts(torch, T, cols, 13)
