@@ -25,7 +25,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "inclu
 SOURCES = [("cbk_api.cpp", False), ("cbk_kernels.hip", True), ("cbk_encode.hip", True),
            ("cbk_ec_host.cpp", False), ("cbk_ec.hip", True),
            ("cbk_nn_host.cpp", False), ("cbk_nn.hip", True)] + [
-    (f"cbk_nn_fused_{x}.hip", True) for x in "abcd"]
+    (f"cbk_nn_fused_{b}.hip", True) for b in range(8, 15)]
 
 
 def _run(cmd):

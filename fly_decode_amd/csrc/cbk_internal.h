@@ -56,7 +56,7 @@ struct NnPlan {
     uint64_t rows;    // rows of one tensor in a piece
     uint64_t Rp;      // columns of a piece's gradients (those of both tensors, for the feed-forward block)
     uint64_t pieces;
-    uint32_t fused;   // 0: pieces are decoded into memory; else the token tile of k_fused: 16, 64, 128 or 256
+    uint32_t fused;   // 0: pieces are decoded into memory; else the token tile of k_fused
     uint32_t grid;    // k_fused: most workgroups
     uint64_t pack, w, part, g, acc, stat, top;  // offsets in bytes
     uint64_t bytes;

@@ -830,7 +830,7 @@ struct Weights {
         a.M = p.M;
         a.row0 = row0;
         a.nrows = static_cast<uint32_t>(nrows);
-        a.groups = static_cast<uint32_t>(pl.Kp / 32);
+        a.cols = static_cast<uint32_t>(ts[0]->cols);
         a.slices_of_first = ~0u;
         if (nn) {
             a.tiles = ceil_div(pl.Kp, kFusedTile);

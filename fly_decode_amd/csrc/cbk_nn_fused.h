@@ -1,6 +1,6 @@
-// The matrix product of up to 256 tokens with weights that are decoded on the way (no decoded copy
-// in memory), for widths 8 to 14 and rows of whole 64-field units.  Included by cbk_nn_fused_*.hip,
-// which instantiate it for some widths each (they compile side by side).
+// The matrix product of up to 384 tokens with weights that are decoded on the way (no decoded copy
+// in memory), for widths 8 to 14.  Included by cbk_nn_fused_*.hip, which instantiate it for one
+// width each (they compile side by side).
 //
 // At these token counts the weights' decoding costs more than the product, and decoding a piece
 // into memory first costs several times the compressed bytes in traffic, so each weight is decoded
@@ -15,7 +15,9 @@
 // timing).
 //
 // A slice's 128 x 64 weights are 256 tasks of 32 consecutive fields, which are exactly b dwords of
-// the stream.  The 8 waves form two groups that decode alternate slices one ahead of the product:
+// the stream where rows are whole 32-field groups; where they are not (RAG) a task's fields start
+// anywhere in a dword, one more is loaded, and a funnel shift by the lane's own amount moves them
+// into place.  The 8 waves form two groups that decode alternate slices one ahead of the product:
 // in a slice's interval the waves of one group decode (LDS gathers) while those of the other, one
 // on each SIMD as well, feed the matrix cores, so the two pipes overlap by construction.  A lane's
 // dwords are loaded two slices ahead into registers; the tokens' slice is copied straight into LDS.
@@ -34,8 +36,7 @@ constexpr uint32_t fused_lds(uint32_t tables) {
 
 // This lane's dwords of a slice: as many loads as fused_loads<B>() says, so that a wait can leave
 // exactly them in flight.
-template <int B>
-constexpr int fused_loads() { return (B + 3) / 4; }
+constexpr int fused_loads(int dwords) { return (dwords + 3) / 4; }
 
 template <int B>
 __device__ __forceinline__ void load_fields(uint32_t (&d)[B], __amdgpu_buffer_rsrc_t rs, uint32_t off) {
@@ -56,10 +57,11 @@ __device__ __forceinline__ void load_fields(uint32_t (&d)[B], __amdgpu_buffer_rs
     }
 }
 
-// 32 fields to four 16-byte chunks of a row in LDS, chunk c0 + i in slot (c0 + i) ^ swz.
-template <int B>
+// 32 fields to four 16-byte chunks of a row in LDS, chunk c0 + i in slot (c0 + i) ^ swz.  Fields from
+// `have` on are zeros where MASK is set.
+template <int B, bool MASK>
 __device__ __forceinline__ void decode_fields(const uint32_t (&d)[B], const uint16_t *tbl, unsigned char *row, uint32_t c0,
-                                              uint32_t swz, bool live) {
+                                              uint32_t swz, uint32_t have) {
     uint32_t w[2][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[0][i] = unit_gather<B>(tbl, d, i);
@@ -69,22 +71,26 @@ __device__ __forceinline__ void decode_fields(const uint32_t (&d)[B], const uint
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[(g + 1) & 1][i] = unit_gather<B>(tbl, d, 8 * (g + 1) + i);
         }
-        const uint32_t *v = w[g & 1];
-        u32x4 t = {v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
-        if (!live) t = (u32x4){0u, 0u, 0u, 0u};
+        uint32_t *v = w[g & 1];
+        if constexpr (MASK) {
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) v[i] = 8 * g + i < have ? v[i] : 0u;
+        }
+        const u32x4 t = {v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
         *reinterpret_cast<u32x4 *>(row + ((c0 + g) ^ swz) * 16) = t;
     }
 }
 
 // Waves of a workgroup over the 128 columns; the other factor of 8 goes over the tokens.
-constexpr int fused_wn(int BM) { return BM >= 256 ? 2 : BM >= 64 ? 4 : 8; }
+constexpr int fused_wn(int BM) { return BM >= 192 ? 2 : BM >= 64 ? 4 : 8; }
 
-template <int B, int BM, bool NN>
+template <int B, int BM, bool NN, bool RAG>
 __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
     constexpr int WN = fused_wn(BM), WM = 8 / WN;
     constexpr int FM = BM / WM / 16, FN = kFusedTile / WN / 16;
     constexpr uint32_t XBYTES = BM * 128, WBYTES = kFusedTile * 128;
-    constexpr int XC = BM / 8;  // copies of a slice of the tokens
+    constexpr int XC = BM / 8;           // copies of a slice of the tokens
+    constexpr int DW = RAG ? B + 1 : B;  // dwords of a task
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     uint16_t *tables = reinterpret_cast<uint16_t *>(smem);
     unsigned char *xs = smem + p.count * Table<B>::SIZE * 2, *wsl = xs + 2 * XBYTES;
@@ -135,37 +141,58 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
         const uint32_t tile = static_cast<uint32_t>(pos / p.slices), s0 = static_cast<uint32_t>(pos - static_cast<uint64_t>(tile) * p.slices);
         const uint32_t s1 = static_cast<uint32_t>(min(static_cast<uint64_t>(p.slices), s0 + (end - pos)));
 
-        // The tensor, the table and the resource of a slice's weights, and this lane's offset in it.
-        auto load = [&](uint32_t (&d)[B], uint32_t s) {
-            uint32_t which, off;
-            uint64_t row;  // of the tensor, first of the resource
+        auto which_of = [&](uint32_t s) -> uint32_t {
+            if constexpr (NN) return s >= p.slices_of_first;
+            return p.count == 2 ? static_cast<uint32_t>(wave & 2) >> 1 : 0u;  // tasks 0..127 are gate's rows, the others up's
+        };
+        // The rows [row, ...) of the tensor that slice s takes, and this lane's first field after the
+        // start of row `row`.
+        auto fields_at = [&](uint32_t s, uint64_t &row) -> uint32_t {
+            const uint32_t which = which_of(s);
             if constexpr (NN) {
-                which = s >= p.slices_of_first;
                 row = p.row0 + static_cast<uint64_t>(s - (which ? p.slices_of_first : 0u)) * 64;
-                off = trow * p.groups + min(tile * 4 + tgrp, p.groups - 1);
+                return trow * p.cols + tile * kFusedTile + tgrp * 32;
             } else {
-                which = p.count == 2 ? static_cast<uint32_t>(wave & 2) >> 1 : 0u;  // tasks 0..127 are gate's rows, the others up's
-                row = p.row0 + (p.count == 2 ? static_cast<uint64_t>(tile) * 64 : static_cast<uint64_t>(tile) * 128);
-                off = (trow - which * 64) * p.groups + s * 2 + tgrp;
+                row = p.row0 + static_cast<uint64_t>(tile) * (p.count == 2 ? 64 : kFusedTile);
+                return (trow - which * 64) * p.cols + s * 64 + tgrp * 32;
             }
-            const FusedTensor &T = p.t[which];
-            const uint64_t start = row * p.groups * (4ull * B);
+        };
+        uint32_t shift = 0;  // RAG: where the task's first field starts in d[0]
+        auto load = [&](uint32_t (&d)[DW], uint32_t s) {
+            const FusedTensor &T = p.t[which_of(s)];
+            uint64_t row;
+            const uint32_t f = fields_at(s, row);
+            // a base on a dword; what is past the stream's end reads as zeros
+            const uint64_t bits = row * p.cols * B, start = (bits >> 5) * 4;
             const uint64_t rest = T.bytes > start ? T.bytes - start : 0;
             const auto rs = wave_rsrc(reinterpret_cast<const unsigned char *>(T.words) + (rest ? start : 0),
                                       static_cast<uint32_t>(min(rest, static_cast<uint64_t>(0x7FFFFFF0u))));
-            load_fields<B>(d, rs, off * (4u * B));
-        };
-        auto decode = [&](const uint32_t (&d)[B], uint32_t s, uint32_t buf) {
-            uint32_t which;
-            bool live = true;
-            if constexpr (NN) {
-                which = s >= p.slices_of_first;
-                // rows past the piece are part of the reduction: zeros
-                live = (s - (which ? p.slices_of_first : 0u)) * 64 + trow < p.nrows;
+            if constexpr (RAG) {
+                const uint32_t bit = f * B + (static_cast<uint32_t>(bits) & 31u);
+                shift = bit & 31u;
+                load_fields<DW>(d, rs, (bit >> 5) * 4u);
             } else {
-                which = p.count == 2 ? static_cast<uint32_t>(wave & 2) >> 1 : 0u;
+                load_fields<DW>(d, rs, f / 32u * (4u * B));
             }
-            decode_fields<B>(d, tables + which * Table<B>::SIZE, wsl + buf * WBYTES + wrow, tgrp * 4, swz, live);
+        };
+        auto decode = [&](const uint32_t (&d)[DW], uint32_t s, uint32_t buf) {
+            const uint32_t which = which_of(s);
+            // zeros where the reduction runs past the piece's rows (gradient) or the rows' ends
+            uint32_t have = 32;
+            if constexpr (NN)
+                have = (s - (which ? p.slices_of_first : 0u)) * 64 + trow < p.nrows ? 32u : 0u;
+            else if constexpr (RAG)
+                have = p.cols > s * 64 + tgrp * 32 ? p.cols - (s * 64 + tgrp * 32) : 0u;
+            const uint16_t *tbl = tables + which * Table<B>::SIZE;
+            unsigned char *to = wsl + buf * WBYTES + wrow;
+            if constexpr (RAG) {
+                uint32_t e[B];
+#pragma unroll
+                for (int i = 0; i < B; ++i) e[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], shift);
+                decode_fields<B, true>(e, tbl, to, tgrp * 4, swz, have);
+            } else {
+                decode_fields<B, NN>(d, tbl, to, tgrp * 4, swz, have);
+            }
         };
         auto copy = [&](uint32_t s, uint32_t buf) {
 #pragma unroll
@@ -214,7 +241,7 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
         // Before the first interval: slice s0 decoded and copied, the words of s0 + 1 (by the group
         // that decodes it) and s0 + 2 (by the other) on their way.  Words of slices past the run
         // are not loaded.
-        uint32_t d[B];
+        uint32_t d[DW];
         const bool first = role == 0;  // this group decodes s0, s0 + 2, ...
         lds_barrier();                 // the previous part's last reads of the buffers; the tables' stores
         copy(s0, 0);
@@ -247,7 +274,7 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
             // the copies have landed (the words asked for after them may still be on their way, and
             // are waited for an interval later), this wave's LDS writes are done
             if (mine && s + 3 < s1)
-                __builtin_amdgcn_s_waitcnt(0x0070 | fused_loads<B>());
+                __builtin_amdgcn_s_waitcnt(0x0070 | fused_loads(DW));
             else
                 __builtin_amdgcn_s_waitcnt(0x0070);
             __builtin_amdgcn_s_barrier();
@@ -278,28 +305,33 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
     }
 }
 
-template <int B, int BM, bool NN>
+template <int B, int BM, bool NN, bool RAG>
 cbk_status fused_run(const FusedArgs &a, hipStream_t s) {
     const uint32_t lds = fused_lds<B, BM>(a.count);
-    if (!allow_lds(k_fused<B, BM, NN>, lds)) return CBK_E_HIP;
-    hipLaunchKernelGGL((k_fused<B, BM, NN>), dim3(a.grid), dim3(512), lds, s, a);
+    if (!allow_lds(k_fused<B, BM, NN, RAG>, lds)) return CBK_E_HIP;
+    hipLaunchKernelGGL((k_fused<B, BM, NN, RAG>), dim3(a.grid), dim3(512), lds, s, a);
     return launched();
+}
+
+template <int B, int BM>
+cbk_status fused_kind(const FusedArgs &a, bool nn, hipStream_t s) {
+    const bool rag = a.cols % 64 != 0;
+    if (nn) return rag ? fused_run<B, BM, true, true>(a, s) : fused_run<B, BM, true, false>(a, s);
+    return rag ? fused_run<B, BM, false, true>(a, s) : fused_run<B, BM, false, false>(a, s);
 }
 
 }  // namespace
 
 template <int B>
 cbk_status launch_fused(const FusedArgs &a, uint32_t bm, bool nn, hipStream_t s) {
-    if (nn) {
-        if (bm == 16) return fused_run<B, 16, true>(a, s);
-        if (bm == 64) return fused_run<B, 64, true>(a, s);
-        if (bm == 128) return fused_run<B, 128, true>(a, s);
-        return fused_run<B, 256, true>(a, s);
+    switch (bm) {
+        case 16: return fused_kind<B, 16>(a, nn, s);
+        case 64: return fused_kind<B, 64>(a, nn, s);
+        case 128: return fused_kind<B, 128>(a, nn, s);
+        case 192: return fused_kind<B, 192>(a, nn, s);
+        case 256: return fused_kind<B, 256>(a, nn, s);
+        default: return fused_kind<B, 384>(a, nn, s);
     }
-    if (bm == 16) return fused_run<B, 16, false>(a, s);
-    if (bm == 64) return fused_run<B, 64, false>(a, s);
-    if (bm == 128) return fused_run<B, 128, false>(a, s);
-    return fused_run<B, 256, false>(a, s);
 }
 
 }  // namespace cbk

@@ -1,4 +1,4 @@
-// cbk_nn_fused.h for index widths: 13.
+// cbk_nn_fused.h for index width 13.
 #include "cbk_nn_fused.h"
 
 namespace cbk {

@@ -1,7 +1,6 @@
-// cbk_nn_fused.h for index widths: 12 14.
+// cbk_nn_fused.h for index width 14.
 #include "cbk_nn_fused.h"
 
 namespace cbk {
-template cbk_status launch_fused<12>(const FusedArgs &, uint32_t, bool, hipStream_t);
 template cbk_status launch_fused<14>(const FusedArgs &, uint32_t, bool, hipStream_t);
 }  // namespace cbk

@@ -1,7 +1,6 @@
-// cbk_nn_fused.h for index widths: 8 9.
+// cbk_nn_fused.h for index width 8.
 #include "cbk_nn_fused.h"
 
 namespace cbk {
 template cbk_status launch_fused<8>(const FusedArgs &, uint32_t, bool, hipStream_t);
-template cbk_status launch_fused<9>(const FusedArgs &, uint32_t, bool, hipStream_t);
 }  // namespace cbk

@@ -1,0 +1,6 @@
+// cbk_nn_fused.h for index width 9.
+#include "cbk_nn_fused.h"
+
+namespace cbk {
+template cbk_status launch_fused<9>(const FusedArgs &, uint32_t, bool, hipStream_t);
+}  // namespace cbk

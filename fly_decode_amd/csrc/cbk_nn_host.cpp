@@ -71,15 +71,14 @@ namespace cbk {
 namespace {
 
 // The token tile of k_fused, or 0 where the tensors or the number of tokens are not its kind: widths
-// 8 to 14 (equal, for a pair), rows of whole 64-field units, up to 256 tokens, and a workgroup's
-// tables and slices within the LDS.
+// 8 to 14 (equal, for a pair), up to 384 tokens, and a workgroup's tables and slices within the LDS.
 uint32_t fused_tile(const cbk_tensor *const *ts, uint64_t count, uint64_t tokens) {
-    if (tokens > 256) return 0;
+    if (tokens > 384) return 0;
     for (uint64_t i = 0; i < count; ++i) {
         const cbk_tensor &t = *ts[i];
-        if (t.b < 8 || t.b > 14 || t.b != ts[0]->b || t.cols == 0 || t.cols % 64 != 0 || !aligned(t.codebook, 16)) return 0;
+        if (t.b < 8 || t.b > 14 || t.b != ts[0]->b || t.cols == 0 || !aligned(t.codebook, 16)) return 0;
     }
-    const uint32_t bm = tokens <= 16 ? 16 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256;
+    const uint32_t bm = tokens <= 16 ? 16 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : tokens <= 192 ? 192 : tokens <= 256 ? 256 : 384;
     return nn_fused_lds(ts[0]->b, bm, static_cast<uint32_t>(count)) <= 160 * 1024 ? bm : 0;
 }
 
@@ -91,7 +90,7 @@ uint32_t nn_fused_lds(uint32_t b, uint32_t bm, uint32_t count) { return count * 
 // A decoded piece takes up to kPieceBytes and kPieceRows, so that a call's scratch stays far below
 // the tensor's uncompressed size; chunks of kChunk tokens bound what is kept per token.
 NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
-    constexpr uint64_t kPieceBytes = uint64_t(128) << 20;
+    constexpr uint64_t kPieceBytes = uint64_t(256) << 20;
     constexpr uint64_t kPieceRows = 32768;
     constexpr uint64_t kChunk = 8192;
     const uint64_t rows = ts[0]->rows, cols = ts[0]->cols;

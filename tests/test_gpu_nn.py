@@ -14,11 +14,13 @@ SHAPES = [
     (33, 129, 100, 1000), (64, 256, 256, 5000), (65, 255, 321, 9000), (128, 128, 64, 1), (129, 100, 640, 300),
     (200, 515, 1000, 3000), (257, 384, 320, 40000), (31, 2000, 72, 30), (5, 700, 448, 20000),
 ]
-# up to 256 tokens, rows of whole 64-field units and widths 8 to 14 (here 8, 9, 10, 11, 12, 13, 14): decoded on the way
+# up to 384 tokens and widths 8 to 14 (all of them here), whole 64-field units a row and not: decoded on the way
 FUSED = [
     (1, 128, 64, 250), (2, 1000, 1024, 500), (13, 515, 448, 1000), (16, 64, 4096, 2000), (17, 2113, 192, 4000),
     (63, 640, 1088, 8000), (64, 130, 64, 5000), (65, 384, 512, 16000), (128, 900, 320, 3000), (129, 1000, 576, 260),
     (200, 1291, 704, 16000), (256, 257, 2048, 7000),
+    (257, 700, 129, 2000), (384, 260, 1001, 6000), (320, 384, 256, 10000), (12, 999, 333, 14000), (150, 129, 63, 300),
+    (192, 65, 1025, 500), (7, 4097, 95, 1000),
 ]
 
 
