@@ -225,16 +225,20 @@ __global__ __launch_bounds__(64 * kUnpackWaves) void k_unpack(const UnpackArgs a
 // A workgroup of WM x WN waves owns a BM x BN tile, a wave (BM / WM) x (BN / WN) of it in 16 x 16
 // fragments of v_mfma_f32_16x16x32_bf16.  The weights are the instruction's A operand and the
 // tokens its B operand, so lane l holds columns n = 4 (l / 16) + 0..3 of token m = l % 16 of a
-// fragment: four neighbours in the output's rows.  Slices of 64 of the reduction are copied
-// straight into LDS (16 bytes a lane), the next one while the current one is multiplied.
+// fragment: four neighbours in the output's rows.  Slices of 32 of the reduction are copied
+// straight into LDS (16 bytes a lane).
 //
 // LDS layout.  A copy fills 1024 consecutive bytes, so what is permuted is which 16-byte chunk a
-// lane fetches.  Rows of 64 reduction elements (A, and B when NN is false) are 8 chunks, chunk c
-// of row r in slot c ^ (r & 7): the 8 lanes that read 8 rows' chunks at once hit 8 different
-// slots.  When NN is true B's slice is 64 reduction rows of BN columns, read with the transposing
-// 64-bit LDS read (a group of 16 lanes reads 4 rows x 16 columns, and lane i gets column i); chunk
-// c of row r sits in slot c ^ (2 (r & 3) + 8 ((r / 8) & 1..3)), so the 4 rows of a group and
-// neighbouring groups hit different banks.
+// lane fetches.  Rows of 32 reduction elements (A, and B when NN is false) are 4 chunks, chunk c
+// of row r in slot c ^ (-(r / 4) & 3).  A 128-bit read serves 16 lanes at a time, of which lanes
+// 0-3 and 12-15 take one chunk of rows 0-3 and 12-15 and lanes 20-27 the next chunk of rows 4-11 (and
+// so on); this order puts the 16 into different banks, where c ^ ((r / 4) & 3) made two meet.  When NN is true B's slice is 32 reduction rows of BN columns, read with the
+// transposing 64-bit LDS read (a group of 16 lanes reads 4 rows x 16 columns, and lane i gets
+// column i); chunk c of row r sits in slot c ^ (2 (r & 3) + 8 ((r / 8) & 1..3)), so the 4 rows of a
+// group and neighbouring groups hit different banks.
+constexpr uint32_t kRing = 5;  // slices of 32 in LDS
+constexpr int kMmTile = 256, kMmWm = 2, kMmWn = 4;  // tile and its waves
+
 enum Epi { kOut, kGated, kGatedBwd, kStats, kProb };
 
 struct MmArgs {
@@ -244,6 +248,8 @@ struct MmArgs {
     uint32_t ldb;
     uint32_t M, N;  // tokens; columns of C that exist
     uint32_t ktiles, tm, tn;
+    uint32_t whole;  // tiles that one workgroup does from end to end; the others' slices are shared
+    float *part;     // the sharers' sums, [sharers + shared tiles][kMmTile][kMmTile]
 
     uint16_t *out;  // kOut, kGated: [M][ldo] BF16
     uint64_t ldo;
@@ -354,26 +360,69 @@ __device__ __forceinline__ void emit_prob(const MmArgs &p, uint32_t m, uint32_t 
     store4(p.G + static_cast<uint64_t>(m) * p.ldG + n, v, 4, true);
 }
 
-template <int BM, int BN, int WM, int WN, bool NN, int EPI>
-__global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
-    constexpr int NW = WM * WN;
+// Four column fragments by transposing reads, their second halves HI bytes after the first; `at` are
+// LDS addresses.  Written out because the compiler holds the transposing read back until every copy
+// into LDS has landed, also those of slices still to come; the block waits for its own reads.
+template <int HI>
+__device__ __forceinline__ void read_columns(bf16x8_t (&x)[4], const uint32_t (&at)[4]) {
+    u32x2 a0, a1, a2, a3, b0, b1, b2, b3;
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8\n"
+        "ds_read_b64_tr_b16 %1, %8 offset:%c12\n"
+        "ds_read_b64_tr_b16 %2, %9\n"
+        "ds_read_b64_tr_b16 %3, %9 offset:%c12\n"
+        "ds_read_b64_tr_b16 %4, %10\n"
+        "ds_read_b64_tr_b16 %5, %10 offset:%c12\n"
+        "ds_read_b64_tr_b16 %6, %11\n"
+        "ds_read_b64_tr_b16 %7, %11 offset:%c12\n"
+        "s_waitcnt lgkmcnt(0)\n"
+        : "=&v"(a0), "=&v"(b0), "=&v"(a1), "=&v"(b1), "=&v"(a2), "=&v"(b2), "=&v"(a3), "=&v"(b3)
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "i"(HI)
+        : "memory");
+    x[0] = __builtin_bit_cast(bf16x8_t, (u32x4){a0.x, a0.y, b0.x, b0.y});
+    x[1] = __builtin_bit_cast(bf16x8_t, (u32x4){a1.x, a1.y, b1.x, b1.y});
+    x[2] = __builtin_bit_cast(bf16x8_t, (u32x4){a2.x, a2.y, b2.x, b2.y});
+    x[3] = __builtin_bit_cast(bf16x8_t, (u32x4){a3.x, a3.y, b3.x, b3.y});
+}
+
+// Token and column where tile number `tile` starts: tiles are ordered in groups of 8 token tiles.
+__device__ __forceinline__ void mm_tile_at(const MmArgs &p, uint32_t tile, uint32_t &m0, uint32_t &n0) {
+    const uint32_t per = 8 * p.tn, grp = tile / per, g0 = grp * 8, gm = min(8u, p.tm - g0), in = tile - grp * per;
+    m0 = (g0 + in % gm) * kMmTile;
+    n0 = (in / gm) * kMmTile;
+}
+
+template <bool NN, int EPI>
+__global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
+    constexpr int BM = kMmTile, BN = kMmTile, WM = kMmWm, WN = kMmWn, NW = WM * WN;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-    constexpr uint32_t ABYTES = BM * 128, BBYTES = BN * 128;  // one slice
+    constexpr uint32_t ABYTES = BM * 64, BBYTES = BN * 64, SLICE = ABYTES + BBYTES;
     constexpr int IA = ABYTES / 1024 / NW, IB = BBYTES / 1024 / NW;
-    static_assert(IA * NW * 1024 == ABYTES && IB * NW * 1024 == BBYTES, "whole copies");
+    static_assert(IA * NW * 1024 == ABYTES && IB * NW * 1024 == BBYTES && FN == 4, "whole copies, four column fragments");
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const uint32_t li = lane & 15, lg = lane >> 4;
 
-    // Workgroups go to the 8 XCDs in turn; give each XCD a run of consecutive tiles, and order the
-    // tiles in groups of GM token tiles, so that an XCD's workgroups share rows and columns in its L2.
-    const uint32_t all = p.tm * p.tn, q = all >> 3, rem = all & 7, xcd = blockIdx.x & 7;
-    const uint32_t lin = xcd * q + min(xcd, rem) + (blockIdx.x >> 3);
-    constexpr uint32_t GM = 8;
-    const uint32_t per = GM * p.tn, grp = lin / per, g0 = grp * GM, gm = min(GM, p.tm - g0);
-    const uint32_t in = lin - grp * per;
-    const uint32_t m0 = (g0 + in % gm) * BM, n0 = (in / gm) * BN;
+    // Whole tiles first, then the workgroups that share the last tiles' slices evenly.  Workgroups go
+    // to the 8 XCDs in turn; each XCD gets a run of consecutive whole tiles, so that its workgroups
+    // share rows and columns in its L2.
+    uint64_t pos, end;
+    if (blockIdx.x < p.whole) {
+        const uint32_t q = p.whole >> 3, rem = p.whole & 7, xcd = blockIdx.x & 7;
+        pos = static_cast<uint64_t>(xcd * q + min(xcd, rem) + (blockIdx.x >> 3)) * p.ktiles;
+        end = pos + p.ktiles;
+    } else {
+        const uint64_t shared = static_cast<uint64_t>(p.tm * p.tn - p.whole) * p.ktiles;
+        const uint32_t w = blockIdx.x - p.whole, ws = gridDim.x - p.whole;
+        pos = static_cast<uint64_t>(p.whole) * p.ktiles + w * shared / ws;
+        end = static_cast<uint64_t>(p.whole) * p.ktiles + (w + 1) * shared / ws;
+    }
+    while (pos < end) {
+    const uint32_t tile = static_cast<uint32_t>(pos / p.ktiles), k0 = static_cast<uint32_t>(pos - static_cast<uint64_t>(tile) * p.ktiles);
+    const uint32_t kn = static_cast<uint32_t>(min(static_cast<uint64_t>(p.ktiles - k0), end - pos));
+    uint32_t m0, n0;
+    mm_tile_at(p, tile, m0, n0);
 
     // copies: this lane's byte offsets within A's and B's resources
     const auto ra = wave_rsrc(p.A + static_cast<uint64_t>(m0) * p.lda, 0x7FFFFFF0u);
@@ -381,7 +430,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
     uint32_t va[IA], vb[IB];
 #pragma unroll
     for (int i = 0; i < IA; ++i) {
-        const uint32_t r = (wave + NW * i) * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+        const uint32_t r = (wave + NW * i) * 16 + (lane >> 2), c = (lane & 3) ^ (-(lane >> 4) & 3);
         va[i] = min(r, p.M - 1 - m0) * static_cast<uint32_t>(p.lda) * 2u + c * 16u;  // rows past M repeat the last one
     }
 #pragma unroll
@@ -392,24 +441,22 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
             const uint32_t c = (lane % CH) ^ (2 * (r & 3) + 8 * ((r >> 3) & (CH / 8 - 1)));
             vb[i] = (r * p.ldb + min(n0 + c * 8, p.ldb - 8)) * 2u;  // columns past the piece repeat its last chunk
         } else {
-            const uint32_t r = (wave + NW * i) * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+            const uint32_t r = (wave + NW * i) * 16 + (lane >> 2), c = (lane & 3) ^ (-(lane >> 4) & 3);
             vb[i] = r * p.ldb * 2u + c * 16u;
         }
     }
-    auto fetch = [&](uint32_t kt, uint32_t buf) {
-        unsigned char *da = smem + buf * ABYTES, *db = smem + 2 * ABYTES + buf * BBYTES;
+    const uint32_t step_b = NN ? 64 * p.ldb : 64;
+    auto copy = [&](uint32_t s, uint32_t at) {
+        unsigned char *to = smem + at;
 #pragma unroll
-        for (int i = 0; i < IA; ++i)
-            copy_to_lds(ra, da + (wave + NW * i) * 1024, va[i], kt * 128);
-        const uint32_t sb = NN ? kt * 128 * p.ldb : kt * 128;
+        for (int i = 0; i < IA; ++i) copy_to_lds(ra, to + (wave + NW * i) * 1024, va[i], (2 * k0 + s) * 64);
 #pragma unroll
-        for (int i = 0; i < IB; ++i)
-            copy_to_lds(rb, db + (wave + NW * i) * 1024, vb[i], sb);
+        for (int i = 0; i < IB; ++i) copy_to_lds(rb, to + ABYTES + (wave + NW * i) * 1024, vb[i], (2 * k0 + s) * step_b);
     };
 
     // fragment reads: byte offsets of this lane
-    const uint32_t fa = (wm * (BM / WM) + li) * 128 + ((lg ^ (li & 7)) * 16);
-    const uint32_t fb = (wn * (BN / WN) + li) * 128 + ((lg ^ (li & 7)) * 16);
+    const uint32_t swz = (lg ^ (-(li >> 2) & 3)) * 16;
+    const uint32_t fa = (wm * (BM / WM) + li) * 64 + swz, fb = ABYTES + (wn * (BN / WN) + li) * 64 + swz;
     uint32_t ft[FN];
     if constexpr (NN) {
         constexpr uint32_t CH = BN / 8;
@@ -417,51 +464,95 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
         for (int j = 0; j < FN; ++j) {
             const uint32_t r = 8 * lg + (li >> 2);
             const uint32_t c = (wn * (BN / WN) + 16 * j) / 8 + ((li & 3) >> 1);
-            ft[j] = r * (BN * 2) + (c ^ (2 * (r & 3) + 8 * (lg & (CH / 8 - 1)))) * 16 + (li & 1) * 8;
+            ft[j] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((CBK_LDS unsigned char *)(smem))) + ABYTES + r * (BN * 2) +
+                    (c ^ (2 * (r & 3) + 8 * (lg & (CH / 8 - 1)))) * 16 + (li & 1) * 8;
         }
     }
+    struct Frags {
+        bf16x8_t a[FM], b[FN];
+    };
+    auto read = [&](Frags &f, uint32_t at) {
+        if constexpr (NN) {
+            const uint32_t t[4] = {ft[0] + at, ft[1] + at, ft[2] + at, ft[3] + at};
+            read_columns<4 * BN * 2>(f.b, t);
+        } else {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) f.b[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(smem + at + fb + j * 1024));
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) f.a[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(smem + at + fa + i * 1024));
+    };
 
     f32x4_t acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const Frags &f) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+    };
 
-    fetch(0, 0);
-    for (uint32_t kt = 0; kt < p.ktiles; ++kt) {
-        const uint32_t buf = kt & 1;
-        // this slice has arrived, and no wave still reads the buffer that the next one goes to
-        __builtin_amdgcn_s_waitcnt(0x0070);
+    // Slices of 32 in a ring of five buffers: while slice s is multiplied from registers, s + 1 is read
+    // from LDS, s + 2 has to arrive by the interval's end, s + 3 is on its way and s + 4 is asked for
+    // (into the buffer of s - 1, whose reads ended before the last barrier).  Every slice is new to
+    // the XCD's L2, so a copy takes the time of several intervals.  There is an even number of slices.
+    constexpr int CP = IA + IB;
+    const uint32_t n = kn * 2;
+    Frags f0, f1;
+    uint32_t ahead = 0, behind = 0;  // byte offsets of the buffers of the next copy and the next read
+    auto step = [](uint32_t &at) { at = at == (kRing - 1) * SLICE ? 0u : at + SLICE; };
+    for (uint32_t s = 0; s < 4 && s < n; ++s) {
+        copy(s, ahead);
+        step(ahead);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read(f0, behind);
+    step(behind);
+    auto interval = [&](uint32_t s, const Frags &now, Frags &next) {
+        read(next, behind);              // after the last slice: old contents of a buffer, not used
+        step(behind);
+        copy(min(s + 4, n - 1), ahead);  // past the end: the last slice again, into a buffer that is not read
+        step(ahead);
+        multiply(now);
+        // the reads, then the copies, between the multiplications
+        constexpr int RD = NN ? FM : FM + FN, MF = FM * FN - RD;
+#pragma unroll
+        for (int i = 0; i < RD; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < CP; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, MF / CP, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, MF - MF / CP * CP, 0);
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * CP));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        if (kt + 1 < p.ktiles) fetch(kt + 1, buf ^ 1);
-        const unsigned char *sa = smem + buf * ABYTES, *sb = smem + 2 * ABYTES + buf * BBYTES;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8_t xa[FM], xb[FN];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if constexpr (NN) {
-                    const unsigned char *at = sb + ft[j] + ks * 32 * BN * 2;
-                    const s16x4 lo = read_transposed(at);
-                    const s16x4 hi = read_transposed(at + 4 * BN * 2);
-                    xb[j] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                } else {
-                    xb[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sb + (fb ^ (ks * 64)) + j * 2048));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-                xa[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sa + (fa ^ (ks * 64)) + i * 2048));
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[j], xa[i], acc[i][j], 0, 0, 0);
-        }
+    };
+    for (uint32_t s = 0; s < n; s += 2) {
+        interval(s, f0, f1);
+        interval(s + 1, f1, f0);
     }
+    __builtin_amdgcn_s_waitcnt(0x0070);  // no copy is left in flight
+    pos += kn;
 
     const uint32_t mw = m0 + wm * (BM / WM) + li, nw = n0 + wn * (BN / WN) + 4 * lg;  // of fragment (0, 0)
-    if constexpr (EPI == kOut || EPI == kProb) {
+    if (EPI == kOut && kn < p.ktiles) {
+        // a part of a tile: its sums, for k_mm_join
+        float *part = p.part + (static_cast<uint64_t>(blockIdx.x - p.whole) + (tile - p.whole)) * (BM * BN);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                *reinterpret_cast<f32x4_t *>(part + (mw - m0 + 16 * i) * BN + (nw - n0) + 16 * j) = acc[i][j];
+    } else if constexpr (EPI == kOut || EPI == kProb) {
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const uint32_t m = mw + 16 * i;
@@ -529,19 +620,44 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mm(const MmArgs p) {
             if (lg == 0) part[(wm * (BM / WM) + 16 * i + li) * WN + wn] = (f32x2){mx, s};
         }
         __syncthreads();
-        if (tid < BM && m0 + tid < p.M) {
+        constexpr int W128 = 128 / (BN / WN);  // waves that share 128 columns
+        for (uint32_t t = tid; t < BM * (BN / 128); t += 64 * NW) {
+            const uint32_t row = t / (BN / 128), h = t % (BN / 128);
+            if (m0 + row >= p.M || n0 + 128 * h >= p.N) continue;
+            const f32x2 *w = part + row * WN + h * W128;
             float mx = -__builtin_inff(), s = 0.f;
 #pragma unroll
-            for (int w = 0; w < WN; ++w) mx = fmaxf(mx, part[tid * WN + w][0]);
+            for (int i = 0; i < W128; ++i) mx = fmaxf(mx, w[i][0]);
             const float base = exp_base(mx);
 #pragma unroll
-            for (int w = 0; w < WN; ++w) {
-                const f32x2 t = part[tid * WN + w];
-                if (t[1] != 0.f) s += t[1] * __expf(exp_base(t[0]) - base);
-            }
-            p.stat[static_cast<uint64_t>(m0 + tid) * p.ldstat + p.stat0 + n0 / BN] = (f32x2){mx, s};
+            for (int i = 0; i < W128; ++i)
+                if (w[i][1] != 0.f) s += w[i][1] * __expf(exp_base(w[i][0]) - base);
+            p.stat[static_cast<uint64_t>(m0 + row) * p.ldstat + p.stat0 + n0 / 128 + h] = (f32x2){mx, s};
         }
     }
+    // the next part's copies go to buffers that other waves may still be reading
+    if (pos < end) __syncthreads();
+    }
+}
+
+// The shared tiles' parts added in order.  A workgroup takes 4 tokens of a tile.
+__global__ __launch_bounds__(256) void k_mm_join(const MmArgs p, uint32_t sharers) {
+    const uint32_t tile = p.whole + blockIdx.x, row = blockIdx.y * 4 + (threadIdx.x >> 6), c = (threadIdx.x & 63) * 4;
+    uint32_t m0, n0;
+    mm_tile_at(p, tile, m0, n0);
+    if (m0 + row >= p.M) return;
+    // run w starts at floor(w * total / sharers)
+    const uint64_t total = static_cast<uint64_t>(p.tm * p.tn - p.whole) * p.ktiles, at = static_cast<uint64_t>(blockIdx.x) * p.ktiles;
+    const uint32_t g0 = static_cast<uint32_t>(((at + 1) * sharers - 1) / total);
+    const uint32_t g1 = static_cast<uint32_t>(((at + p.ktiles) * sharers - 1) / total);
+    if (g0 == g1) return;  // one workgroup had it whole
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t g = g0; g <= g1; ++g) {
+        const f32x4_t t = *reinterpret_cast<const f32x4_t *>(p.part + static_cast<uint64_t>(g + blockIdx.x) * (kMmTile * kMmTile) + row * kMmTile + c);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += t[r];
+    }
+    emit_out(p, m0 + row, n0 + c, v);
 }
 
 // The parts of a tile that k_fused left, added in order, and the operator's work on the sums.  A
@@ -722,20 +838,34 @@ cbk_status unpack(const cbk_tensor *const *ts, uint32_t count, uint64_t row0, ui
     return CBK_OK;
 }
 
-template <int BM, int BN, int WM, int WN, bool NN, int EPI>
-cbk_status mm_tile(MmArgs &p, uint32_t columns, hipStream_t s) {
-    constexpr uint32_t lds = 2 * (BM + BN) * 128;
-    if (!allow_lds(k_mm<BM, BN, WM, WN, NN, EPI>, lds)) return CBK_E_HIP;
-    p.tm = ceil_div(p.M, BM);
-    p.tn = ceil_div(columns, BN);
-    hipLaunchKernelGGL((k_mm<BM, BN, WM, WN, NN, EPI>), dim3(p.tm * p.tn), dim3(64 * WM * WN), lds, s, p);
-    return launched();
-}
-
 // `columns`: the columns of C to cover.
 template <bool NN, int EPI>
 cbk_status mm(MmArgs &p, uint32_t columns, hipStream_t s) {
-    return mm_tile<128, 128, 2, 2, NN, EPI>(p, columns, s);
+    constexpr uint32_t lds = kRing * 2 * kMmTile * 64;
+    if (!allow_lds(k_mm<NN, EPI>, lds)) return CBK_E_HIP;
+    p.tm = ceil_div(p.M, kMmTile);
+    p.tn = ceil_div(columns, kMmTile);
+    const uint32_t tiles = p.tm * p.tn, cus = 256;
+    // One workgroup runs on a CU, so the tiles are done in rounds of 256.  What is left over after
+    // the whole rounds is shared by a round's workgroups where that pays for writing and adding its
+    // parts (about 0.12 us a part, where a slice of 64 takes 1.9 us a round).
+    uint32_t sharers = 0;
+    p.whole = tiles;
+    if (EPI == kOut) {
+        const uint32_t over = tiles % cus;
+        if (over > 0 && over <= kMmShared) {
+            const double saved = (1.0 - static_cast<double>(over) / cus) * p.ktiles * 1.9;
+            if (saved > 0.12 * (cus + over) + 5.0) {
+                sharers = static_cast<uint32_t>(std::min<uint64_t>(cus, static_cast<uint64_t>(over) * p.ktiles / 4));
+                p.whole = tiles - over;
+            }
+        }
+    }
+    hipLaunchKernelGGL((k_mm<NN, EPI>), dim3(p.whole + sharers), dim3(64 * kMmWm * kMmWn), lds, s, p);
+    CBK_TRY(launched());
+    if (sharers == 0) return CBK_OK;
+    hipLaunchKernelGGL(k_mm_join, dim3(tiles - p.whole, kMmTile / 4), dim3(256), 0, s, p, sharers);
+    return launched();
 }
 
 // The tokens' side of a product: used as it is if the copies to LDS can read whole 64-wide slices
@@ -868,6 +998,7 @@ struct Weights {
             return join<EPI>(p, q);
         }
         p.B = at<uint16_t>(ws, pl.w);
+        p.part = at<float>(ws, pl.part);
         p.ldb = static_cast<uint32_t>(pl.Kp);
         p.ktiles = static_cast<uint32_t>(pl.Kp / 64);
         const uint64_t rows = piece_rows(nrows, count == 2);
@@ -891,6 +1022,7 @@ struct Weights {
             return join<kOut>(p, q);
         }
         p.B = at<uint16_t>(ws, pl.w);
+        p.part = at<float>(ws, pl.part);
         p.ldb = static_cast<uint32_t>(pl.Kp);
         p.ktiles = static_cast<uint32_t>(reduction() / 64);
         return mm<true, kOut>(p, p.N, s);

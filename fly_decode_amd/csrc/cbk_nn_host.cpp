@@ -120,6 +120,9 @@ NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
         p.part = take((p.grid + std::max(p.Rp, p.Kp + 64) / 128) * p.Tc * 128 * 4);
     } else {
         p.w = take(p.Rp * p.Kp * 2);
+        // no more tiles are shared than the largest product of the call has
+        const uint64_t tiles = up_to(p.Tc, 256) / 256 * (up_to(std::max(p.Kp, p.Rp), 256) / 256);
+        p.part = take((256 + std::min<uint64_t>(kMmShared, tiles)) * 256 * 256 * 4);
     }
     p.g = op == NnOp::linear ? at : take(p.Tc * p.Rp * 2);
     p.acc = p.pieces > 1 ? take(p.Tc * p.Kp * 4) : at;

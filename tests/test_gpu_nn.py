@@ -23,6 +23,12 @@ FUSED = [
     (192, 65, 1025, 500), (7, 4097, 95, 1000),
 ]
 
+# more tokens: pieces of the weights are decoded first; the first two share a tile's reduction among workgroups
+MANY = [
+    (500, 300, 20000, 3000), (385, 20000, 300, 2000), (600, 1000, 130, 40000), (1025, 515, 640, 900), (700, 129, 77, 5),
+    (513, 33, 1088, 9000),
+]
+
 
 @pytest.fixture(scope="module")
 def env():
@@ -53,7 +59,7 @@ def acts(torch, T, n, seed, scale=1.0):
     return (torch.randn(T, n, generator=torch.Generator().manual_seed(seed)) * scale).bfloat16()
 
 
-@pytest.mark.parametrize("T,rows,cols,U", SHAPES + FUSED)
+@pytest.mark.parametrize("T,rows,cols,U", SHAPES + FUSED + MANY)
 def test_linear(env, T, rows, cols, U):
     torch, cbk = env
     w, x = weights(torch, rows, cols, U, 1), acts(torch, T, cols, 2)
@@ -61,7 +67,7 @@ def test_linear(env, T, rows, cols, U):
     ref.assert_within(y, *ref.linear(x, w), "linear")
 
 
-@pytest.mark.parametrize("T,rows,cols,U", SHAPES + FUSED)
+@pytest.mark.parametrize("T,rows,cols,U", SHAPES + FUSED + MANY)
 def test_linear_dx(env, T, rows, cols, U):
     torch, cbk = env
     w, dy = weights(torch, rows, cols, U, 3), acts(torch, T, rows, 4)
@@ -90,7 +96,7 @@ def test_ffn_gated_bwd(env, T, rows, cols, U, act):
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
-@pytest.mark.parametrize("T,rows,cols,U", FUSED)
+@pytest.mark.parametrize("T,rows,cols,U", FUSED + MANY)
 def test_ffn_pair_of_one_width(env, T, rows, cols, U, act):
     """Forward and gradient where gate and up have the same width (one launch decodes both)."""
     torch, cbk = env
@@ -105,7 +111,7 @@ def test_ffn_pair_of_one_width(env, T, rows, cols, U, act):
         ref.assert_within(v, *want, name)
 
 
-@pytest.mark.parametrize("T,rows,cols,U", SHAPES + FUSED)
+@pytest.mark.parametrize("T,rows,cols,U", SHAPES + FUSED + MANY)
 def test_xent_and_gradient(env, T, rows, cols, U):
     torch, cbk = env
     w, x = weights(torch, rows, cols, U, 12, 0.1), acts(torch, T, cols, 13)
