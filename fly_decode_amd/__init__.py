@@ -689,13 +689,15 @@ class _Call:
     """Device, stream, outputs and workspace of one call on the device of ``x``: allocations come
     from torch's allocator and, where the caller names a stream of its own, are recorded on it."""
 
+    __slots__ = ("torch", "device", "given", "stream")
+
     def __init__(self, x, stream):
         import torch
-        if x.device.type != "cuda":
-            raise ValueError("the operators run on GPU tensors")
         self.torch, self.device = torch, x.device
+        if self.device.type != "cuda":
+            raise ValueError("the operators run on GPU tensors")
         self.given = stream is not None
-        self.stream = stream if self.given else torch.cuda.current_stream(x.device)
+        self.stream = stream if self.given else torch.cuda.current_stream(self.device)
 
     def empty(self, shape, dtype):
         out = self.torch.empty(shape, dtype=dtype, device=self.device)
@@ -703,20 +705,21 @@ class _Call:
             out.record_stream(self.stream)
         return out
 
-    def run(self, name, need, workspace, *args):
+    def run(self, name, sizes, workspace, *args):
+        """Calls ``name``; the workspace is allocated as ``sizes``, a name and its arguments, says
+        where none is given."""
+        lib = load_library()
         if workspace is None:
             # at least one element, so that there is an address; torch's blocks are 512-byte aligned
-            workspace = self.empty((max(need, 1),), self.torch.uint8)
+            workspace = self.empty((getattr(lib, sizes[0])(*sizes[1:]) or 1,), self.torch.uint8)
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
-        nbytes = workspace.numel() * workspace.element_size()
-        tail = (ctypes.c_void_p(workspace.data_ptr() or None), nbytes, ctypes.c_void_p(self.stream.cuda_stream))
-        fn = getattr(load_library(), name)
+        args += (workspace.data_ptr() or None, workspace.numel() * workspace.element_size(), self.stream.cuda_stream)
         if self.torch.cuda.current_device() == self.device.index:
-            st = fn(*args, *tail)
+            st = getattr(lib, name)(*args)
         else:
             with self.torch.cuda.device(self.device):
-                st = fn(*args, *tail)
+                st = getattr(lib, name)(*args)
         _check(st, name)
 
 
@@ -733,8 +736,7 @@ def linear(t: Compressed, X, out=None, workspace=None, stream=None):
     if out.shape[0] != T:
         raise ValueError("out and X differ in tokens")
     ts = ctypes.byref(t._struct())
-    call.run("cbk_linear", int(load_library().cbk_linear_workspace_bytes(ts, T)) if workspace is None else 0, workspace,
-             ts, xp, ldx, T, op, ldo)
+    call.run("cbk_linear", ("cbk_linear_workspace_bytes", ts, T), workspace, ts, xp, ldx, T, op, ldo)
     return out
 
 
@@ -750,8 +752,7 @@ def linear_dx(t: Compressed, dY, out=None, workspace=None, stream=None):
     if out.shape[0] != T:
         raise ValueError("out and dY differ in tokens")
     ts = ctypes.byref(t._struct())
-    call.run("cbk_linear_dx", int(load_library().cbk_linear_workspace_bytes(ts, T)) if workspace is None else 0, workspace,
-             ts, gp, ldg, T, op, ldo)
+    call.run("cbk_linear_dx", ("cbk_linear_workspace_bytes", ts, T), workspace, ts, gp, ldg, T, op, ldo)
     return out
 
 
@@ -771,8 +772,7 @@ def ffn_gated(gate: Compressed, up: Compressed, X, act: str = "silu", out=None, 
     if out.shape[0] != T:
         raise ValueError("out and X differ in tokens")
     gs, us = ctypes.byref(gate._struct()), ctypes.byref(up._struct())
-    call.run("cbk_ffn_gated", int(load_library().cbk_ffn_workspace_bytes(gs, us, T)) if workspace is None else 0, workspace,
-             gs, us, _ACTS[act], xp, ldx, T, op, ldo)
+    call.run("cbk_ffn_gated", ("cbk_ffn_workspace_bytes", gs, us, T), workspace, gs, us, _ACTS[act], xp, ldx, T, op, ldo)
     return out
 
 
@@ -799,8 +799,7 @@ def ffn_gated_bwd(gate: Compressed, up: Compressed, X, dH, act: str = "silu", dX
     if projections:
         dG, dU = call.empty((T, gate.rows), X.dtype), call.empty((T, gate.rows), X.dtype)
     gs, us = ctypes.byref(gate._struct()), ctypes.byref(up._struct())
-    call.run("cbk_ffn_gated_bwd", int(load_library().cbk_ffn_workspace_bytes(gs, us, T)) if workspace is None else 0,
-             workspace, gs, us, _ACTS[act], xp, ldx, hp, ldh, T, dp, ldd, (dG.data_ptr() or None) if projections else None,
+    call.run("cbk_ffn_gated_bwd", ("cbk_ffn_workspace_bytes", gs, us, T), workspace, gs, us, _ACTS[act], xp, ldx, hp, ldh, T, dp, ldd, (dG.data_ptr() or None) if projections else None,
              (dU.data_ptr() or None) if projections else None, gate.rows)
     return dX, dG, dU
 
@@ -817,8 +816,7 @@ def xent(head: Compressed, X, labels, ignore_index: int = -100, workspace=None, 
     call = _Call(X, stream)
     loss, lse = call.empty((T,), torch.float32), call.empty((T,), torch.float32)
     hs = ctypes.byref(head._struct())
-    call.run("cbk_xent", int(load_library().cbk_xent_workspace_bytes(hs, T)) if workspace is None else 0, workspace,
-             hs, xp, ldx, lp, T, ignore_index, loss.data_ptr() or None, lse.data_ptr() or None)
+    call.run("cbk_xent", ("cbk_xent_workspace_bytes", hs, T), workspace, hs, xp, ldx, lp, T, ignore_index, loss.data_ptr() or None, lse.data_ptr() or None)
     return loss, lse
 
 
@@ -839,6 +837,5 @@ def xent_bwd(head: Compressed, X, labels, lse, dloss, ignore_index: int = -100, 
     if out.shape[0] != T:
         raise ValueError("out and X differ in tokens")
     hs = ctypes.byref(head._struct())
-    call.run("cbk_xent_bwd", int(load_library().cbk_xent_workspace_bytes(hs, T)) if workspace is None else 0, workspace,
-             hs, xp, ldx, lp, sp, dp, T, ignore_index, op, ldo)
+    call.run("cbk_xent_bwd", ("cbk_xent_workspace_bytes", hs, T), workspace, hs, xp, ldx, lp, sp, dp, T, ignore_index, op, ldo)
     return out

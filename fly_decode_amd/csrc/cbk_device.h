@@ -246,6 +246,19 @@ bool allow_lds(K kernel, uint32_t lds) {
                                static_cast<int>(lds)) == hipSuccess;
 }
 
+// The same, asked of the runtime once for a kernel and device (Tag: a type of the kernel's own).
+template <typename Tag, typename K>
+bool allow_lds_once(K kernel, uint32_t lds) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return false;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return true;
+    if (!allow_lds(kernel, lds)) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
 // Runs Fn<b>::run(args) for the b in Bs that matches; false when none does or run declines.
 template <template <int> class Fn, typename Args, int... Bs>
 bool dispatch_b(int b, Args &args, std::integer_sequence<int, Bs...>) {

@@ -661,43 +661,52 @@ __global__ __launch_bounds__(256) void k_mm_join(const MmArgs p, uint32_t sharer
 }
 
 // The parts of a tile that k_fused left, added in order, and the operator's work on the sums.  A
-// workgroup takes 8 tokens of a tile, 32 lanes of 4 columns each (16 lanes with a column's gate and
-// up sums for a pair).
+// workgroup takes 8 tokens of a tile, 32 lanes of 4 columns each.  `count` 2: the second tensor's tile
+// holds the up sums of the same columns (forward), or the second half of one sum (gradient).
 struct JoinArgs {
     const float *part;
-    uint32_t tiles, slices, grid, up_col;  // up_col: where dU starts in G
+    uint32_t count, tiles, slices, grid, up_col;  // up_col: where dU starts in G
 };
+
+// The sum of virtual tile vt's parts at token m, columns c..c + 3, added to v.
+__device__ __forceinline__ void add_parts(const JoinArgs &q, uint32_t M, uint32_t vt, uint32_t m, uint32_t c, float (&v)[4]) {
+    // The workgroups whose runs hold the tile's first and last slice: run g starts at
+    // floor(g * total / grid).
+    const uint64_t total = static_cast<uint64_t>(q.count * q.tiles) * q.slices, at = static_cast<uint64_t>(vt) * q.slices;
+    const uint32_t g0 = static_cast<uint32_t>(((at + 1) * q.grid - 1) / total);
+    const uint32_t g1 = static_cast<uint32_t>(((at + q.slices) * q.grid - 1) / total);
+    const float *src = q.part + (static_cast<uint64_t>(vt) * M + m) * kFusedTile + c;
+    for (uint32_t g = g0; g <= g1; g += 4) {  // four loads at a time (the last part again past the end)
+        f32x4_t t[4];
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+            t[k] = *reinterpret_cast<const f32x4_t *>(src + static_cast<uint64_t>(min(g + k, g1)) * M * kFusedTile);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+            if (g + k <= g1) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] += t[k][r];
+            }
+    }
+}
 
 template <int EPI>
 __global__ __launch_bounds__(256) void k_join(const MmArgs p, const JoinArgs q) {
-    constexpr bool pair = EPI == kGated || EPI == kGatedBwd;
-    constexpr uint32_t QUADS = pair ? 16 : 32, ROWS = 256 / QUADS;
-    const uint32_t tile = blockIdx.x, m = blockIdx.y * ROWS + threadIdx.x / QUADS, c = threadIdx.x % QUADS * 4;
+    const uint32_t tile = blockIdx.x, m = blockIdx.y * 8 + threadIdx.x / 32, c = threadIdx.x % 32 * 4;
     if (m >= p.M) return;
-    // The workgroups whose runs hold the tile's first and last slice: run g starts at
-    // floor(g * total / grid).
-    const uint64_t total = static_cast<uint64_t>(q.tiles) * q.slices, at = static_cast<uint64_t>(tile) * q.slices;
-    const uint32_t g0 = static_cast<uint32_t>(((at + 1) * q.grid - 1) / total);
-    const uint32_t g1 = static_cast<uint32_t>(((at + q.slices) * q.grid - 1) / total);
     float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t g = g0; g <= g1; ++g) {
-        const float *src = q.part + (static_cast<uint64_t>(g + tile) * p.M + m) * kFusedTile + c;
-        const f32x4_t t = *reinterpret_cast<const f32x4_t *>(src);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] += t[r];
-        if constexpr (pair) {
-            const f32x4_t w = *reinterpret_cast<const f32x4_t *>(src + 64);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) u[r] += w[r];
-        }
-    }
+    add_parts(q, p.M, tile, m, c, v);
+    if constexpr (EPI == kGated || EPI == kGatedBwd)
+        add_parts(q, p.M, q.tiles + tile, m, c, u);
+    else if (EPI == kOut && q.count == 2)
+        add_parts(q, p.M, q.tiles + tile, m, c, v);
     const uint32_t n = tile * kFusedTile + c;
     if constexpr (EPI == kOut) {
         emit_out(p, m, n, v);
     } else if constexpr (EPI == kGated) {
-        emit_gated(p, m, p.f0 + tile * 64 + c, v, u);
+        emit_gated(p, m, p.f0 + n, v, u);
     } else if constexpr (EPI == kGatedBwd) {
-        emit_gated_bwd(p, m, p.f0 + tile * 64 + c, tile * 64 + c, q.up_col + tile * 64 + c, v, u);
+        if (n < q.up_col) emit_gated_bwd(p, m, p.f0 + n, n, q.up_col + n, v, u);
     } else if constexpr (EPI == kProb) {
         emit_prob(p, m, n, p.labels[m] - p.f0, p.lse[m], v);
     } else {
@@ -758,6 +767,11 @@ uint32_t grid_for(uint64_t items, uint32_t per) {
     return static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>((items + per - 1) / per, 65536)));
 }
 
+template <bool, int>
+struct MmTag;
+template <int, bool>
+struct UnpackTag;
+
 struct UnpackRunArgs {
     UnpackArgs a;
     uint32_t count;
@@ -775,10 +789,10 @@ struct UnpackRun {
         // two workgroups per CU, whose waves take every so-manieth step
         const dim3 grid(std::min(ceil_div(r.a.steps, kUnpackWaves), std::max(1u, 2 * static_cast<uint32_t>(cu_count()) / r.count)), r.count);
         if (r.a.cols % 8 == 0) {
-            if (!allow_lds(k_unpack<B, true>, lds)) return false;
+            if (!allow_lds_once<UnpackTag<B, true>>(k_unpack<B, true>, lds)) return false;
             hipLaunchKernelGGL((k_unpack<B, true>), grid, dim3(64 * kUnpackWaves), lds, r.s, r.a);
         } else {
-            if (!allow_lds(k_unpack<B, false>, lds)) return false;
+            if (!allow_lds_once<UnpackTag<B, false>>(k_unpack<B, false>, lds)) return false;
             hipLaunchKernelGGL((k_unpack<B, false>), grid, dim3(64 * kUnpackWaves), lds, r.s, r.a);
         }
         r.st = launched();
@@ -842,7 +856,7 @@ cbk_status unpack(const cbk_tensor *const *ts, uint32_t count, uint64_t row0, ui
 template <bool NN, int EPI>
 cbk_status mm(MmArgs &p, uint32_t columns, hipStream_t s) {
     constexpr uint32_t lds = kRing * 2 * kMmTile * 64;
-    if (!allow_lds(k_mm<NN, EPI>, lds)) return CBK_E_HIP;
+    if (!allow_lds_once<MmTag<NN, EPI>>(k_mm<NN, EPI>, lds)) return CBK_E_HIP;
     p.tm = ceil_div(p.M, kMmTile);
     p.tn = ceil_div(columns, kMmTile);
     const uint32_t tiles = p.tm * p.tn, cus = 256;
@@ -961,32 +975,44 @@ struct Weights {
         a.row0 = row0;
         a.nrows = static_cast<uint32_t>(nrows);
         a.cols = static_cast<uint32_t>(ts[0]->cols);
-        a.slices_of_first = ~0u;
-        if (nn) {
-            a.tiles = ceil_div(pl.Kp, kFusedTile);
-            a.slices = static_cast<uint32_t>(reduction() / 64);
-            if (count == 2) a.slices_of_first = a.slices / 2;
-        } else {
-            a.tiles = ceil_div(nrows, kFusedTile / count);
-            a.slices = static_cast<uint32_t>(pl.Kp / 64);
-        }
-        // at least four slices a workgroup, so that the start of its pipeline is paid for
-        const uint64_t total = static_cast<uint64_t>(a.tiles) * a.slices;
-        a.grid = static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>(pl.grid, total / 4)));
+        a.tiles = ceil_div(nn ? pl.Kp : nrows, kFusedTile);
+        a.slices = static_cast<uint32_t>((nn ? up64(nrows) : pl.Kp) / 64);
+        // Even rounds of the CUs where each workgroup gets eight slices, so that the start of its pipeline is
+        // paid for (a 4096 x 4096 gradient of 8 tokens: 16.7 us with 256 workgroups of eight, 19.4 with 512
+        // of four, 23 with 341 of six); below that, three slices each.
+        const uint64_t total = static_cast<uint64_t>(count * a.tiles) * a.slices;
+        a.grid = static_cast<uint32_t>(total >= 8 * pl.grid ? pl.grid : std::max<uint64_t>(1, std::min<uint64_t>(256, total / 3)));
         a.part = at<float>(ws, pl.part);
         r.bm = pl.fused;
         r.nn = nn;
         r.s = s;
         if (!dispatch_b<FusedRun>(static_cast<int>(ts[0]->b), r, FusedB{})) return CBK_E_UNSUPPORTED;
-        q = JoinArgs{a.part, a.tiles, a.slices, a.grid, static_cast<uint32_t>(up64(nrows))};
+        q = JoinArgs{a.part, count, a.tiles, a.slices, a.grid, static_cast<uint32_t>(up64(nrows))};
         return r.st;
     }
 
     template <int EPI>
     cbk_status join(MmArgs &p, const JoinArgs &q) const {
-        constexpr uint32_t rows = EPI == kGated || EPI == kGatedBwd ? 16 : 8;
-        hipLaunchKernelGGL((k_join<EPI>), dim3(q.tiles, ceil_div(p.M, rows)), dim3(256), 0, s, p, q);
+        hipLaunchKernelGGL((k_join<EPI>), dim3(q.tiles, ceil_div(p.M, 8)), dim3(256), 0, s, p, q);
         return launched();
+    }
+
+    // One token: the batch-1 GEMV, whose rows' sums lie as one part of every tile.  It streams the index
+    // words of whole rows (a pair of 4096 x 11008: 30 us against 44 by k_fused).
+    bool one_token(const MmArgs &p) const { return pl.fused && p.M == 1 && ts[0]->cols % 64 == 0 && ts[0]->cols <= 16384; }
+
+    cbk_status gemv(const MmArgs &p, JoinArgs &q) const {
+        const uint32_t tiles = ceil_div(nrows, kFusedTile);
+        cbk_tensor piece[2];
+        float *ys[2];
+        for (uint32_t i = 0; i < count; ++i) {
+            piece[i] = *ts[i];
+            piece[i].rows = nrows;
+            piece[i].words += row0 * piece[i].cols / 32 * piece[i].b;  // row0 is a multiple of 128: whole 16-byte chunks
+            ys[i] = at<float>(ws, pl.part) + i * tiles * kFusedTile;
+        }
+        q = JoinArgs{at<float>(ws, pl.part), count, tiles, 1, 1, static_cast<uint32_t>(up64(nrows))};
+        return launch_gemv_group(piece, count, p.A, ys, s);
     }
 
     // C = A . (piece)^T with the epilogue EPI.
@@ -994,7 +1020,7 @@ struct Weights {
     cbk_status forward(MmArgs &p) const {
         if (pl.fused) {
             JoinArgs q;
-            CBK_TRY(fused(p, false, q));
+            CBK_TRY(one_token(p) ? gemv(p, q) : fused(p, false, q));
             return join<EPI>(p, q);
         }
         p.B = at<uint16_t>(ws, pl.w);

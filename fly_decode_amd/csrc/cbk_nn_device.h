@@ -23,19 +23,18 @@ struct FusedTensor {
 struct FusedArgs {
     FusedTensor t[2];
     uint32_t count;            // 1, or 2: a gate and up pair
-    const uint16_t *A;         // tokens' side, [M][lda]; 64 * slices columns are readable
+    const uint16_t *A;         // tokens' side, [M][lda]; 64 * slices columns are readable (gradient: for each tensor)
     uint64_t lda;
     uint32_t M;
     uint64_t row0;             // the piece's first row of the tensors, and how many rows it has
     uint32_t nrows;
     uint32_t cols;             // of the tensors
-    uint32_t tiles, slices;
-    uint32_t slices_of_first;  // gradient: slices before the second tensor's
-    float *part;               // [grid + tiles][M][kFusedTile]
+    uint32_t tiles, slices;    // of one tensor
+    float *part;               // [grid + count * tiles][M][kFusedTile]
     uint32_t grid;
 };
 
-// bm: 16, 64, 128, 192, 256 or 384, at least M.  B: 8 to 14.
+// bm: 16, 64, 128, 192, 256, 320 or 384, at least M.  B: 8 to 14.
 template <int B>
 cbk_status launch_fused(const FusedArgs &a, uint32_t bm, bool nn, hipStream_t s);
 

@@ -6,79 +6,138 @@
 // into memory first costs several times the compressed bytes in traffic, so each weight is decoded
 // once, by the one workgroup that multiplies it with all tokens.
 //
-// Tiles and slices.  A tile is 128 columns of C; forward (NN false) these are 128 rows of the
-// tensor (64 of gate and 64 of up for a pair), gradient (NN true) 128 of its columns.  The
-// reduction is walked in slices of 64.  All (tile, slice) pairs in order are divided evenly among
-// the grid's workgroups, whatever the shape, so a workgroup takes a run of slices that may cover
-// parts of several tiles; each part's fp32 sums [tokens][128] go to slot (workgroup + tile) of the
-// partial buffer, and the kernel that follows adds a tile's parts in order (nothing depends on
-// timing).
+// Tiles and slices.  A tile is 128 columns of C: forward (NN false) 128 rows of a tensor, gradient
+// (NN true) 128 of its columns.  A pair's second tensor has tiles of its own after the first's, so a
+// workgroup holds one table at a time.  The reduction is walked in slices of 64.  All (tile, slice)
+// pairs in order are divided evenly among the grid's workgroups, whatever the shape, so a workgroup
+// takes a run of slices that may cover parts of several tiles; each part's fp32 sums [tokens][128]
+// go to slot (workgroup + tile) of the partial buffer, and the kernel that follows adds a tile's
+// parts in order (nothing depends on timing).
 //
-// A slice's 128 x 64 weights are 256 tasks of 32 consecutive fields, which are exactly b dwords of
-// the stream where rows are whole 32-field groups; where they are not (RAG) a task's fields start
-// anywhere in a dword, one more is loaded, and a funnel shift by the lane's own amount moves them
-// into place.  The 8 waves form two groups that decode alternate slices one ahead of the product:
-// in a slice's interval the waves of one group decode (LDS gathers) while those of the other, one
-// on each SIMD as well, feed the matrix cores, so the two pipes overlap by construction.  A lane's
-// dwords are loaded two slices ahead into registers; the tokens' slice is copied straight into LDS.
-// LDS layouts and fragment reads are those of k_mm.
+// A slice's 128 x 64 weights are 512 tasks of 16 consecutive fields, one a lane.  A task's fields start
+// on a dword, or half-way into one for odd widths, where rows are whole 64-field units; where they are
+// not (RAG) they start anywhere.  A funnel shift by the lane's own amount moves them into place.  A lane's
+// dwords are loaded two slices before they are decoded.
+//
+// The weights are decoded, and the tokens' part of the slice copied straight into LDS, two slices ahead of
+// the product, into a ring of three buffers (fused_ring).  In a slice's interval a wave reads the second half of this
+// slice's fragments and the first half of the next one's while it multiplies the halves it has, and decodes
+// its tasks (LDS gathers) in between: one barrier an interval, and no wait on anything asked for in it.
+// LDS layouts: rows of 128 bytes (64 reduction elements) hold chunk c of row r in slot c ^ (r & 7), the
+// gradient's rows of 256 bytes in c ^ (2 (r & 3) + 8 ((r / 8) & 1)), which keeps fragment reads, transposing
+// reads and decoded stores free of bank conflicts.
 #pragma once
+#include <type_traits>
+
 #include "cbk_device.h"
 #include "cbk_nn_device.h"
 
 namespace cbk {
 namespace {
 
+// Slices in LDS.  Past 256 tokens three do not fit; two are decoded and copied one slice ahead, and an
+// interval starts by reading its own fragments.
+constexpr uint32_t fused_ring(int BM) { return BM <= 256 ? 3 : 2; }
+
 template <int B, int BM>
-constexpr uint32_t fused_lds(uint32_t tables) {
-    return tables * Table<B>::SIZE * 2 + 2 * BM * 128 + 2 * kFusedTile * 128;
+constexpr uint32_t fused_lds() {
+    return Table<B>::SIZE * 2 + fused_ring(BM) * (BM + kFusedTile) * 128;
 }
 
-// This lane's dwords of a slice: as many loads as fused_loads<B>() says, so that a wait can leave
-// exactly them in flight.
-constexpr int fused_loads(int dwords) { return (dwords + 3) / 4; }
+// Dwords of a task of 16 fields, wherever it may start: with RAG anywhere, else on a dword or half-way.
+template <int B, bool RAG>
+constexpr int task_dwords() { return RAG ? (16 * B + 62) / 32 : (B + 1) / 2; }
 
-template <int B>
-__device__ __forceinline__ void load_fields(uint32_t (&d)[B], __amdgpu_buffer_rsrc_t rs, uint32_t off) {
+// D dwords at byte offset off, in (D + 3) / 4 loads.
+template <int D>
+__device__ __forceinline__ void load_fields(uint32_t (&d)[D], __amdgpu_buffer_rsrc_t rs, uint32_t off) {
 #pragma unroll
-    for (int i = 0; i < B / 4; ++i) {
+    for (int i = 0; i < D / 4; ++i) {
         const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(rs, static_cast<int>(off + 16 * i), 0, 0);
         d[4 * i] = t.x; d[4 * i + 1] = t.y; d[4 * i + 2] = t.z; d[4 * i + 3] = t.w;
     }
-    constexpr int at = B / 4 * 4;
-    if constexpr (B % 4 == 3) {
+    constexpr int at = D / 4 * 4;
+    if constexpr (D % 4 == 3) {
         const u32x3 t = __builtin_amdgcn_raw_buffer_load_b96(rs, static_cast<int>(off + 4 * at), 0, 0);
         d[at] = t.x; d[at + 1] = t.y; d[at + 2] = t.z;
-    } else if constexpr (B % 4 == 2) {
+    } else if constexpr (D % 4 == 2) {
         const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rs, static_cast<int>(off + 4 * at), 0, 0);
         d[at] = t.x; d[at + 1] = t.y;
-    } else if constexpr (B % 4 == 1) {
+    } else if constexpr (D % 4 == 1) {
         d[at] = __builtin_amdgcn_raw_buffer_load_b32(rs, static_cast<int>(off + 4 * at), 0, 0);
     }
 }
 
-// 32 fields to four 16-byte chunks of a row in LDS, chunk c0 + i in slot (c0 + i) ^ swz.  Fields from
+// 16 fields to two 16-byte chunks of a row in LDS, chunk c0 + i in slot (c0 + i) ^ swz.  Fields from
 // `have` on are zeros where MASK is set.
-template <int B, bool MASK>
-__device__ __forceinline__ void decode_fields(const uint32_t (&d)[B], const uint16_t *tbl, unsigned char *row, uint32_t c0,
+template <int B, bool MASK, int N>
+__device__ __forceinline__ void decode_fields(const uint32_t (&d)[N], const uint16_t *tbl, unsigned char *row, uint32_t c0,
                                               uint32_t swz, uint32_t have) {
-    uint32_t w[2][8];
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[0][i] = unit_gather<B>(tbl, d, i);
+    for (int i = 0; i < 16; ++i) w[i] = unit_gather<B>(tbl, d, i);
+    if constexpr (MASK) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        if (g + 1 < 4) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[(g + 1) & 1][i] = unit_gather<B>(tbl, d, 8 * (g + 1) + i);
-        }
-        uint32_t *v = w[g & 1];
-        if constexpr (MASK) {
-#pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) v[i] = 8 * g + i < have ? v[i] : 0u;
-        }
-        const u32x4 t = {v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
-        *reinterpret_cast<u32x4 *>(row + ((c0 + g) ^ swz) * 16) = t;
+        for (uint32_t i = 0; i < 16; ++i) w[i] = i < have ? w[i] : 0u;
     }
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const uint32_t *v = w + 8 * g;
+        *reinterpret_cast<u32x4 *>(row + ((c0 + g) ^ swz) * 16) =
+            (u32x4){v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
+    }
+}
+
+// N column fragments by transposing reads, their second halves HI bytes after the first; `at` are LDS
+// addresses, OFF an offset for all.  Written out because the compiler holds the transposing read back
+// until every copy into LDS has landed; the block waits for its own reads.
+template <int HI, int OFF>
+__device__ __forceinline__ void read_columns(bf16x8_t (&x)[1], const uint32_t (&at)[1]) {
+    u32x2 a0, b0;
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %2 offset:%c3\n"
+        "ds_read_b64_tr_b16 %1, %2 offset:%c4\n"
+        "s_waitcnt lgkmcnt(0)\n"
+        : "=&v"(a0), "=&v"(b0)
+        : "v"(at[0]), "i"(OFF), "i"(OFF + HI)
+        : "memory");
+    x[0] = __builtin_bit_cast(bf16x8_t, (u32x4){a0.x, a0.y, b0.x, b0.y});
+}
+template <int HI, int OFF>
+__device__ __forceinline__ void read_columns(bf16x8_t (&x)[2], const uint32_t (&at)[2]) {
+    u32x2 a0, a1, b0, b1;
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4 offset:%c6\n"
+        "ds_read_b64_tr_b16 %1, %4 offset:%c7\n"
+        "ds_read_b64_tr_b16 %2, %5 offset:%c6\n"
+        "ds_read_b64_tr_b16 %3, %5 offset:%c7\n"
+        "s_waitcnt lgkmcnt(0)\n"
+        : "=&v"(a0), "=&v"(b0), "=&v"(a1), "=&v"(b1)
+        : "v"(at[0]), "v"(at[1]), "i"(OFF), "i"(OFF + HI)
+        : "memory");
+    x[0] = __builtin_bit_cast(bf16x8_t, (u32x4){a0.x, a0.y, b0.x, b0.y});
+    x[1] = __builtin_bit_cast(bf16x8_t, (u32x4){a1.x, a1.y, b1.x, b1.y});
+}
+template <int HI, int OFF>
+__device__ __forceinline__ void read_columns(bf16x8_t (&x)[4], const uint32_t (&at)[4]) {
+    u32x2 a0, a1, a2, a3, b0, b1, b2, b3;
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8 offset:%c12\n"
+        "ds_read_b64_tr_b16 %1, %8 offset:%c13\n"
+        "ds_read_b64_tr_b16 %2, %9 offset:%c12\n"
+        "ds_read_b64_tr_b16 %3, %9 offset:%c13\n"
+        "ds_read_b64_tr_b16 %4, %10 offset:%c12\n"
+        "ds_read_b64_tr_b16 %5, %10 offset:%c13\n"
+        "ds_read_b64_tr_b16 %6, %11 offset:%c12\n"
+        "ds_read_b64_tr_b16 %7, %11 offset:%c13\n"
+        "s_waitcnt lgkmcnt(0)\n"
+        : "=&v"(a0), "=&v"(b0), "=&v"(a1), "=&v"(b1), "=&v"(a2), "=&v"(b2), "=&v"(a3), "=&v"(b3)
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "i"(OFF), "i"(OFF + HI)
+        : "memory");
+    x[0] = __builtin_bit_cast(bf16x8_t, (u32x4){a0.x, a0.y, b0.x, b0.y});
+    x[1] = __builtin_bit_cast(bf16x8_t, (u32x4){a1.x, a1.y, b1.x, b1.y});
+    x[2] = __builtin_bit_cast(bf16x8_t, (u32x4){a2.x, a2.y, b2.x, b2.y});
+    x[3] = __builtin_bit_cast(bf16x8_t, (u32x4){a3.x, a3.y, b3.x, b3.y});
 }
 
 // Waves of a workgroup over the 128 columns; the other factor of 8 goes over the tokens.
@@ -88,36 +147,27 @@ template <int B, int BM, bool NN, bool RAG>
 __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
     constexpr int WN = fused_wn(BM), WM = 8 / WN;
     constexpr int FM = BM / WM / 16, FN = kFusedTile / WN / 16;
-    constexpr uint32_t XBYTES = BM * 128, WBYTES = kFusedTile * 128;
-    constexpr int XC = BM / 8;           // copies of a slice of the tokens
-    constexpr int DW = RAG ? B + 1 : B;  // dwords of a task
+    constexpr uint32_t XBYTES = BM * 128, WBYTES = kFusedTile * 128, SLICE = XBYTES + WBYTES;
+    constexpr int XC = BM / 8, IX = (XC + 7) / 8;  // copies of a slice of the tokens, by a wave
+    constexpr int DW = task_dwords<B, RAG>(), NL = (DW + 3) / 4;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    uint16_t *tables = reinterpret_cast<uint16_t *>(smem);
-    unsigned char *xs = smem + p.count * Table<B>::SIZE * 2, *wsl = xs + 2 * XBYTES;
+    uint16_t *table = reinterpret_cast<uint16_t *>(smem);
+    constexpr uint32_t RING = fused_ring(BM), AHEAD = RING - 1;
+    unsigned char *ring = smem + Table<B>::SIZE * 2;  // slices: the tokens' part, then the weights'
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t li = lane & 15, lg = lane >> 4;
     const int wm = wave / WN, wn = wave % WN;
-    const int role = wave >> 2;                       // decodes the slices of this parity
-    const uint32_t task = static_cast<uint32_t>(wave & 3) * 64 + lane;
 
-    {
-        CbStage<B, 512> cs;
-        for (uint32_t i = 0; i < p.count; ++i) {
-            cs.issue(p.t[i].cb, p.t[i].U, reinterpret_cast<const u32x4 *>(p.t[i].words), tid);
-            cs.store(tables + i * Table<B>::SIZE, p.t[i].U, tid);
-        }
-    }
-
-    // this lane's task: its row and 32-field group within a slice
-    const uint32_t trow = NN ? task >> 2 : task >> 1, tgrp = NN ? task & 3 : task & 1;
+    // this lane's task: its row and 16-field group within a slice
+    const uint32_t trow = NN ? tid >> 3 : tid >> 2, tgrp = NN ? tid & 7 : tid & 3;
     const uint32_t swz = NN ? 2 * (trow & 3) + 8 * ((trow >> 3) & 1) : trow & 7;
     const uint32_t wrow = trow * (NN ? 256u : 128u);
-    // copies of the tokens' slice
-    constexpr int IX = (XC + 7) / 8;
-    uint32_t vx[IX];
+    // copies of the tokens' slice; where there are fewer than eight, the waves past them repeat the last
+    uint32_t vx[IX], wx[IX];
 #pragma unroll
     for (int i = 0; i < IX; ++i) {
-        const uint32_t r = (wave + 8 * i) * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+        wx[i] = min(wave + 8 * i, XC - 1);
+        const uint32_t r = wx[i] * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
         vx[i] = min(r, p.M - 1) * static_cast<uint32_t>(p.lda) * 2u + c * 16u;
     }
     const auto rx = wave_rsrc(p.A, 0x7FFFFFF0u);
@@ -130,75 +180,66 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
         for (int j = 0; j < FN; ++j) {
             const uint32_t r = 8 * lg + (li >> 2);
             const uint32_t c = (wn * (kFusedTile / WN) + 16 * j) / 8 + ((li & 3) >> 1);
-            ft[j] = r * 256 + (c ^ (2 * (r & 3) + 8 * (lg & 1))) * 16 + (li & 1) * 8;
+            ft[j] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((CBK_LDS unsigned char *)(ring))) + XBYTES + r * 256 + (c ^ (2 * (r & 3) + 8 * (lg & 1))) * 16 + (li & 1) * 8;
         }
     }
 
-    const uint64_t total = static_cast<uint64_t>(p.tiles) * p.slices;
+    const uint64_t total = static_cast<uint64_t>(p.count * p.tiles) * p.slices;
     uint64_t pos = blockIdx.x * total / gridDim.x;
     const uint64_t end = (blockIdx.x + 1) * total / gridDim.x;
+    uint32_t staged = ~0u;  // the tensor whose table is in LDS
     while (pos < end) {
-        const uint32_t tile = static_cast<uint32_t>(pos / p.slices), s0 = static_cast<uint32_t>(pos - static_cast<uint64_t>(tile) * p.slices);
+        const uint32_t vt = static_cast<uint32_t>(pos / p.slices), s0 = static_cast<uint32_t>(pos - static_cast<uint64_t>(vt) * p.slices);
         const uint32_t s1 = static_cast<uint32_t>(min(static_cast<uint64_t>(p.slices), s0 + (end - pos)));
+        const uint32_t which = vt >= p.tiles, tile = vt - which * p.tiles;
+        const FusedTensor &T = p.t[which];
 
-        auto which_of = [&](uint32_t s) -> uint32_t {
-            if constexpr (NN) return s >= p.slices_of_first;
-            return p.count == 2 ? static_cast<uint32_t>(wave & 2) >> 1 : 0u;  // tasks 0..127 are gate's rows, the others up's
+        // Where this lane's task of slice s0 starts: the tensor's row `row` (a base on a dword), and the
+        // lane's first field after its start.  A slice on is 64 fields, or 64 rows, which are whole dwords,
+        // so `shift`, where the first field starts in its dword, stays.
+        const uint64_t row = p.row0 + (NN ? static_cast<uint64_t>(s0) * 64 : static_cast<uint64_t>(tile) * kFusedTile);
+        const uint64_t base_bits = row * p.cols * B;
+        const uint32_t bit = (trow * p.cols + (NN ? tile * kFusedTile : s0 * 64) + tgrp * 16) * B + (RAG ? static_cast<uint32_t>(base_bits) & 31u : 0u);
+        const uint32_t shift = bit & 31u, first = (bit >> 5) * 4u;
+        const uint64_t start = (base_bits >> 5) * 4, step = NN ? static_cast<uint64_t>(p.cols) * (8 * B) : 8 * B;  // bytes
+        uint64_t words_at = reinterpret_cast<uint64_t>(T.words) + start, rest = T.bytes > start ? T.bytes - start : 0;
+        // kept in scalar registers: loading them again in the loop would wait for the LDS too
+        asm volatile("" : "+s"(words_at), "+s"(rest));
+        struct Words {
+            uint32_t d[DW];
         };
-        // The rows [row, ...) of the tensor that slice s takes, and this lane's first field after the
-        // start of row `row`.
-        auto fields_at = [&](uint32_t s, uint64_t &row) -> uint32_t {
-            const uint32_t which = which_of(s);
-            if constexpr (NN) {
-                row = p.row0 + static_cast<uint64_t>(s - (which ? p.slices_of_first : 0u)) * 64;
-                return trow * p.cols + tile * kFusedTile + tgrp * 32;
-            } else {
-                row = p.row0 + static_cast<uint64_t>(tile) * (p.count == 2 ? 64 : kFusedTile);
-                return (trow - which * 64) * p.cols + s * 64 + tgrp * 32;
-            }
+        // The dwords of the task in slice s (past the run, those of its last slice again); what is past the
+        // stream's end reads as zeros.
+        auto load = [&](Words &w, uint32_t s) {
+            const uint32_t n = min(s, s1 - 1) - s0;
+            const uint64_t at = NN ? n * step : 0, have = rest > at ? rest - at : 0;
+            const auto rs = wave_rsrc(reinterpret_cast<const unsigned char *>(words_at + (rest > at ? at : 0)),
+                                      static_cast<uint32_t>(min(have, static_cast<uint64_t>(0x7FFFFFF0u))));
+            load_fields<DW>(w.d, rs, first + (NN ? 0u : n * (8 * B)));
         };
-        uint32_t shift = 0;  // RAG: where the task's first field starts in d[0]
-        auto load = [&](uint32_t (&d)[DW], uint32_t s) {
-            const FusedTensor &T = p.t[which_of(s)];
-            uint64_t row;
-            const uint32_t f = fields_at(s, row);
-            // a base on a dword; what is past the stream's end reads as zeros
-            const uint64_t bits = row * p.cols * B, start = (bits >> 5) * 4;
-            const uint64_t rest = T.bytes > start ? T.bytes - start : 0;
-            const auto rs = wave_rsrc(reinterpret_cast<const unsigned char *>(T.words) + (rest ? start : 0),
-                                      static_cast<uint32_t>(min(rest, static_cast<uint64_t>(0x7FFFFFF0u))));
-            if constexpr (RAG) {
-                const uint32_t bit = f * B + (static_cast<uint32_t>(bits) & 31u);
-                shift = bit & 31u;
-                load_fields<DW>(d, rs, (bit >> 5) * 4u);
-            } else {
-                load_fields<DW>(d, rs, f / 32u * (4u * B));
-            }
-        };
-        auto decode = [&](const uint32_t (&d)[DW], uint32_t s, uint32_t buf) {
-            const uint32_t which = which_of(s);
+        auto decode = [&](const Words &w, uint32_t s, uint32_t at) {
             // zeros where the reduction runs past the piece's rows (gradient) or the rows' ends
-            uint32_t have = 32;
+            uint32_t have = 16;
             if constexpr (NN)
-                have = (s - (which ? p.slices_of_first : 0u)) * 64 + trow < p.nrows ? 32u : 0u;
+                have = s * 64 + trow < p.nrows ? 16u : 0u;
             else if constexpr (RAG)
-                have = p.cols > s * 64 + tgrp * 32 ? p.cols - (s * 64 + tgrp * 32) : 0u;
-            const uint16_t *tbl = tables + which * Table<B>::SIZE;
-            unsigned char *to = wsl + buf * WBYTES + wrow;
-            if constexpr (RAG) {
-                uint32_t e[B];
+                have = p.cols > s * 64 + tgrp * 16 ? p.cols - (s * 64 + tgrp * 16) : 0u;
+            unsigned char *to = ring + at + XBYTES + wrow;
+            if constexpr (RAG || B % 2 == 1) {
+                constexpr int N = (B + 1) / 2;
+                uint32_t e[N];
 #pragma unroll
-                for (int i = 0; i < B; ++i) e[i] = __builtin_amdgcn_alignbit(d[i + 1], d[i], shift);
-                decode_fields<B, true>(e, tbl, to, tgrp * 4, swz, have);
+                for (int i = 0; i < N; ++i) e[i] = __builtin_amdgcn_alignbit(i + 1 < DW ? w.d[i + 1] : 0u, w.d[i], shift);
+                decode_fields<B, NN || RAG>(e, table, to, tgrp * 2, swz, have);
             } else {
-                decode_fields<B, NN>(d, tbl, to, tgrp * 4, swz, have);
+                decode_fields<B, NN>(w.d, table, to, tgrp * 2, swz, have);
             }
         };
-        auto copy = [&](uint32_t s, uint32_t buf) {
+        // the tokens' part of slice s of this tensor (past the run: the last slice again)
+        auto copy = [&](uint32_t s, uint32_t at) {
+            const uint32_t from = min(s, s1 - 1) + (NN ? which * p.slices : 0u);
 #pragma unroll
-            for (int i = 0; i < IX; ++i)
-                if (XC % 8 == 0 || wave + 8 * i < XC)
-                    copy_to_lds(rx, xs + buf * XBYTES + (wave + 8 * i) * 1024, vx[i], s * 128);
+            for (int i = 0; i < IX; ++i) copy_to_lds(rx, ring + at + wx[i] * 1024, vx[i], from * 128);
         };
 
         f32x4_t acc[FM][FN];
@@ -206,93 +247,107 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-        // Column fragments of a slice.  The compiler holds transposing reads back until every copy
-        // into LDS has landed, so they are all made at the start of an interval, before its copies.
-        auto columns = [&](bf16x8_t (&xb)[2][FN], uint32_t buf) {
-            const unsigned char *sb = wsl + buf * WBYTES;
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    if constexpr (NN) {
-                        const unsigned char *at = sb + ft[j] + ks * 32 * 256;
-                        const s16x4 lo = read_transposed(at), hi = read_transposed(at + 4 * 256);
-                        xb[ks][j] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                    } else {
-                        xb[ks][j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sb + (fb ^ (ks * 64)) + j * 2048));
-                    }
-                }
+        // The fragments of half KS of the slice at ring offset `at`.
+        struct Frags {
+            bf16x8_t a[FM], b[FN];
         };
-        auto multiply = [&](const bf16x8_t (&xb)[2][FN], uint32_t buf) {
-            const unsigned char *sa = xs + buf * XBYTES;
+        auto read = [&](Frags &f, uint32_t at, auto half) {
+            constexpr int KS = decltype(half)::value;
+            const unsigned char *sa = ring + at, *sb = sa + XBYTES;
+            if constexpr (NN) {
+                uint32_t t[FN];
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8_t xa[FM];
+                for (int j = 0; j < FN; ++j) t[j] = ft[j] + at;
+                read_columns<4 * 256, KS * 32 * 256>(f.b, t);
+            } else {
 #pragma unroll
-                for (int i = 0; i < FM; ++i)
-                    xa[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sa + (fa ^ (ks * 64)) + i * 2048));
-#pragma unroll
-                for (int i = 0; i < FM; ++i)
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[ks][j], xa[i], acc[i][j], 0, 0, 0);
+                for (int j = 0; j < FN; ++j)
+                    f.b[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sb + (fb ^ (KS * 64)) + j * 2048));
             }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                f.a[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sa + (fa ^ (KS * 64)) + i * 2048));
+        };
+        const std::integral_constant<int, 0> lower;
+        const std::integral_constant<int, 1> upper;
+        auto multiply = [&](const Frags &f) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
         };
 
-        // Before the first interval: slice s0 decoded and copied, the words of s0 + 1 (by the group
-        // that decodes it) and s0 + 2 (by the other) on their way.  Words of slices past the run
-        // are not loaded.
-        uint32_t d[DW];
-        const bool first = role == 0;  // this group decodes s0, s0 + 2, ...
-        lds_barrier();                 // the previous part's last reads of the buffers; the tables' stores
+        // Before the first interval: the table; the AHEAD first slices decoded and copied; the words of the
+        // two after them on their way.  Everything that does not wait for anything else is asked for at once.
+        Words w0, w1;
+        lds_barrier();  // the previous part's last reads
         copy(s0, 0);
-        if (first) {
-            load(d, s0);
-            decode(d, s0, 0);
-            if (s0 + 2 < s1) load(d, s0 + 2);
-        } else if (s0 + 1 < s1) {
-            load(d, s0 + 1);
+        if constexpr (AHEAD == 2) copy(s0 + 1, SLICE);
+        if (staged != which) {
+            staged = which;
+            CbStage<B, 512> cs;
+            cs.issue(T.cb, T.U, reinterpret_cast<const u32x4 *>(T.words), tid);
+            load(w0, s0);
+            load(w1, s0 + 1);
+            cs.store(table, T.U, tid);
+            lds_barrier();
+        } else {
+            load(w0, s0);
+            load(w1, s0 + 1);
         }
-        __builtin_amdgcn_s_waitcnt(0x0070);
+        decode(w0, s0, 0);
+        load(w0, s0 + 2);
+        if constexpr (AHEAD == 2) {
+            decode(w1, s0 + 1, SLICE);
+            load(w1, s0 + 3);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0070 | (2 * NL));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
 
-        // One interval: slice s is multiplied, slice s + 1 copied and, by its group, decoded.
-        auto interval = [&](uint32_t s, bool mine) {
-            const uint32_t buf = (s - s0) & 1;
-            bf16x8_t xb[2][FN];
-            columns(xb, buf);
-            if (s + 1 < s1) {
-                if (mine) {
-                    decode(d, s + 1, buf ^ 1);
-                    copy(s + 1, buf ^ 1);
-                    if (s + 3 < s1) load(d, s + 3);
-                } else {
-                    copy(s + 1, buf ^ 1);
+        uint32_t now = 0, fill = AHEAD * SLICE;  // ring offsets of slices s and s + AHEAD
+        Frags f0, f1;
+        if constexpr (AHEAD == 2) read(f0, 0, lower);
+        // One interval: slice s is multiplied, slice s + AHEAD copied and decoded from w, which then takes
+        // the words of two slices later.  At its end the copies have landed, and every word but those.
+        auto interval = [&](uint32_t s, Words &w) {
+            const uint32_t next = now == (RING - 1) * SLICE ? 0 : now + SLICE;
+            copy(s + AHEAD, fill);
+            if constexpr (AHEAD == 1) read(f0, now, lower);
+            read(f1, now, upper);
+            multiply(f0);
+            if constexpr (AHEAD == 2) read(f0, next, lower);  // after the last slice: old contents of a buffer, not used
+            decode(w, s + AHEAD, fill);
+            load(w, s + AHEAD + 2);
+            multiply(f1);
+            // the multiplications between the LDS reads and the decoding's arithmetic
+            if constexpr (BM >= 64) {
+                constexpr int MF = 2 * FM * FN, RD = 16 + (NN ? 2 * FM : 2 * (FM + FN));
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, (RD + MF - 1) / MF, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 96 / MF, 0);
                 }
             }
-            multiply(xb, buf);
-            // the copies have landed (the words asked for after them may still be on their way, and
-            // are waited for an interval later), this wave's LDS writes are done
-            if (mine && s + 3 < s1)
-                __builtin_amdgcn_s_waitcnt(0x0070 | fused_loads(DW));
-            else
-                __builtin_amdgcn_s_waitcnt(0x0070);
+            // multiplications are not put off past the barrier
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0x0070 | NL);
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
+            fill = now;
+            now = next;
         };
-        if (first) {
-            for (uint32_t s = s0; s < s1; s += 2) {
-                interval(s, false);
-                if (s + 1 < s1) interval(s + 1, true);
-            }
-        } else {
-            for (uint32_t s = s0; s < s1; s += 2) {
-                interval(s, true);
-                if (s + 1 < s1) interval(s + 1, false);
-            }
+        Words &wa = AHEAD == 2 ? w0 : w1, &wb = AHEAD == 2 ? w1 : w0;  // those of s0 + AHEAD, and the next
+        uint32_t s = s0;
+        for (; s + 1 < s1; s += 2) {
+            interval(s, wa);
+            interval(s + 1, wb);
         }
+        if (s < s1) interval(s, wa);
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // no copy is left in flight
 
-        float *out = p.part + (static_cast<uint64_t>(blockIdx.x) + tile) * p.M * kFusedTile;
+        float *out = p.part + (static_cast<uint64_t>(blockIdx.x) + vt) * p.M * kFusedTile;
         const uint32_t mw = wm * (BM / WM) + li, nw = wn * (kFusedTile / WN) + 4 * lg;
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -305,10 +360,13 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
     }
 }
 
+template <int, int, bool, bool>
+struct FusedTag;
+
 template <int B, int BM, bool NN, bool RAG>
 cbk_status fused_run(const FusedArgs &a, hipStream_t s) {
-    const uint32_t lds = fused_lds<B, BM>(a.count);
-    if (!allow_lds(k_fused<B, BM, NN, RAG>, lds)) return CBK_E_HIP;
+    constexpr uint32_t lds = fused_lds<B, BM>();
+    if (!allow_lds_once<FusedTag<B, BM, NN, RAG>>(k_fused<B, BM, NN, RAG>, lds)) return CBK_E_HIP;
     hipLaunchKernelGGL((k_fused<B, BM, NN, RAG>), dim3(a.grid), dim3(512), lds, s, a);
     return launched();
 }
@@ -330,6 +388,7 @@ cbk_status launch_fused(const FusedArgs &a, uint32_t bm, bool nn, hipStream_t s)
         case 128: return fused_kind<B, 128>(a, nn, s);
         case 192: return fused_kind<B, 192>(a, nn, s);
         case 256: return fused_kind<B, 256>(a, nn, s);
+        case 320: return fused_kind<B, 320>(a, nn, s);
         default: return fused_kind<B, 384>(a, nn, s);
     }
 }

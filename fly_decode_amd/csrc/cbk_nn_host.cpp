@@ -71,27 +71,37 @@ namespace cbk {
 namespace {
 
 // The token tile of k_fused, or 0 where the tensors or the number of tokens are not its kind: widths
-// 8 to 14 (equal, for a pair), up to 384 tokens, and a workgroup's tables and slices within the LDS.
+// 8 to 14 (equal, for a pair), and a workgroup's table and ring within the LDS.  Up to 384 tokens it is
+// ahead of decoding a piece first (a pair of 4096 x 11008: 49 us against 128 at 64 tokens, 129 against
+// 153 at 384, 170 in two halves against 154 at 512); short rows leave it more sums to pass on per product
+// (a pair of 384 x 11008: 37 against 34 at 256, 45 against 36 at 384; of 1024 x 11008: 55 against 52 at
+// 384, its gradient 102 against 109).
 uint32_t fused_tile(const cbk_tensor *const *ts, uint64_t count, uint64_t tokens) {
-    if (tokens > 384) return 0;
+    if (tokens > (ts[0]->cols < 1024 ? 256 : 384)) return 0;
     for (uint64_t i = 0; i < count; ++i) {
         const cbk_tensor &t = *ts[i];
         if (t.b < 8 || t.b > 14 || t.b != ts[0]->b || t.cols == 0 || !aligned(t.codebook, 16)) return 0;
     }
-    const uint32_t bm = tokens <= 16 ? 16 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : tokens <= 192 ? 192 : tokens <= 256 ? 256 : 384;
-    return nn_fused_lds(ts[0]->b, bm, static_cast<uint32_t>(count)) <= 160 * 1024 ? bm : 0;
+    uint32_t bm = 384;
+    for (uint32_t x : {320u, 256u, 192u, 128u, 64u, 16u})
+        if (tokens <= x) bm = x;
+    return nn_fused_lds(ts[0]->b, bm) <= 160 * 1024 ? bm : 0;
 }
 
 }  // namespace
 
-// LDS of a workgroup of k_fused: the tables, and two slices of the tokens and of the weights.
-uint32_t nn_fused_lds(uint32_t b, uint32_t bm, uint32_t count) { return count * (2u << b) + 2 * 128 * bm + 2 * 128 * 128; }
+// LDS of a workgroup of k_fused: a table, and three slices of the tokens and of the weights (two past
+// 256 tokens).
+uint32_t nn_fused_lds(uint32_t b, uint32_t bm) { return (2u << b) + (bm <= 256 ? 3 : 2) * 128 * (bm + 128); }
 
-// A decoded piece takes up to kPieceBytes and kPieceRows, so that a call's scratch stays far below
-// the tensor's uncompressed size; chunks of kChunk tokens bound what is kept per token.
+// A decoded piece takes up to kPieceBytes and kPieceRows, and the sums of a piece's rows for a chunk of
+// tokens (k_fused) up to kSumBytes, so that a call's scratch stays far below the tensor's uncompressed
+// size and no call keeps what grows with tokens times rows; chunks of kChunk tokens bound what is
+// kept per token.
 NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
     constexpr uint64_t kPieceBytes = uint64_t(256) << 20;
     constexpr uint64_t kPieceRows = 32768;
+    constexpr uint64_t kSumBytes = uint64_t(64) << 20;
     constexpr uint64_t kChunk = 8192;
     const uint64_t rows = ts[0]->rows, cols = ts[0]->cols;
     NnPlan p{};
@@ -101,7 +111,7 @@ NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
     p.Tc = std::min(tokens, kChunk);
     p.fused = fused_tile(ts, pair, tokens);
     const uint64_t total = up_to(pair * up_to(rows, 16), 256);
-    const uint64_t most = p.fused ? kPieceRows : std::min(kPieceRows, std::max<uint64_t>(256, kPieceBytes / (2 * p.Kp) / 256 * 256));
+    const uint64_t most = p.fused ? std::max<uint64_t>(256, kSumBytes / (4 * p.Tc) / 256 * 256) : std::min(kPieceRows, std::max<uint64_t>(256, kPieceBytes / (2 * p.Kp) / 256 * 256));
     p.pieces = (total + most - 1) / most;
     p.Rp = up_to((total + p.pieces - 1) / p.pieces, 256);
     p.rows = p.Rp / pair;
@@ -116,8 +126,8 @@ NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
     p.pack = take(p.Tc * std::max(p.Kp, op == NnOp::linear ? p.Rp : 0) * 2);
     if (p.fused) {
         // as many workgroups as the LDS lets run at once on 256 CUs, and their parts of the tiles
-        p.grid = nn_fused_lds(ts[0]->b, p.fused, static_cast<uint32_t>(pair)) <= 80 * 1024 ? 512 : 256;
-        p.part = take((p.grid + std::max(p.Rp, p.Kp + 64) / 128) * p.Tc * 128 * 4);
+        p.grid = 256 * std::min<uint32_t>(3, 160 * 1024 / nn_fused_lds(ts[0]->b, p.fused));
+        p.part = take((p.grid + pair * (std::max(p.rows + 127, p.Kp + 64) / 128)) * p.Tc * 128 * 4);
     } else {
         p.w = take(p.Rp * p.Kp * 2);
         // no more tiles are shared than the largest product of the call has
