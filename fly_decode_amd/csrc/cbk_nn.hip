@@ -253,7 +253,8 @@ struct MmArgs {
 
     uint16_t *out;  // kOut, kGated: [M][ldo] BF16
     uint64_t ldo;
-    uint32_t vec;   // out (and dH, dG, dU) can be accessed 8 bytes at a time
+    uint32_t vec;   // out (and dH, dG, dU) can be accessed 8 bytes at a time,
+    uint32_t vec16;  // and 16
     float *acc;     // kOut over several pieces: fp32 sums [M][ldacc]
     uint32_t ldacc, acc_in, last;
     const int64_t *labels;
@@ -284,27 +285,22 @@ __device__ __forceinline__ void store4(uint16_t *out, const float (&v)[4], uint3
             if (r < n) out[r] = to_bf16(v[r]);
     }
 }
-__device__ __forceinline__ void load4(const uint16_t *in, float (&v)[4], uint32_t n, bool vec) {
-    if (n >= 4 && vec) {
-        const u32x2 t = *reinterpret_cast<const u32x2 *>(in);
-        v[0] = bf16_value(static_cast<uint16_t>(t.x));
-        v[1] = bf16_value(static_cast<uint16_t>(t.x >> 16));
-        v[2] = bf16_value(static_cast<uint16_t>(t.y));
-        v[3] = bf16_value(static_cast<uint16_t>(t.y >> 16));
-    } else {
+// in[0..3], of which `n` exist (zeros for the others).
+__device__ __forceinline__ u32x2 load4(const uint16_t *in, uint32_t n, bool vec) {
+    if (n >= 4 && vec) return *reinterpret_cast<const u32x2 *>(in);
+    uint32_t v[4];
 #pragma unroll
-        for (uint32_t r = 0; r < 4; ++r) v[r] = r < n ? bf16_value(in[r]) : 0.f;
-    }
+    for (uint32_t r = 0; r < 4; ++r) v[r] = r < n ? in[r] : 0u;
+    return (u32x2){v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
 }
 __device__ __forceinline__ uint32_t left(uint32_t n, uint32_t at) { return at < n ? n - at : 0u; }
 
 // Reference point of a sum of exponentials whose largest argument is m: 0 where m is infinite.
 __device__ __forceinline__ float exp_base(float m) { return fabsf(m) == __builtin_inff() ? 0.f : m; }
 
-// What the operators do with four neighbouring sums (columns n..n + 3) of token m.
-__device__ __forceinline__ void emit_out(const MmArgs &p, uint32_t m, uint32_t n, float (&v)[4]) {
-    const uint32_t have = left(p.N, n);
-    if (have == 0) return;
+// What the operators make of four neighbouring sums (columns n..n + 3) of token m.
+// kOut: the sum over the pieces; false where it is only kept for the next piece.
+__device__ __forceinline__ bool finish_out(const MmArgs &p, uint32_t m, uint32_t n, float (&v)[4]) {
     f32x4_t *sum = reinterpret_cast<f32x4_t *>(p.acc + static_cast<uint64_t>(m) * p.ldacc + n);
     if (p.acc_in) {
         const f32x4_t t = *sum;
@@ -313,7 +309,7 @@ __device__ __forceinline__ void emit_out(const MmArgs &p, uint32_t m, uint32_t n
     }
     if (!p.last) {
         *sum = (f32x4_t){v[0], v[1], v[2], v[3]};
-        return;
+        return false;
     }
     if (p.scale) {
         const int64_t lab = p.labels[m];
@@ -321,30 +317,44 @@ __device__ __forceinline__ void emit_out(const MmArgs &p, uint32_t m, uint32_t n
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] = lab == p.ignore ? 0.f : v[r] * f;
     }
-    store4(p.out + m * p.ldo + n, v, have, p.vec);
+    return true;
+}
+__device__ __forceinline__ void emit_out(const MmArgs &p, uint32_t m, uint32_t n, float (&v)[4]) {
+    const uint32_t have = left(p.N, n);
+    if (have && finish_out(p, m, n, v)) store4(p.out + m * p.ldo + n, v, have, p.vec);
+}
+__device__ __forceinline__ void gated(int act, const float (&g)[4], const float (&u)[4], float (&h)[4]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) h[r] = activation(act, g[r], nullptr) * u[r];
 }
 __device__ __forceinline__ void emit_gated(const MmArgs &p, uint32_t m, uint32_t f, const float (&g)[4], const float (&u)[4]) {
     const uint32_t have = left(p.F, f);
     if (have == 0) return;
     float h[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) h[r] = activation(p.act, g[r], nullptr) * u[r];
+    gated(p.act, g, u, h);
     store4(p.out + m * p.ldo + f, h, have, p.vec);
 }
-// G: where the piece's dG and dU go (gcol, ucol).  Rows past the tensors' end are part of the next
-// product's reduction: zeros.
-__device__ __forceinline__ void emit_gated_bwd(const MmArgs &p, uint32_t m, uint32_t f, uint32_t gcol, uint32_t ucol,
-                                               const float (&g)[4], const float (&u)[4]) {
-    const uint32_t have = left(p.F, f);
-    float dh[4] = {0.f, 0.f, 0.f, 0.f}, dg[4], du[4];
-    if (have) load4(p.dH + m * p.lddh + f, dh, have, p.vec);
+// dG and dU of four rows, of which `have` exist, from their dH.  Rows past the tensors' end are part of the
+// next product's reduction: zeros.
+__device__ __forceinline__ void gated_bwd(int act, uint32_t have, u32x2 dH, const float (&g)[4], const float (&u)[4],
+                                          float (&dg)[4], float (&du)[4]) {
+    const float dh[4] = {bf16_value(static_cast<uint16_t>(dH.x)), bf16_value(static_cast<uint16_t>(dH.x >> 16)),
+                         bf16_value(static_cast<uint16_t>(dH.y)), bf16_value(static_cast<uint16_t>(dH.y >> 16))};
 #pragma unroll
     for (uint32_t r = 0; r < 4; ++r) {
         float d;
-        const float a = activation(p.act, g[r], &d);
+        const float a = activation(act, g[r], &d);
         dg[r] = r < have ? dh[r] * u[r] * d : 0.f;
         du[r] = r < have ? dh[r] * a : 0.f;
     }
+}
+// gcol, ucol: their columns in G.
+__device__ __forceinline__ void emit_gated_bwd(const MmArgs &p, uint32_t m, uint32_t f, uint32_t gcol, uint32_t ucol,
+                                               const float (&g)[4], const float (&u)[4]) {
+    const uint32_t have = left(p.F, f);
+    const u32x2 dh = have ? load4(p.dH + m * p.lddh + f, have, p.vec) : (u32x2){0u, 0u};
+    float dg[4], du[4];
+    gated_bwd(p.act, have, dh, g, u, dg, du);
     uint16_t *G = p.G + static_cast<uint64_t>(m) * p.ldG;
     store4(G + gcol, dg, 4, true);
     store4(G + ucol, du, 4, true);
@@ -352,12 +362,22 @@ __device__ __forceinline__ void emit_gated_bwd(const MmArgs &p, uint32_t m, uint
     if (have && p.dU) store4(p.dU + m * p.ldg + f, du, have, p.vec);
 }
 // exp(z - lse) - [label], the columns of the next product's reduction (zeros past the piece).
-__device__ __forceinline__ void emit_prob(const MmArgs &p, uint32_t m, uint32_t n, int64_t lab, float lse, const float (&z)[4]) {
-    float v[4];
+__device__ __forceinline__ void prob(const MmArgs &p, uint32_t n, int64_t lab, float lse, const float (&z)[4], float (&v)[4]) {
 #pragma unroll
     for (uint32_t r = 0; r < 4; ++r)
         v[r] = n + r < p.N ? __expf(z[r] - lse) - (static_cast<int64_t>(n + r) == lab ? 1.f : 0.f) : 0.f;
-    store4(p.G + static_cast<uint64_t>(m) * p.ldG + n, v, 4, true);
+}
+
+// Eight values to out[0..7], of which `n` exist.
+__device__ __forceinline__ void store8(uint16_t *out, u32x4 v, uint32_t n, bool vec) {
+    if (n >= 8 && vec) {
+        *reinterpret_cast<u32x4 *>(out) = v;
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r)
+            if (r < n) out[r] = static_cast<uint16_t>(w[r >> 1] >> (16 * (r & 1)));
+    }
 }
 
 // Four column fragments by transposing reads, their second halves HI bytes after the first; `at` are
@@ -552,38 +572,82 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 *reinterpret_cast<f32x4_t *>(part + (mw - m0 + 16 * i) * BN + (nw - n0) + 16 * j) = acc[i][j];
-    } else if constexpr (EPI == kOut || EPI == kProb) {
+    } else if constexpr (EPI != kStats) {
+        // The rounded tile goes through LDS, so that rows leave in 16-byte pieces next to each other.  Stored
+        // from the fragments, 8 bytes a lane and with each dH waited for in turn, the gated block's backward
+        // pass took 404 us on 2048 tokens of a 4096 x 11008 pair; so, 376.
+        constexpr uint32_t COLS = EPI == kGated ? BN / 2 : BN, LDW = COLS + 8;
+        uint16_t *st = reinterpret_cast<uint16_t *>(smem);
+        u32x2 dh[FM][FN / 2];  // kGatedBwd: all of the wave's dH asked for before any is used
+        if constexpr (EPI == kGatedBwd) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN / 2; ++j) {
+                    const uint32_t m = min(mw + 16 * i, p.M - 1), n = nw + 32 * j, f = p.f0 + (n >> 5) * 16 + (n & 15);
+                    const uint32_t have = left(p.F, f);
+                    dh[i][j] = have ? load4(p.dH + m * p.lddh + f, have, p.vec) : (u32x2){0u, 0u};
+                }
+        }
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const uint32_t m = mw + 16 * i;
             if (m >= p.M) continue;
+            uint16_t *row = st + (m - m0) * LDW;
             const int64_t lab = EPI == kProb ? p.labels[m] - p.f0 : 0;
             const float lse = EPI == kProb ? p.lse[m] : 0.f;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
+            for (int j = 0; j < FN; j += EPI == kGated || EPI == kGatedBwd ? 2 : 1) {
+                const uint32_t n = nw + 16 * j;
                 float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                if constexpr (EPI == kProb)
-                    emit_prob(p, m, nw + 16 * j, lab, lse, v);
-                else
-                    emit_out(p, m, nw + 16 * j, v);
+                if constexpr (EPI == kGated || EPI == kGatedBwd) {
+                    // n is gate's row of the piece, n + 16 up's; f their row in the tensors
+                    const uint32_t f = p.f0 + (n >> 5) * 16 + (n & 15);
+                    const float u[4] = {acc[i][j + 1][0], acc[i][j + 1][1], acc[i][j + 1][2], acc[i][j + 1][3]};
+                    float x[4], y[4];
+                    if constexpr (EPI == kGated) {
+                        gated(p.act, v, u, x);
+                        store4(row + ((n - n0) >> 5) * 16 + (n & 15), x, 4, true);
+                    } else {
+                        gated_bwd(p.act, left(p.F, f), dh[i][j / 2], v, u, x, y);
+                        store4(row + (n - n0), x, 4, true);
+                        store4(row + (n - n0) + 16, y, 4, true);
+                    }
+                } else if constexpr (EPI == kProb) {
+                    float x[4];
+                    prob(p, n, lab, lse, v, x);
+                    store4(row + (n - n0), x, 4, true);
+                } else if (n < p.N && finish_out(p, m, n, v)) {
+                    store4(row + (n - n0), v, 4, true);
+                }
             }
         }
-    } else if constexpr (EPI == kGated || EPI == kGatedBwd) {
-        static_assert(FN % 2 == 0, "a wave holds whole pairs of gate and up fragments");
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const uint32_t m = mw + 16 * i;
-            if (m >= p.M) continue;
-#pragma unroll
-            for (int j = 0; j < FN; j += 2) {
-                const uint32_t n = nw + 16 * j;                    // gate's row of the piece; up's is n + 16
-                const uint32_t f = p.f0 + (n >> 5) * 16 + (n & 15);  // their row in the tensors
-                const float g[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                const float u[4] = {acc[i][j + 1][0], acc[i][j + 1][1], acc[i][j + 1][2], acc[i][j + 1][3]};
-                if constexpr (EPI == kGated)
-                    emit_gated(p, m, f, g, u);
-                else if (n < p.ldG)
-                    emit_gated_bwd(p, m, f, n, n + 16, g, u);
+        __syncthreads();
+        if (EPI != kOut || p.last) {
+            constexpr uint32_t CH = COLS / 8;
+            for (uint32_t t = tid; t < BM * CH; t += 64 * NW) {
+                const uint32_t m = m0 + t / CH, c = t % CH * 8;
+                if (m >= p.M) continue;
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(st + (t / CH) * LDW + c);
+                if constexpr (EPI == kOut) {
+                    if (n0 + c < p.N) store8(p.out + m * p.ldo + n0 + c, v, p.N - (n0 + c), p.vec16);
+                } else if constexpr (EPI == kGated) {
+                    const uint32_t f = p.f0 + n0 / 2 + c;
+                    if (f < p.F) store8(p.out + m * p.ldo + f, v, p.F - f, p.vec16);
+                } else if (n0 + c < p.ldG) {
+                    *reinterpret_cast<u32x4 *>(p.G + static_cast<uint64_t>(m) * p.ldG + n0 + c) = v;
+                }
+            }
+        }
+        if constexpr (EPI == kGatedBwd) {
+            constexpr uint32_t CH = BN / 16;
+            for (uint32_t t = tid; t < BM * CH; t += 64 * NW) {
+                const uint32_t m = m0 + t / CH, c = t % CH, f = p.f0 + n0 / 2 + c * 8;
+                if (m >= p.M || f >= p.F) continue;
+                const uint16_t *src = st + (t / CH) * LDW + (c >> 1) * 32 + (c & 1) * 8;
+                if (p.dG) store8(p.dG + m * p.ldg + f, *reinterpret_cast<const u32x4 *>(src), p.F - f, p.vec16);
+                if (p.dU) store8(p.dU + m * p.ldg + f, *reinterpret_cast<const u32x4 *>(src + 16), p.F - f, p.vec16);
             }
         }
     } else if constexpr (EPI == kStats) {
@@ -668,13 +732,13 @@ struct JoinArgs {
     uint32_t count, tiles, slices, grid, up_col;  // up_col: where dU starts in G
 };
 
-// The sum of virtual tile vt's parts at token m, columns c..c + 3, added to v.
+// The sum of tile vt's parts at token m, columns c..c + 3, added to v.
 __device__ __forceinline__ void add_parts(const JoinArgs &q, uint32_t M, uint32_t vt, uint32_t m, uint32_t c, float (&v)[4]) {
     // The workgroups whose runs hold the tile's first and last slice: run g starts at
     // floor(g * total / grid).
     const uint64_t total = static_cast<uint64_t>(q.count * q.tiles) * q.slices, at = static_cast<uint64_t>(vt) * q.slices;
-    const uint32_t g0 = static_cast<uint32_t>(((at + 1) * q.grid - 1) / total);
-    const uint32_t g1 = static_cast<uint32_t>(((at + q.slices) * q.grid - 1) / total);
+    const uint32_t g0 = static_cast<uint32_t>(quotient((at + 1) * q.grid - 1, total));
+    const uint32_t g1 = static_cast<uint32_t>(quotient((at + q.slices) * q.grid - 1, total));
     const float *src = q.part + (static_cast<uint64_t>(vt) * M + m) * kFusedTile + c;
     for (uint32_t g = g0; g <= g1; g += 4) {  // four loads at a time (the last part again past the end)
         f32x4_t t[4];
@@ -708,7 +772,9 @@ __global__ __launch_bounds__(256) void k_join(const MmArgs p, const JoinArgs q) 
     } else if constexpr (EPI == kGatedBwd) {
         if (n < q.up_col) emit_gated_bwd(p, m, p.f0 + n, n, q.up_col + n, v, u);
     } else if constexpr (EPI == kProb) {
-        emit_prob(p, m, n, p.labels[m] - p.f0, p.lse[m], v);
+        float x[4];
+        prob(p, n, p.labels[m] - p.f0, p.lse[m], v, x);
+        store4(p.G + static_cast<uint64_t>(m) * p.ldG + n, x, 4, true);
     } else {
         const int64_t lab = p.labels[m] - p.f0;
         float mx = -__builtin_inff(), s = 0.f;
@@ -899,6 +965,7 @@ cbk_status token_side(MmArgs &p, const uint16_t *X, uint64_t ld, uint64_t T, uin
 }
 
 bool vec8(const void *p, uint64_t ld) { return aligned_to(p, 8) && ld % 4 == 0; }
+bool vec16(const void *p, uint64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
 
 uint64_t up64(uint64_t n) { return (n + 63) / 64 * 64; }
 
@@ -1042,6 +1109,7 @@ struct Weights {
         p.out = dX;
         p.ldo = lddx;
         p.vec = vec8(dX, lddx);
+        p.vec16 = vec16(dX, lddx);
         if (pl.fused) {
             JoinArgs q;
             CBK_TRY(fused(p, true, q));
@@ -1082,6 +1150,7 @@ cbk_status launch_linear(const cbk_tensor &t, const uint16_t *X, uint64_t ldx, u
             p.out = Y + c * ldy + r;
             p.ldo = ldy;
             p.vec = vec8(p.out, ldy);
+            p.vec16 = vec16(p.out, ldy);
             p.last = 1;
             CBK_TRY(w.forward<kOut>(p));
         }
@@ -1119,6 +1188,7 @@ cbk_status launch_ffn(const cbk_tensor &gate, const cbk_tensor &up, int act, con
         p.out = H + c * ldh;
         p.ldo = ldh;
         p.vec = vec8(p.out, ldh);
+        p.vec16 = vec16(p.out, ldh);
         for (uint64_t r = 0; r < gate.rows; r += pl.rows) {
             CBK_TRY(w.piece(r));
             p.f0 = static_cast<uint32_t>(r);
@@ -1146,6 +1216,7 @@ cbk_status launch_ffn_bwd(const cbk_tensor &gate, const cbk_tensor &up, int act,
         p.dU = dU ? dU + c * ldg : nullptr;
         p.ldg = ldg;
         p.vec = vec8(p.dH, lddh) && (!dG || vec8(p.dG, ldg)) && (!dU || vec8(p.dU, ldg));
+        p.vec16 = (!dG || vec16(p.dG, ldg)) && (!dU || vec16(p.dU, ldg));  // of the outputs
         p.G = at<uint16_t>(ws, pl.g);
         for (uint64_t r = 0; r < gate.rows; r += pl.rows) {
             CBK_TRY(w.piece(r));

@@ -43,6 +43,12 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
 
+// a / b, by the short division where it is enough (it nearly always is; the long one takes a microsecond).
+__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // Copies 16 bytes a lane from the resource (at the lane's voff plus the wave's soff) straight into
 // LDS, lane l to dst + 16 l; dst is the same in every lane.  The wave's vmcnt counts it.  The
 // host's pass over this file does not know this chip's wide copies and transposing reads, so it

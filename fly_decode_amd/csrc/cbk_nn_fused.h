@@ -185,11 +185,11 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
     }
 
     const uint64_t total = static_cast<uint64_t>(p.count * p.tiles) * p.slices;
-    uint64_t pos = blockIdx.x * total / gridDim.x;
-    const uint64_t end = (blockIdx.x + 1) * total / gridDim.x;
+    uint64_t pos = quotient(blockIdx.x * total, gridDim.x);
+    const uint64_t end = quotient((blockIdx.x + 1) * total, gridDim.x);
     uint32_t staged = ~0u;  // the tensor whose table is in LDS
     while (pos < end) {
-        const uint32_t vt = static_cast<uint32_t>(pos / p.slices), s0 = static_cast<uint32_t>(pos - static_cast<uint64_t>(vt) * p.slices);
+        const uint32_t vt = static_cast<uint32_t>(quotient(pos, p.slices)), s0 = static_cast<uint32_t>(pos - static_cast<uint64_t>(vt) * p.slices);
         const uint32_t s1 = static_cast<uint32_t>(min(static_cast<uint64_t>(p.slices), s0 + (end - pos)));
         const uint32_t which = vt >= p.tiles, tile = vt - which * p.tiles;
         const FusedTensor &T = p.t[which];
