@@ -552,6 +552,8 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
             __builtin_amdgcn_sched_group_barrier(0x008, MF / CP, 0);
         }
         __builtin_amdgcn_sched_group_barrier(0x008, MF - MF / CP * CP, 0);
+        // multiplications are not put off past the barrier: their reads end before it
+        __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * CP));
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
@@ -852,7 +854,7 @@ struct UnpackRun {
         constexpr uint32_t stage = G::STAGE_CHUNKS * 16 > 64 * 144 ? G::STAGE_CHUNKS * 16 : 64 * 144;
         constexpr uint32_t lds = kUnpackWaves * stage;
         r.a.steps = ceil_div(static_cast<uint64_t>(r.a.nrows) * r.a.cols, 4096);
-        // two workgroups per CU, whose waves take every so-manieth step
+        // two workgroups per CU, whose waves take every n-th step
         const dim3 grid(std::min(ceil_div(r.a.steps, kUnpackWaves), std::max(1u, 2 * static_cast<uint32_t>(cu_count()) / r.count)), r.count);
         if (r.a.cols % 8 == 0) {
             if (!allow_lds_once<UnpackTag<B, true>>(k_unpack<B, true>, lds)) return false;

@@ -140,6 +140,11 @@ __device__ __forceinline__ void read_columns(bf16x8_t (&x)[4], const uint32_t (&
     x[3] = __builtin_bit_cast(bf16x8_t, (u32x4){a3.x, a3.y, b3.x, b3.y});
 }
 
+// Keeps memory loads and copies into LDS in the order in which they stand: the waits that let the words
+// of later slices stay in flight count on the copies having been asked for first.  Arithmetic, matrix and
+// LDS instructions may still move past.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x78F); }
+
 // Waves of a workgroup over the 128 columns; the other factor of 8 goes over the tokens.
 constexpr int fused_wn(int BM) { return BM >= 192 ? 2 : BM >= 64 ? 4 : 8; }
 
@@ -283,6 +288,7 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
         lds_barrier();  // the previous part's last reads
         copy(s0, 0);
         if constexpr (AHEAD == 2) copy(s0 + 1, SLICE);
+        keep_order();
         if (staged != which) {
             staged = which;
             CbStage<B, 512> cs;
@@ -318,6 +324,7 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
             multiply(f0);
             if constexpr (AHEAD == 2) read(f0, next, lower);  // after the last slice: old contents of a buffer, not used
             decode(w, s + AHEAD, fill);
+            keep_order();
             load(w, s + AHEAD + 2);
             multiply(f1);
             // the multiplications between the LDS reads and the decoding's arithmetic

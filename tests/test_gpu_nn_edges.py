@@ -431,3 +431,25 @@ def test_the_loss_changes_as_its_gradient_says(env):
     off = (lp - lm - 2 * (g * d.double()).sum(1)).abs()
     assert bool((off <= bound).all()), (off - bound).max()
     assert float((lp - lm).abs().max()) > 10 * float(bound.max())  # the test can tell a wrong gradient
+
+
+@pytest.mark.parametrize("T", [17, 40, 64, 65, 100, 128])
+def test_width_8_and_ragged_rows(env, T):
+    """Long runs of slices whose fields start anywhere in a dword, at the width with the fewest of them."""
+    torch, cbk = env
+    rows, cols = 1500, 2001
+    w, x = weights(torch, rows, cols, 200, 91), acts(torch, T, cols, 92)
+    d = compress(cbk, w)
+    assert d.b == 8
+    ref.assert_within(cbk.linear(d, x.cuda()), *ref.linear(x, w), "linear")
+
+
+@pytest.mark.parametrize("T", [1, 30, 500])
+def test_one_tensor_as_gate_and_up(env, T):
+    torch, cbk = env
+    rows, cols = 300, 192
+    w, x, dh = weights(torch, rows, cols, 900, 93, 0.2), acts(torch, T, cols, 94), acts(torch, T, rows, 95, 0.1)
+    d = compress(cbk, w)
+    ref.assert_within(cbk.ffn_gated(d, d, x.cuda()), *ref.ffn("silu", x, w, w), "ffn_gated")
+    for name, v, want in zip(("dX", "dG", "dU"), cbk.ffn_gated_bwd(d, d, x.cuda(), dh.cuda()), ref.ffn_bwd("silu", x, w, w, dh)):
+        ref.assert_within(v, *want, name)
