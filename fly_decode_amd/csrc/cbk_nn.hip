@@ -5,9 +5,12 @@
 // All are products with a tensor W [N][K] that is stored as b-bit indices into a codebook:
 //   forward   Y = X W^T   (reduction over W's columns)
 //   gradient  dX = G W    (reduction over W's rows)
-// A piece of W is decoded into the workspace once ([rows][Kp] BF16, Kp = K rounded up to 64, zero
-// padded), and one matrix-core kernel, k_mm, multiplies it in either orientation; what differs
-// between the operators is the work it does on its accumulators (the epilogue).
+// Up to a few hundred tokens (nn_plan) the weights are decoded on the way, once, by the workgroup that
+// multiplies them: k_fused (cbk_nn_fused.h), or the batch-1 GEMV for one token.  Both leave fp32 sums,
+// and k_join does the operator's work on them.  With more tokens, and for widths that k_fused does not
+// take, a piece of W is decoded into the workspace once (k_unpack: [rows][Kp] BF16, Kp = K rounded up
+// to 64, zero padded), and one matrix-core kernel, k_mm, multiplies it in either orientation; the
+// operator's work is its epilogue.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -138,7 +141,9 @@ __global__ __launch_bounds__(256) void k_unpack_pad(const UnpackArgs a) {
 // codebook in LDS), and each run of 8 fields, or each field where a row's length is no multiple of
 // 8, goes to its row's place in the piece.  Both tensors of a pair go in one launch (blockIdx.y).
 // row0 * cols is a multiple of 128, so a piece starts on a 16-byte chunk of the stream.  The stores keep the ordinary cache
-// policy: the matrix product reads the piece next.
+// policy: the matrix product reads the piece next.  A pair of 4096 x 11008 at 13 bits, 147 MB in and 180 MB
+// out, takes 54 us: 6.0 TB/s, bound by that traffic.  It pays from some 400 tokens on, where it is a sixth
+// of the product's time or less.
 constexpr int kUnpackWaves = 4;
 
 template <int B, bool RUNS>
@@ -236,6 +241,12 @@ __global__ __launch_bounds__(64 * kUnpackWaves) void k_unpack(const UnpackArgs a
 // transposing 64-bit LDS read (a group of 16 lanes reads 4 rows x 16 columns, and lane i gets
 // column i); chunk c of row r sits in slot c ^ (2 (r & 3) + 8 ((r / 8) & 1..3)), so the 4 rows of a
 // group and neighbouring groups hit different banks.
+//
+// Measured on 2048 tokens and a pair of 4096 x 11008 (369 GFLOP a product): 306 us forward, 1.21 PFLOP/s,
+// and 278 for dX, 1.33; 128 x 128 tiles took 350 forward.  On a 4096-wide head of 32000 rows (537 GFLOP),
+// multiplications and barriers alone took 320 us, 1.68 PFLOP/s at the clock that the chip holds under
+// them; with the fragments' reads 364, and with the copies, which are new to an XCD's L2, 470.  Groups of
+// 4 or 16 token tiles, the 32 x 32 instruction and a raised wave priority were no faster.
 constexpr uint32_t kRing = 5;  // slices of 32 in LDS
 constexpr int kMmTile = 256, kMmWm = 2, kMmWn = 4;  // tile and its waves
 
@@ -706,7 +717,8 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
     }
 }
 
-// The shared tiles' parts added in order.  A workgroup takes 4 tokens of a tile.
+// The shared tiles' parts added in order.  A workgroup takes 4 tokens of a tile.  It is bound by reading
+// them (2048 tokens of 4096 columns: up to 384 parts of 256 KB in 16 us).
 __global__ __launch_bounds__(256) void k_mm_join(const MmArgs p, uint32_t sharers) {
     const uint32_t tile = p.whole + blockIdx.x, row = blockIdx.y * 4 + (threadIdx.x >> 6), c = (threadIdx.x & 63) * 4;
     uint32_t m0, n0;
@@ -727,7 +739,9 @@ __global__ __launch_bounds__(256) void k_mm_join(const MmArgs p, uint32_t sharer
 }
 
 // The parts of a tile that k_fused left, added in order, and the operator's work on the sums.  A
-// workgroup takes 8 tokens of a tile, 32 lanes of 4 columns each.  `count` 2: the second tensor's tile
+// workgroup takes 8 tokens of a tile, 32 lanes of 4 columns each.  With few tokens it takes the 4 us that a
+// launch does; with many it is bound by reading the parts (300 tokens of 42752 rows, 110 MB with its
+// output: 22 us).  `count` 2: the second tensor's tile
 // holds the up sums of the same columns (forward), or the second half of one sum (gradient).
 struct JoinArgs {
     const float *part;

@@ -1,5 +1,5 @@
-// What the kernels of the operators in cbk_nn.h share (cbk_nn.hip, cbk_nn_fused.h): copies into LDS
-// and transposing reads, and the arguments of the product that decodes on the way.
+// What the kernels of the operators in cbk_nn.h share (cbk_nn.hip, cbk_nn_fused.h): copies into LDS,
+// and the arguments of the product that decodes on the way.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -40,7 +40,6 @@ cbk_status launch_fused(const FusedArgs &a, uint32_t bm, bool nn, hipStream_t s)
 
 namespace {
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
 
 // a / b, by the short division where it is enough (it nearly always is; the long one takes a microsecond).
@@ -51,21 +50,10 @@ __device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
 
 // Copies 16 bytes a lane from the resource (at the lane's voff plus the wave's soff) straight into
 // LDS, lane l to dst + 16 l; dst is the same in every lane.  The wave's vmcnt counts it.  The
-// host's pass over this file does not know this chip's wide copies and transposing reads, so it
-// gets empty bodies.
+// host's pass over this file does not know this chip's wide copies, so it gets an empty body.
 __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, unsigned char *dst, uint32_t voff, uint32_t soff) {
 #ifdef __HIP_DEVICE_COMPILE__
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (CBK_LDS void *)(dst), 16, static_cast<int>(voff), static_cast<int>(soff), 0, 0);
-#endif
-}
-
-// The transposing 64-bit LDS read: the 16 lanes of a group read 4 rows of 16 BF16 (lane s the 4
-// values at row s / 4, columns 4 (s % 4)..), and lane i gets column i of the 4 rows.
-__device__ __forceinline__ s16x4 read_transposed(const unsigned char *src) {
-#ifdef __HIP_DEVICE_COMPILE__
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((CBK_LDS s16x4 *)(src));
-#else
-    return s16x4{};
 #endif
 }
 

@@ -28,7 +28,7 @@
  *    leading dimension is a multiple of 8 (others are copied into the workspace first, or stored
  *    element by element).
  *  - results do not depend on timing: equal inputs give equal bits.
- *  - limits: cols <= 2^20, rows < 2^31, tokens < 2^31, leading dimensions < 2^40;
+ *  - limits: cols <= 2^20, rows < 2^31, tokens < 2^31, leading dimensions < 2^32;
  *    CBK_E_UNSUPPORTED beyond.
  */
 #ifndef CBK_NN_H
