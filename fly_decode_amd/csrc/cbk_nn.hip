@@ -9,7 +9,7 @@
 // multiplies them: k_fused (cbk_nn_fused.h), or the batch-1 GEMV for one token.  Both leave fp32 sums,
 // and k_join does the operator's work on them.  With more tokens, and for widths that k_fused does not
 // take, a piece of W is decoded into the workspace once (k_unpack: [rows][Kp] BF16, Kp = K rounded up
-// to 64, zero padded), and one matrix-core kernel, k_mm, multiplies it in either orientation; the
+// to 64, zero padded, in blocks), and one matrix-core kernel, k_mm, multiplies it in either orientation; the
 // operator's work is its epilogue.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256) void k_zero_rows(uint16_t *__restrict__ out, u
 }
 
 // ------------------------------------------------------------------------- decoding a piece
-// Rows [row0, row0 + nrows) of a tensor into out [rows_out][Kp]; columns past cols and rows past
+// Rows [row0, row0 + nrows) of a tensor into out [rows_out][Kp] (piece_at); columns past cols and rows past
 // nrows are zero.  `pair` 0: row f goes to row f.  1 and 2: the gate and up tensors share the
 // piece, 16 rows of each in turn (row f to 32 (f / 16) + 16 (pair - 1) + f % 16), so that a wave
 // of k_mm has a column's gate and up sums in the same lanes.
@@ -108,6 +108,37 @@ __device__ __forceinline__ uint32_t piece_row(uint32_t f, uint32_t pair) {
     return pair == 0 ? f : (f >> 4) * 32 + (pair - 1) * 16 + (f & 15);
 }
 
+// Where element (row, k) of a piece lies: blocks of 16 rows x 32 columns, 1 KB each, one after the other
+// along the rows and then down.  A wave's copy into LDS takes one block, so it reads whole cache lines in
+// either orientation of the product.
+__device__ __forceinline__ uint64_t piece_at(uint32_t row, uint32_t k, uint32_t Kp) {
+    return static_cast<uint64_t>(row >> 4) * (Kp * 16) + ((k >> 5) * 512 + (row & 15) * 32 + (k & 31));
+}
+
+// X [T][K] with leading dimension ld into such blocks, columns past K zero: a thread per 16 bytes.
+__global__ __launch_bounds__(256) void k_pack_rows(const uint16_t *__restrict__ X, uint64_t ld, uint32_t T, uint32_t K,
+                                                   uint32_t Kp, uint32_t whole, uint16_t *__restrict__ P) {
+    const uint64_t n = static_cast<uint64_t>((T + 15) / 16) * (Kp / 32) * 64, stride = static_cast<uint64_t>(gridDim.x) * blockDim.x;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+        const uint64_t blk = i >> 6, down = quotient(blk, Kp / 32);
+        const uint32_t t = static_cast<uint32_t>(down) * 16 + (static_cast<uint32_t>(i) >> 2 & 15);
+        const uint32_t k = static_cast<uint32_t>(blk - down * (Kp / 32)) * 32 + (static_cast<uint32_t>(i) & 3) * 8;
+        if (t >= T) continue;
+        const uint16_t *x = X + t * ld + k;
+        u32x4 v = (u32x4){0u, 0u, 0u, 0u};
+        if (whole && k + 8 <= K) {
+            v = *reinterpret_cast<const u32x4 *>(x);
+        } else {
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+                if (k + j < K) w[j >> 1] |= static_cast<uint32_t>(x[j]) << (16 * (j & 1));
+            v = (u32x4){w[0], w[1], w[2], w[3]};
+        }
+        *reinterpret_cast<u32x4 *>(P + i * 8) = v;
+    }
+}
+
 // Any width, any number of columns: a thread per 4 columns.
 __global__ __launch_bounds__(256) void k_unpack_generic(const UnpackArgs a) {
     const UnpackTensor &T = a.t[0];
@@ -123,7 +154,7 @@ __global__ __launch_bounds__(256) void k_unpack_generic(const UnpackArgs a) {
                 v[j] = idx < T.U ? T.cb[idx] : kCorrupt;
             }
         }
-        *reinterpret_cast<u32x2 *>(a.out + static_cast<uint64_t>(piece_row(f, a.pair)) * a.Kp + k) = (u32x2){v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
+        *reinterpret_cast<u32x2 *>(a.out + piece_at(piece_row(f, a.pair), k, a.Kp)) = (u32x2){v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
     }
 }
 
@@ -131,8 +162,8 @@ __global__ __launch_bounds__(256) void k_unpack_generic(const UnpackArgs a) {
 __global__ __launch_bounds__(256) void k_unpack_pad(const UnpackArgs a) {
     for (uint32_t f = blockIdx.x; f < a.rows_out; f += gridDim.x)
         for (uint32_t pr = a.pair ? 1 : 0; pr <= a.pair; ++pr) {
-            uint16_t *row = a.out + static_cast<uint64_t>(piece_row(f, pr)) * a.Kp;
-            for (uint32_t k = (f < a.nrows ? a.cols : 0) + threadIdx.x; k < a.Kp; k += blockDim.x) row[k] = 0;
+            for (uint32_t k = (f < a.nrows ? a.cols : 0) + threadIdx.x; k < a.Kp; k += blockDim.x)
+                a.out[piece_at(piece_row(f, pr), k, a.Kp)] = 0;
         }
 }
 
@@ -142,7 +173,7 @@ __global__ __launch_bounds__(256) void k_unpack_pad(const UnpackArgs a) {
 // 8, goes to its row's place in the piece.  Both tensors of a pair go in one launch (blockIdx.y).
 // row0 * cols is a multiple of 128, so a piece starts on a 16-byte chunk of the stream.  The stores keep the ordinary cache
 // policy: the matrix product reads the piece next.  A pair of 4096 x 11008 at 13 bits, 147 MB in and 180 MB
-// out, takes 54 us: 6.0 TB/s, bound by that traffic.  It pays from some 400 tokens on, where it is a sixth
+// out, takes 60 us: 5.4 TB/s, bound by that traffic (54 into plain rows, whose stores are longer).  It pays from some 400 tokens on, where it is a sixth
 // of the product's time or less.
 constexpr int kUnpackWaves = 4;
 
@@ -204,7 +235,7 @@ __global__ __launch_bounds__(64 * kUnpackWaves) void k_unpack(const UnpackArgs a
                 ++r;
                 k -= a.cols;
             }
-            return a.out + static_cast<uint64_t>(piece_row(r, pair)) * a.Kp + k;
+            return a.out + piece_at(piece_row(r, pair), k, a.Kp);
         };
         if constexpr (RUNS) {
 #pragma unroll
@@ -231,22 +262,23 @@ __global__ __launch_bounds__(64 * kUnpackWaves) void k_unpack(const UnpackArgs a
 // fragments of v_mfma_f32_16x16x32_bf16.  The weights are the instruction's A operand and the
 // tokens its B operand, so lane l holds columns n = 4 (l / 16) + 0..3 of token m = l % 16 of a
 // fragment: four neighbours in the output's rows.  Slices of 32 of the reduction are copied
-// straight into LDS (16 bytes a lane).
+// straight into LDS (16 bytes a lane), a block of 16 x 32 by an instruction.
 //
 // LDS layout.  A copy fills 1024 consecutive bytes, so what is permuted is which 16-byte chunk a
 // lane fetches.  Rows of 32 reduction elements (A, and B when NN is false) are 4 chunks, chunk c
 // of row r in slot c ^ (-(r / 4) & 3).  A 128-bit read serves 16 lanes at a time, of which lanes
 // 0-3 and 12-15 take one chunk of rows 0-3 and 12-15 and lanes 20-27 the next chunk of rows 4-11 (and
-// so on); this order puts the 16 into different banks, where c ^ ((r / 4) & 3) made two meet.  When NN is true B's slice is 32 reduction rows of BN columns, read with the
-// transposing 64-bit LDS read (a group of 16 lanes reads 4 rows x 16 columns, and lane i gets
-// column i); chunk c of row r sits in slot c ^ (2 (r & 3) + 8 ((r / 8) & 1..3)), so the 4 rows of a
-// group and neighbouring groups hit different banks.
+// so on); this order puts the 16 into different banks, where c ^ ((r / 4) & 3) made two meet.  When NN is
+// true B's slice is 2 x 8 blocks of 16 reduction rows x 32 columns, read with the transposing 64-bit LDS
+// read (a group of 16 lanes reads 4 rows x 16 columns, and lane i gets column i); chunk c of row r sits in
+// slot c ^ (2 (r / 8)), so the 4 rows of a group and those of its neighbour hit different banks.
 //
-// Measured on 2048 tokens and a pair of 4096 x 11008 (369 GFLOP a product): 306 us forward, 1.21 PFLOP/s,
-// and 278 for dX, 1.33; 128 x 128 tiles took 350 forward.  On a 4096-wide head of 32000 rows (537 GFLOP),
+// Measured on 2048 tokens and a pair of 4096 x 11008 (369 GFLOP a product): 286 us forward, 1.29 PFLOP/s,
+// and 270 for dX, 1.37; 128 x 128 tiles took 350 forward.  On a 4096-wide head of 32000 rows (537 GFLOP),
 // multiplications and barriers alone took 320 us, 1.68 PFLOP/s at the clock that the chip holds under
-// them; with the fragments' reads 364, and with the copies, which are new to an XCD's L2, 470.  Groups of
-// 4 or 16 token tiles, the 32 x 32 instruction and a raised wave priority were no faster.
+// them; with the fragments' reads 364, and with the copies, which are new to an XCD's L2, 400 (470 where A
+// and B lay row after row and a copy read half a cache line of each).  Groups of 4 or 16 token tiles, the
+// 32 x 32 instruction and a raised wave priority were no faster.
 constexpr uint32_t kRing = 5;  // slices of 32 in LDS
 constexpr int kMmTile = 256, kMmWm = 2, kMmWn = 4;  // tile and its waves
 
@@ -256,7 +288,7 @@ struct MmArgs {
     const uint16_t *A;
     const uint16_t *B;
     uint64_t lda;   // elements
-    uint32_t ldb;
+    uint32_t ldb, blocks;  // blocks: A lies in blocks of 16 x 32 as B does, else row after row
     uint32_t M, N;  // tokens; columns of C that exist
     uint32_t ktiles, tm, tn;
     uint32_t whole;  // tiles that one workgroup does from end to end; the others' slices are shared
@@ -276,7 +308,8 @@ struct MmArgs {
     int act;
     uint32_t f0, F;  // first row of the tensors in this piece, and all of them
     const uint16_t *dH;
-    uint16_t *dG, *dU, *G;  // G: the piece's gradients at the projections [M][ldG], columns as the piece's rows
+    // G: the piece's gradients at the projections [M][ldG], columns as the piece's rows; k_mm writes and reads it in blocks
+    uint16_t *dG, *dU, *G;
     uint64_t lddh, ldg;
     uint32_t ldG;
 
@@ -461,26 +494,25 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
     uint32_t va[IA], vb[IB];
 #pragma unroll
     for (int i = 0; i < IA; ++i) {
-        const uint32_t r = (wave + NW * i) * 16 + (lane >> 2), c = (lane & 3) ^ (-(lane >> 4) & 3);
-        va[i] = min(r, p.M - 1 - m0) * static_cast<uint32_t>(p.lda) * 2u + c * 16u;  // rows past M repeat the last one
+        // blocks, or rows, past M repeat the last one
+        const uint32_t blk = wave + NW * i, at = lane ^ (-(lane >> 4) & 3), lda = static_cast<uint32_t>(p.lda);
+        va[i] = p.blocks ? min(blk, (p.M - 1 - m0) / 16) * 32 * lda + at * 16
+                         : min(blk * 16 + (at >> 2), p.M - 1 - m0) * 2 * lda + (at & 3) * 16;
     }
 #pragma unroll
     for (int i = 0; i < IB; ++i) {
         if constexpr (NN) {
-            constexpr uint32_t CH = BN / 8, RPI = 64 / CH;  // chunks of a row, rows of a copy
-            const uint32_t r = (wave + NW * i) * RPI + lane / CH;
-            const uint32_t c = (lane % CH) ^ (2 * (r & 3) + 8 * ((r >> 3) & (CH / 8 - 1)));
-            vb[i] = (r * p.ldb + min(n0 + c * 8, p.ldb - 8)) * 2u;  // columns past the piece repeat its last chunk
+            const uint32_t blk = wave + NW * i, rows = blk / (BN / 32);  // columns past the piece repeat its last block
+            vb[i] = rows * 32 * p.ldb + min(n0 / 32 + blk % (BN / 32), p.ldb / 32 - 1) * 1024 + (lane ^ (lane >> 5) * 2) * 16;
         } else {
-            const uint32_t r = (wave + NW * i) * 16 + (lane >> 2), c = (lane & 3) ^ (-(lane >> 4) & 3);
-            vb[i] = r * p.ldb * 2u + c * 16u;
+            vb[i] = (wave + NW * i) * 32 * p.ldb + (lane ^ (-(lane >> 4) & 3)) * 16;
         }
     }
-    const uint32_t step_b = NN ? 64 * p.ldb : 64;
+    const uint32_t step_a = p.blocks ? 1024 : 64, step_b = NN ? 64 * p.ldb : 1024;
     auto copy = [&](uint32_t s, uint32_t at) {
         unsigned char *to = smem + at;
 #pragma unroll
-        for (int i = 0; i < IA; ++i) copy_to_lds(ra, to + (wave + NW * i) * 1024, va[i], (2 * k0 + s) * 64);
+        for (int i = 0; i < IA; ++i) copy_to_lds(ra, to + (wave + NW * i) * 1024, va[i], (2 * k0 + s) * step_a);
 #pragma unroll
         for (int i = 0; i < IB; ++i) copy_to_lds(rb, to + ABYTES + (wave + NW * i) * 1024, vb[i], (2 * k0 + s) * step_b);
     };
@@ -490,13 +522,12 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
     const uint32_t fa = (wm * (BM / WM) + li) * 64 + swz, fb = ABYTES + (wn * (BN / WN) + li) * 64 + swz;
     uint32_t ft[FN];
     if constexpr (NN) {
-        constexpr uint32_t CH = BN / 8;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const uint32_t r = 8 * lg + (li >> 2);
-            const uint32_t c = (wn * (BN / WN) + 16 * j) / 8 + ((li & 3) >> 1);
-            ft[j] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((CBK_LDS unsigned char *)(smem))) + ABYTES + r * (BN * 2) +
-                    (c ^ (2 * (r & 3) + 8 * (lg & (CH / 8 - 1)))) * 16 + (li & 1) * 8;
+            const uint32_t blk = (lg >> 1) * (BN / 32) + (wn * (BN / WN) + 16 * j) / 32, r = 8 * (lg & 1) + (li >> 2);
+            const uint32_t c = (2 * j + ((li & 3) >> 1)) & 3;
+            ft[j] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((CBK_LDS unsigned char *)(smem))) + ABYTES + blk * 1024 +
+                    (r * 4 + (c ^ (2 * (lg & 1)))) * 16 + (li & 1) * 8;
         }
     }
     struct Frags {
@@ -505,7 +536,7 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
     auto read = [&](Frags &f, uint32_t at) {
         if constexpr (NN) {
             const uint32_t t[4] = {ft[0] + at, ft[1] + at, ft[2] + at, ft[3] + at};
-            read_columns<4 * BN * 2>(f.b, t);
+            read_columns<256>(f.b, t);
         } else {
 #pragma unroll
             for (int j = 0; j < FN; ++j) f.b[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(smem + at + fb + j * 1024));
@@ -639,17 +670,21 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
         __syncthreads();
         if (EPI != kOut || p.last) {
             constexpr uint32_t CH = COLS / 8;
+            constexpr bool kBlocks = EPI == kGatedBwd || EPI == kProb;  // G: a wave writes a block of 16 x 32
             for (uint32_t t = tid; t < BM * CH; t += 64 * NW) {
-                const uint32_t m = m0 + t / CH, c = t % CH * 8;
+                const uint32_t blk = t >> 6;
+                const uint32_t row = kBlocks ? blk / (CH / 4) * 16 + (lane >> 2) : t / CH;
+                const uint32_t c = kBlocks ? (blk % (CH / 4) * 4 + (lane & 3)) * 8 : t % CH * 8;
+                const uint32_t m = m0 + row;
                 if (m >= p.M) continue;
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(st + (t / CH) * LDW + c);
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(st + row * LDW + c);
                 if constexpr (EPI == kOut) {
                     if (n0 + c < p.N) store8(p.out + m * p.ldo + n0 + c, v, p.N - (n0 + c), p.vec16);
                 } else if constexpr (EPI == kGated) {
                     const uint32_t f = p.f0 + n0 / 2 + c;
                     if (f < p.F) store8(p.out + m * p.ldo + f, v, p.F - f, p.vec16);
                 } else if (n0 + c < p.ldG) {
-                    *reinterpret_cast<u32x4 *>(p.G + static_cast<uint64_t>(m) * p.ldG + n0 + c) = v;
+                    *reinterpret_cast<u32x4 *>(p.G + piece_at(m, n0 + c, p.ldG)) = v;
                 }
             }
         }
@@ -964,24 +999,34 @@ cbk_status mm(MmArgs &p, uint32_t columns, hipStream_t s) {
     return launched();
 }
 
-// The tokens' side of a product: used as it is if the copies to LDS can read whole 64-wide slices
-// of it (16-byte aligned rows, no ragged end, and 256 rows within 31 bits), else padded into P.
-cbk_status token_side(MmArgs &p, const uint16_t *X, uint64_t ld, uint64_t T, uint64_t K, uint64_t Kp, uint16_t *P,
-                      hipStream_t s) {
-    if (K == Kp && aligned_to(X, 16) && ld % 8 == 0 && ld <= (uint64_t(1) << 21)) {
+bool vec8(const void *p, uint64_t ld) { return aligned_to(p, 8) && ld % 4 == 0; }
+bool vec16(const void *p, uint64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
+
+// The tokens' side of a product: used as it is if the copies to LDS can read whole 64-wide slices of it
+// (16-byte aligned rows, no ragged end, and 384 rows within 31 bits), else a copy in P, padded for k_fused
+// and in blocks for k_mm.  k_mm's forward product takes the blocks in any case (2048 tokens and 32000 rows
+// of 4096: 7 us for the copy, 404 us instead of 425 for the product); its gradient reads the weights in longer
+// rows and gains nothing (2048 tokens of 4096, 11008 columns: 182 us either way).
+cbk_status token_side(MmArgs &p, bool fused, bool nn, const uint16_t *X, uint64_t ld, uint64_t T, uint64_t K, uint64_t Kp,
+                      uint16_t *P, hipStream_t s) {
+    const uint32_t k = static_cast<uint32_t>(K), kp = static_cast<uint32_t>(Kp);
+    p.blocks = 0;
+    if ((fused || nn) && K == Kp && vec16(X, ld) && ld <= (uint64_t(1) << 21)) {
         p.A = X;
         p.lda = ld;
         return CBK_OK;
     }
     p.A = P;
     p.lda = Kp;
-    hipLaunchKernelGGL(k_pad_rows, dim3(grid_for(T * (Kp / 4), 256)), dim3(256), 0, s, X, ld, T, static_cast<uint32_t>(K),
-                       static_cast<uint32_t>(Kp), P);
+    if (fused) {
+        hipLaunchKernelGGL(k_pad_rows, dim3(grid_for(T * (Kp / 4), 256)), dim3(256), 0, s, X, ld, T, k, kp, P);
+    } else {
+        p.blocks = 1;
+        hipLaunchKernelGGL(k_pack_rows, dim3(grid_for((T + 15) / 16 * (Kp / 32) * 64, 256)), dim3(256), 0, s, X, ld,
+                           static_cast<uint32_t>(T), k, kp, vec16(X, ld) ? 1u : 0u, P);
+    }
     return launched();
 }
-
-bool vec8(const void *p, uint64_t ld) { return aligned_to(p, 8) && ld % 4 == 0; }
-bool vec16(const void *p, uint64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
 
 uint64_t up64(uint64_t n) { return (n + 63) / 64 * 64; }
 
@@ -1159,7 +1204,7 @@ cbk_status launch_linear(const cbk_tensor &t, const uint16_t *X, uint64_t ldx, u
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
-        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, t.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        CBK_TRY(token_side(p, pl.fused, false, X + c * ldx, ldx, p.M, t.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
         for (uint64_t r = 0; r < t.rows; r += pl.rows) {
             CBK_TRY(w.piece(r));
             p.N = static_cast<uint32_t>(w.nrows);
@@ -1184,7 +1229,7 @@ cbk_status launch_linear_dx(const cbk_tensor &t, const uint16_t *dY, uint64_t ld
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
         for (uint64_t r = 0; r < t.rows; r += pl.rows) {
             CBK_TRY(w.piece(r));
-            CBK_TRY(token_side(p, dY + c * lddy + r, lddy, p.M, w.nrows, up64(w.nrows), at<uint16_t>(ws, pl.pack), s));
+            CBK_TRY(token_side(p, pl.fused, true, dY + c * lddy + r, lddy, p.M, w.nrows, up64(w.nrows), at<uint16_t>(ws, pl.pack), s));
             CBK_TRY(w.gradient(p, dX + c * lddx, lddx));
         }
     }
@@ -1198,7 +1243,7 @@ cbk_status launch_ffn(const cbk_tensor &gate, const cbk_tensor &up, int act, con
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
-        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, gate.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        CBK_TRY(token_side(p, pl.fused, false, X + c * ldx, ldx, p.M, gate.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
         p.act = act;
         p.F = static_cast<uint32_t>(gate.rows);
         p.out = H + c * ldh;
@@ -1223,7 +1268,7 @@ cbk_status launch_ffn_bwd(const cbk_tensor &gate, const cbk_tensor &up, int act,
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
-        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, gate.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        CBK_TRY(token_side(p, pl.fused, false, X + c * ldx, ldx, p.M, gate.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
         p.act = act;
         p.F = static_cast<uint32_t>(gate.rows);
         p.dH = dH + c * lddh;
@@ -1244,6 +1289,7 @@ cbk_status launch_ffn_bwd(const cbk_tensor &gate, const cbk_tensor &up, int act,
             d.M = p.M;
             d.A = p.G;
             d.lda = p.ldG;
+            d.blocks = !pl.fused;
             CBK_TRY(w.gradient(d, dX + c * lddx, lddx));
         }
     }
@@ -1257,7 +1303,7 @@ cbk_status launch_xent(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, 
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
-        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, head.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        CBK_TRY(token_side(p, pl.fused, false, X + c * ldx, ldx, p.M, head.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
         p.stat = at<f32x2>(ws, pl.stat);
         p.top = at<float>(ws, pl.top);
         p.labels = labels + c;
@@ -1286,7 +1332,7 @@ cbk_status launch_xent_bwd(const cbk_tensor &head, const uint16_t *X, uint64_t l
     for (uint64_t c = 0; c < T; c += pl.Tc) {
         MmArgs p{};
         p.M = static_cast<uint32_t>(std::min(pl.Tc, T - c));
-        CBK_TRY(token_side(p, X + c * ldx, ldx, p.M, head.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
+        CBK_TRY(token_side(p, pl.fused, false, X + c * ldx, ldx, p.M, head.cols, pl.Kp, at<uint16_t>(ws, pl.pack), s));
         p.labels = labels + c;
         p.lse = lse + c;
         p.G = at<uint16_t>(ws, pl.g);
@@ -1300,6 +1346,7 @@ cbk_status launch_xent_bwd(const cbk_tensor &head, const uint16_t *X, uint64_t l
             d.M = p.M;
             d.A = p.G;
             d.lda = p.ldG;
+            d.blocks = !pl.fused;
             d.labels = p.labels;
             d.ignore = ignore;
             d.scale = dloss + c;

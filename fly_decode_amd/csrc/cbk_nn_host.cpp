@@ -122,8 +122,8 @@ NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
         at += up_to(bytes, 256);
         return o;
     };
-    // a padded copy of the chunk's X (or of a piece's columns of dY)
-    p.pack = take(p.Tc * std::max(p.Kp, op == NnOp::linear ? p.Rp : 0) * 2);
+    // a copy of the chunk's X (or of a piece's columns of dY), padded or in blocks of 16 tokens
+    p.pack = take(up_to(p.Tc, 16) * std::max(p.Kp, op == NnOp::linear ? p.Rp : 0) * 2);
     if (p.fused) {
         // as many workgroups as the LDS lets run at once on 256 CUs, and their parts of the tiles
         p.grid = 256 * std::min<uint32_t>(3, 160 * 1024 / nn_fused_lds(ts[0]->b, p.fused));
@@ -134,7 +134,7 @@ NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
         const uint64_t tiles = up_to(p.Tc, 256) / 256 * (up_to(std::max(p.Kp, p.Rp), 256) / 256);
         p.part = take((256 + std::min<uint64_t>(kMmShared, tiles)) * 256 * 256 * 4);
     }
-    p.g = op == NnOp::linear ? at : take(p.Tc * p.Rp * 2);
+    p.g = op == NnOp::linear ? at : take(up_to(p.Tc, 16) * p.Rp * 2);
     p.acc = p.pieces > 1 ? take(p.Tc * p.Kp * 4) : at;
     p.stat = op == NnOp::xent ? take(p.Tc * p.pieces * (p.Rp / 128) * 8) : at;
     p.top = op == NnOp::xent ? take(p.Tc * 4) : at;
