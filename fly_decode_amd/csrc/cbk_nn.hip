@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cbk_nn_device.h"
 
@@ -791,18 +792,26 @@ __device__ __forceinline__ void add_parts(const JoinArgs &q, uint32_t M, uint32_
     const uint32_t g0 = static_cast<uint32_t>(quotient((at + 1) * q.grid - 1, total));
     const uint32_t g1 = static_cast<uint32_t>(quotient((at + q.slices) * q.grid - 1, total));
     const float *src = q.part + (static_cast<uint64_t>(vt) * M + m) * kFusedTile + c;
-    for (uint32_t g = g0; g <= g1; g += 4) {  // four loads at a time (the last part again past the end)
-        f32x4_t t[4];
+    // N loads at a time (the last part again past the end)
+    auto add = [&](auto batch) {
+        constexpr uint32_t N = decltype(batch)::value;
+        for (uint32_t g = g0; g <= g1; g += N) {
+            f32x4_t t[N];
 #pragma unroll
-        for (uint32_t k = 0; k < 4; ++k)
-            t[k] = *reinterpret_cast<const f32x4_t *>(src + static_cast<uint64_t>(min(g + k, g1)) * M * kFusedTile);
+            for (uint32_t k = 0; k < N; ++k)
+                t[k] = *reinterpret_cast<const f32x4_t *>(src + static_cast<uint64_t>(min(g + k, g1)) * M * kFusedTile);
 #pragma unroll
-        for (uint32_t k = 0; k < 4; ++k)
-            if (g + k <= g1) {
+            for (uint32_t k = 0; k < N; ++k)
+                if (g + k <= g1) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] += t[k][r];
-            }
-    }
+                    for (int r = 0; r < 4; ++r) v[r] += t[k][r];
+                }
+        }
+    };
+    if (g1 - g0 < 4)
+        add(std::integral_constant<uint32_t, 4>{});
+    else
+        add(std::integral_constant<uint32_t, 16>{});
 }
 
 template <int EPI>

@@ -24,9 +24,9 @@
  *    entry do not matter.  Calls that may overlap (two streams, two captured graphs that are
  *    replayed side by side) need separate workspaces.  workspace_bytes is its size;
  *    CBK_E_CAPACITY when that is too small.  A workspace may be NULL only when 0 bytes are needed.
- *  - BF16 pointers must be 2-byte aligned; the fast kernels want 16-byte aligned matrices whose
- *    leading dimension is a multiple of 8 (others are copied into the workspace first, or stored
- *    element by element).
+ *  - BF16 pointers must be 2-byte aligned.  Matrices that are 16-byte aligned with a leading
+ *    dimension that is a multiple of 8 are read and written 16 bytes at a time; others give the same
+ *    bits, more slowly.  X and dY may be copied into the workspace first.
  *  - results do not depend on timing: equal inputs give equal bits.
  *  - limits: cols <= 2^20, rows < 2^31, tokens < 2^31, leading dimensions < 2^32;
  *    CBK_E_UNSUPPORTED beyond.
