@@ -58,6 +58,7 @@ struct NnPlan {
     uint64_t pieces;
     uint32_t fused;   // 0: pieces are decoded into memory; else the token tile of k_fused
     uint32_t grid;    // k_fused: most workgroups
+    uint32_t split;   // k_fused: a launch for each tensor of the pair
     // part: the parts of tiles whose slices several workgroups share
     uint64_t pack, w, part, g, acc, stat, top;  // offsets in bytes
     uint64_t bytes;

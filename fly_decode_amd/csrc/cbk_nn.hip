@@ -782,16 +782,23 @@ __global__ __launch_bounds__(256) void k_mm_join(const MmArgs p, uint32_t sharer
 struct JoinArgs {
     const float *part;
     uint32_t count, tiles, slices, grid, up_col;  // up_col: where dU starts in G
+    uint32_t split;  // each tensor's parts by themselves, the second's after grid + tiles of the first's
 };
 
 // The sum of tile vt's parts at token m, columns c..c + 3, added to v.
 __device__ __forceinline__ void add_parts(const JoinArgs &q, uint32_t M, uint32_t vt, uint32_t m, uint32_t c, float (&v)[4]) {
+    const uint32_t runs = q.split ? 1 : q.count;  // tensors that a launch's runs go through
+    uint64_t slot = vt;
+    if (q.split && vt >= q.tiles) {
+        vt -= q.tiles;
+        slot += q.grid;
+    }
     // The workgroups whose runs hold the tile's first and last slice: run g starts at
     // floor(g * total / grid).
-    const uint64_t total = static_cast<uint64_t>(q.count * q.tiles) * q.slices, at = static_cast<uint64_t>(vt) * q.slices;
+    const uint64_t total = static_cast<uint64_t>(runs * q.tiles) * q.slices, at = static_cast<uint64_t>(vt) * q.slices;
     const uint32_t g0 = static_cast<uint32_t>(quotient((at + 1) * q.grid - 1, total));
     const uint32_t g1 = static_cast<uint32_t>(quotient((at + q.slices) * q.grid - 1, total));
-    const float *src = q.part + (static_cast<uint64_t>(vt) * M + m) * kFusedTile + c;
+    const float *src = q.part + (slot * M + m) * kFusedTile + c;
     // N loads at a time (the last part again past the end)
     auto add = [&](auto batch) {
         constexpr uint32_t N = decltype(batch)::value;
@@ -1105,7 +1112,8 @@ struct Weights {
         FusedArgs &a = r.a;
         for (uint32_t i = 0; i < count; ++i)
             a.t[i] = FusedTensor{ts[i]->words, ts[i]->codebook, cbk_words_for(ts[i]->rows * ts[i]->cols, ts[i]->b) * 4, ts[i]->U, 0};
-        a.count = count;
+        const uint32_t launches = pl.split ? 2 : 1;
+        a.count = count / launches;
         a.A = p.A;
         a.lda = p.lda;
         a.M = p.M;
@@ -1117,15 +1125,23 @@ struct Weights {
         // Even rounds of the CUs where each workgroup gets eight slices, so that the start of its pipeline is
         // paid for (a 4096 x 4096 gradient of 8 tokens: 16.7 us with 256 workgroups of eight, 19.4 with 512
         // of four, 23 with 341 of six); below that, three slices each.
-        const uint64_t total = static_cast<uint64_t>(count * a.tiles) * a.slices;
+        const uint64_t total = static_cast<uint64_t>(a.count * a.tiles) * a.slices;
         a.grid = static_cast<uint32_t>(total >= 8 * pl.grid ? pl.grid : std::max<uint64_t>(1, std::min<uint64_t>(256, total / 3)));
         a.part = at<float>(ws, pl.part);
         r.bm = pl.fused;
         r.nn = nn;
         r.s = s;
-        if (!dispatch_b<FusedRun>(static_cast<int>(ts[0]->b), r, FusedB{})) return CBK_E_UNSUPPORTED;
-        q = JoinArgs{a.part, count, a.tiles, a.slices, a.grid, static_cast<uint32_t>(up64(nrows))};
-        return r.st;
+        q = JoinArgs{a.part, count, a.tiles, a.slices, a.grid, static_cast<uint32_t>(up64(nrows)), pl.split};
+        for (uint32_t i = 0; i < launches; ++i) {
+            if (i > 0) {
+                a.t[0] = a.t[1];
+                if (nn) a.A += a.slices * 64;
+                a.part += static_cast<uint64_t>(a.grid + a.tiles) * a.M * kFusedTile;
+            }
+            if (!dispatch_b<FusedRun>(static_cast<int>(ts[i]->b), r, FusedB{})) return CBK_E_UNSUPPORTED;
+            CBK_TRY(r.st);
+        }
+        return CBK_OK;
     }
 
     template <int EPI>
@@ -1148,7 +1164,7 @@ struct Weights {
             piece[i].words += row0 * piece[i].cols / 32 * piece[i].b;  // row0 is a multiple of 128: whole 16-byte chunks
             ys[i] = at<float>(ws, pl.part) + i * tiles * kFusedTile;
         }
-        q = JoinArgs{at<float>(ws, pl.part), count, tiles, 1, 1, static_cast<uint32_t>(up64(nrows))};
+        q = JoinArgs{at<float>(ws, pl.part), count, tiles, 1, 1, static_cast<uint32_t>(up64(nrows)), 0};
         return launch_gemv_group(piece, count, p.A, ys, s);
     }
 

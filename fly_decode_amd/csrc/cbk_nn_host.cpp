@@ -71,21 +71,26 @@ namespace cbk {
 namespace {
 
 // The token tile of k_fused, or 0 where the tensors or the number of tokens are not its kind: widths
-// 8 to 14 (equal, for a pair), and a workgroup's table and ring within the LDS.  Up to 384 tokens it is
+// 8 to 14, and a workgroup's table and ring within the LDS.  Up to 384 tokens it is
 // ahead of decoding a piece first (a pair of 4096 x 11008: 49 us against 128 at 64 tokens, 129 against
 // 153 at 384, 170 in two halves against 154 at 512); short rows leave it more sums to pass on per product
 // (a pair of 384 x 11008: 37 against 34 at 256, 45 against 36 at 384; of 1024 x 11008: 55 against 52 at
-// 384, its gradient 102 against 109).
+// 384, its gradient 102 against 109).  A pair of two widths takes a launch for each
+// tensor (13 and 11 bits, 4096 x 11008: 36 us against 140 at 1 token, 56 against 134 at 64, 143 against 152
+// at 384; 512 x 11008: 30 against 39 at 64, 50 against 43 at 200).
 uint32_t fused_tile(const cbk_tensor *const *ts, uint64_t count, uint64_t tokens) {
-    if (tokens > (ts[0]->cols < 1024 ? 256 : 384)) return 0;
+    const bool split = count == 2 && ts[0]->b != ts[1]->b;
+    if (tokens > (ts[0]->cols >= 1024 ? 384 : split ? 128 : 256)) return 0;
+    uint32_t b = 0;
     for (uint64_t i = 0; i < count; ++i) {
         const cbk_tensor &t = *ts[i];
-        if (t.b < 8 || t.b > 14 || t.b != ts[0]->b || t.cols == 0 || !aligned(t.codebook, 16)) return 0;
+        if (t.b < 8 || t.b > 14 || t.cols == 0 || !aligned(t.codebook, 16)) return 0;
+        b = std::max(b, t.b);
     }
     uint32_t bm = 384;
     for (uint32_t x : {320u, 256u, 192u, 128u, 64u, 16u})
         if (tokens <= x) bm = x;
-    return nn_fused_lds(ts[0]->b, bm) <= 160 * 1024 ? bm : 0;
+    return nn_fused_lds(b, bm) <= 160 * 1024 ? bm : 0;
 }
 
 }  // namespace
@@ -125,9 +130,11 @@ NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
     // a copy of the chunk's X (or of a piece's columns of dY), padded or in blocks of 16 tokens
     p.pack = take(up_to(p.Tc, 16) * std::max(p.Kp, op == NnOp::linear ? p.Rp : 0) * 2);
     if (p.fused) {
-        // as many workgroups as the LDS lets run at once on 256 CUs, and their parts of the tiles
-        p.grid = 256 * std::min<uint32_t>(3, 160 * 1024 / nn_fused_lds(ts[0]->b, p.fused));
-        p.part = take((p.grid + pair * (std::max(p.rows + 127, p.Kp + 64) / 128)) * p.Tc * 128 * 4);
+        // as many workgroups as the LDS lets run at once on 256 CUs, and their parts of the tiles; a pair
+        // of two widths takes two launches
+        p.split = pair == 2 && ts[0]->b != ts[1]->b;
+        p.grid = 256 * std::min<uint32_t>(3, 160 * 1024 / nn_fused_lds(std::max(ts[0]->b, ts[pair - 1]->b), p.fused));
+        p.part = take(((p.split ? 2 : 1) * p.grid + pair * (std::max(p.rows + 127, p.Kp + 64) / 128)) * p.Tc * 128 * 4);
     } else {
         p.w = take(p.Rp * p.Kp * 2);
         // no more tiles are shared than the largest product of the call has

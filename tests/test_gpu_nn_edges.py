@@ -453,3 +453,16 @@ def test_one_tensor_as_gate_and_up(env, T):
     ref.assert_within(cbk.ffn_gated(d, d, x.cuda()), *ref.ffn("silu", x, w, w), "ffn_gated")
     for name, v, want in zip(("dX", "dG", "dU"), cbk.ffn_gated_bwd(d, d, x.cuda(), dh.cuda()), ref.ffn_bwd("silu", x, w, w, dh)):
         ref.assert_within(v, *want, name)
+
+
+@pytest.mark.parametrize("T", [1, 2, 16, 45, 200, 300, 384, 500])
+@pytest.mark.parametrize("rows,cols,U,V", [(515, 1088, 3000, 700), (300, 1027, 200, 9000)])
+def test_pairs_of_two_widths(env, T, rows, cols, U, V):
+    torch, cbk = env
+    wg, wu = weights(torch, rows, cols, U, 96, 0.1), weights(torch, rows, cols, V, 97, 0.1)
+    x, dh = acts(torch, T, cols, 98), acts(torch, T, rows, 99, 0.1)
+    g, u = compress(cbk, wg), compress(cbk, wu)
+    assert g.b != u.b and min(g.b, u.b) >= 8 and max(g.b, u.b) <= 14
+    ref.assert_within(cbk.ffn_gated(g, u, x.cuda()), *ref.ffn("silu", x, wg, wu), "ffn_gated")
+    for name, v, want in zip(("dX", "dG", "dU"), cbk.ffn_gated_bwd(g, u, x.cuda(), dh.cuda()), ref.ffn_bwd("silu", x, wg, wu, dh)):
+        ref.assert_within(v, *want, name)
