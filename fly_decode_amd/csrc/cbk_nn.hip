@@ -56,7 +56,7 @@ __device__ __forceinline__ float activation(int act, float z, float *D) {
     }
     // (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y)); past |z| = 16 it is 0 or 1 to every bit and z^3 might overflow
     const float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float w = fminf(fmaxf(z, -16.f), 16.f);
+    const float w = z > 16.f ? 16.f : z < -16.f ? -16.f : z;  // NaN stays NaN, where fmaxf and fminf would drop it
     const float s = 1.f / (1.f + __expf(-c * (w + 0.044715f * w * w * w)));
     if (D) *D = s + w * s * (1.f - s) * c * (1.f + 3.f * 0.044715f * w * w);
     return z * s;
