@@ -686,23 +686,28 @@ def _one_device(first, *others):
 
 
 class _Call:
-    """Device, stream, outputs and workspace of one call on the device of ``x``: allocations come
-    from torch's allocator and, where the caller names a stream of its own, are recorded on it."""
+    """Device, stream, outputs and workspace of one call on the device of ``x``.  Allocations come from
+    the pool of the stream that the call runs on: a block of another stream's pool may have been freed
+    with that stream's work on it still to run.  Where the caller names a stream of its own, outputs
+    are recorded on the current one as well, on which the caller will go on with them."""
 
-    __slots__ = ("torch", "device", "given", "stream")
+    __slots__ = ("torch", "device", "current", "stream")
 
     def __init__(self, x, stream):
         import torch
         self.torch, self.device = torch, x.device
         if self.device.type != "cuda":
             raise ValueError("the operators run on GPU tensors")
-        self.given = stream is not None
-        self.stream = stream if self.given else torch.cuda.current_stream(self.device)
+        self.current = torch.cuda.current_stream(self.device)
+        self.stream = self.current if stream is None else stream
 
-    def empty(self, shape, dtype):
-        out = self.torch.empty(shape, dtype=dtype, device=self.device)
-        if self.given:
-            out.record_stream(self.stream)
+    def empty(self, shape, dtype, scratch=False):
+        if self.stream == self.current:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.stream):
+            out = self.torch.empty(shape, dtype=dtype, device=self.device)
+        if not scratch:
+            out.record_stream(self.current)
         return out
 
     def run(self, name, sizes, workspace, *args):
@@ -711,7 +716,7 @@ class _Call:
         lib = load_library()
         if workspace is None:
             # at least one element, so that there is an address; torch's blocks are 512-byte aligned
-            workspace = self.empty((getattr(lib, sizes[0])(*sizes[1:]) or 1,), self.torch.uint8)
+            workspace = self.empty((getattr(lib, sizes[0])(*sizes[1:]) or 1,), self.torch.uint8, scratch=True)
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
         args += (workspace.data_ptr() or None, workspace.numel() * workspace.element_size(), self.stream.cuda_stream)
@@ -726,7 +731,9 @@ class _Call:
 def linear(t: Compressed, X, out=None, workspace=None, stream=None):
     """out[tokens][rows] (bfloat16) = X . W^T for a bfloat16 X[tokens][cols], any number of tokens
     (row strides may exceed the widths).  ``workspace``: a uint8 device tensor of at least
-    ``linear_workspace_bytes(t, tokens)`` bytes; allocated when not given."""
+    ``linear_workspace_bytes(t, tokens)`` bytes; allocated when not given.  ``stream``: the torch
+    stream to run on (default: the current one); the caller orders it behind the work that makes the
+    inputs, and keeps them until it has run."""
     xp, ldx = _tokens(X, t.cols, "X")
     _one_device(X, t.words, t.codebook, out)
     call, T = _Call(X, stream), X.shape[0]
