@@ -700,6 +700,8 @@ class _Call:
             raise ValueError("the operators run on GPU tensors")
         self.current = torch.cuda.current_stream(self.device)
         self.stream = self.current if stream is None else stream
+        if self.stream.device != self.device:
+            raise ValueError(f"the stream is on {self.stream.device}, the arguments on {self.device}")
 
     def empty(self, shape, dtype, scratch=False):
         if self.stream == self.current:

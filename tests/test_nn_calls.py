@@ -63,3 +63,9 @@ def test_outputs_are_kept_for_the_current_stream_too(streams):
     current, other = streams
     assert call_on(other).empty((4,), torch.uint8).recorded == [current]
     assert call_on(None).empty((4,), torch.uint8).recorded == []
+
+
+def test_a_stream_of_another_device_is_refused(streams):
+    elsewhere = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=48)
+    with pytest.raises(ValueError, match="stream"):
+        call_on(elsewhere)
