@@ -68,6 +68,8 @@ NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens);
 // Most tiles whose slices the workgroups of k_mm share, of 256 x 256 sums each.
 constexpr uint32_t kMmShared = 160;
 uint32_t nn_fused_lds(uint32_t b, uint32_t bm);
+// Whether rows [row0, row0 + nrows) of a tensor can be decoded in the stream's own order (k_unpack).
+bool nn_unpack_in_order(const cbk_tensor &t, uint64_t row0, uint64_t nrows);
 
 cbk_status launch_linear(const cbk_tensor &t, const uint16_t *X, uint64_t ldx, uint64_t T, uint16_t *Y, uint64_t ldy,
                          void *ws, hipStream_t s);

@@ -224,8 +224,8 @@ __global__ __launch_bounds__(64 * kUnpackWaves) void k_unpack(const UnpackArgs a
                 (u32x4){w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16)};
         }
         asm volatile("" ::: "memory");
-        // Row and column of field i of the piece: with at most 2^15 rows the product with the
-        // rounded reciprocal is off by less than 2^15 * 2^-22, so one step mends the row.
+        // Row and column of field i of the piece (nn_unpack_in_order): with at most 2^15 rows the product with
+        // the rounded reciprocal, of three roundings, is off by less than 2^15 * 2^-22, so one step mends the row.
         auto place = [&](uint32_t i) {
             uint32_t r = static_cast<uint32_t>(static_cast<float>(i) * a.inv_cols);
             int32_t k = static_cast<int32_t>(i - r * a.cols);
@@ -951,12 +951,11 @@ cbk_status unpack(const cbk_tensor *const *ts, uint32_t count, uint64_t row0, ui
     r.a.pair = count == 2 ? 2 : 0;
     r.a.out = out;
     r.a.inv_cols = 1.f / static_cast<float>(std::max(1u, r.a.cols));
-    bool fast = r.a.cols > 0 && row0 * r.a.cols % 128 == 0 && nrows <= 32768 && nrows * r.a.cols < (uint64_t(1) << 27);
+    bool fast = true;
     for (uint32_t i = 0; i < count; ++i) {
         const cbk_tensor &t = *ts[i];
-        const uint64_t chunks = cbk_words_for(t.rows * t.cols, t.b) / 4;
-        r.a.t[i] = UnpackTensor{t.words, t.codebook, t.U, static_cast<uint32_t>(chunks)};
-        fast = fast && t.b >= 1 && t.b <= 15 && aligned_to(t.codebook, 16) && chunks < (uint64_t(1) << 32);
+        r.a.t[i] = UnpackTensor{t.words, t.codebook, t.U, static_cast<uint32_t>(cbk_words_for(t.rows * t.cols, t.b) / 4)};
+        fast = fast && nn_unpack_in_order(t, row0, nrows);
     }
     if (fast) {
         const bool together = count == 1 || ts[0]->b == ts[1]->b;

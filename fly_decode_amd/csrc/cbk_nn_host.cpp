@@ -99,13 +99,26 @@ uint32_t fused_tile(const cbk_tensor *const *ts, uint64_t count, uint64_t tokens
 // 256 tokens).
 uint32_t nn_fused_lds(uint32_t b, uint32_t bm) { return (2u << b) + (bm <= 256 ? 3 : 2) * 128 * (bm + 128); }
 
+namespace {
+constexpr uint64_t kPieceBytes = uint64_t(256) << 20;
+constexpr uint64_t kPieceRows = 32768;
+constexpr uint64_t kPieceLeast = 256;  // rows, whatever they take
+}  // namespace
+
+// Widths 1 to 15 with the table's loads aligned.  Every piece of nn_plan starts on a multiple of 128 weights and
+// holds at most 2^15 rows and 2^28 weights, which is what k_unpack's 32-bit fields and its rows by a
+// reciprocal take (512 tokens and a piece of 2^27 weights, 32768 x 4096: 214 us, 396 by the generic kernel).
+bool nn_unpack_in_order(const cbk_tensor &t, uint64_t row0, uint64_t nrows) {
+    constexpr uint64_t kMost = std::max(kPieceBytes / 2, kPieceLeast * kMaxCols);
+    return t.b >= 1 && t.b <= 15 && aligned(t.codebook, 16) && cbk_words_for(t.rows * t.cols, t.b) / 4 < (uint64_t(1) << 32) &&
+           t.cols > 0 && row0 * t.cols % 128 == 0 && nrows <= kPieceRows && nrows * t.cols <= kMost;
+}
+
 // A decoded piece takes up to kPieceBytes and kPieceRows, and the sums of a piece's rows for a chunk of
 // tokens (k_fused) up to kSumBytes, so that a call's scratch stays far below the tensor's uncompressed
 // size and no call keeps what grows with tokens times rows; chunks of kChunk tokens bound what is
 // kept per token.
 NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
-    constexpr uint64_t kPieceBytes = uint64_t(256) << 20;
-    constexpr uint64_t kPieceRows = 32768;
     constexpr uint64_t kSumBytes = uint64_t(64) << 20;
     constexpr uint64_t kChunk = 8192;
     const uint64_t rows = ts[0]->rows, cols = ts[0]->cols;
@@ -116,7 +129,7 @@ NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens) {
     p.Tc = std::min(tokens, kChunk);
     p.fused = fused_tile(ts, pair, tokens);
     const uint64_t total = up_to(pair * up_to(rows, 16), 256);
-    const uint64_t most = p.fused ? std::max<uint64_t>(256, kSumBytes / (4 * p.Tc) / 256 * 256) : std::min(kPieceRows, std::max<uint64_t>(256, kPieceBytes / (2 * p.Kp) / 256 * 256));
+    const uint64_t most = p.fused ? std::max<uint64_t>(256, kSumBytes / (4 * p.Tc) / 256 * 256) : std::min(kPieceRows, std::max<uint64_t>(kPieceLeast, kPieceBytes / (2 * p.Kp) / 256 * 256));
     p.pieces = (total + most - 1) / most;
     p.Rp = up_to((total + p.pieces - 1) / p.pieces, 256);
     p.rows = p.Rp / pair;
