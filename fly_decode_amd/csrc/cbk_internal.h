@@ -67,7 +67,12 @@ enum class NnOp { linear, ffn, xent };
 NnPlan nn_plan(NnOp op, const cbk_tensor *const *ts, uint64_t tokens);
 // Most tiles whose slices the workgroups of k_mm share, of 256 x 256 sums each.
 constexpr uint32_t kMmShared = 160;
-uint32_t nn_fused_lds(uint32_t b, uint32_t bm);
+// Slices in k_fused's ring, and a workgroup's LDS: the table, and the slices of the tokens and of the weights.  A
+// ring of three where the LDS has room for it (not past 256 tokens, nor with 193 to 256 and 14 bits), else two
+// (200 tokens, 14 bits, 11008 x 4096: 51 us, 103 if the tensor is decoded first; 192 tokens and three 45).
+constexpr uint32_t nn_ring_lds(uint32_t b, uint32_t bm, uint32_t ring) { return (2u << b) + ring * 128 * (bm + 128); }
+constexpr uint32_t nn_fused_ring(uint32_t b, uint32_t bm) { return nn_ring_lds(b, bm, 3) <= 160 * 1024 ? 3 : 2; }
+constexpr uint32_t nn_fused_lds(uint32_t b, uint32_t bm) { return nn_ring_lds(b, bm, nn_fused_ring(b, bm)); }
 // Whether rows [row0, row0 + nrows) of a tensor can be decoded in the stream's own order (k_unpack).
 bool nn_unpack_in_order(const cbk_tensor &t, uint64_t row0, uint64_t nrows);
 

@@ -20,7 +20,7 @@
 // dwords are loaded two slices before they are decoded.
 //
 // The weights are decoded, and the tokens' part of the slice copied straight into LDS, two slices ahead of
-// the product, into a ring of three buffers (fused_ring).  In a slice's interval a wave reads the second half of this
+// the product, into a ring of three buffers (or one slice ahead, into a ring of two: nn_fused_ring).  In a slice's interval a wave reads the second half of this
 // slice's fragments and the first half of the next one's while it multiplies the halves it has, and decodes
 // its tasks (LDS gathers) in between: one barrier an interval, and no wait on anything asked for in it.
 // LDS layouts: rows of 128 bytes (64 reduction elements) hold chunk c of row r in slot c ^ (r & 7), the
@@ -41,13 +41,12 @@
 namespace cbk {
 namespace {
 
-// Slices in LDS.  Past 256 tokens three do not fit; two are decoded and copied one slice ahead, and an
-// interval starts by reading its own fragments.
-constexpr uint32_t fused_ring(int BM) { return BM <= 256 ? 3 : 2; }
-
+// LDS of a workgroup.  With a ring of three, slices are decoded and copied two ahead of the product; with two,
+// one ahead, and an interval starts by reading its own fragments.
 template <int B, int BM>
 constexpr uint32_t fused_lds() {
-    return Table<B>::SIZE * 2 + fused_ring(BM) * (BM + kFusedTile) * 128;
+    static_assert(Table<B>::SIZE * 2 == (2u << B) && nn_fused_lds(B, BM) <= kLdsLimit, "the LDS that the plan counts with");
+    return nn_fused_lds(B, BM);
 }
 
 // Dwords of a task of 16 fields, wherever it may start: with RAG anywhere, else on a dword or half-way.
@@ -163,7 +162,7 @@ __global__ __launch_bounds__(512) void k_fused(const FusedArgs p) {
     constexpr int DW = task_dwords<B, RAG>(), NL = (DW + 3) / 4;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     uint16_t *table = reinterpret_cast<uint16_t *>(smem);
-    constexpr uint32_t RING = fused_ring(BM), AHEAD = RING - 1;
+    constexpr uint32_t RING = nn_fused_ring(B, BM), AHEAD = RING - 1;
     unsigned char *ring = smem + Table<B>::SIZE * 2;  // slices: the tokens' part, then the weights'
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t li = lane & 15, lg = lane >> 4;

@@ -71,7 +71,7 @@ namespace cbk {
 namespace {
 
 // The token tile of k_fused, or 0 where the tensors or the number of tokens are not its kind: widths
-// 8 to 14, and a workgroup's table and ring within the LDS.  Up to 384 tokens it is
+// 8 to 14, whose table and ring the LDS holds at every tile.  Up to 384 tokens it is
 // ahead of decoding a piece first (a pair of 4096 x 11008: 49 us against 128 at 64 tokens, 129 against
 // 153 at 384, 170 in two halves against 154 at 512); short rows leave it more sums to pass on per product
 // (a pair of 384 x 11008: 37 against 34 at 256, 45 against 36 at 384; of 1024 x 11008: 55 against 52 at
@@ -81,23 +81,17 @@ namespace {
 uint32_t fused_tile(const cbk_tensor *const *ts, uint64_t count, uint64_t tokens) {
     const bool split = count == 2 && ts[0]->b != ts[1]->b;
     if (tokens > (ts[0]->cols >= 1024 ? 384 : split ? 128 : 256)) return 0;
-    uint32_t b = 0;
     for (uint64_t i = 0; i < count; ++i) {
         const cbk_tensor &t = *ts[i];
         if (t.b < 8 || t.b > 14 || t.cols == 0 || !aligned(t.codebook, 16)) return 0;
-        b = std::max(b, t.b);
     }
     uint32_t bm = 384;
     for (uint32_t x : {320u, 256u, 192u, 128u, 64u, 16u})
         if (tokens <= x) bm = x;
-    return nn_fused_lds(b, bm) <= 160 * 1024 ? bm : 0;
+    return bm;
 }
 
 }  // namespace
-
-// LDS of a workgroup of k_fused: a table, and three slices of the tokens and of the weights (two past
-// 256 tokens).
-uint32_t nn_fused_lds(uint32_t b, uint32_t bm) { return (2u << b) + (bm <= 256 ? 3 : 2) * 128 * (bm + 128); }
 
 namespace {
 constexpr uint64_t kPieceBytes = uint64_t(256) << 20;

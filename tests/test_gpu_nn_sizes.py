@@ -37,3 +37,59 @@ def test_a_piece_of_the_most_weights(env, rows, cols):
     rows_of = torch.empty(at.numel(), dtype=torch.long).scatter_(0, first, torch.arange(first.numel()))
     dx = cbk.linear_dx(t, dy.cuda())
     ref.assert_within(dx, *ref.linear_dx(dy[:, at], part[rows_of]), "linear_dx")
+
+
+def of_width(torch, rows, cols, b, seed):
+    """BF16 weights whose index width is b (at most 15): as many finite patterns as it holds, less three,
+    of falling exponents from 2^-4 on (2^-1 for 15 bits, whose patterns end at 32000); each occurs."""
+    U = min(32000, max((1 << (b - 1)) + 1, (1 << b) - 3))
+    top = 123 if b < 15 else 126
+    i = torch.arange(U)
+    patterns = (i & 1) << 15 | (top - (i >> 8)) << 7 | (i >> 1) & 127
+    values = torch.where(patterns >= 1 << 15, patterns - (1 << 16), patterns).short().view(torch.bfloat16)
+    g = torch.Generator().manual_seed(seed)
+    w = values[torch.randint(0, U, (rows * cols,), generator=g)]
+    w[torch.randperm(rows * cols, generator=g)[:U]] = values
+    return w.reshape(rows, cols)
+
+
+def every_operator(env, T, w, v, seed):
+    """Each operator on W (and the pair W, V) against the reference."""
+    torch, cbk = env
+    rows, cols = w.shape
+    a, b = compress(cbk, w), compress(cbk, v)
+    x, dy = acts(torch, T, cols, seed), acts(torch, T, rows, seed + 1, 0.1)
+    ref.assert_within(cbk.linear(a, x.cuda()), *ref.linear(x, w), "linear")
+    ref.assert_within(cbk.linear_dx(a, dy.cuda()), *ref.linear_dx(dy, w), "linear_dx")
+    ref.assert_within(cbk.ffn_gated(a, b, x.cuda()), *ref.ffn("silu", x, w, v), "ffn_gated")
+    for name, got, want in zip(("dX", "dG", "dU"), cbk.ffn_gated_bwd(a, b, x.cuda(), dy.cuda()), ref.ffn_bwd("silu", x, w, v, dy)):
+        ref.assert_within(got, *want, name)
+    labels = torch.randint(0, rows, (T,), generator=torch.Generator().manual_seed(seed + 2))
+    loss, lse = cbk.xent(a, x.cuda(), labels.cuda())
+    (want, bound), (wl, bl) = ref.xent(x, w, labels, -100)
+    ref.assert_within(loss, want, bound, "loss")
+    ref.assert_within(lse, wl, bl, "lse")
+    dx = cbk.xent_bwd(a, x.cuda(), labels.cuda(), lse, torch.ones(T).cuda())
+    ref.assert_within(dx, *ref.xent_bwd(x, w, labels, torch.ones(T), -100), "dX of the head")
+    return a, b
+
+
+@pytest.mark.parametrize("T", [192, 193, 224, 255, 256, 257])
+@pytest.mark.parametrize("rows,cols", [(700, 1088), (515, 1027), (260, 320)])
+def test_14_bits_around_256_tokens(env, T, rows, cols):
+    """The widest table beside the token tiles of 192, 256 and 320: rings of three and of two slices."""
+    torch, _ = env
+    a, b = every_operator(env, T, of_width(torch, rows, cols, 14, 124), of_width(torch, rows, cols, 14, 125), 126)
+    assert a.b == 14 and b.b == 14
+
+
+@pytest.mark.parametrize("b", range(1, 16))
+@pytest.mark.parametrize("T", [1, 13, 45, 100, 192, 300, 400])
+@pytest.mark.parametrize("rows,cols", [(515, 1088), (300, 1027)])
+def test_every_width(env, T, rows, cols, b):
+    """Whole units a row and ragged rows, at each token tile; the pair's second tensor is narrower by one bit
+    at odd numbers of tokens."""
+    torch, _ = env
+    second = b - 1 if T % 2 and b > 1 else b
+    a, c = every_operator(env, T, of_width(torch, rows, cols, b, 130), of_width(torch, rows, cols, second, 131), 132)
+    assert a.b == b and c.b == second

@@ -45,3 +45,13 @@ def test_every_piece_is_decoded_in_the_streams_order(plans):
              for b, b2 in ((1, 15), (13, 13)) for tokens in (385, 2048)]
     for case, p in zip(cases, plans(cases)):
         assert p.fused == 0 and p.in_order == 1, (case, p)
+
+
+def test_up_to_384_tokens_are_decoded_on_the_way(plans):
+    """Widths 8 to 14: every number of tokens up to the limit that the row length and the pair's widths give."""
+    cases = [(op, 4096, cols, b, b2, tokens)
+             for b in range(8, 15) for op, b2 in ((LINEAR, b), (HEAD, b), (BLOCK, b), (BLOCK, 8 if b > 8 else 9))
+             for cols, most in ((4096, 384), (1023, 128 if op == BLOCK and b != b2 else 256))
+             for tokens in range(1, most + 1)]
+    for case, p in zip(cases, plans(cases)):
+        assert p.fused >= case[5] and p.grid >= 256, (case, p)
