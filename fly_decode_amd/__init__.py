@@ -640,7 +640,8 @@ def ec_gemv_group(ts, x, ys=None, stream=None, indexes=None):
     return ys
 
 
-# ---- operators on any number of tokens, and their gradients (include/cbk_nn.h)
+# ---- operators on any number of tokens, and their gradients (include/cbk_nn.h).  They record no graph: each
+# gradient is a call of its own.
 
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
@@ -679,10 +680,18 @@ def _vector(x, n, dtype, name):
     return x.data_ptr() or None
 
 
-def _one_device(first, *others):
-    for x in others:
-        if x is not None and x.device != first.device:
+def _arguments(first, *others):
+    """Checks that the tensors (None: not given) are on one device and ask for no gradient: the operators
+    record no graph."""
+    import torch
+    for x in (first, *others):
+        if x is None:
+            continue
+        if x.device != first.device:
             raise ValueError(f"the arguments are on {first.device} and {x.device}")
+        if x.requires_grad and torch.is_grad_enabled():
+            raise ValueError("an argument requires a gradient, and the operators record no graph: call them under "
+                             "torch.no_grad(), or from a torch.autograd.Function with the gradient's call")
 
 
 class _Call:
@@ -737,7 +746,7 @@ def linear(t: Compressed, X, out=None, workspace=None, stream=None):
     stream to run on (default: the current one); the caller orders it behind the work that makes the
     inputs, and keeps them until it has run."""
     xp, ldx = _tokens(X, t.cols, "X")
-    _one_device(X, t.words, t.codebook, out)
+    _arguments(X, t.words, t.codebook, out)
     call, T = _Call(X, stream), X.shape[0]
     if out is None:
         out = call.empty((T, t.rows), X.dtype)
@@ -753,7 +762,7 @@ def linear_dx(t: Compressed, dY, out=None, workspace=None, stream=None):
     """The gradient of ``linear``'s X: out[tokens][cols] (bfloat16) = dY . W for a bfloat16
     dY[tokens][rows]."""
     gp, ldg = _tokens(dY, t.rows, "dY")
-    _one_device(dY, t.words, t.codebook, out)
+    _arguments(dY, t.words, t.codebook, out)
     call, T = _Call(dY, stream), dY.shape[0]
     if out is None:
         out = call.empty((T, t.cols), dY.dtype)
@@ -773,7 +782,7 @@ def ffn_gated(gate: Compressed, up: Compressed, X, act: str = "silu", out=None, 
     if (gate.rows, gate.cols) != (up.rows, up.cols):
         raise ValueError("gate and up must have the same shape")
     xp, ldx = _tokens(X, gate.cols, "X")
-    _one_device(X, gate.words, gate.codebook, up.words, up.codebook, out)
+    _arguments(X, gate.words, gate.codebook, up.words, up.codebook, out)
     call, T = _Call(X, stream), X.shape[0]
     if out is None:
         out = call.empty((T, gate.rows), X.dtype)
@@ -799,7 +808,7 @@ def ffn_gated_bwd(gate: Compressed, up: Compressed, X, dH, act: str = "silu", dX
     T = X.shape[0]
     if dH.shape[0] != T or (dX is not None and dX.shape[0] != T):
         raise ValueError("X, dH and dX differ in tokens")
-    _one_device(X, dH, gate.words, gate.codebook, up.words, up.codebook, dX)
+    _arguments(X, dH, gate.words, gate.codebook, up.words, up.codebook, dX)
     call = _Call(X, stream)
     if dX is None:
         dX = call.empty((T, gate.cols), X.dtype)
@@ -821,7 +830,7 @@ def xent(head: Compressed, X, labels, ignore_index: int = -100, workspace=None, 
     xp, ldx = _tokens(X, head.cols, "X")
     T = X.shape[0]
     lp = _vector(labels, T, torch.int64, "labels")
-    _one_device(X, labels, head.words, head.codebook)
+    _arguments(X, labels, head.words, head.codebook)
     call = _Call(X, stream)
     loss, lse = call.empty((T,), torch.float32), call.empty((T,), torch.float32)
     hs = ctypes.byref(head._struct())
@@ -838,7 +847,7 @@ def xent_bwd(head: Compressed, X, labels, lse, dloss, ignore_index: int = -100, 
     lp = _vector(labels, T, torch.int64, "labels")
     sp = _vector(lse, T, torch.float32, "lse")
     dp = _vector(dloss, T, torch.float32, "dloss")
-    _one_device(X, labels, lse, dloss, head.words, head.codebook, out)
+    _arguments(X, labels, lse, dloss, head.words, head.codebook, out)
     call = _Call(X, stream)
     if out is None:
         out = call.empty((T, head.cols), X.dtype)

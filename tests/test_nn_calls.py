@@ -69,3 +69,35 @@ def test_a_stream_of_another_device_is_refused(streams):
     elsewhere = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=48)
     with pytest.raises(ValueError, match="stream"):
         call_on(elsewhere)
+
+
+def host_tensor(cbk):
+    import numpy as np
+    c = cbk.encode(np.arange(64 * 8, dtype=np.uint16).reshape(8, 64))
+    return c.to("cpu")
+
+
+@pytest.mark.parametrize("name", ["linear", "linear_dx", "ffn_gated", "ffn_gated_bwd", "xent", "xent_bwd"])
+def test_tensors_that_ask_for_a_gradient_are_refused(name):
+    """The results carry no graph, so a tensor whose gradient autograd is to compute is refused where autograd
+    records, and taken under no_grad (the next check, for GPU tensors, is reached)."""
+    import fly_decode_amd as cbk
+    t = host_tensor(cbk)
+
+    def call(wants):
+        x, dy = (torch.zeros(3, n, dtype=torch.bfloat16) for n in (64, 8))
+        labels, lse, dloss = torch.zeros(3, dtype=torch.int64), torch.zeros(3), torch.zeros(3)
+        named = {"X": x, "dY": dy, "lse": lse, "dloss": dloss}
+        named[wants].requires_grad_()
+        return {"linear": lambda: cbk.linear(t, x), "linear_dx": lambda: cbk.linear_dx(t, dy),
+                "ffn_gated": lambda: cbk.ffn_gated(t, t, x), "ffn_gated_bwd": lambda: cbk.ffn_gated_bwd(t, t, x, dy),
+                "xent": lambda: cbk.xent(t, x, labels),
+                "xent_bwd": lambda: cbk.xent_bwd(t, x, labels, lse, dloss)}[name]()
+
+    takes = {"linear": ["X"], "linear_dx": ["dY"], "ffn_gated": ["X"], "ffn_gated_bwd": ["X", "dY"], "xent": ["X"],
+             "xent_bwd": ["X", "lse", "dloss"]}[name]
+    for wants in takes:
+        with pytest.raises(ValueError, match="no_grad"):
+            call(wants)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+            call(wants)
