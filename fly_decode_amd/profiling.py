@@ -9,7 +9,8 @@ benchmark calls them (``bench.py --summarize-trace`` and ``--summarize-traffic``
 * ``summarize_traffic``: HBM bytes per dispatch of one kernel from two ``--pmc`` runs (``FETCH_SIZE``,
   then ``WRITE_SIZE``), each scaled by what the same counter reads for a plain device-to-device copy
   of known size (``bench.py --copy-calibration``).  The JSON records the SHA-256 of the kernel
-  source it was measured on; ``traffic_for`` returns the figure only while that source is unchanged.
+  source and the device helpers it was measured on; ``traffic_for`` returns the figure only while
+  they are unchanged.
 """
 from __future__ import annotations
 
@@ -22,25 +23,38 @@ import statistics
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "fly_decode_amd", "csrc")
-KERNEL_SOURCE = os.path.join(CSRC, "cbk_kernels.hip")
 ENCODER_SOURCE = os.path.join(CSRC, "cbk_encode.hip")
 EC_SOURCE = os.path.join(CSRC, "cbk_ec.hip")
 PROFILES = os.path.join(ROOT, "profiles")
 
 
-def source_for(kernel: str) -> str:
-    """The source file that defines a kernel: the GPU encoder's are named k_enc_*, the entropy-coded
-    format's k_ec_*, the rest live in cbk_kernels.hip."""
+def sources_for(kernel: str):
+    """The files whose text fixes a kernel's code, the one that defines it first: the GPU encoder's kernels
+    are named k_enc_*, the entropy-coded format's k_ec_*; those on codebook-compressed tensors share the
+    device helpers of cbk_device.h."""
     if kernel.startswith("k_enc"):
-        return ENCODER_SOURCE
+        return [ENCODER_SOURCE]
     if kernel.startswith("k_ec"):
-        return EC_SOURCE
-    return KERNEL_SOURCE
+        return [EC_SOURCE]
+    names = ["cbk_kernels.hip"]
+    if kernel.startswith("k_fused"):
+        names = ["cbk_nn_fused.h", "cbk_nn_device.h"]
+    elif kernel.startswith(("k_mm", "k_join", "k_unpack", "k_pack_rows", "k_pad_rows", "k_zero_rows", "k_xent")):
+        names = ["cbk_nn.hip", "cbk_nn_device.h"]
+    return [os.path.join(CSRC, name) for name in names + ["cbk_device.h"]]
+
+
+def source_for(kernel: str) -> str:
+    """The source file that defines a kernel."""
+    return sources_for(kernel)[0]
 
 
 def kernel_source_sha256(kernel: str = "") -> str:
-    with open(source_for(kernel), "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()
+    h = hashlib.sha256()
+    for path in sources_for(kernel):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
 
 
 def _short_name(name: str) -> str:
