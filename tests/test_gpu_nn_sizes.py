@@ -93,3 +93,32 @@ def test_every_width(env, T, rows, cols, b):
     second = b - 1 if T % 2 and b > 1 else b
     a, c = every_operator(env, T, of_width(torch, rows, cols, b, 130), of_width(torch, rows, cols, second, 131), 132)
     assert a.b == b and c.b == second
+
+
+@pytest.mark.parametrize("T,rows,cols,b,second", [(256, 40000, 64, 11, 11), (300, 30000, 1088, 12, 12), (128, 70000, 64, 11, 9)])
+def test_a_block_decoded_on_the_way_in_pieces(env, T, rows, cols, b, second):
+    """More rows than one piece's sums are kept for, one launch a pair and one a tensor."""
+    torch, cbk = env
+    wg, wu = of_width(torch, rows, cols, b, 141), of_width(torch, rows, cols, second, 142)
+    x, dh = acts(torch, T, cols, 143), acts(torch, T, rows, 144, 0.1)
+    g, u = compress(cbk, wg), compress(cbk, wu)
+    assert (g.b, u.b) == (b, second)
+    ref.assert_within(cbk.ffn_gated(g, u, x.cuda()), *ref.ffn("silu", x, wg, wu), "ffn_gated")
+    for name, got, want in zip(("dX", "dG", "dU"), cbk.ffn_gated_bwd(g, u, x.cuda(), dh.cuda()), ref.ffn_bwd("silu", x, wg, wu, dh)):
+        ref.assert_within(got, *want, name)
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh"])
+@pytest.mark.parametrize("T", [300, 400, 600])
+@pytest.mark.parametrize("b", [8, 11, 13, 14])
+def test_activations_with_many_tokens(env, T, b, act):
+    torch, cbk = env
+    rows, cols = 515, 1088
+    wg, wu = of_width(torch, rows, cols, b, 145), of_width(torch, rows, cols, b, 146)
+    x, dh = acts(torch, T, cols, 147), acts(torch, T, rows, 148, 0.1)
+    g, u = compress(cbk, wg), compress(cbk, wu)
+    assert g.b == b == u.b
+    ref.assert_within(cbk.ffn_gated(g, u, x.cuda(), act=act), *ref.ffn(act, x, wg, wu), "ffn_gated")
+    got = cbk.ffn_gated_bwd(g, u, x.cuda(), dh.cuda(), act=act)
+    for name, v, want in zip(("dX", "dG", "dU"), got, ref.ffn_bwd(act, x, wg, wu, dh)):
+        ref.assert_within(v, *want, name)
