@@ -667,8 +667,8 @@ def _tokens(x, cols, name):
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != cols or (cols > 1 and x.shape[0] > 0 and x.stride(1) != 1):
         raise ValueError(f"{name} must be a [tokens][{cols}] bfloat16 matrix with unit column stride")
     rows, ld = x.shape[0], x.stride(0)
-    if rows <= 1:  # a single row's stride means nothing
-        ld = max(ld, cols)
+    if rows <= 1:  # a single row's stride means nothing: whole 16-byte pieces
+        ld = (cols + 7) // 8 * 8
     elif ld < cols:
         raise ValueError(f"the rows of {name} overlap")
     return x.data_ptr() or None, ld

@@ -101,3 +101,15 @@ def test_tensors_that_ask_for_a_gradient_are_refused(name):
             call(wants)
         with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
             call(wants)
+
+
+def test_the_stride_of_a_single_row_means_nothing():
+    """One row, or none, of a view whose row stride is past the limit on leading dimensions, or below the width."""
+    import fly_decode_amd as cbk
+    x = torch.zeros(64, dtype=torch.bfloat16)
+    for stride in (0, 1, 64, 1 << 33):
+        for rows in (0, 1):
+            _, ld = cbk._tokens(x.as_strided((rows, 64), (stride, 1)), 64, "X")
+            assert 64 <= ld < 1 << 32
+    with pytest.raises(ValueError, match="overlap"):
+        cbk._tokens(x.as_strided((2, 32), (16, 1)), 32, "X")
