@@ -406,11 +406,16 @@ __device__ __forceinline__ void emit_gated_bwd(const MmArgs &p, uint32_t m, uint
     if (have && p.dG) store4(p.dG + m * p.ldg + f, dg, have, p.vec);
     if (have && p.dU) store4(p.dU + m * p.ldg + f, du, have, p.vec);
 }
+// A label's column in the piece, unsigned: labels before the piece, and those that are none, whatever they
+// hold, wrap past every column.
+__device__ __forceinline__ uint64_t label_column(const MmArgs &p, uint32_t m) {
+    return static_cast<uint64_t>(p.labels[m]) - p.f0;
+}
 // exp(z - lse) - [label], the columns of the next product's reduction (zeros past the piece).
-__device__ __forceinline__ void prob(const MmArgs &p, uint32_t n, int64_t lab, float lse, const float (&z)[4], float (&v)[4]) {
+__device__ __forceinline__ void prob(const MmArgs &p, uint32_t n, uint64_t lab, float lse, const float (&z)[4], float (&v)[4]) {
 #pragma unroll
     for (uint32_t r = 0; r < 4; ++r)
-        v[r] = n + r < p.N ? __expf(z[r] - lse) - (static_cast<int64_t>(n + r) == lab ? 1.f : 0.f) : 0.f;
+        v[r] = n + r < p.N ? __expf(z[r] - lse) - (n + r == lab ? 1.f : 0.f) : 0.f;
 }
 
 // Eight values to out[0..7], of which `n` exist.
@@ -640,7 +645,7 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
             const uint32_t m = mw + 16 * i;
             if (m >= p.M) continue;
             uint16_t *row = st + (m - m0) * LDW;
-            const int64_t lab = EPI == kProb ? p.labels[m] - p.f0 : 0;
+            const uint64_t lab = EPI == kProb ? label_column(p, m) : 0;
             const float lse = EPI == kProb ? p.lse[m] : 0.f;
 #pragma unroll
             for (int j = 0; j < FN; j += EPI == kGated || EPI == kGatedBwd ? 2 : 1) {
@@ -706,8 +711,8 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const uint32_t m = mw + 16 * i;
-            int64_t lab = -1;
-            if (m < p.M) lab = p.labels[m] - p.f0;  // the label's column in this piece, if it is one
+            uint64_t lab = ~uint64_t(0);
+            if (m < p.M) lab = label_column(p, m);
             float mx = -__builtin_inff();
 #pragma unroll
             for (int j = 0; j < FN; ++j)
@@ -725,7 +730,7 @@ __global__ __launch_bounds__(64 * kMmWm * kMmWn, 2) void k_mm(const MmArgs p) {
                     const uint32_t n = nw + 16 * j + r;
                     if (n < p.N) {
                         s += __expf(acc[i][j][r] - base);
-                        if (static_cast<int64_t>(n) == lab) p.top[m] = acc[i][j][r];
+                        if (n == lab) p.top[m] = acc[i][j][r];
                     }
                 }
             s += __shfl_xor(s, 16, 64);
@@ -844,10 +849,10 @@ __global__ __launch_bounds__(256) void k_join(const MmArgs p, const JoinArgs q) 
         if (n < q.up_col) emit_gated_bwd(p, m, p.f0 + n, n, q.up_col + n, v, u);
     } else if constexpr (EPI == kProb) {
         float x[4];
-        prob(p, n, p.labels[m] - p.f0, p.lse[m], v, x);
+        prob(p, n, label_column(p, m), p.lse[m], v, x);
         store4(p.G + static_cast<uint64_t>(m) * p.ldG + n, x, 4, true);
     } else {
-        const int64_t lab = p.labels[m] - p.f0;
+        const uint64_t lab = label_column(p, m);
         float mx = -__builtin_inff(), s = 0.f;
 #pragma unroll
         for (uint32_t r = 0; r < 4; ++r)
@@ -859,7 +864,7 @@ __global__ __launch_bounds__(256) void k_join(const MmArgs p, const JoinArgs q) 
         for (uint32_t r = 0; r < 4; ++r)
             if (n + r < p.N) {
                 s += __expf(v[r] - base);
-                if (static_cast<int64_t>(n + r) == lab) p.top[m] = v[r];
+                if (n + r == lab) p.top[m] = v[r];
             }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);

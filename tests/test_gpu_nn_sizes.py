@@ -122,3 +122,22 @@ def test_activations_with_many_tokens(env, T, b, act):
     got = cbk.ffn_gated_bwd(g, u, x.cuda(), dh.cuda(), act=act)
     for name, v, want in zip(("dX", "dG", "dU"), got, ref.ffn_bwd(act, x, wg, wu, dh)):
         ref.assert_within(v, *want, name)
+
+
+@pytest.mark.parametrize("T,rows", [(200, 90000), (400, 40000)])
+def test_labels_of_every_piece_and_of_none(env, T, rows):
+    """A head in several pieces: first and last labels of the head, and the least and largest of all integers."""
+    torch, cbk = env
+    cols = 64
+    w, x = of_width(torch, rows, cols, 10, 151), acts(torch, T, cols, 152)
+    labels = torch.arange(T) * 1000003 % rows
+    labels[0], labels[1], labels[2], labels[3], labels[4] = 0, rows - 1, rows // 2, -(1 << 63), (1 << 63) - 1
+    none = torch.zeros(T, dtype=torch.bool)
+    none[3:5] = True
+    a = compress(cbk, w)
+    loss, lse = (t.cpu() for t in cbk.xent(a, x.cuda(), labels.cuda()))
+    dx = cbk.xent_bwd(a, x.cuda(), labels.cuda(), lse.cuda(), torch.ones(T).cuda()).cpu()
+    assert bool(torch.isnan(loss[none]).all()) and bool(torch.isnan(dx[none]).all()) and bool(torch.isfinite(lse).all())
+    x, labels = x[~none], labels[~none]
+    ref.assert_within(loss[~none], *ref.xent(x, w, labels, -100)[0], "loss")
+    ref.assert_within(dx[~none], *ref.xent_bwd(x, w, labels, torch.ones(len(labels)), -100), "dX")
