@@ -141,3 +141,25 @@ def test_labels_of_every_piece_and_of_none(env, T, rows):
     x, labels = x[~none], labels[~none]
     ref.assert_within(loss[~none], *ref.xent(x, w, labels, -100)[0], "loss")
     ref.assert_within(dx[~none], *ref.xent_bwd(x, w, labels, torch.ones(len(labels)), -100), "dX")
+
+
+@pytest.mark.parametrize("T", [1, 20, 300, 400])
+def test_a_codebook_on_an_odd_element(env, T):
+    """2-byte alignment is all that a codebook needs."""
+    torch, cbk = env
+    rows, cols = 300, 192
+    w, v = of_width(torch, rows, cols, 11, 155), of_width(torch, rows, cols, 9, 156)
+
+    def moved(t):
+        cb = torch.zeros(t.U + 1, dtype=torch.int16, device="cuda")[1:]
+        cb.copy_(t.codebook)
+        return cbk.Compressed(t.rows, t.cols, t.U, t.b, cb, t.words)
+
+    a, b = compress(cbk, w), moved(compress(cbk, v))
+    x, dh = acts(torch, T, cols, 157), acts(torch, T, rows, 158, 0.1)
+    ref.assert_within(cbk.linear(b, x.cuda()), *ref.linear(x, v), "linear")
+    ref.assert_within(cbk.linear_dx(b, dh.cuda()), *ref.linear_dx(dh, v), "linear_dx")
+    for g, u, wg, wu in ((a, b, w, v), (b, a, v, w)):
+        ref.assert_within(cbk.ffn_gated(g, u, x.cuda()), *ref.ffn("silu", x, wg, wu), "ffn_gated")
+        for name, got, want in zip(("dX", "dG", "dU"), cbk.ffn_gated_bwd(g, u, x.cuda(), dh.cuda()), ref.ffn_bwd("silu", x, wg, wu, dh)):
+            ref.assert_within(got, *want, name)

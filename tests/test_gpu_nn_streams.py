@@ -69,3 +69,39 @@ def test_an_output_is_kept_while_the_current_stream_reads_it(env, T):
     ref.assert_within(copy, *ref.linear(x[0], w), "the first output")
     for z in later:
         ref.assert_within(z, *ref.linear(x[1], w), "the later ones")
+
+
+@pytest.mark.parametrize("T", [1, 40, 400])
+def test_a_captured_call_on_a_forked_stream(env, T):
+    """Inside a capture, a call on a stream that was forked from the captured one, its outputs used behind the
+    join: every replay against the eager call's bits, with eager calls between."""
+    torch, cbk = env
+    rows, cols = 320, 192
+    wg, wu = (weights(torch, rows, cols, 1500, 118 + i, 0.2) for i in range(2))
+    a, b = compress(cbk, wg), compress(cbk, wu)
+    X, dH = (torch.empty(T, n, dtype=torch.bfloat16, device="cuda") for n in (cols, rows))
+    s = torch.cuda.Stream()
+
+    def run(side):
+        now = torch.cuda.current_stream()
+        if side is not None:
+            side.wait_stream(now)
+        h = cbk.ffn_gated(a, b, X, stream=side)
+        y = cbk.linear(a, X)
+        dx = cbk.ffn_gated_bwd(a, b, X, dH, stream=side)[0]
+        if side is not None:
+            now.wait_stream(side)
+        return h, y, dx, h.float() + y.float()
+
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        outs = run(s)
+    for i in range(4):
+        X.copy_(acts(torch, T, cols, 120 + i))
+        dH.copy_(acts(torch, T, rows, 130 + i, 0.1))
+        g.replay()
+        want = run(None)
+        torch.cuda.synchronize()
+        for got, w in zip(outs, want):
+            assert torch.equal(got, w), i
