@@ -683,15 +683,17 @@ def _vector(x, n, dtype, name):
 def _arguments(first, *others):
     """Checks that the tensors (None: not given) are on one device and ask for no gradient: the operators
     record no graph."""
-    import torch
+    device = first.device
     for x in (first, *others):
         if x is None:
             continue
-        if x.device != first.device:
-            raise ValueError(f"the arguments are on {first.device} and {x.device}")
-        if x.requires_grad and torch.is_grad_enabled():
-            raise ValueError("an argument requires a gradient, and the operators record no graph: call them under "
-                             "torch.no_grad(), or from a torch.autograd.Function with the gradient's call")
+        if x.device != device:
+            raise ValueError(f"the arguments are on {device} and {x.device}")
+        if x.requires_grad:
+            import torch
+            if torch.is_grad_enabled():
+                raise ValueError("an argument requires a gradient, and the operators record no graph: call them under "
+                                 "torch.no_grad(), or from a torch.autograd.Function with the gradient's call")
 
 
 class _Call:
@@ -707,13 +709,14 @@ class _Call:
         self.torch, self.device = torch, x.device
         if self.device.type != "cuda":
             raise ValueError("the operators run on GPU tensors")
-        self.current = torch.cuda.current_stream(self.device)
-        self.stream = self.current if stream is None else stream
-        if self.stream.device != self.device:
-            raise ValueError(f"the stream is on {self.stream.device}, the arguments on {self.device}")
+        self.current = self.stream = torch.cuda.current_stream(self.device)
+        if stream is not None and stream != self.current:
+            if stream.device != self.device:
+                raise ValueError(f"the stream is on {stream.device}, the arguments on {self.device}")
+            self.stream = stream
 
     def empty(self, shape, dtype, scratch=False):
-        if self.stream == self.current:
+        if self.stream is self.current:
             return self.torch.empty(shape, dtype=dtype, device=self.device)
         with self.torch.cuda.stream(self.stream):
             out = self.torch.empty(shape, dtype=dtype, device=self.device)
@@ -741,7 +744,7 @@ class _Call:
 
 def linear(t: Compressed, X, out=None, workspace=None, stream=None):
     """out[tokens][rows] (bfloat16) = X . W^T for a bfloat16 X[tokens][cols], any number of tokens
-    (row strides may exceed the widths).  ``workspace``: a uint8 device tensor of at least
+    (row strides may exceed the widths; out must not share memory with X).  ``workspace``: a uint8 device tensor of at least
     ``linear_workspace_bytes(t, tokens)`` bytes; allocated when not given.  ``stream``: the torch
     stream to run on (default: the current one); the caller orders it behind the work that makes the
     inputs, and keeps them until it has run."""
