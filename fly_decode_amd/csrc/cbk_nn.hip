@@ -274,8 +274,8 @@ __global__ __launch_bounds__(64 * kUnpackWaves) void k_unpack(const UnpackArgs a
 // read (a group of 16 lanes reads 4 rows x 16 columns, and lane i gets column i); chunk c of row r sits in
 // slot c ^ (2 (r / 8)), so the 4 rows of a group and those of its neighbour hit different banks.
 //
-// Measured on 2048 tokens and a pair of 4096 x 11008 (369 GFLOP a product): 286 us forward, 1.29 PFLOP/s,
-// and 270 for dX, 1.37; 128 x 128 tiles took 350 forward.  On a 4096-wide head of 32000 rows (537 GFLOP),
+// Measured on 2048 tokens and a pair of 4096 x 11008 (369 GFLOP a product; the shortest of six calls): 289 us
+// forward, 1.28 PFLOP/s, and 272 for dX, 1.36; 128 x 128 tiles took 350 forward.  On a 4096-wide head of 32000 rows (537 GFLOP),
 // multiplications and barriers alone took 320 us, 1.68 PFLOP/s at the clock that the chip holds under
 // them; with the fragments' reads 364, and with the copies, which are new to an XCD's L2, 400 (470 where A
 // and B lay row after row and a copy read half a cache line of each).  Groups of 4 or 16 token tiles, the
