@@ -309,7 +309,10 @@ struct MmArgs {
     int act;
     uint32_t f0, F;  // first row of the tensors in this piece, and all of them
     const uint16_t *dH;
-    // G: the piece's gradients at the projections [M][ldG], columns as the piece's rows; k_mm writes and reads it in blocks
+    // G: the piece's gradients at the projections (or p - [label]) [M][ldG], columns as the piece's rows; k_mm writes
+    // and reads it in blocks.  Rounded to BF16, which the matrix instruction's operands are: two BF16 parts of each
+    // value would double the second product.  The block's dX is 0.0023 of its norm from 64 bits, 0.0017 with fp32 in
+    // between; the head's stays at 0.0017.
     uint16_t *dG, *dU, *G;
     uint64_t lddh, ldg;
     uint32_t ldG;
