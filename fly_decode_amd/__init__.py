@@ -1,8 +1,9 @@
 """fly_decode_amd -- lossless codebook-compressed BF16 weights decoded on MI355X (gfx950).
 
 A thin ctypes binding over ``libcbk.so`` (C ABI declared in ``include/cbk.h``, for the exponent
-entropy-coded format in ``include/cbk_ec.h``, and for the operators on any number of tokens and
-their gradients in ``include/cbk_nn.h``).  Every step of the
+entropy-coded format in ``include/cbk_ec.h``, for the operators on any number of tokens and
+their gradients in ``include/cbk_nn.h``, for experts in ``include/cbk_moe.h`` and for drawing
+tokens in ``include/cbk_sample.h``).  Every step of the
 hot path runs in the library's HIP kernels; this module only marshals arguments.  PyTorch is used
 for device memory and streams: inputs and outputs are torch tensors whose ``data_ptr()`` is handed
 to the library, and GPU calls are enqueued on ``torch.cuda.current_stream()``.
@@ -22,7 +23,8 @@ __all__ = ["CBK_OK", "CbkError", "bits_for", "words_for", "compressed_bytes", "e
            "load_library", "ECTensor", "ec_encode", "ec_decode_bf16", "ec_gemv", "ec_build_index",
            "ec_decode_group", "ec_gemv_group", "cap_patterns",
            "GemvChain", "linear", "linear_dx", "ffn_gated", "ffn_gated_bwd", "xent", "xent_bwd",
-           "linear_workspace_bytes", "ffn_workspace_bytes", "xent_workspace_bytes"]
+           "linear_workspace_bytes", "ffn_workspace_bytes", "xent_workspace_bytes",
+           "route", "route_bwd", "Experts", "ffn_experts", "ffn_experts_bwd", "experts_workspace_bytes", "sample"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # CBK_LIBRARY names another build of the same library (for side-by-side comparisons)
@@ -69,6 +71,21 @@ class _ECTensor(ctypes.Structure):
     _fields_ = [("n", ctypes.c_uint64), ("total_bits", ctypes.c_uint64), ("sm", ctypes.c_void_p),
                 ("stream", ctypes.c_void_p), ("gaps", ctypes.c_void_p), ("bases", ctypes.c_void_p),
                 ("lut", ctypes.c_void_p), ("max_block_codes", ctypes.c_uint32)]
+
+
+class _Router(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_uint32), ("k", ctypes.c_uint32), ("score", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("groups", ctypes.c_uint32), ("top_groups", ctypes.c_uint32), ("group_top", ctypes.c_uint32)]
+
+
+class _Experts(ctypes.Structure):
+    _fields_ = [("buffer", ctypes.c_void_p), ("rows", ctypes.c_uint64), ("cols", ctypes.c_uint64), ("out", ctypes.c_uint64),
+                ("count", ctypes.c_uint32), ("b", ctypes.c_uint32), ("b_down", ctypes.c_uint32), ("device", ctypes.c_uint32)]
+
+
+class _Sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_p", ctypes.c_float), ("min_p", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("temperatures", ctypes.c_void_p), ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p), ("top_ks", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -181,6 +198,20 @@ def load_library():
                 ("cbk_xent_bwd", [tp, vp, u64, vp, vp, vp, u64, ctypes.c_int64, vp, u64])):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = types + [vp, sz, vp]
+        rp, ep, i32, u32 = ctypes.POINTER(_Router), ctypes.POINTER(_Experts), ctypes.c_int, ctypes.c_uint32
+        lib.cbk_experts_bytes.restype = sz
+        lib.cbk_experts_bytes.argtypes = [u32]
+        lib.cbk_experts_workspace_bytes.restype = sz
+        lib.cbk_experts_workspace_bytes.argtypes = [ep, u64, u32, i32]
+        for name, types in (
+                ("cbk_route", [rp, vp, i32, u64, u64, vp, vp, vp, vp]),
+                ("cbk_route_bwd", [rp, vp, i32, u64, u64, vp, vp, vp, u64, vp]),
+                ("cbk_experts_init", [tp, tp, tp, u32, vp, sz, ep]),
+                ("cbk_ffn_experts", [ep, i32, vp, u64, u64, vp, vp, u32, vp, u64, vp, sz, vp]),
+                ("cbk_ffn_experts_bwd", [ep, i32, vp, u64, u64, vp, vp, u32, vp, u64, vp, u64, vp, vp, sz, vp]),
+                ("cbk_sample", [ctypes.POINTER(_Sampling), vp, i32, u64, u64, u64, vp, vp, vp, vp])):
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = types
         _lib = lib
     return _lib
 
@@ -726,14 +757,18 @@ class _Call:
 
     def run(self, name, sizes, workspace, *args):
         """Calls ``name``; the workspace is allocated as ``sizes``, a name and its arguments, says
-        where none is given."""
+        where none is given (``sizes`` None: the call takes none)."""
         lib = load_library()
-        if workspace is None:
+        if sizes is None:
+            pass
+        elif workspace is None:
             # at least one element, so that there is an address; torch's blocks are 512-byte aligned
             workspace = self.empty((getattr(lib, sizes[0])(*sizes[1:]) or 1,), self.torch.uint8, scratch=True)
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
-        args += (workspace.data_ptr() or None, workspace.numel() * workspace.element_size(), self.stream.cuda_stream)
+        if sizes is not None:
+            args += (workspace.data_ptr() or None, workspace.numel() * workspace.element_size())
+        args += (self.stream.cuda_stream,)
         if self.torch.cuda.current_device() == self.device.index:
             st = getattr(lib, name)(*args)
         else:
@@ -860,3 +895,194 @@ def xent_bwd(head: Compressed, X, labels, lse, dloss, ignore_index: int = -100, 
     hs = ctypes.byref(head._struct())
     call.run("cbk_xent_bwd", ("cbk_xent_workspace_bytes", hs, T), workspace, hs, xp, ldx, lp, sp, dp, T, ignore_index, op, ldo)
     return out
+
+
+# ---- experts (include/cbk_moe.h) and drawing tokens (include/cbk_sample.h), called as the operators above
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _matrix(x, cols, name):
+    """Checks a [tokens][cols] float32 or bfloat16 matrix with unit column stride; returns (pointer, dtype, row stride)."""
+    import torch
+    dtypes = {torch.float32: 0, torch.bfloat16: 1}
+    if x.dtype not in dtypes or x.dim() != 2 or x.shape[1] != cols or (cols > 1 and x.shape[0] > 0 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a [tokens][{cols}] float32 or bfloat16 matrix with unit column stride")
+    rows, ld = x.shape[0], x.stride(0)
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return x.data_ptr() or None, dtypes[x.dtype], ld
+
+
+def _slots(x, shape, dtype, name):
+    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
+    return x.data_ptr() or None
+
+
+def _router(experts, k, score, renormalise, scale, groups=1, top_groups=1, group_top=1):
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    if min(k, groups, top_groups, group_top) < 0:
+        raise ValueError("k, groups, top_groups and group_top must not be negative")
+    return ctypes.byref(_Router(experts, k, _SCORES[score], int(bool(renormalise)), scale, groups, top_groups, group_top))
+
+
+def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int | None = None,
+          group_top: int = 1, renormalise: bool = True, scale: float = 1.0, stream=None):
+    """Routes tokens to experts: (experts int32[tokens][k], weights float32[tokens][k]) for logits[tokens][experts] in
+    float32 or bfloat16.  The k experts with the largest score (softmax or sigmoid of the logits) plus ``bias``
+    (float32[experts]; it only steers the choice), out of the ``top_groups`` best of ``groups`` groups of neighbouring
+    experts (by the best, or the sum of the two best, ``group_top``), equal ones by the lower index; weights are the
+    scores, divided by their sum if ``renormalise``, times ``scale``.  Experts with a logit of -inf are never chosen;
+    slots left over get -1 and a weight of 0."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens][experts]")
+    T, E = logits.shape
+    zp, dtype, ld = _matrix(logits, E, "logits")
+    bp = None if bias is None else _vector(bias, E, torch.float32, "bias")
+    _arguments(logits, bias)
+    r = _router(E, k, score, renormalise, scale, groups, groups if top_groups is None else top_groups, group_top)
+    call = _Call(logits, stream)
+    experts, weights = call.empty((T, k), torch.int32), call.empty((T, k), torch.float32)
+    call.run("cbk_route", None, None, r, zp, dtype, ld, T, bp, experts.data_ptr() or None, weights.data_ptr() or None)
+    return experts, weights
+
+
+def route_bwd(logits, experts, dweights, score: str = "softmax", renormalise: bool = True, scale: float = 1.0, out=None,
+              stream=None):
+    """The gradient of ``route``'s logits, out[tokens][experts] in their type, for the experts it chose and the gradient
+    dweights[tokens][k] (float32) of its weights.  Choosing has no gradient."""
+    import torch
+    if logits.dim() != 2 or experts.dim() != 2:
+        raise ValueError("logits must be [tokens][experts], experts [tokens][k]")
+    T, E = logits.shape
+    k = experts.shape[1]
+    zp, dtype, ld = _matrix(logits, E, "logits")
+    ep = _slots(experts, (T, k), torch.int32, "experts")
+    dp = _slots(dweights, (T, k), torch.float32, "dweights")
+    _arguments(logits, experts, dweights, out)
+    r = _router(E, k, score, renormalise, scale)
+    call = _Call(logits, stream)
+    if out is None:
+        out = call.empty((T, E), logits.dtype)
+    op, odtype, ldo = _matrix(out, E, "out")
+    if out.shape[0] != T or odtype != dtype:
+        raise ValueError("out and logits differ in tokens or type")
+    call.run("cbk_route_bwd", None, None, r, zp, dtype, ld, T, ep, dp, op, ldo)
+    return out
+
+
+class Experts:
+    """The experts of a layer: lists of device ``Compressed`` tensors, gate and up [rows][cols] and down [out][rows], of
+    one shape each (their codebooks and widths may differ).  Holds a table of them in device memory, made here (not
+    inside a graph's capture), and references to them."""
+
+    def __init__(self, gates, ups, downs):
+        import torch
+        kinds = [list(gates), list(ups), list(downs)]
+        n = len(kinds[0])
+        if n == 0 or any(len(ts) != n for ts in kinds):
+            raise ValueError("gates, ups and downs must be as many, and at least one")
+        self.tensors = kinds
+        self.device = kinds[0][0].words.device
+        if self.device.type != "cuda":
+            raise ValueError("the experts' tensors must be on a GPU")
+        for t in (t for ts in kinds for t in ts):
+            if t.words.device != self.device or t.codebook.device != self.device:
+                raise ValueError("the experts' tensors are on different devices")
+        lib = load_library()
+        arrays = [(_Tensor * n)(*[t._struct() for t in ts]) for ts in kinds]
+        nbytes = int(lib.cbk_experts_bytes(n))
+        self._struct = _Experts()
+        with torch.cuda.device(self.device):
+            self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            torch.cuda.current_stream(self.device).synchronize()  # the block may have been another stream work's
+            _check(lib.cbk_experts_init(*arrays, n, self.buffer.data_ptr(), nbytes, ctypes.byref(self._struct)), "cbk_experts_init")
+        self.count, self.rows, self.cols, self.out = n, int(self._struct.rows), int(self._struct.cols), int(self._struct.out)
+
+
+def experts_workspace_bytes(ex: Experts, tokens: int, k: int, backward: bool = False) -> int:
+    """Workspace of ``ffn_experts``, or of ``ffn_experts_bwd`` (0: none)."""
+    return int(load_library().cbk_experts_workspace_bytes(ctypes.byref(ex._struct), tokens, k, int(backward)))
+
+
+def _routed(ex, X, experts, weights):
+    import torch
+    xp, ldx = _tokens(X, ex.cols, "X")
+    if experts.dim() != 2:
+        raise ValueError("experts must be [tokens][k]")
+    T, k = X.shape[0], experts.shape[1]
+    return xp, ldx, T, k, _slots(experts, (T, k), torch.int32, "experts"), _slots(weights, (T, k), torch.float32, "weights")
+
+
+def ffn_experts(ex: Experts, X, experts, weights, act: str = "silu", out=None, workspace=None, stream=None):
+    """The experts' gated feed-forward blocks: out[t] (bfloat16[tokens][ex.out]) = the sum over a token's slots of
+    weights[t][j] * Wd . (act(Wg . x) * (Wu . x)) with the tensors of expert experts[t][j].  X is bfloat16[tokens][ex.cols],
+    experts int32[tokens][k] and weights float32[tokens][k] as ``route`` gives them; slots whose expert is outside
+    [0, ex.count) contribute nothing."""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    xp, ldx, T, k, ep, wp = _routed(ex, X, experts, weights)
+    _arguments(X, experts, weights, ex.buffer, out)
+    call = _Call(X, stream)
+    if out is None:
+        out = call.empty((T, ex.out), X.dtype)
+    op, ldo = _tokens(out, ex.out, "out")
+    if out.shape[0] != T:
+        raise ValueError("out and X differ in tokens")
+    es = ctypes.byref(ex._struct)
+    call.run("cbk_ffn_experts", ("cbk_experts_workspace_bytes", es, T, k, 0), workspace, es, _ACTS[act], xp, ldx, T, ep, wp, k, op, ldo)
+    return out
+
+
+def ffn_experts_bwd(ex: Experts, X, experts, weights, dY, act: str = "silu", dX=None, workspace=None, stream=None):
+    """The gradient of ``ffn_experts`` for the same X, experts and weights and the gradient dY[tokens][ex.out] (bfloat16)
+    of its output: (dX bfloat16[tokens][ex.cols], dweights float32[tokens][k])."""
+    import torch
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    xp, ldx, T, k, ep, wp = _routed(ex, X, experts, weights)
+    yp, ldy = _tokens(dY, ex.out, "dY")
+    if dY.shape[0] != T or (dX is not None and dX.shape[0] != T):
+        raise ValueError("X, dY and dX differ in tokens")
+    _arguments(X, experts, weights, ex.buffer, dY, dX)
+    call = _Call(X, stream)
+    if dX is None:
+        dX = call.empty((T, ex.cols), X.dtype)
+    dp, ldd = _tokens(dX, ex.cols, "dX")
+    dweights = call.empty((T, k), torch.float32)
+    es = ctypes.byref(ex._struct)
+    call.run("cbk_ffn_experts_bwd", ("cbk_experts_workspace_bytes", es, T, k, 1), workspace, es, _ACTS[act], xp, ldx, T, ep, wp, k, yp, ldy,
+             dp, ldd, dweights.data_ptr() or None)
+    return dX, dweights
+
+
+def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
+    """Draws a token from each row of logits[tokens][vocabulary] (float32 or bfloat16) by a random number uniform[tokens]
+    (float32 in [0, 1)): (token int64[tokens], logprob float32[tokens], the logarithm of the probability that it was drawn
+    with).  ``temperature`` 0 takes the largest logit; ``top_k`` (0: all), ``min_p`` (times the largest probability) and
+    ``top_p`` (of what those two leave) bound what may be drawn.  Each is a number, or a device vector with one for each
+    row (float32; top_k int32).  A row that is all -inf or holds a NaN gives -1 and NaN."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens][vocabulary]")
+    T, V = logits.shape
+    zp, dtype, ld = _matrix(logits, V, "logits")
+    up = _vector(uniform, T, torch.float32, "uniform")
+    p, vectors = _Sampling(1.0, 1.0, 0.0, 0), []
+    for name, value, kind in (("temperature", temperature, torch.float32), ("top_p", top_p, torch.float32),
+                              ("min_p", min_p, torch.float32), ("top_k", top_k, torch.int32)):
+        if isinstance(value, torch.Tensor):
+            setattr(p, name + "s", _vector(value, T, kind, name))
+            vectors.append(value)
+        else:
+            setattr(p, name, value)
+    _arguments(logits, uniform, *vectors)
+    call = _Call(logits, stream)
+    token, logprob = call.empty((T,), torch.int64), call.empty((T,), torch.float32)
+    call.run("cbk_sample", None, None, ctypes.byref(p), zp, dtype, ld, V, T, up, token.data_ptr() or None, logprob.data_ptr() or None)
+    return token, logprob

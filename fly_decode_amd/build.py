@@ -24,7 +24,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "inclu
 
 SOURCES = [("cbk_api.cpp", False), ("cbk_kernels.hip", True), ("cbk_encode.hip", True),
            ("cbk_ec_host.cpp", False), ("cbk_ec.hip", True),
-           ("cbk_nn_host.cpp", False), ("cbk_nn.hip", True)] + [
+           ("cbk_nn_host.cpp", False), ("cbk_nn.hip", True),
+           ("cbk_moe_host.cpp", False), ("cbk_moe.hip", True), ("cbk_moe_mm.hip", True), ("cbk_sample.hip", True)] + [
     (f"cbk_nn_fused_{b}.hip", True) for b in range(8, 15)]
 
 

@@ -1,5 +1,6 @@
-// Internal interface between the host API (cbk_api.cpp, cbk_ec_host.cpp, cbk_nn_host.cpp) and the HIP
-// launchers (cbk_kernels.hip, cbk_encode.hip, cbk_ec.hip, cbk_nn.hip).
+// Internal interface between the host API (cbk_api.cpp, cbk_ec_host.cpp, cbk_nn_host.cpp,
+// cbk_moe_host.cpp) and the HIP launchers (cbk_kernels.hip, cbk_encode.hip, cbk_ec.hip, cbk_nn.hip, cbk_moe.hip,
+// cbk_sample.hip).
 // Arguments reaching these launchers are already validated.
 #pragma once
 #include <hip/hip_runtime.h>
@@ -8,6 +9,8 @@
 #include "../../include/cbk.h"
 #include "../../include/cbk_ec.h"
 #include "../../include/cbk_nn.h"
+#include "../../include/cbk_moe.h"
+#include "../../include/cbk_sample.h"
 
 namespace cbk {
 
@@ -90,5 +93,41 @@ cbk_status launch_xent(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, 
 cbk_status launch_xent_bwd(const cbk_tensor &head, const uint16_t *X, uint64_t ldx, const int64_t *labels,
                            const float *lse, const float *dloss, uint64_t T, int64_t ignore, uint16_t *dX,
                            uint64_t lddx, void *ws, hipStream_t s);
+
+// X [T][K] into P [T][Kp] with zeros past K (cbk_nn.hip).
+cbk_status launch_pad_rows(const uint16_t *X, uint64_t ld, uint64_t T, uint32_t K, uint32_t Kp, uint16_t *P, hipStream_t s);
+
+// Routing (cbk_moe.hip) and drawing (cbk_sample.hip).
+cbk_status launch_route(const cbk_router &r, const void *logits, int dtype, uint64_t ld, uint64_t tokens, const float *bias,
+                        int32_t *experts, float *weights, hipStream_t s);
+cbk_status launch_route_bwd(const cbk_router &r, const void *logits, int dtype, uint64_t ld, uint64_t tokens,
+                            const int32_t *experts, const float *dweights, void *dlogits, uint64_t ldd, hipStream_t s);
+cbk_status launch_sample(const cbk_sampling &p, const void *logits, int dtype, uint64_t ld, uint64_t V, uint64_t tokens,
+                         const float *uniform, int64_t *token, float *logprob, hipStream_t s);
+
+// Blocks of experts (cbk_moe.hip, cbk_moe_mm.hip).  As for NnPlan, a plan depends on the shapes and the number of
+// tokens alone.  Tokens are taken Tc at a time; a token's k slots are sorted by expert.
+struct ExPlan {
+    uint64_t Tc;
+    uint64_t Kp, Fp, Op;     // cols, rows and out rounded up to 64
+    uint64_t ldK, ldF, ldO;  // and to a tile's 128 columns: leading dimensions of fp32 results
+    uint32_t tile;           // slots of one expert that a workgroup takes at most
+    uint32_t max_tiles;      // token tiles of a chunk, at most
+    uint32_t split_down, split_dt, split_x;  // workgroups that share a reduction
+    uint32_t dw_parts;       // partial sums of a slot's dweights
+    uint64_t s_stride, d_stride;  // floats between the shares of a reduction
+    // offsets in bytes
+    uint64_t ntiles, tiles, token_of, slot_of, place_of, xpack, ypack, h, g, s, d, dw;
+    uint64_t bytes;
+};
+ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward);
+// Fills the table at `buffer` (three runs of `count` records) and names the device.
+cbk_status experts_table(const cbk_tensor *gate, const cbk_tensor *up, const cbk_tensor *down, uint32_t count, void *buffer,
+                         uint32_t &device);
+constexpr uint64_t kExTensorBytes = 32;
+// Forward where dY is null (out: Y), else the gradient (out: dX).
+cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, const uint16_t *X, uint64_t ldx, uint64_t T,
+                          const int32_t *experts, const float *weights, uint32_t k, const uint16_t *dY, uint64_t lddy,
+                          uint16_t *out, uint64_t ldo, float *dweights, void *ws, hipStream_t s);
 
 }  // namespace cbk

@@ -1,0 +1,678 @@
+// HIP kernels for gfx950 (CDNA4) of cbk_moe.h, but for the experts' products (cbk_moe_mm.hip): routing and its
+// gradient, the order of slots by expert, and what gathers the experts' results by token.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "cbk_moe_device.h"
+
+namespace cbk {
+namespace {
+
+// ------------------------------------------------------------------------------- routing
+// A wave has a token, lane l the experts l, l + 64, ..: up to 16 of them (NPL).
+
+struct RouteArgs {
+    cbk_router r;
+    const void *logits;
+    uint64_t ld, tokens;
+    const float *bias;
+    int32_t *experts;
+    float *weights;
+    const float *dweights;
+    void *dlogits;
+    uint64_t ldd;
+};
+
+__device__ __forceinline__ float logit(const float *p, uint64_t i) { return p[i]; }
+__device__ __forceinline__ float logit(const uint16_t *p, uint64_t i) { return bf16_value(p[i]); }
+__device__ __forceinline__ void put(float *p, uint64_t i, float v) { p[i] = v; }
+__device__ __forceinline__ void put(uint16_t *p, uint64_t i, float v) { p[i] = to_bf16(v); }
+
+// Ascending unsigned numbers above 0 for ascending doubles (-0 as +0; no NaN).
+__device__ __forceinline__ uint64_t ascending(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
+    return u >> 63 ? ~u : u | (uint64_t(1) << 63);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_max(uint64_t v) {
+    const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
+    const uint32_t ol = __builtin_amdgcn_update_dpp(lo, lo, CTRL, ROWS, 0xF, false);
+    const uint32_t oh = __builtin_amdgcn_update_dpp(hi, hi, CTRL, ROWS, 0xF, false);
+    const uint64_t o = (static_cast<uint64_t>(oh) << 32) | ol;
+    return o > v ? o : v;
+}
+// The largest of the 64 lanes' v, in every lane.
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+    v = dpp_max<0x111, 0xF>(v);
+    v = dpp_max<0x112, 0xF>(v);
+    v = dpp_max<0x114, 0xF>(v);
+    v = dpp_max<0x118, 0xF>(v);
+    v = dpp_max<0x142, 0xA>(v);
+    v = dpp_max<0x143, 0xC>(v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v)), 63);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v >> 32)), 63);
+    return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+__device__ __forceinline__ float wave_top(float v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+
+// Experts are chosen one after the other by the wave's largest key.  Without a bias and sums of two scores the
+// order is that of the logits, whose keys are exact; with them (WIDE) scores are formed and compared in fp64, where
+// rounding does not decide between two that an fp32 sum could not tell apart.  Weights take an fp64 exponential for
+// each chosen expert (and each expert, for a softmax that is not renormalised), which nothing waits for.
+template <typename T, int NPL, bool WIDE>
+__global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
+    extern __shared__ uint64_t keys_lds[];  // groups only: a wave's keys
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t t = static_cast<uint64_t>(blockIdx.x) * 4 + wave;
+    if (t >= a.tokens) return;
+    const uint32_t E = a.r.experts, k = a.r.k;
+    const T *row = static_cast<const T *>(a.logits) + t * a.ld;
+    const bool sigmoid = a.r.score == CBK_SCORE_SIGMOID;
+
+    float z[NPL];
+    double s[NPL];
+    uint64_t key[NPL];  // 0: not to be chosen
+    bool bad = false;
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+        const uint32_t e = j * 64 + lane;
+        z[j] = e < E ? logit(row, e) : -__builtin_inff();
+        bad = bad || z[j] != z[j] || z[j] == __builtin_inff();
+        top = fmaxf(top, z[j]);
+    }
+    top = wave_top(top);
+    const double base = top == -__builtin_inff() ? 0.0 : static_cast<double>(top);
+    double denominator = 1.0;
+    if (WIDE || !(sigmoid || a.r.renormalise)) {
+        double sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            s[j] = sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(z[j]))) : exp(static_cast<double>(z[j]) - base);
+            sum += s[j];
+        }
+        if (!sigmoid) {
+            denominator = wave_sum(sum);
+            if (denominator == 0.0) denominator = 1.0;
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int j = 0; j < NPL; ++j) s[j] /= denominator;
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+        const uint32_t e = j * 64 + lane;
+        const float bias = a.bias && e < E ? a.bias[e] : 0.f;
+        const bool out = z[j] == -__builtin_inff() || bias == -__builtin_inff();
+        if constexpr (WIDE) {
+            s[j] += bias;
+            bad = bad || s[j] != s[j];
+            key[j] = out ? 0 : ascending(s[j]);
+        } else {
+            key[j] = out ? 0 : static_cast<uint64_t>(ascending(static_cast<double>(z[j])));
+        }
+    }
+    bad = __any(bad);
+
+    if (a.r.groups > 1) {
+        // a group's mark: lanes take groups in turn; 0 where it has nothing to choose
+        uint64_t *mine = keys_lds + wave * (NPL * 64);
+        const uint32_t size = E / a.r.groups;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) mine[j * 64 + lane] = key[j];
+        asm volatile("" ::: "memory");  // one wave's LDS accesses run in order
+        uint64_t marks[NPL];
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            const uint32_t g = j * 64 + lane;
+            uint64_t first = 0, second = 0;
+            if (g < a.r.groups)
+                for (uint32_t i = 0; i < size; ++i) {
+                    const uint32_t at = i + lane;  // lanes start at different banks
+                    const uint64_t v = mine[g * size + at % size];
+                    if (v > first) {
+                        second = first;
+                        first = v;
+                    } else if (v > second) {
+                        second = v;
+                    }
+                }
+            if constexpr (WIDE) {
+                auto value = [](uint64_t u) { return __builtin_bit_cast(double, u >> 63 ? u & ~(uint64_t(1) << 63) : ~u); };
+                if (a.r.group_top == 2 && second) first = ascending(value(first) + value(second));
+            }
+            marks[j] = first;
+        }
+        asm volatile("" ::: "memory");
+        // keep the best groups: mark them in LDS
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) mine[j * 64 + lane] = 0;
+        asm volatile("" ::: "memory");
+        for (uint32_t n = 0; n < a.r.top_groups; ++n) {
+            uint64_t best = marks[0];
+#pragma unroll
+            for (int j = 1; j < NPL; ++j) best = marks[j] > best ? marks[j] : best;
+            best = wave_max(best);
+            if (best == 0) break;
+            bool found = false;
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) {
+                const uint64_t has = __ballot(marks[j] == best);
+                if (!found && has) {
+                    found = true;
+                    if (lane == static_cast<uint32_t>(__ffsll(static_cast<unsigned long long>(has)) - 1)) {
+                        marks[j] = 0;
+                        mine[j * 64 + lane] = 1;
+                    }
+                }
+            }
+        }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            const uint32_t e = j * 64 + lane;
+            if (e < E && mine[e / size] == 0) key[j] = 0;
+        }
+    }
+
+    int32_t chosen = -1;  // of slot `lane`
+    float cz = 0.f;
+    for (uint32_t n = 0; n < k; ++n) {
+        uint64_t best = key[0];
+#pragma unroll
+        for (int j = 1; j < NPL; ++j) best = key[j] > best ? key[j] : best;
+        best = wave_max(best);
+        if (best == 0) break;
+        bool found = false;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            const uint64_t has = __ballot(key[j] == best);
+            if (!found && has) {
+                found = true;
+                const int who = __ffsll(static_cast<unsigned long long>(has)) - 1;
+                const float v = __shfl(z[j], who, 64);
+                if (lane == n) {
+                    chosen = j * 64 + who;
+                    cz = v;
+                }
+                if (lane == static_cast<uint32_t>(who)) key[j] = 0;
+            }
+        }
+    }
+    const bool have = chosen >= 0;
+    double w = 0.0;
+    if (sigmoid) {
+        if (have) w = 1.0 / (1.0 + exp(-static_cast<double>(cz)));
+    } else {
+        // renormalised: relative to the largest of the chosen, so that something is left to divide by
+        const float ref = a.r.renormalise ? wave_top(have ? cz : -__builtin_inff()) : top;
+        if (have) w = exp(static_cast<double>(cz) - static_cast<double>(ref)) / (a.r.renormalise ? 1.0 : denominator);
+    }
+    if (a.r.renormalise) {
+        const double sum = wave_sum(w);
+        if (sum > 0.0) w /= sum;
+    }
+    if (lane < k) {
+        a.experts[t * k + lane] = bad ? static_cast<int32_t>(lane) : chosen;
+        a.weights[t * k + lane] = bad ? __builtin_nanf("") : static_cast<float>(w * static_cast<double>(a.r.scale));
+    }
+}
+
+// Lane i < k has slot i.  With w = s / (sum of the chosen s), d the gradient of a weight times scale and m = <d, w>,
+// a softmax gives dz = w (d - m) at the chosen experts alone: the others' share cancels.
+template <typename T, int NPL>
+__global__ __launch_bounds__(256) void k_route_bwd(const RouteArgs a) {
+    const uint32_t lane = threadIdx.x & 63;
+    const uint64_t t = static_cast<uint64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (t >= a.tokens) return;
+    const uint32_t E = a.r.experts, k = a.r.k;
+    const T *row = static_cast<const T *>(a.logits) + t * a.ld;
+    const bool sigmoid = a.r.score == CBK_SCORE_SIGMOID, dense = !sigmoid && !a.r.renormalise;
+
+    int32_t e = -1;
+    float d = 0.f, cz = -__builtin_inff();
+    if (lane < k) {
+        e = a.experts[t * k + lane];
+        if (e < 0 || static_cast<uint32_t>(e) >= E) e = -1;
+        if (e >= 0) {
+            d = a.dweights[t * k + lane] * a.r.scale;
+            cz = logit(row, e);
+        }
+    }
+    float z[NPL], out[NPL];
+    float top = -__builtin_inff();
+    bool odd = false;  // a NaN, or a +inf that a softmax has no gradient at: the row is NaN
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+        const uint32_t x = j * 64 + lane;
+        z[j] = x < E ? logit(row, x) : -__builtin_inff();
+        odd = odd || z[j] != z[j] || z[j] == __builtin_inff();
+        top = fmaxf(top, z[j]);
+        out[j] = 0.f;
+    }
+    odd = __any(odd);
+    float part = 0.f;  // of slot `lane`
+    float mean = 0.f, inv = 0.f;
+    if (sigmoid) {
+        const float s = e >= 0 ? 1.f / (1.f + expf(-cz)) : 0.f, r = e >= 0 ? 1.f / (1.f + expf(cz)) : 0.f;
+        if (a.r.renormalise) {
+            // w = s / sum, w (1 - s) (d - m): formed so that scores far below 1 lose nothing
+            const float best = wave_top(s), rel = best > 0.f ? s / best : 0.f;
+            const float sum = wave_sum(rel), w = sum > 0.f ? rel / sum : 0.f;
+            const float m = wave_sum(e >= 0 ? d * w : 0.f);
+            part = e >= 0 ? w * r * (d - m) : 0.f;
+        } else {
+            part = d * s * r;
+        }
+    } else if (a.r.renormalise) {
+        const float best = wave_top(cz), at = best == -__builtin_inff() ? 0.f : best;
+        const float x = e >= 0 ? expf(cz - at) : 0.f, sum = wave_sum(x), w = sum > 0.f ? x / sum : 0.f;
+        const float m = wave_sum(e >= 0 ? d * w : 0.f);
+        part = e >= 0 ? w * (d - m) : 0.f;
+    } else {
+        top = wave_top(top);
+        if (top == -__builtin_inff()) top = 0.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            out[j] = expf(z[j] - top);
+            sum += out[j];
+        }
+        sum = wave_sum(sum);
+        inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float s = e >= 0 ? expf(cz - top) * inv : 0.f;
+        mean = wave_sum(d * s);
+        part = d * s;
+    }
+    if (dense) {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) out[j] = -out[j] * inv * mean;
+    }
+    for (uint32_t n = 0; n < k; ++n) {
+        const int32_t who = __builtin_amdgcn_readlane(e, n);
+        const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(part), n));
+        if (who < 0) continue;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j)
+            if (static_cast<uint32_t>(who) == j * 64 + lane) out[j] += v;
+    }
+    T *to = static_cast<T *>(a.dlogits) + t * a.ldd;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j)
+        if (j * 64 + lane < E) put(to, j * 64 + lane, odd ? __builtin_nanf("") : out[j]);
+}
+
+// --------------------------------------------------------------------------- slots by expert
+// One workgroup sorts the slots by expert, stably, and cuts each expert's run into token tiles of equal size.
+// Each wave counts a run of slots, then places them: the rank of a slot among the wave's 64 of the same expert comes
+// from ballots over the expert's bits.
+struct SortArgs {
+    const int32_t *experts;
+    uint32_t slots, k, count, tile, unit;  // tokens of a tile at most, and what its size is rounded up to
+    uint32_t *token_of, *slot_of;
+    int32_t *place_of;
+    ExTile *tiles;
+    uint32_t *ntiles;
+};
+constexpr int kSortWaves = 16;
+
+__global__ __launch_bounds__(64 * kSortWaves) void k_sort(const SortArgs a) {
+    extern __shared__ uint32_t lds[];  // [waves][count]: how many, then where the wave's next one goes
+    __shared__ uint32_t wave_sum[kSortWaves], wave_tiles[kSortWaves];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t n = a.count;
+    for (uint32_t i = tid; i < kSortWaves * n; i += blockDim.x) lds[i] = 0;
+    __syncthreads();
+    const uint32_t steps = (a.slots + 64 * kSortWaves - 1) / (64 * kSortWaves);  // of 64 slots, for a wave
+    const uint32_t from = wave * steps * 64;
+    uint32_t *mine = lds + wave * n;
+    for (uint32_t i = 0; i < steps; ++i) {
+        const uint32_t s = from + i * 64 + lane;
+        const uint32_t e = s < a.slots ? static_cast<uint32_t>(a.experts[s]) : ~0u;
+        if (e < n) atomicAdd(&mine[e], 1u);
+    }
+    __syncthreads();
+    // expert `tid`: its slots, and its tiles
+    uint32_t m = 0;
+    if (tid < n)
+        for (int w = 0; w < kSortWaves; ++w) m += lds[w * n + tid];
+    const uint32_t parts = (m + a.tile - 1) / a.tile;
+    const uint32_t size = m ? min(a.tile, ((m + parts - 1) / parts + a.unit - 1) / a.unit * a.unit) : 1;
+    const uint32_t tiles = (m + size - 1) / size;
+    uint32_t ms = m, ts = tiles;
+#pragma unroll
+    for (int by = 1; by < 64; by *= 2) {
+        const uint32_t x = __shfl_up(ms, by, 64), y = __shfl_up(ts, by, 64);
+        if (lane >= static_cast<uint32_t>(by)) {
+            ms += x;
+            ts += y;
+        }
+    }
+    if (lane == 63) {
+        wave_sum[wave] = ms;
+        wave_tiles[wave] = ts;
+    }
+    __syncthreads();
+    uint32_t start = ms - m, tile = ts - tiles;
+    for (uint32_t w = 0; w < wave; ++w) {
+        start += wave_sum[w];
+        tile += wave_tiles[w];
+    }
+    if (tid < n) {
+        uint32_t at = start;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const uint32_t c = lds[w * n + tid];
+            lds[w * n + tid] = at;
+            at += c;
+        }
+        for (uint32_t i = 0; i < tiles; ++i) a.tiles[tile + i] = ExTile{tid, start + i * size, min(size, m - i * size), 0};
+    }
+    if (tid == blockDim.x - 1) *a.ntiles = tile + tiles;
+    __syncthreads();
+    uint32_t bits = 0;
+    while ((1u << bits) < n) ++bits;
+    for (uint32_t i = 0; i < steps; ++i) {
+        const uint32_t s = from + i * 64 + lane;
+        const uint32_t e = s < a.slots ? static_cast<uint32_t>(a.experts[s]) : ~0u;
+        const bool in = e < n;
+        uint64_t same = __ballot(in);
+        for (uint32_t b = 0; b < bits; ++b) {
+            const uint64_t has = __ballot((e >> b) & 1);
+            same &= (e >> b) & 1 ? has : ~has;
+        }
+        const uint32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+        uint32_t at = 0;
+        if (in) at = mine[e] + rank;
+        asm volatile("" ::: "memory");  // one wave's LDS accesses run in order
+        if (in && (same >> lane) == 1) mine[e] = at + 1;  // the last of them
+        asm volatile("" ::: "memory");
+        if (in) {
+            a.slot_of[at] = s;
+            a.token_of[at] = s / a.k;
+        }
+        if (s < a.slots) a.place_of[s] = in ? static_cast<int32_t>(at) : -1;
+    }
+}
+
+// ------------------------------------------------------------------------------- by token
+struct GatherArgs {
+    const float *S;        // [splits][slots][lds]
+    uint64_t split_stride;
+    uint32_t splits, lds, k, width;
+    uint64_t tokens;
+    const int32_t *place_of;
+    uint16_t *Y;
+    uint64_t ldy;
+    uint32_t vec;
+};
+
+// Y[t] = the sum of its slots' results, in the slots' order.  A thread has 4 columns of a token.
+__global__ __launch_bounds__(256) void k_gather(const GatherArgs a) {
+    const uint32_t c = (blockIdx.x * 256 + threadIdx.x) * 4;
+    const uint64_t t = blockIdx.y + static_cast<uint64_t>(blockIdx.z) * gridDim.y;
+    if (c >= a.width || t >= a.tokens) return;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t j = 0; j < a.k; ++j) {
+        const int32_t at = a.place_of[t * a.k + j];
+        if (at < 0) continue;
+        const float *s = a.S + static_cast<uint64_t>(at) * a.lds + c;
+        for (uint32_t i = 0; i < a.splits; ++i) {
+            const f32x4_t x = *reinterpret_cast<const f32x4_t *>(s + i * a.split_stride);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += x[r];
+        }
+    }
+    uint16_t *y = a.Y + t * a.ldy + c;
+    if (a.vec && c + 4 <= a.width) {
+        *reinterpret_cast<u32x2 *>(y) = (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    } else {
+#pragma unroll
+        for (uint32_t r = 0; r < 4; ++r)
+            if (c + r < a.width) y[r] = to_bf16(v[r]);
+    }
+}
+
+// dweights from their parts over the hidden columns, a wave a slot.
+__global__ __launch_bounds__(256) void k_dweights(const float *__restrict__ parts, uint32_t n, const int32_t *__restrict__ place_of,
+                                                  uint32_t slots, float *__restrict__ dweights) {
+    const uint32_t s = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (s >= slots) return;
+    const int32_t at = place_of[s];
+    float v = 0.f;
+    if (at >= 0)
+        for (uint32_t i = lane; i < n; i += 64) v += parts[static_cast<uint64_t>(at) * n + i];
+    v = wave_sum(v);
+    if (lane == 0) dweights[s] = v;
+}
+
+template <typename T, int NPL>
+void route_as(const RouteArgs &a, bool wide, bool backward, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>((a.tokens + 3) / 4)), block(256);
+    const uint32_t lds = a.r.groups > 1 ? 4 * NPL * 64 * 8 : 0;
+    if (backward)
+        hipLaunchKernelGGL((k_route_bwd<T, NPL>), grid, block, 0, s, a);
+    else if (wide)
+        hipLaunchKernelGGL((k_route<T, NPL, true>), grid, block, lds, s, a);
+    else
+        hipLaunchKernelGGL((k_route<T, NPL, false>), grid, block, lds, s, a);
+}
+template <typename T>
+void route_of(const RouteArgs &a, bool wide, bool backward, hipStream_t s) {
+    const uint32_t E = a.r.experts;
+    if (E <= 64) route_as<T, 1>(a, wide, backward, s);
+    else if (E <= 128) route_as<T, 2>(a, wide, backward, s);
+    else if (E <= 256) route_as<T, 4>(a, wide, backward, s);
+    else if (E <= 512) route_as<T, 8>(a, wide, backward, s);
+    else route_as<T, 16>(a, wide, backward, s);
+}
+
+}  // namespace
+
+cbk_status launch_route(const cbk_router &r, const void *logits, int dtype, uint64_t ld, uint64_t tokens, const float *bias,
+                        int32_t *experts, float *weights, hipStream_t s) {
+    RouteArgs a{};
+    a.r = r;
+    a.logits = logits;
+    a.ld = ld;
+    a.tokens = tokens;
+    a.bias = bias;
+    a.experts = experts;
+    a.weights = weights;
+    const bool wide = bias || (r.groups > 1 && r.group_top == 2);
+    if (dtype == CBK_F32) route_of<float>(a, wide, false, s);
+    else route_of<uint16_t>(a, wide, false, s);
+    return launched();
+}
+
+cbk_status launch_route_bwd(const cbk_router &r, const void *logits, int dtype, uint64_t ld, uint64_t tokens,
+                            const int32_t *experts, const float *dweights, void *dlogits, uint64_t ldd, hipStream_t s) {
+    RouteArgs a{};
+    a.r = r;
+    a.logits = logits;
+    a.ld = ld;
+    a.tokens = tokens;
+    a.experts = const_cast<int32_t *>(experts);
+    a.dweights = dweights;
+    a.dlogits = dlogits;
+    a.ldd = ldd;
+    if (dtype == CBK_F32) route_of<float>(a, false, true, s);
+    else route_of<uint16_t>(a, false, true, s);
+    return launched();
+}
+
+// ------------------------------------------------------------------------------- the block of experts
+namespace {
+
+template <typename T>
+T *at(void *ws, uint64_t offset) { return reinterpret_cast<T *>(static_cast<unsigned char *>(ws) + offset); }
+
+bool vec16(const void *p, uint64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
+
+// What the products read of a matrix of tokens: itself where whole 64-wide slices of its rows can be copied 16
+// bytes at a time and the chunk's rows lie within 31 bits of bytes, else a padded copy in the workspace.
+cbk_status token_rows(const uint16_t *X, uint64_t ld, uint64_t T, uint64_t K, uint64_t Kp, uint16_t *P, const uint16_t *&A,
+                      uint32_t &lda, hipStream_t s) {
+    if (K == Kp && vec16(X, ld) && T * ld * 2 < 0x7F000000u) {
+        A = X;
+        lda = static_cast<uint32_t>(ld);
+        return CBK_OK;
+    }
+    A = P;
+    lda = static_cast<uint32_t>(Kp);
+    return launch_pad_rows(X, ld, T, static_cast<uint32_t>(K), static_cast<uint32_t>(Kp), P, s);
+}
+
+cbk_status gather(const float *S, uint64_t split_stride, uint32_t splits, uint64_t ldS, const int32_t *place_of, uint32_t k,
+                  uint64_t T, uint16_t *Y, uint64_t ldy, uint64_t width, hipStream_t s) {
+    GatherArgs g{S, split_stride, splits, static_cast<uint32_t>(ldS), k, static_cast<uint32_t>(width), T, place_of, Y, ldy,
+                 (reinterpret_cast<uintptr_t>(Y) & 7) == 0 && ldy % 4 == 0 ? 1u : 0u};
+    const uint32_t rows = static_cast<uint32_t>(std::min<uint64_t>(T, 32768));
+    hipLaunchKernelGGL(k_gather, dim3(static_cast<uint32_t>((width + 1023) / 1024), rows, static_cast<uint32_t>((T + rows - 1) / rows)), dim3(256), 0, s, g);
+    return launched();
+}
+
+}  // namespace
+
+cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, const uint16_t *X, uint64_t ldx, uint64_t T,
+                          const int32_t *experts, const float *weights, uint32_t k, const uint16_t *dY, uint64_t lddy,
+                          uint16_t *out, uint64_t ldo, float *dweights, void *ws, hipStream_t s) {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return CBK_E_HIP;
+    if (static_cast<uint32_t>(dev) != ex.device) return CBK_E_INVALID;
+    for (uint64_t c = 0; c < T; c += pl.Tc) {
+        const uint64_t n = std::min(pl.Tc, T - c);
+        SortArgs so{};
+        so.experts = experts + c * k;
+        so.slots = static_cast<uint32_t>(n * k);
+        so.k = k;
+        so.count = ex.count;
+        so.tile = pl.tile;
+        so.unit = pl.tile / 4;
+        so.token_of = at<uint32_t>(ws, pl.token_of);
+        so.slot_of = at<uint32_t>(ws, pl.slot_of);
+        so.place_of = at<int32_t>(ws, pl.place_of);
+        so.tiles = at<ExTile>(ws, pl.tiles);
+        so.ntiles = at<uint32_t>(ws, pl.ntiles);
+        hipLaunchKernelGGL(k_sort, dim3(1), dim3(64 * kSortWaves), kSortWaves * ex.count * 4, s, so);
+        cbk_status st = launched();
+        if (st != CBK_OK) return st;
+
+        ExArgs a{};
+        a.tiles = so.tiles;
+        a.ntiles = so.ntiles;
+        a.token_of = so.token_of;
+        a.slot_of = so.slot_of;
+        a.weights = weights + c * k;
+        a.act = act;
+        a.rows = static_cast<uint32_t>(ex.rows);
+        a.Fp = static_cast<uint32_t>(pl.Fp);
+        const ExTensor *table = static_cast<const ExTensor *>(ex.buffer);
+        const uint16_t *Xa;
+        uint32_t ldxa;
+        st = token_rows(X + c * ldx, ldx, n, ex.cols, pl.Kp, at<uint16_t>(ws, pl.xpack), Xa, ldxa, s);
+        if (st != CBK_OK) return st;
+        if (!dY) {
+            // H, and its product with down
+            ExArgs h = a;
+            h.t[0] = table;
+            h.t[1] = table + ex.count;
+            h.A = Xa;
+            h.lda = ldxa;
+            h.H = at<uint16_t>(ws, pl.h);
+            st = ex_hidden(h, pl, ex, false, s);
+            if (st != CBK_OK) return st;
+            ExArgs d = a;
+            d.t[0] = table + 2 * ex.count;
+            d.A = h.H;
+            d.lda = static_cast<uint32_t>(pl.Fp);
+            d.by_slot = 1;
+            d.scaled = 1;
+            d.S = at<float>(ws, pl.s);
+            st = ex_down(d, pl, ex, s);
+            if (st != CBK_OK) return st;
+            st = gather(d.S, pl.s_stride, pl.split_down, pl.ldO, so.place_of, k, n, out + c * ldo, ldo, ex.out, s);
+            if (st != CBK_OK) return st;
+            continue;
+        }
+        const uint16_t *Ya;
+        uint32_t ldya;
+        st = token_rows(dY + c * lddy, lddy, n, ex.out, pl.Op, at<uint16_t>(ws, pl.ypack), Ya, ldya, s);
+        if (st != CBK_OK) return st;
+        // D = dY . down, then dG and dU, then their product with gate and up
+        ExArgs d = a;
+        d.t[0] = table + 2 * ex.count;
+        d.A = Ya;
+        d.lda = ldya;
+        d.S = at<float>(ws, pl.d);
+        st = ex_down_t(d, pl, ex, s);
+        if (st != CBK_OK) return st;
+        ExArgs g = a;
+        g.t[0] = table;
+        g.t[1] = table + ex.count;
+        g.A = Xa;
+        g.lda = ldxa;
+        g.D = d.S;
+        g.G = at<uint16_t>(ws, pl.g);
+        g.dw = at<float>(ws, pl.dw);
+        st = ex_hidden(g, pl, ex, true, s);
+        if (st != CBK_OK) return st;
+        ExArgs x = a;
+        x.t[0] = table;
+        x.t[1] = table + ex.count;
+        x.A = g.G;
+        x.lda = static_cast<uint32_t>(2 * pl.Fp);
+        x.by_slot = 1;
+        x.S = at<float>(ws, pl.s);
+        st = ex_dx(x, pl, ex, s);
+        if (st != CBK_OK) return st;
+        st = gather(x.S, pl.s_stride, pl.split_x, pl.ldK, so.place_of, k, n, out + c * ldo, ldo, ex.cols, s);
+        if (st != CBK_OK) return st;
+        if (dweights) {
+            hipLaunchKernelGGL(k_dweights, dim3((so.slots + 3) / 4), dim3(256), 0, s, g.dw, pl.dw_parts, so.place_of, so.slots, dweights + c * k);
+            st = launched();
+            if (st != CBK_OK) return st;
+        }
+    }
+    return CBK_OK;
+}
+
+cbk_status experts_table(const cbk_tensor *gate, const cbk_tensor *up, const cbk_tensor *down, uint32_t count, void *buffer,
+                         uint32_t &device) {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return CBK_E_HIP;
+    device = static_cast<uint32_t>(dev);
+    ExTensor part[64];
+    const cbk_tensor *kinds[3] = {gate, up, down};
+    for (uint32_t kind = 0; kind < 3; ++kind)
+        for (uint32_t e = 0; e < count; e += 64) {
+            const uint32_t n = std::min<uint32_t>(64, count - e);
+            for (uint32_t i = 0; i < n; ++i) {
+                const cbk_tensor &t = kinds[kind][e + i];
+                part[i] = ExTensor{t.words, t.codebook, t.b ? cbk_words_for(t.rows * t.cols, t.b) * 4 : 0, t.U, t.b};
+            }
+            if (hipMemcpy(static_cast<ExTensor *>(buffer) + static_cast<uint64_t>(kind) * count + e, part, n * sizeof(ExTensor),
+                          hipMemcpyHostToDevice) != hipSuccess)
+                return CBK_E_HIP;
+        }
+    return CBK_OK;
+}
+
+}  // namespace cbk

@@ -1,0 +1,458 @@
+// The experts' products of cbk_moe.h for gfx950 (CDNA4): codebook-compressed weights of every expert that tokens were
+// routed to, decoded on the way to the matrix cores.
+//
+// Units of work.  A workgroup takes one token tile (up to BM slots of one expert, as k_sort cut them) and one tile of
+// 128 columns of the result: forward (NN false) 128 rows of a tensor, or 64 rows of gate and of up side by side (PAIR),
+// so that a lane has a hidden column's two sums; gradient (NN true) 128 columns of a tensor, over gate's rows and then
+// up's (PAIR).  It holds the sums of the whole reduction, so the operator's work is its epilogue and nothing is joined;
+// where units are few (splits) a reduction's shares lie side by side in S and are added by who reads them.  How many
+// tiles there are is known on the device alone: the grid covers the most there can be, and workgroups past them end.
+//
+// Widths.  The index width is read from the tensor's record and the same code takes all of 0 to 16: experts, and the two
+// tensors of a pair, may differ in it, which tensors of some 2^12 distinct patterns do by chance.  Fields are taken in
+// groups of 4, at most 64 bits: 3 dwords cover a group wherever it starts; 12 operations find its four table offsets.
+// (Static widths would save some of the shifts, and would need a launch for each width among the experts.)  Tables lie in
+// LDS; those of 2^15 and 2^16 entries do not fit beside the slices and are read through the caches (GT).
+//
+// Slices.  The reduction is walked in slices of 64: while one is multiplied, the tokens' part of the next is copied
+// straight into LDS and the workgroup's 512 lanes decode 16 fields of it each into the same layout as k_fused's
+// (cbk_nn_fused.h).  Two buffers, one barrier a slice.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "cbk_moe_device.h"
+
+namespace cbk {
+namespace {
+
+constexpr uint32_t kColumns = 128;  // of a tile
+enum Epi { kSum, kHidden, kHiddenBwd };
+
+constexpr int waves_n(int BM) { return BM >= 192 ? 2 : 4; }
+constexpr uint32_t slice_bytes(int BM) { return (BM + kColumns) * 128; }
+
+// A tensor's table of 2^b entries, those from U on corrupt, into LDS by all threads.
+__device__ __forceinline__ void stage_table(unsigned char *to, const ExTensor &T, uint32_t tid, uint32_t threads) {
+    const uint32_t n = 1u << T.b;
+    uint16_t *table = reinterpret_cast<uint16_t *>(to);
+    if ((reinterpret_cast<uintptr_t>(T.cb) & 15) == 0) {
+        const uint32_t whole = T.U / 8;
+        for (uint32_t i = tid; i < whole; i += threads) reinterpret_cast<u32x4 *>(table)[i] = reinterpret_cast<const u32x4 *>(T.cb)[i];
+        for (uint32_t i = whole * 8 + tid; i < n; i += threads) table[i] = i < T.U ? T.cb[i] : kCorrupt;
+    } else {
+        for (uint32_t i = tid; i < n; i += threads) table[i] = i < T.U ? T.cb[i] : kCorrupt;
+    }
+}
+
+// Twice the four fields (byte offsets into a table) of b bits that start at bit `shift` of d; m2 = 2 (2^b - 1).
+__device__ __forceinline__ void fields4(u32x3 d, uint32_t shift, uint32_t b, uint32_t m2, uint32_t (&off)[4]) {
+    const uint32_t lo = __builtin_amdgcn_alignbit(d.y, d.x, shift), hi = __builtin_amdgcn_alignbit(d.z, d.y, shift);
+    off[0] = (lo << 1) & m2;
+    off[1] = __builtin_amdgcn_alignbit(hi, lo, b - 1) & m2;
+    off[2] = __builtin_amdgcn_alignbit(hi, lo, 2 * b - 1) & m2;
+    off[3] = static_cast<uint32_t>(((static_cast<uint64_t>(hi) << 32) | lo) >> ((3 * b - 1) & 63)) & m2;
+}
+
+// A value that is the same in every lane, in scalar registers.
+__device__ __forceinline__ uint64_t in_scalars(uint64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(v)));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(v >> 32)));
+    return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+// Keeps memory loads and copies into LDS in the order in which they stand (see k_fused's).
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x78F); }
+
+// Column fragments by transposing reads (see k_fused's).
+template <int HI, int OFF, int N>
+__device__ __forceinline__ void read_columns(bf16x8_t (&x)[N], const uint32_t (&at)[N]) {
+    static_assert(N == 2 || N == 4, "two or four column fragments");
+    u32x2 a[N], b[N];
+    if constexpr (N == 2) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %4 offset:%c6\n"
+            "ds_read_b64_tr_b16 %1, %4 offset:%c7\n"
+            "ds_read_b64_tr_b16 %2, %5 offset:%c6\n"
+            "ds_read_b64_tr_b16 %3, %5 offset:%c7\n"
+            "s_waitcnt lgkmcnt(0)\n"
+            : "=&v"(a[0]), "=&v"(b[0]), "=&v"(a[1]), "=&v"(b[1])
+            : "v"(at[0]), "v"(at[1]), "i"(OFF), "i"(OFF + HI)
+            : "memory");
+    } else {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8 offset:%c12\n"
+            "ds_read_b64_tr_b16 %1, %8 offset:%c13\n"
+            "ds_read_b64_tr_b16 %2, %9 offset:%c12\n"
+            "ds_read_b64_tr_b16 %3, %9 offset:%c13\n"
+            "ds_read_b64_tr_b16 %4, %10 offset:%c12\n"
+            "ds_read_b64_tr_b16 %5, %10 offset:%c13\n"
+            "ds_read_b64_tr_b16 %6, %11 offset:%c12\n"
+            "ds_read_b64_tr_b16 %7, %11 offset:%c13\n"
+            "s_waitcnt lgkmcnt(0)\n"
+            : "=&v"(a[0]), "=&v"(b[0]), "=&v"(a[1]), "=&v"(b[1]), "=&v"(a[2]), "=&v"(b[2]), "=&v"(a[3]), "=&v"(b[3])
+            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "i"(OFF), "i"(OFF + HI)
+            : "memory");
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __builtin_bit_cast(bf16x8_t, (u32x4){a[i].x, a[i].y, b[i].x, b[i].y});
+}
+
+template <int BM, bool NN, bool PAIR, int EPI, bool GT>
+__global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
+    constexpr int WN = waves_n(BM), WM = 8 / WN;
+    constexpr int FM = BM / WM / 16, FN = kColumns / WN / 16;
+    constexpr uint32_t XBYTES = BM * 128, SLICE = slice_bytes(BM);
+    constexpr uint32_t NL = 4;  // loads of a lane's words
+    static_assert(EPI == kSum || (PAIR && !NN), "gate and up side by side");
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    unsigned char *ring = smem + (GT ? 0 : (PAIR ? 2 : 1) * p.table);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t li = lane & 15, lg = lane >> 4;
+    const int wm = wave / WN, wn = wave % WN;
+
+    // Units in order of token tile, column tile and share; an XCD (workgroups go to the 8 of them in turn) gets a run of
+    // them, whose tokens its L2 keeps.
+    const uint32_t units = *p.ntiles * p.col_tiles * p.splits, per = (units + 7) / 8;
+    const uint32_t unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || unit >= units) return;
+    const uint32_t share = unit % p.splits, col_tile = unit / p.splits % p.col_tiles;
+    const ExTile tile = p.tiles[unit / p.splits / p.col_tiles];
+    const ExTensor T0 = p.t[0][tile.expert], T1 = PAIR ? p.t[1][tile.expert] : T0;
+
+    // this lane's task in a slice: 16 fields of a row
+    const uint32_t trow = NN ? tid >> 3 : tid >> 2, tgrp = NN ? tid & 7 : tid & 3;
+    const uint32_t swz = NN ? 2 * (trow & 3) + 8 * ((trow >> 3) & 1) : trow & 7;
+    const uint32_t wrow = trow * (NN ? 256u : 128u);
+    // copies of the tokens' part: 8 rows by a wave, rows past the tile's end repeat the last one
+    constexpr int IX = BM / 64;
+    uint32_t vx[IX];
+#pragma unroll
+    for (int i = 0; i < IX; ++i) {
+        const uint32_t r = min(static_cast<uint32_t>((i * 8 + wave) * 8 + (lane >> 3)), tile.count - 1);
+        const uint32_t row = p.by_slot ? r : p.token_of[tile.start + r];
+        vx[i] = row * p.lda * 2 + ((lane & 7) ^ (lane >> 3)) * 16;
+    }
+    const auto rx = wave_rsrc(p.A + (p.by_slot ? static_cast<uint64_t>(tile.start) * p.lda : 0), 0x7FFFFFF0u);
+    // fragment reads; fragment i of this wave is tokens 16 (i WM + wm) and on
+    const uint32_t fa = (wm * 16 + li) * 128 + ((lg ^ (li & 7)) * 16);
+    const uint32_t fb = (wn * (kColumns / WN) + li) * 128 + ((lg ^ (li & 7)) * 16);
+    uint32_t ft[FN];
+    if constexpr (NN) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t r = 8 * lg + (li >> 2);
+            const uint32_t c = (wn * (kColumns / WN) + 16 * j) / 8 + ((li & 3) >> 1);
+            ft[j] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((CBK_LDS unsigned char *)(ring))) + XBYTES + r * 256 + (c ^ (2 * (r & 3) + 8 * (lg & 1))) * 16 + (li & 1) * 8;
+        }
+    }
+
+    f32x4_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+
+    const uint32_t all = p.slices * (NN && PAIR ? 2 : 1);  // the reduction's slices, of which this share's:
+    const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(all) * share / p.splits);
+    const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(all) * (share + 1) / p.splits);
+    if constexpr (!GT) {
+        stage_table(smem, T0, tid, 512);
+        if (PAIR) stage_table(smem + p.table, T1, tid, 512);
+    }
+
+    // The reduction over slices [s0, s1) of tensor `which` (forward pairs: the wave's own of the two).
+    auto pass = [&](uint32_t which, uint32_t s0, uint32_t s1, auto active) __attribute__((always_inline)) {
+        constexpr int NF = decltype(active)::value;          // fragments of tokens that there are
+        constexpr int NC = BM == 256 ? NF : 1;               // copies of 64 tokens
+        const ExTensor &T = which ? T1 : T0;
+        const uint32_t b = __builtin_amdgcn_readfirstlane(T.b), m2 = ((1u << b) - 1) << 1;
+        const unsigned char *table = smem + which * p.table;
+        // where this lane's fields start: a row (a base on a dword), and the bits after it
+        const uint32_t row0 = NN ? s0 * 64 : PAIR ? col_tile * 64 : col_tile * kColumns;
+        const uint32_t cols = NN ? p.N : p.R;
+        const uint64_t base = static_cast<uint64_t>(row0) * cols * b;
+        const uint32_t trel = NN || !PAIR ? trow : 16 * (trow >> 5) + (trow & 15);
+        const uint32_t bit = (trel * cols + (NN ? col_tile * kColumns : s0 * 64) + tgrp * 16) * b + (static_cast<uint32_t>(base) & 31u);
+        uint32_t first[4], shift[4];
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) {
+            first[q] = ((bit + 4 * q * b) >> 5) * 4;
+            shift[q] = (bit + 4 * q * b) & 31u;
+        }
+        const uint64_t start = (base >> 5) * 4, step = NN ? static_cast<uint64_t>(cols) * (8 * b) : 8 * b;
+        uint64_t words_at = in_scalars(reinterpret_cast<uint64_t>(T.words) + start), rest = in_scalars(T.bytes > start ? T.bytes - start : 0);
+        // kept in scalar registers: loading them again in the loop would wait for the LDS too
+        asm volatile("" : "+s"(words_at), "+s"(rest));
+        struct Words {
+            u32x3 q[4];
+        } w;
+        // The words of slice s; what is past the stream's end reads as zeros.
+        auto load = [&](uint32_t s) {
+            const uint32_t n = s - s0;
+            const uint64_t at = NN ? n * step : 0, have = rest > at ? rest - at : 0;
+            const auto rs = wave_rsrc(reinterpret_cast<const unsigned char *>(words_at + (rest > at ? at : 0)),
+                                      static_cast<uint32_t>(min(have, static_cast<uint64_t>(0x7FFFFFF0u))));
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                w.q[q] = __builtin_amdgcn_raw_buffer_load_b96(rs, static_cast<int>(first[q] + (NN ? 0u : n * (8 * b))), 0, 0);
+        };
+        // Decodes them to the buffer at `to`; `masked`: terms past the reduction's end are zeros.
+        auto decode = [&](uint32_t s, uint32_t to, auto masked) {
+            uint32_t v[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t off[4];
+                fields4(w.q[q], shift[q], b, m2, off);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (GT)
+                        v[4 * q + i] = (off[i] >> 1) < T.U ? T.cb[off[i] >> 1] : kCorrupt;
+                    else
+                        v[4 * q + i] = *reinterpret_cast<const uint16_t *>(table + off[i]);
+                }
+            }
+            if constexpr (decltype(masked)::value) {
+                const uint32_t at = s * 64 + (NN ? trow : tgrp * 16), have = p.R > at ? p.R - at : 0u;
+#pragma unroll
+                for (uint32_t i = 0; i < 16; ++i) v[i] = (NN ? have > 0 : i < have) ? v[i] : 0u;
+            }
+            unsigned char *row = ring + to + XBYTES + wrow;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t *x = v + 8 * g;
+                *reinterpret_cast<u32x4 *>(row + ((tgrp * 2 + g) ^ swz) * 16) =
+                    (u32x4){x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16)};
+            }
+        };
+        auto copy = [&](uint32_t s, uint32_t to) {
+            const uint32_t from = (s + (NN && PAIR ? which * p.slices : 0u)) * 128;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) copy_to_lds(rx, ring + to + (i * 8 + wave) * 1024, vx[i], from);
+        };
+        struct Frags {
+            bf16x8_t a[NF], b[FN];
+        };
+        auto read = [&](Frags &f, uint32_t at, auto half) {
+            constexpr int KS = decltype(half)::value;
+            const unsigned char *sa = ring + at, *sb = sa + XBYTES;
+            if constexpr (NN) {
+                uint32_t t[FN];
+#pragma unroll
+                for (int j = 0; j < FN; ++j) t[j] = ft[j] + at;
+                read_columns<4 * 256, KS * 32 * 256>(f.b, t);
+            } else {
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    f.b[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sb + (fb ^ (KS * 64)) + j * 2048));
+            }
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+                f.a[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(sa + (fa ^ (KS * 64)) + i * (WM * 2048)));
+        };
+        auto multiply = [&](const Frags &f) {
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+        };
+        const std::integral_constant<int, 0> lower;
+        const std::integral_constant<int, 1> upper;
+        const std::true_type yes;
+        const std::false_type no;
+
+        copy(s0, 0);
+        keep_order();
+        load(s0);
+        lds_barrier();  // the tables
+        decode(s0, 0, yes);
+        keep_order();
+        load(min(s0 + 1, s1 - 1));
+        __builtin_amdgcn_s_waitcnt(GT ? 0x0070 : 0x0070 | NL);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        uint32_t now = 0;
+        // Slice s is multiplied; the next one (`more`) copied and decoded, and, unless that is the `last`, the words of
+        // the one after asked for.  At the end the copies have landed, and every word but those.
+        auto interval = [&](uint32_t s, auto more, auto last) {
+            constexpr bool MORE = decltype(more)::value, WORDS = MORE && !decltype(last)::value;
+            Frags f0, f1;
+            if constexpr (MORE) copy(s + 1, SLICE - now);
+            read(f0, now, lower);
+            read(f1, now, upper);
+            multiply(f0);
+            if constexpr (MORE) {
+                decode(s + 1, SLICE - now, last);
+                keep_order();
+                if constexpr (WORDS) load(s + 2);
+            }
+            multiply(f1);
+            if constexpr (MORE && !GT) {
+                constexpr int MF = 2 * NF * FN, RD = 16 + (NN ? 2 * NF : 2 * (NF + FN));
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, (RD + MF - 1) / MF, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 96 / MF, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(GT || !WORDS ? 0x0070 : 0x0070 | NL);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            now = SLICE - now;
+        };
+        uint32_t s = s0;
+        for (; s + 2 < s1; ++s) interval(s, yes, no);
+        if (s + 1 < s1) {
+            interval(s, yes, yes);
+            ++s;
+        }
+        interval(s, no, no);
+    };
+    // as many fragments as the tile has tokens for, in steps of 16 WM
+    auto passes = [&](auto active) {
+        if constexpr (NN && PAIR) {
+#pragma unroll 1
+            for (uint32_t which = c0 >= p.slices; which * p.slices < c1; ++which)
+                pass(which, max(c0, which * p.slices) - which * p.slices, min(c1, (which + 1) * p.slices) - which * p.slices, active);
+        } else {
+            pass(PAIR ? wave & 1 : 0, c0, c1, active);
+        }
+    };
+    const uint32_t frags = (tile.count + 16 * WM - 1) / (16 * WM);
+    if constexpr (FM == 2) {
+        if (frags == 1) passes(std::integral_constant<int, 1>{});
+        else passes(std::integral_constant<int, 2>{});
+    } else {
+        if (frags == 1) passes(std::integral_constant<int, 1>{});
+        else if (frags == 2) passes(std::integral_constant<int, 2>{});
+        else if (frags == 3) passes(std::integral_constant<int, 3>{});
+        else passes(std::integral_constant<int, 4>{});
+    }
+
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const uint32_t m = (i * WM + wm) * 16 + li;
+        const bool there = m < tile.count;
+        const uint64_t at = tile.start + (there ? m : 0);
+        if constexpr (EPI == kSum) {
+            if (!there) continue;
+            const float f = p.scaled ? p.weights[p.slot_of[at]] : 1.f;
+            float *out = p.S + share * p.split_stride + at * p.ldS + col_tile * kColumns + wn * (kColumns / WN) + 4 * lg;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4_t *>(out + 16 * j) = p.scaled ? acc[i][j] * f : acc[i][j];
+        } else if constexpr (EPI == kHidden) {
+            if (!there) continue;
+#pragma unroll
+            for (int j = 0; j < FN; j += 2) {
+                const uint32_t f = col_tile * 64 + (wn * (kColumns / WN) + 16 * j) / 2 + 4 * lg;
+                float h[4];
+#pragma unroll
+                for (uint32_t r = 0; r < 4; ++r) h[r] = f + r < p.rows ? activation(p.act, acc[i][j][r], nullptr) * acc[i][j + 1][r] : 0.f;
+                *reinterpret_cast<u32x2 *>(p.H + at * p.Fp + f) = (u32x2){pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
+            }
+        } else {
+            float sum = 0.f;  // <H, D> over this wave's columns
+            const float w = p.weights[p.slot_of[at]];
+#pragma unroll
+            for (int j = 0; j < FN; j += 2) {
+                const uint32_t f = col_tile * 64 + (wn * (kColumns / WN) + 16 * j) / 2 + 4 * lg;
+                f32x4_t d = *reinterpret_cast<const f32x4_t *>(p.D + at * p.ldD + f);
+                for (uint32_t k = 1; k < p.d_splits; ++k) d += *reinterpret_cast<const f32x4_t *>(p.D + k * p.d_stride + at * p.ldD + f);
+                float dg[4], du[4];
+#pragma unroll
+                for (uint32_t r = 0; r < 4; ++r) {
+                    float slope;
+                    const float a = activation(p.act, acc[i][j][r], &slope), u = acc[i][j + 1][r], dh = w * d[r];
+                    const bool in = f + r < p.rows;
+                    sum += in ? a * u * d[r] : 0.f;
+                    dg[r] = in ? dh * u * slope : 0.f;
+                    du[r] = in ? dh * a : 0.f;
+                }
+                if (there) {
+                    uint16_t *G = p.G + at * (2 * p.Fp) + f;
+                    *reinterpret_cast<u32x2 *>(G) = (u32x2){pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3])};
+                    *reinterpret_cast<u32x2 *>(G + p.Fp) = (u32x2){pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3])};
+                }
+            }
+            sum += __shfl_xor(sum, 16, 64);
+            sum += __shfl_xor(sum, 32, 64);
+            if (there && lg == 0) p.dw[at * p.dw_parts + col_tile * WN + wn] = sum;
+        }
+    }
+}
+
+template <int, bool, bool, int, bool>
+struct ExTag;
+
+template <int BM, bool NN, bool PAIR, int EPI, bool GT>
+cbk_status run(ExArgs &a, const ExPlan &pl, hipStream_t s) {
+    const uint32_t lds = (GT ? 0 : (PAIR ? 2 : 1) * a.table) + 2 * slice_bytes(BM);
+    if (!allow_lds_once<ExTag<BM, NN, PAIR, EPI, GT>>(k_experts<BM, NN, PAIR, EPI, GT>, kLdsLimit)) return CBK_E_HIP;
+    const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles * a.splits;
+    if (units > (uint64_t(1) << 30)) return CBK_E_UNSUPPORTED;
+    hipLaunchKernelGGL((k_experts<BM, NN, PAIR, EPI, GT>), dim3(static_cast<uint32_t>((units + 7) / 8 * 8)), dim3(512), lds, s, a);
+    return launched();
+}
+
+template <bool NN, bool PAIR, int EPI>
+cbk_status product(ExArgs &a, const ExPlan &pl, uint32_t b, hipStream_t s) {
+    a.table = std::max(16u, 2u << b);
+    if (b > 14) return run<64, NN, PAIR, EPI, true>(a, pl, s);
+    return pl.tile == 256 ? run<256, NN, PAIR, EPI, false>(a, pl, s) : run<64, NN, PAIR, EPI, false>(a, pl, s);
+}
+
+uint32_t tiles_of(uint64_t n, uint64_t m) { return static_cast<uint32_t>((n + m - 1) / m); }
+
+}  // namespace
+
+cbk_status ex_hidden(ExArgs &a, const ExPlan &pl, const cbk_experts &ex, bool backward, hipStream_t s) {
+    a.N = static_cast<uint32_t>(ex.rows);
+    a.R = static_cast<uint32_t>(ex.cols);
+    a.col_tiles = static_cast<uint32_t>(pl.Fp / 64);
+    a.slices = static_cast<uint32_t>(pl.Kp / 64);
+    a.splits = 1;
+    a.ldD = static_cast<uint32_t>(pl.ldF);
+    a.d_splits = pl.split_dt;
+    a.d_stride = pl.d_stride;
+    a.dw_parts = pl.dw_parts;
+    return backward ? product<false, true, kHiddenBwd>(a, pl, ex.b, s) : product<false, true, kHidden>(a, pl, ex.b, s);
+}
+
+cbk_status ex_down(ExArgs &a, const ExPlan &pl, const cbk_experts &ex, hipStream_t s) {
+    a.N = static_cast<uint32_t>(ex.out);
+    a.R = static_cast<uint32_t>(ex.rows);
+    a.col_tiles = tiles_of(ex.out, kColumns);
+    a.slices = static_cast<uint32_t>(pl.Fp / 64);
+    a.splits = pl.split_down;
+    a.ldS = static_cast<uint32_t>(pl.ldO);
+    a.split_stride = pl.s_stride;
+    return product<false, false, kSum>(a, pl, ex.b_down, s);
+}
+
+cbk_status ex_down_t(ExArgs &a, const ExPlan &pl, const cbk_experts &ex, hipStream_t s) {
+    a.N = static_cast<uint32_t>(ex.rows);
+    a.R = static_cast<uint32_t>(ex.out);
+    a.col_tiles = tiles_of(ex.rows, kColumns);
+    a.slices = static_cast<uint32_t>(pl.Op / 64);
+    a.splits = pl.split_dt;
+    a.ldS = static_cast<uint32_t>(pl.ldF);
+    a.split_stride = pl.d_stride;
+    return product<true, false, kSum>(a, pl, ex.b_down, s);
+}
+
+cbk_status ex_dx(ExArgs &a, const ExPlan &pl, const cbk_experts &ex, hipStream_t s) {
+    a.N = static_cast<uint32_t>(ex.cols);
+    a.R = static_cast<uint32_t>(ex.rows);
+    a.col_tiles = tiles_of(ex.cols, kColumns);
+    a.slices = static_cast<uint32_t>(pl.Fp / 64);
+    a.splits = pl.split_x;
+    a.ldS = static_cast<uint32_t>(pl.ldK);
+    a.split_stride = pl.s_stride;
+    return product<true, true, kSum>(a, pl, ex.b, s);
+}
+
+}  // namespace cbk

@@ -35,33 +35,6 @@ inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<ui
 
 // ------------------------------------------------------------------------------- small pieces
 
-// fp32 to BF16, to nearest even (NaN stays NaN).
-__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    return static_cast<uint32_t>(to_bf16(a)) | (static_cast<uint32_t>(to_bf16(b)) << 16);
-}
-
-// act(z) and, where D is not null, act'(z), in fp32.  The tails are formed without subtractions
-// of nearly equal numbers: 1 - tanh and 1 - erf come from a logistic function and from erfc.
-__device__ __forceinline__ float activation(int act, float z, float *D) {
-    if (act == CBK_ACT_SILU) {
-        const float s = 1.f / (1.f + __expf(-z));
-        if (D) *D = s * (1.f + z * (1.f - s));
-        return z * s;
-    }
-    if (act == CBK_ACT_GELU) {
-        const float p = 0.5f * erfcf(z * -0.70710678118654752f);
-        if (D) *D = p + z * 0.39894228040143268f * __expf(-0.5f * z * z);
-        return z * p;
-    }
-    // (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y)); past |z| = 16 it is 0 or 1 to every bit and z^3 might overflow
-    const float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float w = z > 16.f ? 16.f : z < -16.f ? -16.f : z;  // NaN stays NaN, where fmaxf and fminf would drop it
-    const float s = 1.f / (1.f + __expf(-c * (w + 0.044715f * w * w * w)));
-    if (D) *D = s + w * s * (1.f - s) * c * (1.f + 3.f * 0.044715f * w * w);
-    return z * s;
-}
-
 // X [T][K] with leading dimension ld into P [T][Kp], columns past K zero.
 __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t *__restrict__ X, uint64_t ld, uint64_t T, uint32_t K,
                                                   uint32_t Kp, uint16_t *__restrict__ P) {
@@ -1232,6 +1205,11 @@ Weights weights_of(NnOp op, const cbk_tensor *a, const cbk_tensor *b, uint64_t T
 }
 
 }  // namespace
+
+cbk_status launch_pad_rows(const uint16_t *X, uint64_t ld, uint64_t T, uint32_t K, uint32_t Kp, uint16_t *P, hipStream_t s) {
+    hipLaunchKernelGGL(k_pad_rows, dim3(grid_for(T * (Kp / 4), 256)), dim3(256), 0, s, X, ld, T, K, Kp, P);
+    return launched();
+}
 
 cbk_status launch_linear(const cbk_tensor &t, const uint16_t *X, uint64_t ldx, uint64_t T, uint16_t *Y, uint64_t ldy,
                          void *ws, hipStream_t s) {

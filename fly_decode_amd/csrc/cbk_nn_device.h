@@ -1,5 +1,5 @@
-// What the kernels of the operators in cbk_nn.h share (cbk_nn.hip, cbk_nn_fused.h): copies into LDS,
-// and the arguments of the product that decodes on the way.
+// What the kernels of the operators in cbk_nn.h and cbk_moe.h share: rounding, activations, copies into LDS,
+// and the arguments of the product that decodes on the way (cbk_nn_fused.h).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -46,6 +46,33 @@ typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
 __device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
     return a / b;
+}
+
+// fp32 to BF16, to nearest even (NaN stays NaN).
+__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return static_cast<uint32_t>(to_bf16(a)) | (static_cast<uint32_t>(to_bf16(b)) << 16);
+}
+
+// act(z) and, where D is not null, act'(z), in fp32.  The tails are formed without subtractions
+// of nearly equal numbers: 1 - tanh and 1 - erf come from a logistic function and from erfc.
+__device__ __forceinline__ float activation(int act, float z, float *D) {
+    if (act == CBK_ACT_SILU) {
+        const float s = 1.f / (1.f + __expf(-z));
+        if (D) *D = s * (1.f + z * (1.f - s));
+        return z * s;
+    }
+    if (act == CBK_ACT_GELU) {
+        const float p = 0.5f * erfcf(z * -0.70710678118654752f);
+        if (D) *D = p + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+        return z * p;
+    }
+    // (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y)); past |z| = 16 it is 0 or 1 to every bit and z^3 might overflow
+    const float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+    const float w = z > 16.f ? 16.f : z < -16.f ? -16.f : z;  // NaN stays NaN, where fmaxf and fminf would drop it
+    const float s = 1.f / (1.f + __expf(-c * (w + 0.044715f * w * w * w)));
+    if (D) *D = s + w * s * (1.f - s) * c * (1.f + 3.f * 0.044715f * w * w);
+    return z * s;
 }
 
 // Copies 16 bytes a lane from the resource (at the lane's voff plus the wave's soff) straight into

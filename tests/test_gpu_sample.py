@@ -1,0 +1,150 @@
+"""GPU tests of cbk_sample.h against a plain reference in 64 bits (moe_reference.sample): the token has to be the same."""
+import math
+
+import pytest
+
+import moe_reference as moe
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    import fly_decode_amd as cbk
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    cbk.load_library()
+    return torch, cbk
+
+
+def check(torch, cbk, z, u, what="", **settings):
+    """`settings`: numbers, or lists with one for each row."""
+    T = z.shape[0]
+    given = {}
+    for name, v in settings.items():
+        given[name] = torch.tensor(v, dtype=torch.int32 if name == "top_k" else torch.float32).cuda() if isinstance(v, list) else v
+    token, logprob = cbk.sample(z.cuda(), u.cuda(), **given)
+    token, logprob = token.cpu().tolist(), logprob.cpu().tolist()
+    for t in range(T):
+        row = {name: float(torch.tensor(v[t] if isinstance(v, list) else v, dtype=torch.float32)) for name, v in settings.items()}
+        row.setdefault("temperature", 1.0)
+        want, log = moe.sample(z[t].tolist(), float(u[t]), **row)
+        assert token[t] == want, (what, t, row, token[t], want)
+        if math.isnan(log):
+            assert math.isnan(logprob[t])
+        else:  # formed in 64 bits and rounded once
+            assert abs(logprob[t] - log) <= 2.0 ** -24 * abs(log) + 1e-11, (what, t, logprob[t], log)
+
+
+def draws(torch, T, V, dtype, seed, spread=2.5):
+    g = torch.Generator().manual_seed(seed)
+    z = spread * torch.randn(T, V, generator=g)
+    z[torch.rand(T, V, generator=g) < 0.02] = -math.inf
+    z[:, V // 2] = 0.5
+    return z.to(dtype), torch.rand(T, generator=g)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("V", [1, 2, 5, 64, 255, 1000, 4099, 33000])
+def test_sample(env, V, dtype):
+    torch, cbk = env
+    T = 12
+    z, u = draws(torch, T, V, getattr(torch, dtype), 1)
+    check(torch, cbk, z, u, "temperature", temperature=0.8)
+    check(torch, cbk, z, u, "greedy", temperature=0.0)
+    for k in (1, 7, 50, 2500):
+        check(torch, cbk, z, u, "top_k", top_k=k)
+    for p in (0.0, 0.3, 0.9, 0.999):
+        check(torch, cbk, z, u, "top_p", temperature=1.3, top_p=p)
+    for m in (1e-6, 0.05, 1.0, 2.0):
+        check(torch, cbk, z, u, "min_p", min_p=m)
+    check(torch, cbk, z, u, "all", temperature=[0.0, 0.5, 1.0, 2.0, 1e-3, 50.0] * 2, top_k=[0, 3, 40, -1] * 3, top_p=[0.5, 0.95, 1.0] * 4,
+          min_p=[0.0, 0.01, 0.2, 0.0, 0.001, 0.0] * 2)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_sample_ties(env, dtype):
+    """Many equal logits: a cut in the middle of them goes by index, also where they are too many to sort."""
+    torch, cbk = env
+    g = torch.Generator().manual_seed(2)
+    z = torch.randint(-3, 4, (10, 9000), generator=g).float()
+    z[0] = 1.0
+    z[1] = 0.0
+    z[1, ::3] = -0.0
+    u = torch.rand(10, generator=g)
+    z = z.to(getattr(torch, dtype))
+    for kw in ({"top_k": 100}, {"top_k": 2000}, {"top_k": 8999}, {"top_p": 0.1}, {"top_p": 0.7, "top_k": 3000}, {"top_p": 0.5, "min_p": 0.3}):
+        check(torch, cbk, z, u, str(kw), **kw)
+
+
+def test_sample_extremes(env):
+    torch, cbk = env
+    low, inf = torch.finfo(torch.float32).min, math.inf
+    z = torch.randn(14, 300, generator=torch.Generator().manual_seed(3))
+    z[0] = -inf
+    z[1] = -inf
+    z[1, 299] = 3.0
+    z[2] = low
+    z[3, 10:] = low
+    z[4, 7] = math.nan
+    z[5, 3] = inf
+    z[6, 5:9] = inf
+    z[7] = -inf
+    z[7, 0] = low
+    z[8] *= 1e4
+    z[9] *= 1e-30
+    z[10] = torch.linspace(-80, 0, 300)
+    z[11, 100] = 1e30
+    z[12, 50:] = -inf
+    z[13] = -1e38
+    u = torch.rand(14, generator=torch.Generator().manual_seed(4))
+    for kw in ({}, {"temperature": 0.0}, {"top_k": 5}, {"top_p": 0.5}, {"min_p": 0.1}, {"temperature": 1e-20, "top_p": 0.9},
+               {"temperature": inf, "top_p": 0.4}, {"temperature": math.nan}, {"top_k": 200, "top_p": 0.99, "min_p": 1e-8}):
+        check(torch, cbk, z, u, str(kw), **kw)
+
+
+def test_sample_uniform_at_its_ends(env):
+    torch, cbk = env
+    z, _ = draws(torch, 8, 3000, torch.float32, 5)
+    for v in (0.0, 1.0 - 2.0 ** -24, 1.0, 7.0, -1.0, math.nan):
+        u = torch.full((8,), v)
+        check(torch, cbk, z, u, v)
+        check(torch, cbk, z, u, v, top_k=20, top_p=0.8)
+
+
+def test_sample_rows_anywhere(env):
+    """Rows that start on any element, with a stride; what surrounds them is not read."""
+    torch, cbk = env
+    for dtype in (torch.float32, torch.bfloat16):
+        z, u = draws(torch, 9, 701, dtype, 6)
+        for at in range(5):
+            big = torch.full((9, 713), math.nan, dtype=dtype)
+            big[:, at: at + 701] = z
+            d = big.cuda()
+            got = cbk.sample(d[:, at: at + 701], u.cuda(), top_k=50, top_p=0.9)
+            want = cbk.sample(z.cuda(), u.cuda(), top_k=50, top_p=0.9)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_sample_the_largest_vocabulary(env):
+    torch, cbk = env
+    V = 1 << 20
+    z, u = draws(torch, 3, V, torch.float32, 7)
+    token, logprob = cbk.sample(z.cuda(), u.cuda())
+    p = torch.softmax(z.double(), 1)
+    c = p.cumsum(1)
+    want = (c <= u.double()[:, None] * c[:, -1:]).sum(1)
+    assert torch.equal(token.cpu(), want)
+    assert bool(((logprob.cpu().double() - p.gather(1, want[:, None]).log()[:, 0]).abs() < 2e-6).all())
+    got, _ = cbk.sample(z.cuda(), u.cuda(), top_k=3)
+    assert bool((z.gather(1, got.cpu()[:, None]) >= z.topk(3)[0][:, -1:]).all())
+
+
+def test_sample_draws_as_often_as_its_probabilities(env):
+    torch, cbk = env
+    z = torch.tensor([0.0, 1.0, -1.0, 2.0, 0.5])
+    n = 20000
+    u = (torch.arange(n) + 0.5) / n  # evenly over [0, 1)
+    token, _ = cbk.sample(z.expand(n, 5).contiguous().cuda(), u.cuda(), temperature=0.7)
+    share = torch.bincount(token.cpu(), minlength=5) / n
+    assert bool(((share - torch.softmax(z / 0.7, 0)).abs() <= 1.5 / n).all())  # each interval's ends
