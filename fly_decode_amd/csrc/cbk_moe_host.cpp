@@ -76,7 +76,8 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
     const uint64_t most = std::max<uint64_t>(1, std::min<uint64_t>({kSlots / k, kSlotBytes / (per_slot * k), (uint64_t(1) << 29) / std::max(p.Kp, p.Op)}));
     p.Tc = std::min(tokens, most);
     const uint64_t slots = p.Tc * k, active = std::min<uint64_t>(ex.count, slots);
-    p.tile = std::max(ex.b, ex.b_down) > 14 || slots / active <= 48 ? 64 : 256;
+    // tiles of 256 where the LDS holds their tables: two of gate and up, one of down
+    p.tile = ex.b <= 13 && ex.b_down <= 14 && slots / active > 48 ? 256 : 64;
     p.max_tiles = static_cast<uint32_t>(active + slots / p.tile);
     // few units of work: their reductions are shared until there are two for each CU, of eight slices of 64 at least
     auto split = [&](uint64_t columns, uint64_t slices) {
@@ -109,7 +110,8 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
         p.g = take(slots * p.Fp * 4);
         p.s_stride = slots * p.ldK;
         p.s = take(p.split_x * p.s_stride * 4);
-        p.dw_parts = static_cast<uint32_t>(p.Fp / 64 * (p.tile == 256 ? 2 : 4));
+        // a partial sum for each wave that a row's columns are spread over: 64 columns of 256, or 16 of 64
+        p.dw_parts = static_cast<uint32_t>(p.tile == 256 ? up_to(p.Fp, 128) / 64 : p.Fp / 16);
         p.dw = take(slots * p.dw_parts * 4);
     }
     p.bytes = at;

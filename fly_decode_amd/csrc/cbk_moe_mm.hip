@@ -100,6 +100,65 @@ __device__ __forceinline__ void read_columns(bf16x8_t (&x)[N], const uint32_t (&
     for (int i = 0; i < N; ++i) x[i] = __builtin_bit_cast(bf16x8_t, (u32x4){a[i].x, a[i].y, b[i].x, b[i].y});
 }
 
+// What becomes of a wave's sums of one token (of a tile's token m): FN fragments of 16 columns, of which this lane has
+// columns 4 lg .. 4 lg + 3, from column FN 16 wn of the tile on (the tile has `wn_count` such parts).  Forward pairs
+// have a fragment of gate and then one of up, of the same rows.
+template <int EPI, int FN>
+__device__ __forceinline__ void finish(const ExArgs &p, const f32x4_t (&acc)[FN], const ExTile &tile, uint32_t m, uint32_t share,
+                                       uint32_t col_tile, uint32_t wn, uint32_t wn_count, uint32_t lg) {
+    const bool there = m < tile.count;
+    const uint64_t at = tile.start + (there ? m : 0);
+    if constexpr (EPI == kSum) {
+        if (!there) return;
+        const uint32_t n = (col_tile * wn_count + wn) * (FN * 16) + 4 * lg;
+        const float f = p.scaled ? p.weights[p.slot_of[at]] : 1.f;
+        float *out = p.S + share * p.split_stride + at * p.ldS + n;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            if (n + 16 * j < p.ldS) *reinterpret_cast<f32x4_t *>(out + 16 * j) = p.scaled ? acc[j] * f : acc[j];
+    } else {
+        const uint32_t f0 = (col_tile * wn_count + wn) * (FN * 8) + 4 * lg;
+        float sum = 0.f, w = 0.f;  // <H, D> over this wave's columns; the slot's weight
+        if constexpr (EPI == kHiddenBwd) w = p.weights[p.slot_of[at]];
+#pragma unroll
+        for (int j = 0; j < FN; j += 2) {
+            const uint32_t f = f0 + 8 * j;
+            if (f >= p.Fp) continue;
+            const f32x4_t g = acc[j], u = acc[j + 1];
+            if constexpr (EPI == kHidden) {
+                if (!there) continue;
+                float h[4];
+#pragma unroll
+                for (uint32_t r = 0; r < 4; ++r) h[r] = f + r < p.rows ? activation(p.act, g[r], nullptr) * u[r] : 0.f;
+                *reinterpret_cast<u32x2 *>(p.H + at * p.Fp + f) = (u32x2){pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
+            } else {
+                f32x4_t d = *reinterpret_cast<const f32x4_t *>(p.D + at * p.ldD + f);
+                for (uint32_t k = 1; k < p.d_splits; ++k) d += *reinterpret_cast<const f32x4_t *>(p.D + k * p.d_stride + at * p.ldD + f);
+                float dg[4], du[4];
+#pragma unroll
+                for (uint32_t r = 0; r < 4; ++r) {
+                    float slope;
+                    const float a = activation(p.act, g[r], &slope), dh = w * d[r];
+                    const bool in = f + r < p.rows;
+                    sum += in ? a * u[r] * d[r] : 0.f;
+                    dg[r] = in ? dh * u[r] * slope : 0.f;
+                    du[r] = in ? dh * a : 0.f;
+                }
+                if (there) {
+                    uint16_t *G = p.G + at * (2 * p.Fp) + f;
+                    *reinterpret_cast<u32x2 *>(G) = (u32x2){pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3])};
+                    *reinterpret_cast<u32x2 *>(G + p.Fp) = (u32x2){pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3])};
+                }
+            }
+        }
+        if constexpr (EPI == kHiddenBwd) {
+            sum += __shfl_xor(sum, 16, 64);
+            sum += __shfl_xor(sum, 32, 64);
+            if (there && lg == 0) p.dw[at * p.dw_parts + col_tile * wn_count + wn] = sum;
+        }
+    }
+}
+
 template <int BM, bool NN, bool PAIR, int EPI, bool GT>
 __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
     constexpr int WN = waves_n(BM), WM = 8 / WN;
@@ -336,60 +395,281 @@ __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const uint32_t m = (i * WM + wm) * 16 + li;
-        const bool there = m < tile.count;
-        const uint64_t at = tile.start + (there ? m : 0);
-        if constexpr (EPI == kSum) {
-            if (!there) continue;
-            const float f = p.scaled ? p.weights[p.slot_of[at]] : 1.f;
-            float *out = p.S + share * p.split_stride + at * p.ldS + col_tile * kColumns + wn * (kColumns / WN) + 4 * lg;
-#pragma unroll
-            for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4_t *>(out + 16 * j) = p.scaled ? acc[i][j] * f : acc[i][j];
-        } else if constexpr (EPI == kHidden) {
-            if (!there) continue;
-#pragma unroll
-            for (int j = 0; j < FN; j += 2) {
-                const uint32_t f = col_tile * 64 + (wn * (kColumns / WN) + 16 * j) / 2 + 4 * lg;
-                float h[4];
-#pragma unroll
-                for (uint32_t r = 0; r < 4; ++r) h[r] = f + r < p.rows ? activation(p.act, acc[i][j][r], nullptr) * acc[i][j + 1][r] : 0.f;
-                *reinterpret_cast<u32x2 *>(p.H + at * p.Fp + f) = (u32x2){pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
-            }
-        } else {
-            float sum = 0.f;  // <H, D> over this wave's columns
-            const float w = p.weights[p.slot_of[at]];
-#pragma unroll
-            for (int j = 0; j < FN; j += 2) {
-                const uint32_t f = col_tile * 64 + (wn * (kColumns / WN) + 16 * j) / 2 + 4 * lg;
-                f32x4_t d = *reinterpret_cast<const f32x4_t *>(p.D + at * p.ldD + f);
-                for (uint32_t k = 1; k < p.d_splits; ++k) d += *reinterpret_cast<const f32x4_t *>(p.D + k * p.d_stride + at * p.ldD + f);
-                float dg[4], du[4];
-#pragma unroll
-                for (uint32_t r = 0; r < 4; ++r) {
-                    float slope;
-                    const float a = activation(p.act, acc[i][j][r], &slope), u = acc[i][j + 1][r], dh = w * d[r];
-                    const bool in = f + r < p.rows;
-                    sum += in ? a * u * d[r] : 0.f;
-                    dg[r] = in ? dh * u * slope : 0.f;
-                    du[r] = in ? dh * a : 0.f;
-                }
-                if (there) {
-                    uint16_t *G = p.G + at * (2 * p.Fp) + f;
-                    *reinterpret_cast<u32x2 *>(G) = (u32x2){pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3])};
-                    *reinterpret_cast<u32x2 *>(G + p.Fp) = (u32x2){pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3])};
-                }
-            }
-            sum += __shfl_xor(sum, 16, 64);
-            sum += __shfl_xor(sum, 32, 64);
-            if (there && lg == 0) p.dw[at * p.dw_parts + col_tile * WN + wn] = sum;
-        }
+        finish<EPI, FN>(p, acc[i], tile, m, share, col_tile, wn, WN, lg);
     }
 }
+
+// ------------------------------------------------------------------------------- many tokens
+// A tile of 256 tokens x 256 columns; the reduction in blocks of 64, two buffers of them in LDS.  What bounds it is the
+// LDS: the gathers of a block's 16384 fields take about what its multiplications do.  So nothing else that can stay out
+// of the LDS goes through it: the tokens' fragments come straight from the caches into registers, 32 terms ahead, and
+// only the decoded weights (a wave multiplies 64 tokens with 128 of them) pass through LDS.  While a block is multiplied
+// in halves of 32 terms, a wave decodes the next one in halves of its rows: a row's 64 fields at once by four lanes, whose
+// cache lines are then done with (in slices of 32 terms of all rows, they fell out of the L1 between two slices: 1254 us
+// instead of TODO for 2048 tokens of 4 out of 32 experts of 2048 x 4096).  One barrier a block, before its last multiplications.
+constexpr uint32_t kManyColumns = 256, kManyTokens = 256, kManyBlock = 64;
+constexpr uint32_t kManyBytes = kManyColumns * kManyBlock * 2;  // of a block of weights
+constexpr uint32_t kManyTokenBytes = kManyTokens * kManyBlock * 2;
+
+template <bool NN, bool PAIR, int EPI>
+__global__ __launch_bounds__(512) void k_experts_many(const ExArgs p) {
+    constexpr int WM = 4, FM = 4, FN = 8;
+    constexpr uint32_t NL = 4;  // loads of a lane's words of a half
+    static_assert(kManyBytes == kManyTokenBytes, "one offset for both");
+    static_assert(EPI == kSum || (PAIR && !NN), "gate and up side by side");
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    // forward pairs hold both tables, gradients the one of the tensor that they are at; then two blocks of tokens, and of weights
+    unsigned char *xring = smem + (PAIR && !NN ? 2 : 1) * p.table, *ring = xring + 2 * kManyTokenBytes;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t li = lane & 15, lg = lane >> 4;
+    const int wm = wave >> 1, wn = wave & 1;
+
+    const uint32_t units = *p.ntiles * p.col_tiles * p.splits, per = (units + 7) / 8;
+    const uint32_t unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || unit >= units) return;
+    const uint32_t share = unit % p.splits, col_tile = unit / p.splits % p.col_tiles;
+    const ExTile tile = p.tiles[unit / p.splits / p.col_tiles];
+    const ExTensor T0 = p.t[0][tile.expert], T1 = PAIR ? p.t[1][tile.expert] : T0;
+
+    // This lane's task in a half: 16 fields of a row, `half` rows on in the other half (32 of the reduction; forward 128 of
+    // the tile, whose pairs have 16 rows of gate and of up in turn).
+    const uint32_t trow = NN ? tid >> 4 : tid >> 2, tgrp = NN ? tid & 15 : tid & 3;
+    const uint32_t swz = NN ? 2 * (trow & 3) + 8 * ((trow >> 3) & 1) : trow & 7;
+    const uint32_t wrow = trow * (NN ? 512u : 128u);
+    constexpr uint32_t kHalf = (NN ? 32 * 512 : 128 * 128);  // LDS bytes
+    // copies of the tokens' part: 8 rows by a wave, rows past the tile's end repeat the last one
+    uint32_t vx[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const uint32_t r = min(static_cast<uint32_t>((i * 8 + wave) * 8 + (lane >> 3)), tile.count - 1);
+        vx[i] = (p.by_slot ? r : p.token_of[tile.start + r]) * p.lda * 2 + ((lane & 7) ^ (lane >> 3)) * 16;
+    }
+    const auto rx = wave_rsrc(p.A + (p.by_slot ? static_cast<uint64_t>(tile.start) * p.lda : 0), 0x7FFFFFF0u);
+    // fragment i of this wave is tokens 16 (i WM + wm) and on
+    const uint32_t fa = (wm * 16 + li) * 128 + ((lg ^ (li & 7)) * 16);
+    // weights: fragment j of this wave is columns 128 wn + 16 j and on
+    const uint32_t fb = (wn * 128 + li) * 128 + ((lg ^ (li & 7)) * 16);
+    uint32_t ft[FN];
+    if constexpr (NN) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t r = 8 * lg + (li >> 2), c = (wn * 128 + 16 * j) / 8 + ((li & 3) >> 1);
+            ft[j] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((CBK_LDS unsigned char *)(ring))) + r * 512 + (c ^ (2 * (r & 3) + 8 * (lg & 1))) * 16 + (li & 1) * 8;
+        }
+    }
+
+    f32x4_t acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+
+    const uint32_t all = p.slices * (NN && PAIR ? 2 : 1);  // the reduction's slices, of which this share's:
+    const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(all) * share / p.splits);
+    const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(all) * (share + 1) / p.splits);
+    if constexpr (!(NN && PAIR)) stage_table(smem, T0, tid, 512);
+    if constexpr (!NN && PAIR) stage_table(smem + p.table, T1, tid, 512);
+
+    // The reduction over slices [s0, s1) of tensor `which` (forward pairs: the wave's own of the two).
+    auto pass = [&](uint32_t which, uint32_t s0, uint32_t s1, auto active) __attribute__((always_inline)) {
+        constexpr int NF = decltype(active)::value;  // fragments of tokens that there are
+        const ExTensor &T = which ? T1 : T0;
+        const uint32_t b = __builtin_amdgcn_readfirstlane(T.b), m2 = ((1u << b) - 1) << 1;
+        const unsigned char *table = smem + (NN ? 0 : which * p.table);
+        // where this lane's fields start: a row (a base on a dword), and the bits after it
+        const uint32_t row0 = NN ? s0 * kManyBlock : PAIR ? col_tile * 128 : col_tile * kManyColumns;
+        const uint32_t cols = NN ? p.N : p.R;
+        const uint64_t base = static_cast<uint64_t>(row0) * cols * b;
+        const uint32_t trel = NN || !PAIR ? trow : 16 * (trow >> 5) + (trow & 15);
+        const uint32_t bit = (trel * cols + (NN ? col_tile * kManyColumns : s0 * kManyBlock) + tgrp * 16) * b + (static_cast<uint32_t>(base) & 31u);
+        uint32_t first[4], shift[4];
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) {
+            first[q] = ((bit + 4 * q * b) >> 5) * 4;
+            shift[q] = (bit + 4 * q * b) & 31u;
+        }
+        const uint64_t start = (base >> 5) * 4, step = static_cast<uint64_t>(cols) * (8 * b);
+        // the other half's fields: whole dwords on
+        const uint32_t other = NN ? cols * (4 * b) : (PAIR ? 8 : 16) * cols * b;
+        uint64_t words_at = in_scalars(reinterpret_cast<uint64_t>(T.words) + start), rest = in_scalars(T.bytes > start ? T.bytes - start : 0);
+        // kept in scalar registers: loading them again in the loop would wait for the LDS too
+        asm volatile("" : "+s"(words_at), "+s"(rest));
+        struct Words {
+            u32x3 q[4];
+        } w0, w1;  // of the halves
+        // The words of half h of block s; what is past the stream's end reads as zeros.
+        auto load = [&](Words &w, uint32_t s, uint32_t h) __attribute__((always_inline)) {
+            const uint32_t n = s - s0;
+            const uint64_t at = NN ? n * step : 0, have = rest > at ? rest - at : 0;
+            const auto rs = wave_rsrc(reinterpret_cast<const unsigned char *>(words_at + (rest > at ? at : 0)),
+                                      static_cast<uint32_t>(min(have, static_cast<uint64_t>(0x7FFFFFF0u))));
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                w.q[q] = __builtin_amdgcn_raw_buffer_load_b96(rs, static_cast<int>(first[q] + h * other + (NN ? 0u : n * (8 * b))), 0, 0);
+        };
+        // Decodes them to the buffer at `to`; `masked`: terms past the reduction's end are zeros.
+        auto decode = [&](const Words &w, uint32_t s, uint32_t h, uint32_t to, auto masked) __attribute__((always_inline)) {
+            uint32_t v[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t off[4];
+                fields4(w.q[q], shift[q], b, m2, off);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * q + i] = *reinterpret_cast<const uint16_t *>(table + off[i]);
+            }
+            if constexpr (decltype(masked)::value) {
+                const uint32_t at = s * kManyBlock + (NN ? 32 * h + trow : tgrp * 16), have = p.R > at ? p.R - at : 0u;
+#pragma unroll
+                for (uint32_t i = 0; i < 16; ++i) v[i] = (NN ? have > 0 : i < have) ? v[i] : 0u;
+            }
+            unsigned char *row = ring + to + h * kHalf + wrow;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t *x = v + 8 * g;
+                *reinterpret_cast<u32x4 *>(row + ((tgrp * 2 + g) ^ swz) * 16) =
+                    (u32x4){x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16)};
+            }
+        };
+        auto copy = [&](uint32_t s, uint32_t to) __attribute__((always_inline)) {
+            const uint32_t from = (s + (NN && PAIR ? which * p.slices : 0u)) * (2 * kManyBlock);
+#pragma unroll
+            for (int i = 0; i < NF; ++i) copy_to_lds(rx, xring + to + (i * 8 + wave) * 1024, vx[i], from);
+        };
+        struct Tokens {
+            bf16x8_t f[NF];
+        };
+        // the tokens' fragments for half h of the terms of the block at `at`
+        auto tokens = [&](Tokens &x, uint32_t at, auto half) __attribute__((always_inline)) {
+            constexpr int h = decltype(half)::value;
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+                x.f[i] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(xring + at + (fa ^ (h * 64)) + i * (WM * 2048)));
+        };
+        // weights' fragments 4 c .. 4 c + 3 for half h of the terms of the block at `at`
+        auto read = [&](bf16x8_t (&f)[4], uint32_t at, auto half, int c) __attribute__((always_inline)) {
+            constexpr int h = decltype(half)::value;
+            if constexpr (NN) {
+                const uint32_t t[4] = {ft[4 * c] + at, ft[4 * c + 1] + at, ft[4 * c + 2] + at, ft[4 * c + 3] + at};
+                read_columns<4 * 512, h * 32 * 512>(f, t);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(ring + at + (fb ^ (h * 64)) + (4 * c + j) * 2048));
+            }
+        };
+        auto multiply = [&](const Tokens &x, const bf16x8_t (&f)[4], int c) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][4 * c + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j], x.f[i], acc[i][4 * c + j], 0, 0, 0);
+        };
+        const std::integral_constant<int, 0> lower;
+        const std::integral_constant<int, 1> upper;
+        const std::true_type yes;
+        const std::false_type no;
+
+        Tokens x0, x1;
+        bf16x8_t wa[4], wb[4];
+        copy(s0, 0);
+        keep_order();
+        load(w0, s0, 0);
+        load(w1, s0, 1);
+        if constexpr (NN && PAIR) stage_table(smem, T, tid, 512);
+        lds_barrier();  // the tables
+        decode(w0, s0, 0, 0, yes);
+        decode(w1, s0, 1, 0, yes);
+        keep_order();
+        load(w0, min(s0 + 1, s1 - 1), 0);
+        load(w1, min(s0 + 1, s1 - 1), 1);
+        __builtin_amdgcn_s_waitcnt(0x0070 | 2 * NL);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        read(wa, 0, lower, 0);
+        tokens(x0, 0, lower);
+        uint32_t now = 0;
+        auto schedule = [](auto reads) __attribute__((always_inline)) {
+            if constexpr (!NN) {
+                constexpr int MF = 8 * NF, RD = decltype(reads)::value;
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, (RD + MF - 1) / MF, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 96 / MF, 0);
+                }
+            }
+        };
+        // Block s is multiplied; `more`: the next one is copied and decoded, and the one after asked for unless that is
+        // the `last`.  At the end the copies have landed, and every word but those.
+        auto interval = [&](uint32_t s, auto more, auto last) __attribute__((always_inline)) {
+            constexpr bool MORE = decltype(more)::value, WORDS = MORE && !decltype(last)::value;
+            const uint32_t next = kManyBytes - now;
+            if constexpr (MORE) copy(s + 1, next);
+            keep_order();
+            read(wb, now, lower, 1);
+            multiply(x0, wa, 0);
+            if constexpr (MORE) {
+                decode(w0, s + 1, 0, next, last);
+                keep_order();
+                if constexpr (WORDS) load(w0, s + 2, 0);
+            }
+            read(wa, now, upper, 0);
+            tokens(x1, now, upper);
+            multiply(x0, wb, 1);
+            if constexpr (MORE) schedule(std::integral_constant<int, 24 + NF>{});
+            __builtin_amdgcn_sched_barrier(0);
+            read(wb, now, upper, 1);
+            multiply(x1, wa, 0);
+            if constexpr (MORE) {
+                decode(w1, s + 1, 1, next, last);
+                keep_order();
+                if constexpr (WORDS) load(w1, s + 2, 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(WORDS ? 0x0070 | 2 * NL : 0x0070);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if constexpr (MORE) {
+                read(wa, next, lower, 0);
+                tokens(x0, next, lower);
+            }
+            multiply(x1, wb, 1);
+            now = next;
+        };
+        uint32_t s = s0;
+        for (; s + 2 < s1; ++s) interval(s, yes, no);
+        if (s + 1 < s1) interval(s++, yes, yes);
+        interval(s, no, no);
+    };
+    auto passes = [&](auto active) {
+        if constexpr (NN && PAIR) {
+#pragma unroll 1
+            for (uint32_t which = c0 >= p.slices; which * p.slices < c1; ++which)
+                pass(which, max(c0, which * p.slices) - which * p.slices, min(c1, (which + 1) * p.slices) - which * p.slices, active);
+        } else {
+            pass(PAIR ? wave & 1 : 0, c0, c1, active);
+        }
+    };
+    // as many fragments as the tile has tokens for, in steps of 64
+    const uint32_t frags = (tile.count + 16 * WM - 1) / (16 * WM);
+    if (frags == 1) passes(std::integral_constant<int, 1>{});
+    else if (frags == 2) passes(std::integral_constant<int, 2>{});
+    else if (frags == 3) passes(std::integral_constant<int, 3>{});
+    else passes(std::integral_constant<int, 4>{});
+
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const uint32_t m = (i * WM + wm) * 16 + li;
+        finish<EPI, FN>(p, acc[i], tile, m, share, col_tile, wn, 2, lg);
+    }
+}
+
+uint32_t tiles_of(uint64_t n, uint64_t m) { return static_cast<uint32_t>((n + m - 1) / m); }
 
 template <int, bool, bool, int, bool>
 struct ExTag;
 
 template <int BM, bool NN, bool PAIR, int EPI, bool GT>
-cbk_status run(ExArgs &a, const ExPlan &pl, hipStream_t s) {
+cbk_status run(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s) {
+    a.col_tiles = tiles_of(columns, EPI == kSum ? kColumns : kColumns / 2);
     const uint32_t lds = (GT ? 0 : (PAIR ? 2 : 1) * a.table) + 2 * slice_bytes(BM);
     if (!allow_lds_once<ExTag<BM, NN, PAIR, EPI, GT>>(k_experts<BM, NN, PAIR, EPI, GT>, kLdsLimit)) return CBK_E_HIP;
     const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles * a.splits;
@@ -398,61 +678,71 @@ cbk_status run(ExArgs &a, const ExPlan &pl, hipStream_t s) {
     return launched();
 }
 
+constexpr uint32_t many_lds(uint32_t table, bool two) { return (two ? 2 : 1) * table + 2 * (kManyBytes + kManyTokenBytes); }
+
 template <bool NN, bool PAIR, int EPI>
-cbk_status product(ExArgs &a, const ExPlan &pl, uint32_t b, hipStream_t s) {
-    a.table = std::max(16u, 2u << b);
-    if (b > 14) return run<64, NN, PAIR, EPI, true>(a, pl, s);
-    return pl.tile == 256 ? run<256, NN, PAIR, EPI, false>(a, pl, s) : run<64, NN, PAIR, EPI, false>(a, pl, s);
+cbk_status run_many(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s) {
+    a.col_tiles = tiles_of(columns, EPI == kSum ? kManyColumns : kManyColumns / 2);
+    const uint32_t lds = many_lds(a.table, !NN && PAIR);
+    if (lds > kLdsLimit) return CBK_E_UNSUPPORTED;  // the plan rules it out
+    if (!allow_lds_once<ExTag<256, NN, PAIR, EPI, false>>(k_experts_many<NN, PAIR, EPI>, kLdsLimit)) return CBK_E_HIP;
+    const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles * a.splits;
+    if (units > (uint64_t(1) << 30)) return CBK_E_UNSUPPORTED;
+    hipLaunchKernelGGL((k_experts_many<NN, PAIR, EPI>), dim3(static_cast<uint32_t>((units + 7) / 8 * 8)), dim3(512), lds, s, a);
+    return launched();
 }
 
-uint32_t tiles_of(uint64_t n, uint64_t m) { return static_cast<uint32_t>((n + m - 1) / m); }
+// `columns` of the result, or (gate and up) of the hidden values.
+template <bool NN, bool PAIR, int EPI>
+cbk_status product(ExArgs &a, const ExPlan &pl, uint32_t columns, uint32_t b, hipStream_t s) {
+    a.table = std::max(16u, 2u << b);
+    if (b > 14) return run<64, NN, PAIR, EPI, true>(a, pl, columns, s);
+    return pl.tile == kManyTokens ? run_many<NN, PAIR, EPI>(a, pl, columns, s) : run<64, NN, PAIR, EPI, false>(a, pl, columns, s);
+}
 
 }  // namespace
 
 cbk_status ex_hidden(ExArgs &a, const ExPlan &pl, const cbk_experts &ex, bool backward, hipStream_t s) {
     a.N = static_cast<uint32_t>(ex.rows);
     a.R = static_cast<uint32_t>(ex.cols);
-    a.col_tiles = static_cast<uint32_t>(pl.Fp / 64);
     a.slices = static_cast<uint32_t>(pl.Kp / 64);
     a.splits = 1;
     a.ldD = static_cast<uint32_t>(pl.ldF);
     a.d_splits = pl.split_dt;
     a.d_stride = pl.d_stride;
     a.dw_parts = pl.dw_parts;
-    return backward ? product<false, true, kHiddenBwd>(a, pl, ex.b, s) : product<false, true, kHidden>(a, pl, ex.b, s);
+    return backward ? product<false, true, kHiddenBwd>(a, pl, static_cast<uint32_t>(pl.Fp), ex.b, s)
+                    : product<false, true, kHidden>(a, pl, static_cast<uint32_t>(pl.Fp), ex.b, s);
 }
 
 cbk_status ex_down(ExArgs &a, const ExPlan &pl, const cbk_experts &ex, hipStream_t s) {
     a.N = static_cast<uint32_t>(ex.out);
     a.R = static_cast<uint32_t>(ex.rows);
-    a.col_tiles = tiles_of(ex.out, kColumns);
     a.slices = static_cast<uint32_t>(pl.Fp / 64);
     a.splits = pl.split_down;
     a.ldS = static_cast<uint32_t>(pl.ldO);
     a.split_stride = pl.s_stride;
-    return product<false, false, kSum>(a, pl, ex.b_down, s);
+    return product<false, false, kSum>(a, pl, a.N, ex.b_down, s);
 }
 
 cbk_status ex_down_t(ExArgs &a, const ExPlan &pl, const cbk_experts &ex, hipStream_t s) {
     a.N = static_cast<uint32_t>(ex.rows);
     a.R = static_cast<uint32_t>(ex.out);
-    a.col_tiles = tiles_of(ex.rows, kColumns);
     a.slices = static_cast<uint32_t>(pl.Op / 64);
     a.splits = pl.split_dt;
     a.ldS = static_cast<uint32_t>(pl.ldF);
     a.split_stride = pl.d_stride;
-    return product<true, false, kSum>(a, pl, ex.b_down, s);
+    return product<true, false, kSum>(a, pl, a.N, ex.b_down, s);
 }
 
 cbk_status ex_dx(ExArgs &a, const ExPlan &pl, const cbk_experts &ex, hipStream_t s) {
     a.N = static_cast<uint32_t>(ex.cols);
     a.R = static_cast<uint32_t>(ex.rows);
-    a.col_tiles = tiles_of(ex.cols, kColumns);
     a.slices = static_cast<uint32_t>(pl.Fp / 64);
     a.splits = pl.split_x;
     a.ldS = static_cast<uint32_t>(pl.ldK);
     a.split_stride = pl.s_stride;
-    return product<true, true, kSum>(a, pl, ex.b, s);
+    return product<true, true, kSum>(a, pl, a.N, ex.b, s);
 }
 
 }  // namespace cbk
