@@ -321,7 +321,8 @@ __global__ __launch_bounds__(256) void k_route_bwd(const RouteArgs a) {
 }
 
 // --------------------------------------------------------------------------- slots by expert
-// One workgroup sorts the slots by expert, stably, and cuts each expert's run into token tiles of equal size.
+// One workgroup sorts the slots by expert, stably, and cuts each expert's run into token tiles of equal size, listed by
+// falling quarters of a whole tile (what takes longest is begun first).
 // Each wave counts a run of slots, then places them: the rank of a slot among the wave's 64 of the same expert comes
 // from ballots over the expert's bits.
 struct SortArgs {
@@ -336,7 +337,7 @@ constexpr int kSortWaves = 16;
 
 __global__ __launch_bounds__(64 * kSortWaves) void k_sort(const SortArgs a) {
     extern __shared__ uint32_t lds[];  // [waves][count]: how many, then where the wave's next one goes
-    __shared__ uint32_t wave_sum[kSortWaves], wave_tiles[kSortWaves];
+    __shared__ uint32_t wave_sums[5][kSortWaves];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint32_t n = a.count;
     for (uint32_t i = tid; i < kSortWaves * n; i += blockDim.x) lds[i] = 0;
@@ -357,25 +358,39 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_sort(const SortArgs a) {
     const uint32_t parts = (m + a.tile - 1) / a.tile;
     const uint32_t size = m ? min(a.tile, ((m + parts - 1) / parts + a.unit - 1) / a.unit * a.unit) : 1;
     const uint32_t tiles = (m + size - 1) / size;
-    uint32_t ms = m, ts = tiles;
+    // all of an expert's tiles but the last are of `size`; kind 0 is a whole tile
+    auto kind = [&](uint32_t n) { return 3 - min((n - 1) / max(a.unit, 1u), 3u); };
+    const uint32_t main_kind = kind(size), last_kind = tiles ? kind(m - (tiles - 1) * size) : 0;
+    uint32_t sums[5] = {m, 0, 0, 0, 0};
 #pragma unroll
-    for (int by = 1; by < 64; by *= 2) {
-        const uint32_t x = __shfl_up(ms, by, 64), y = __shfl_up(ts, by, 64);
-        if (lane >= static_cast<uint32_t>(by)) {
-            ms += x;
-            ts += y;
+    for (uint32_t q = 0; q < 4; ++q) sums[1 + q] = tiles ? (main_kind == q ? tiles - 1 : 0) + (last_kind == q ? 1 : 0) : 0;
+    uint32_t before[5];
+#pragma unroll
+    for (int q = 0; q < 5; ++q) {
+        uint32_t v = sums[q];
+#pragma unroll
+        for (int by = 1; by < 64; by *= 2) {
+            const uint32_t x = __shfl_up(v, by, 64);
+            if (lane >= static_cast<uint32_t>(by)) v += x;
         }
-    }
-    if (lane == 63) {
-        wave_sum[wave] = ms;
-        wave_tiles[wave] = ts;
+        if (lane == 63) wave_sums[q][wave] = v;
+        before[q] = v - sums[q];
     }
     __syncthreads();
-    uint32_t start = ms - m, tile = ts - tiles;
-    for (uint32_t w = 0; w < wave; ++w) {
-        start += wave_sum[w];
-        tile += wave_tiles[w];
+    uint32_t kinds = 0;  // tiles of the kinds before
+#pragma unroll
+    for (int q = 0; q < 5; ++q) {
+        uint32_t all = 0;
+        for (uint32_t w = 0; w < kSortWaves; ++w) {
+            if (w == wave) before[q] += all;
+            all += wave_sums[q][w];
+        }
+        if (q > 0) {
+            before[q] += kinds;
+            kinds += all;
+        }
     }
+    const uint32_t start = before[0];
     if (tid < n) {
         uint32_t at = start;
         for (int w = 0; w < kSortWaves; ++w) {
@@ -383,9 +398,14 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_sort(const SortArgs a) {
             lds[w * n + tid] = at;
             at += c;
         }
-        for (uint32_t i = 0; i < tiles; ++i) a.tiles[tile + i] = ExTile{tid, start + i * size, min(size, m - i * size), 0};
+        for (uint32_t i = 0; i < tiles; ++i) {
+            const uint32_t q = i + 1 < tiles ? main_kind : last_kind;
+            // (a chain of selects: the array stays in registers)
+            const uint32_t to = q == 0 ? before[1]++ : q == 1 ? before[2]++ : q == 2 ? before[3]++ : before[4]++;
+            a.tiles[to] = ExTile{tid, start + i * size, min(size, m - i * size), 0};
+        }
     }
-    if (tid == blockDim.x - 1) *a.ntiles = tile + tiles;
+    if (tid == 0) *a.ntiles = kinds;
     __syncthreads();
     uint32_t bits = 0;
     while ((1u << bits) < n) ++bits;
@@ -571,6 +591,7 @@ cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, cons
         so.place_of = at<int32_t>(ws, pl.place_of);
         so.tiles = at<ExTile>(ws, pl.tiles);
         so.ntiles = at<uint32_t>(ws, pl.ntiles);
+        if (!allow_lds_once<SortArgs>(k_sort, kLdsLimit / 2)) return CBK_E_HIP;  // 64 KB of counts, and a little
         hipLaunchKernelGGL(k_sort, dim3(1), dim3(64 * kSortWaves), kSortWaves * ex.count * 4, s, so);
         cbk_status st = launched();
         if (st != CBK_OK) return st;

@@ -424,9 +424,10 @@ __global__ __launch_bounds__(512) void k_experts_many(const ExArgs p) {
     const uint32_t li = lane & 15, lg = lane >> 4;
     const int wm = wave >> 1, wn = wave & 1;
 
-    const uint32_t units = *p.ntiles * p.col_tiles * p.splits, per = (units + 7) / 8;
-    const uint32_t unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || unit >= units) return;
+    // Units in order of token tile, the fullest first (they take longest), column tile and share: the XCDs get them in
+    // turn, so that each has as many of a kind (in runs an XCD's tokens stayed in its L2, and it took 3 % longer).
+    const uint32_t units = *p.ntiles * p.col_tiles * p.splits, unit = blockIdx.x;
+    if (unit >= units) return;
     const uint32_t share = unit % p.splits, col_tile = unit / p.splits % p.col_tiles;
     const ExTile tile = p.tiles[unit / p.splits / p.col_tiles];
     const ExTensor T0 = p.t[0][tile.expert], T1 = PAIR ? p.t[1][tile.expert] : T0;
@@ -586,14 +587,15 @@ __global__ __launch_bounds__(512) void k_experts_many(const ExArgs p) {
         read(wa, 0, lower, 0);
         tokens(x0, 0, lower);
         uint32_t now = 0;
-        auto schedule = [](auto reads) __attribute__((always_inline)) {
+        // Between N multiplications: RD reads of LDS (gathers among them) and the decoding's arithmetic, V a multiplication.
+        auto schedule = [](auto muls, auto reads, auto valu) __attribute__((always_inline)) {
             if constexpr (!NN) {
-                constexpr int MF = 8 * NF, RD = decltype(reads)::value;
+                constexpr int N = decltype(muls)::value, RD = decltype(reads)::value, V = decltype(valu)::value;
 #pragma unroll
-                for (int i = 0; i < MF; ++i) {
+                for (int i = 0; i < N; ++i) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x100, (RD + MF - 1) / MF, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x002, 96 / MF, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, (RD + N - 1) / N, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
                 }
             }
         };
@@ -614,7 +616,7 @@ __global__ __launch_bounds__(512) void k_experts_many(const ExArgs p) {
             read(wa, now, upper, 0);
             tokens(x1, now, upper);
             multiply(x0, wb, 1);
-            if constexpr (MORE) schedule(std::integral_constant<int, 24 + NF>{});
+            if constexpr (MORE) schedule(std::integral_constant<int, 8 * NF>{}, std::integral_constant<int, 24 + NF>{}, std::integral_constant<int, 12 / NF>{});
             __builtin_amdgcn_sched_barrier(0);
             read(wb, now, upper, 1);
             multiply(x1, wa, 0);
@@ -623,6 +625,7 @@ __global__ __launch_bounds__(512) void k_experts_many(const ExArgs p) {
                 keep_order();
                 if constexpr (WORDS) load(w1, s + 2, 1);
             }
+            if constexpr (MORE) schedule(std::integral_constant<int, 4 * NF>{}, std::integral_constant<int, 20>{}, std::integral_constant<int, 20 / NF>{});
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(WORDS ? 0x0070 | 2 * NL : 0x0070);
             __builtin_amdgcn_s_barrier();
@@ -688,7 +691,7 @@ cbk_status run_many(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s
     if (!allow_lds_once<ExTag<256, NN, PAIR, EPI, false>>(k_experts_many<NN, PAIR, EPI>, kLdsLimit)) return CBK_E_HIP;
     const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles * a.splits;
     if (units > (uint64_t(1) << 30)) return CBK_E_UNSUPPORTED;
-    hipLaunchKernelGGL((k_experts_many<NN, PAIR, EPI>), dim3(static_cast<uint32_t>((units + 7) / 8 * 8)), dim3(512), lds, s, a);
+    hipLaunchKernelGGL((k_experts_many<NN, PAIR, EPI>), dim3(static_cast<uint32_t>(units)), dim3(512), lds, s, a);
     return launched();
 }
 
