@@ -77,14 +77,14 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
     p.Tc = std::min(tokens, most);
     const uint64_t slots = p.Tc * k, active = std::min<uint64_t>(ex.count, slots);
     // tiles of 256 where the LDS holds their tables: two of gate and up, one of down
-    p.tile = ex.b <= 13 && ex.b_down <= 14 && slots / active > 48 ? 256 : 64;
+    p.tile = ex.b <= 13 && ex.b_down <= 14 && slots / active > 48 ? 256 : slots / active > 24 ? 64 : slots / active > 8 ? 32 : 16;
     p.max_tiles = static_cast<uint32_t>(active + slots / p.tile);
     // few units of work: their reductions are shared until there are two for each CU, of eight slices of 64 at least
     auto split = [&](uint64_t columns, uint64_t slices) {
         const uint64_t units = p.max_tiles * (up_to(columns, 128) / 128);
         return static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>({512 / units, slices / 8, 8})));
     };
-    p.split_down = split(ex.out, p.Fp / 64);
+    p.split_down = p.tile >= 64 ? split(ex.out, p.Fp / 64) : 1;
     p.split_dt = split(ex.rows, p.Op / 64);
     p.split_x = split(ex.cols, 2 * p.Fp / 64);
     uint64_t at = 0;

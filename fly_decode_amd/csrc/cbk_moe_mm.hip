@@ -56,6 +56,9 @@ __device__ __forceinline__ void fields4(u32x3 d, uint32_t shift, uint32_t b, uin
     off[3] = static_cast<uint32_t>(((static_cast<uint64_t>(hi) << 32) | lo) >> ((3 * b - 1) & 63)) & m2;
 }
 
+// The operand of a wait for vector memory alone, n operations left in flight.
+constexpr int vm(uint32_t n) { return static_cast<int>(0x0F70 | (n & 15) | (n >> 4) << 14); }
+
 // A value that is the same in every lane, in scalar registers.
 __device__ __forceinline__ uint64_t in_scalars(uint64_t v) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(v)));
@@ -399,6 +402,273 @@ __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
     }
 }
 
+// -------------------------------------------------------------------------------- few tokens
+// Forward products of up to 16 NF tokens: bound by reading the weights.  A workgroup goes through a run of units, 32 rows
+// each (16 of gate and 16 of up, or 32 of one tensor) for one token tile; its 8 waves take every eighth step of 128
+// terms, and their sums meet in LDS in a fixed order, one barrier a unit.  A wave works by itself otherwise.  An item is
+// a step of 16 rows: their 128 fields, up to 15 chunks of 16 bytes a row, are copied as they lie straight into one of
+// three places of the wave's own, two items ahead (loads of a lane's own fields, which scatter a wave over 16 rows,
+// took 302 us for 48 tokens of 4 out of 32 experts' gate and up, TODO so).  From there lane l takes 16 fields of row
+// l % 16 at term 16 (l / 16) of each 64, decodes them into the layout of the matrix instruction's operand, and the
+// tokens' fragments are read from the caches with the terms in the same order.
+constexpr uint32_t kFewChunks = 15, kFewStage = 16 * kFewChunks * 16, kFewRing = 3, kFewStep = 128;
+// LDS of the sums: of two units for 16 tokens, so that one barrier a unit is enough, of one for more
+constexpr uint32_t few_sums(int NF) { return (NF == 1 ? 2 : 1) * 8 * NF * 2 * 1024; }
+constexpr uint32_t few_lds(uint32_t tables, int NF) { return tables + 8 * kFewRing * kFewStage + few_sums(NF); }
+
+// The three dwords at each of four LDS addresses.  Written out because the compiler holds reads back until every copy
+// into LDS has landed, also those of items still to come; the block waits for its own reads.
+__device__ __forceinline__ void read_windows(u32x3 (&w)[4], const uint32_t (&at)[4]) {
+    u32x2 a0, a1, a2, a3;
+    uint32_t b0, b1, b2, b3;
+    asm volatile(
+        "ds_read2_b32 %0, %8 offset1:1\n"
+        "ds_read_b32 %4, %8 offset:8\n"
+        "ds_read2_b32 %1, %9 offset1:1\n"
+        "ds_read_b32 %5, %9 offset:8\n"
+        "ds_read2_b32 %2, %10 offset1:1\n"
+        "ds_read_b32 %6, %10 offset:8\n"
+        "ds_read2_b32 %3, %11 offset1:1\n"
+        "ds_read_b32 %7, %11 offset:8\n"
+        "s_waitcnt lgkmcnt(0)\n"
+        : "=&v"(a0), "=&v"(a1), "=&v"(a2), "=&v"(a3), "=&v"(b0), "=&v"(b1), "=&v"(b2), "=&v"(b3)
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+        : "memory");
+    w[0] = (u32x3){a0.x, a0.y, b0};
+    w[1] = (u32x3){a1.x, a1.y, b1};
+    w[2] = (u32x3){a2.x, a2.y, b2};
+    w[3] = (u32x3){a3.x, a3.y, b3};
+}
+
+template <int NF, bool PAIR, int EPI>
+__global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
+    static_assert(PAIR == (EPI != kSum), "gate and up, or one tensor");
+    constexpr uint32_t NX = 4 * NF;  // loads of a step's tokens
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t li = lane & 15, lg = lane >> 4;
+    unsigned char *stages = smem + (PAIR ? 2 : 1) * p.table + wave * (kFewRing * kFewStage);
+    float *sums = reinterpret_cast<float *>(smem + (PAIR ? 2 : 1) * p.table + 8 * kFewRing * kFewStage);
+
+    const uint32_t units = *p.ntiles * p.col_tiles;
+    const uint32_t u0 = static_cast<uint32_t>(static_cast<uint64_t>(units) * blockIdx.x / gridDim.x);
+    const uint32_t u1 = static_cast<uint32_t>(static_cast<uint64_t>(units) * (blockIdx.x + 1) / gridDim.x);
+    if (u0 == u1) return;
+    const uint32_t S = (p.slices + 1) / 2;                   // steps
+    const uint32_t mine = (S + 7 - wave) / 8;                // of them this wave's, in every unit
+    const uint32_t items = 2 * mine * (u1 - u0);             // a step's two runs of 16 rows, one after the other
+
+    struct Tensor {
+        uint64_t words;
+        uint64_t bytes;
+        uint32_t b;
+    };
+    auto tensor = [&](uint32_t expert, uint32_t j) __attribute__((always_inline)) {
+        const ExTensor &T = p.t[PAIR ? j : 0][expert];
+        return Tensor{in_scalars(reinterpret_cast<uint64_t>(T.words)), in_scalars(T.bytes), static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(T.b))};
+    };
+    // first of the 16 rows j of a unit
+    auto first_row = [&](uint32_t u, uint32_t j) { return static_cast<uint64_t>(u % p.col_tiles) * (PAIR ? 16 : 32) + (PAIR ? 0 : 16 * j); };
+
+    // ---- copies: item n is run (n & 1) of a step; they are asked for in order, past the last one the last again
+    uint32_t cu = u0, cs = wave, cn = 0;  // unit, step and number of the next item to copy
+    struct Source {
+        uint64_t base, bytes;
+        uint32_t v[4], b;
+    } from[2];
+    auto source = [&]() __attribute__((always_inline)) {  // of unit cu
+        const uint32_t expert = p.tiles[cu / p.col_tiles].expert;
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) {
+            const Tensor T = tensor(expert, j);
+            const uint64_t bits = first_row(cu, j) * p.R * T.b, start = bits / 128 * 16;
+            from[j].base = T.words + (T.bytes > start ? start : 0);
+            from[j].bytes = T.bytes > start ? T.bytes - start : 0;
+            from[j].b = T.b;
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint32_t g = min(i * 64 + lane, 16 * kFewChunks - 1), row = g / kFewChunks, c = g % kFewChunks;
+                // chunks past the fields' end repeat the last one
+                from[j].v[i] = (((static_cast<uint32_t>(bits) & 127u) + row * p.R * T.b) / 128 + min(c, T.b)) * 16;
+            }
+        }
+    };
+    uint32_t slot = 0;  // where the next item goes
+    auto copy = [&](uint32_t j) __attribute__((always_inline)) {
+        const Source &f = from[j];
+        const auto rs = wave_rsrc(reinterpret_cast<const unsigned char *>(f.base), static_cast<uint32_t>(min(f.bytes, static_cast<uint64_t>(0x7FFFFFF0u))));
+        unsigned char *to = stages + slot * kFewStage;
+        const uint32_t at = cs * (kFewStep / 8) * f.b;
+#pragma unroll
+        for (uint32_t i = 0; i < 3; ++i) copy_to_lds(rs, to + i * 1024, f.v[i] + at, 0);
+        if (lane < 16 * kFewChunks - 192) copy_to_lds(rs, to + 3072, f.v[3] + at, 0);
+        slot = slot == kFewRing - 1 ? 0 : slot + 1;
+        ++cn;
+        if (j == 1 && cn < items) {  // the next step
+            cs += 8;
+            if (cs >= S) {
+                cs = wave;
+                ++cu;
+                source();
+            }
+        }
+    };
+
+    // ---- tokens
+    uint32_t vx[NF], rows_at = ~0u;  // rows of A, and the tile that they are of
+    auto rows_of = [&](uint32_t t) __attribute__((always_inline)) {
+        if (rows_at == t) return;
+        rows_at = t;
+        const ExTile tile = p.tiles[t];
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+            const uint32_t r = min(i * 16 + li, tile.count - 1);
+            vx[i] = (p.by_slot ? tile.start + r : p.token_of[tile.start + r]);
+        }
+    };
+    struct Step {
+        bf16x8_t f[NF][4];
+    };
+    // Fragments for step s (the second 64 terms of a last step that has none: the first again, not used).
+    auto tokens = [&](Step &x, uint32_t s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+            const unsigned char *row = reinterpret_cast<const unsigned char *>(p.A + static_cast<uint64_t>(vx[i]) * p.lda) + lg * 32 + s * (2 * kFewStep);
+            const bool whole = 2 * s + 1 < p.slices;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) x.f[i][h] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(row + (h < 2 ? 16 * h : whole ? 128 + 16 * (h - 2) : 0)));
+        }
+    };
+
+    f32x4_t acc[NF][2];
+    // ---- an item: `place` its stage
+    struct Window {
+        uint32_t at[4], shift[4], b, m2;
+        const unsigned char *table;
+    } win[2];
+    ExTile tile;
+    auto windows = [&](uint32_t u) __attribute__((always_inline)) {
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) {
+            const uint32_t b = tensor(tile.expert, j).b;
+            const uint32_t bits = (static_cast<uint32_t>(first_row(u, j) * p.R * b) + li * p.R * b) & 127u;
+            Window &w = win[j];
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) {
+                const uint32_t bit = bits + (lg * 16 + 4 * q) * b;
+                w.at[q] = li * (kFewChunks * 16) + (bit >> 5) * 4;
+                w.shift[q] = bit & 31u;
+            }
+            w.b = b;
+            w.m2 = ((1u << b) - 1) << 1;
+            w.table = smem + (PAIR ? j : 0) * p.table;
+        }
+    };
+    auto item = [&](const Step &x, uint32_t j, uint32_t s, const unsigned char *place) __attribute__((always_inline)) {
+        const Window &w = win[j];
+#pragma unroll
+        for (uint32_t hh = 0; hh < 2; ++hh) {
+            if (hh == 1 && 2 * s + 1 >= p.slices) break;
+            uint32_t v[16];
+            const uint32_t add = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const CBK_LDS unsigned char *)(place))) + hh * (8 * w.b);
+            const uint32_t from[4] = {w.at[0] + add, w.at[1] + add, w.at[2] + add, w.at[3] + add};
+            u32x3 words[4];
+            read_windows(words, from);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t off[4];
+                fields4(words[q], w.shift[q], w.b, w.m2, off);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * q + i] = *reinterpret_cast<const uint16_t *>(w.table + off[i]);
+            }
+            if (s * kFewStep + hh * 64 + 64 > p.R) {  // terms past the rows' end are zeros
+                const uint32_t at = s * kFewStep + hh * 64 + lg * 16, have = p.R > at ? p.R - at : 0u;
+#pragma unroll
+                for (uint32_t i = 0; i < 16; ++i) v[i] = i < have ? v[i] : 0u;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t *y = v + 8 * h;
+                const bf16x8_t f = __builtin_bit_cast(bf16x8_t, (u32x4){y[0] | (y[1] << 16), y[2] | (y[3] << 16), y[4] | (y[5] << 16), y[6] | (y[7] << 16)});
+#pragma unroll
+                for (int i = 0; i < NF; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, x.f[i][2 * hh + h], acc[i][j], 0, 0, 0);
+            }
+        }
+    };
+
+    Step x;
+    if (mine > 0) {
+        source();
+        rows_of(u0 / p.col_tiles);
+        copy(0);
+        keep_order();
+        tokens(x, wave);
+        keep_order();
+        copy(1);
+        keep_order();
+    }
+    uint32_t staged = ~0u, place = 0;
+    for (uint32_t u = u0; u < u1; ++u) {
+        tile = p.tiles[u / p.col_tiles];
+        windows(u);
+        if (staged != tile.expert) {  // (the previous tables' last reads came before the last barrier)
+            staged = tile.expert;
+            stage_table(smem, p.t[0][staged], tid, 512);
+            if (PAIR) stage_table(smem + p.table, p.t[1][staged], tid, 512);
+            lds_barrier();
+        }
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        for (uint32_t s = wave; s < S; s += 8) {
+            // The next step's tokens (after the last of all the last again), and the copies two items on; then this item's
+            // have landed when no more is in flight than was asked for after them: two copies, and a step's tokens.
+            Step next;
+            const bool more = s + 8 < S;
+            if (!more && u + 1 < u1) rows_of((u + 1) / p.col_tiles);
+            keep_order();
+            tokens(next, more ? s + 8 : u + 1 < u1 ? static_cast<uint32_t>(wave) : s);
+            keep_order();
+            copy(0);
+            keep_order();
+            __builtin_amdgcn_s_waitcnt(vm(8 + NX));
+            asm volatile("" ::: "memory");
+            item(x, 0, s, stages + place * kFewStage);
+            place = place == kFewRing - 1 ? 0 : place + 1;
+            keep_order();
+            asm volatile("" ::: "memory");
+            copy(1);
+            keep_order();
+            __builtin_amdgcn_s_waitcnt(vm(8 + NX));
+            asm volatile("" ::: "memory");
+            item(x, 1, s, stages + place * kFewStage);
+            place = place == kFewRing - 1 ? 0 : place + 1;
+            asm volatile("" ::: "memory");
+            x = next;
+        }
+        float *to = sums + (NF == 1 ? (u & 1) * (8 * 2 * 256) : 0) + lane * 4;
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) *reinterpret_cast<f32x4_t *>(to + ((wave * NF + i) * 2 + j) * 256) = acc[i][j];
+        lds_barrier();
+        // the waves add a unit's sums in turn
+        if (wave == static_cast<int>(u & 7)) {
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                f32x4_t t[2] = {};
+                for (int w = 0; w < 8; ++w)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) t[j] += *reinterpret_cast<const f32x4_t *>(to + ((w * NF + i) * 2 + j) * 256);
+                finish<EPI, 2>(p, t, tile, i * 16 + li, 0, u % p.col_tiles, 0, 1, lg);
+            }
+        }
+        if (NF > 1) lds_barrier();
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);  // no copy is left in flight
+}
+
 // ------------------------------------------------------------------------------- many tokens
 // A tile of 256 tokens x 256 columns; the reduction in blocks of 64, two buffers of them in LDS.  What bounds it is the
 // LDS: the gathers of a block's 16384 fields take about what its multiplications do.  So nothing else that can stay out
@@ -695,12 +965,32 @@ cbk_status run_many(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s
     return launched();
 }
 
+template <int, bool, int>
+struct FewTag;
+
+template <int NF, bool PAIR, int EPI>
+cbk_status run_few(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s) {
+    a.splits = 1;
+    a.col_tiles = tiles_of(columns, PAIR ? 16 : 32);
+    const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles;
+    if (units > (uint64_t(1) << 30)) return CBK_E_UNSUPPORTED;
+    if (!allow_lds_once<FewTag<NF, PAIR, EPI>>(k_experts_few<NF, PAIR, EPI>, kLdsLimit)) return CBK_E_HIP;
+    // a workgroup has a CU's LDS
+    const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(units, cu_count()));
+    hipLaunchKernelGGL((k_experts_few<NF, PAIR, EPI>), dim3(grid), dim3(512), few_lds((PAIR ? 2 : 1) * a.table, NF), s, a);
+    return launched();
+}
+
 // `columns` of the result, or (gate and up) of the hidden values.
 template <bool NN, bool PAIR, int EPI>
 cbk_status product(ExArgs &a, const ExPlan &pl, uint32_t columns, uint32_t b, hipStream_t s) {
     a.table = std::max(16u, 2u << b);
-    if (b > 14) return run<64, NN, PAIR, EPI, true>(a, pl, columns, s);
-    return pl.tile == kManyTokens ? run_many<NN, PAIR, EPI>(a, pl, columns, s) : run<64, NN, PAIR, EPI, false>(a, pl, columns, s);
+    if (pl.tile == kManyTokens) return run_many<NN, PAIR, EPI>(a, pl, columns, s);
+    if constexpr (!NN) {
+        if (pl.tile <= 32 && b <= 14 && few_lds((PAIR ? 2 : 1) * a.table, pl.tile / 16) <= kLdsLimit)
+            return pl.tile == 16 ? run_few<1, PAIR, EPI>(a, pl, columns, s) : run_few<2, PAIR, EPI>(a, pl, columns, s);
+    }
+    return b > 14 ? run<64, NN, PAIR, EPI, true>(a, pl, columns, s) : run<64, NN, PAIR, EPI, false>(a, pl, columns, s);
 }
 
 }  // namespace
