@@ -113,6 +113,7 @@ struct ExPlan {
     uint64_t ldK, ldF, ldO;  // and to a tile's 128 columns: leading dimensions of fp32 results
     uint32_t tile;           // slots of one expert that a workgroup takes at most
     uint32_t max_tiles;      // token tiles of a chunk, at most
+    uint32_t one;            // one token forward: its slots are not sorted
     uint32_t split_down, split_dt, split_x;  // workgroups that share a reduction
     uint32_t dw_parts;       // partial sums of a slot's dweights
     uint64_t s_stride, d_stride;  // floats between the shares of a reduction

@@ -438,26 +438,52 @@ struct GatherArgs {
     uint64_t split_stride;
     uint32_t splits, lds, k, width;
     uint64_t tokens;
-    const int32_t *place_of;
+    const int32_t *place_of;  // of a slot in the sorted order, or -1;
+    const int32_t *experts;   // or null, and S is in the slots' own order: the slots' experts,
+    uint32_t count;           // of which those from here on are none
     uint16_t *Y;
     uint64_t ldy;
     uint32_t vec;
 };
 
-// Y[t] = the sum of its slots' results, in the slots' order.  A thread has 4 columns of a token.
+// Y[t] = the sum of its slots' results, in the slots' order.  A thread has 4 columns of a token, and asks for eight
+// results at a time (one after the other, the four of one token took 6.2 us).
 __global__ __launch_bounds__(256) void k_gather(const GatherArgs a) {
     const uint32_t c = (blockIdx.x * 256 + threadIdx.x) * 4;
     const uint64_t t = blockIdx.y + static_cast<uint64_t>(blockIdx.z) * gridDim.y;
     if (c >= a.width || t >= a.tokens) return;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t j = 0; j < a.k; ++j) {
-        const int32_t at = a.place_of[t * a.k + j];
-        if (at < 0) continue;
-        const float *s = a.S + static_cast<uint64_t>(at) * a.lds + c;
-        for (uint32_t i = 0; i < a.splits; ++i) {
-            const f32x4_t x = *reinterpret_cast<const f32x4_t *>(s + i * a.split_stride);
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    auto place = [&](uint32_t j) {
+        const uint64_t slot = t * a.k + j;
+        if (a.place_of) return a.place_of[slot];
+        return static_cast<uint32_t>(a.experts[slot]) < a.count ? static_cast<int32_t>(slot) : -1;
+    };
+    if (a.splits == 1) {
+        for (uint32_t j = 0; j < a.k; j += 8) {
+            int32_t at[8];
+            f32x4_t x[8];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] += x[r];
+            for (uint32_t i = 0; i < 8; ++i) at[i] = j + i < a.k ? place(j + i) : -1;
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                x[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+                if (at[i] >= 0) x[i] = *reinterpret_cast<const f32x4_t *>(a.S + static_cast<uint64_t>(at[i]) * a.lds + c);
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) v += x[i];
+        }
+    } else {  // up to 8 shares
+        for (uint32_t j = 0; j < a.k; ++j) {
+            const int32_t at = place(j);
+            if (at < 0) continue;
+            f32x4_t x[8];
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                x[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+                if (i < a.splits) x[i] = *reinterpret_cast<const f32x4_t *>(a.S + i * a.split_stride + static_cast<uint64_t>(at) * a.lds + c);
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) v += x[i];
         }
     }
     uint16_t *y = a.Y + t * a.ldy + c;
@@ -560,9 +586,10 @@ cbk_status token_rows(const uint16_t *X, uint64_t ld, uint64_t T, uint64_t K, ui
     return launch_pad_rows(X, ld, T, static_cast<uint32_t>(K), static_cast<uint32_t>(Kp), P, s);
 }
 
-cbk_status gather(const float *S, uint64_t split_stride, uint32_t splits, uint64_t ldS, const int32_t *place_of, uint32_t k,
+cbk_status gather(const float *S, uint64_t split_stride, uint32_t splits, uint64_t ldS, const int32_t *place_of,
+                  const int32_t *experts, uint32_t count, uint32_t k,
                   uint64_t T, uint16_t *Y, uint64_t ldy, uint64_t width, hipStream_t s) {
-    GatherArgs g{S, split_stride, splits, static_cast<uint32_t>(ldS), k, static_cast<uint32_t>(width), T, place_of, Y, ldy,
+    GatherArgs g{S, split_stride, splits, static_cast<uint32_t>(ldS), k, static_cast<uint32_t>(width), T, place_of, experts, count, Y, ldy,
                  (reinterpret_cast<uintptr_t>(Y) & 7) == 0 && ldy % 4 == 0 ? 1u : 0u};
     const uint32_t rows = static_cast<uint32_t>(std::min<uint64_t>(T, 32768));
     hipLaunchKernelGGL(k_gather, dim3(static_cast<uint32_t>((width + 1023) / 1024), rows, static_cast<uint32_t>((T + rows - 1) / rows)), dim3(256), 0, s, g);
@@ -591,8 +618,9 @@ cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, cons
         so.place_of = at<int32_t>(ws, pl.place_of);
         so.tiles = at<ExTile>(ws, pl.tiles);
         so.ntiles = at<uint32_t>(ws, pl.ntiles);
+        if (pl.one) so.place_of = nullptr;
         if (!allow_lds_once<SortArgs>(k_sort, kLdsLimit / 2)) return CBK_E_HIP;  // 64 KB of counts, and a little
-        hipLaunchKernelGGL(k_sort, dim3(1), dim3(64 * kSortWaves), kSortWaves * ex.count * 4, s, so);
+        if (!pl.one) hipLaunchKernelGGL(k_sort, dim3(1), dim3(64 * kSortWaves), kSortWaves * ex.count * 4, s, so);
         cbk_status st = launched();
         if (st != CBK_OK) return st;
 
@@ -601,6 +629,9 @@ cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, cons
         a.ntiles = so.ntiles;
         a.token_of = so.token_of;
         a.slot_of = so.slot_of;
+        a.experts = so.experts;
+        a.k = k;
+        a.count = ex.count;
         a.weights = weights + c * k;
         a.act = act;
         a.rows = static_cast<uint32_t>(ex.rows);
@@ -629,7 +660,7 @@ cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, cons
             d.S = at<float>(ws, pl.s);
             st = ex_down(d, pl, ex, s);
             if (st != CBK_OK) return st;
-            st = gather(d.S, pl.s_stride, pl.split_down, pl.ldO, so.place_of, k, n, out + c * ldo, ldo, ex.out, s);
+            st = gather(d.S, pl.s_stride, pl.split_down, pl.ldO, so.place_of, so.experts, ex.count, k, n, out + c * ldo, ldo, ex.out, s);
             if (st != CBK_OK) return st;
             continue;
         }
@@ -664,7 +695,7 @@ cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, cons
         x.S = at<float>(ws, pl.s);
         st = ex_dx(x, pl, ex, s);
         if (st != CBK_OK) return st;
-        st = gather(x.S, pl.s_stride, pl.split_x, pl.ldK, so.place_of, k, n, out + c * ldo, ldo, ex.cols, s);
+        st = gather(x.S, pl.s_stride, pl.split_x, pl.ldK, so.place_of, so.experts, ex.count, k, n, out + c * ldo, ldo, ex.cols, s);
         if (st != CBK_OK) return st;
         if (dweights) {
             hipLaunchKernelGGL(k_dweights, dim3((so.slots + 3) / 4), dim3(256), 0, s, g.dw, pl.dw_parts, so.place_of, so.slots, dweights + c * k);

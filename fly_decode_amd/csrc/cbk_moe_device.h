@@ -28,6 +28,8 @@ struct ExArgs {
     const uint32_t *ntiles;
     const uint32_t *token_of;  // of a sorted slot
     const uint32_t *slot_of;
+    const int32_t *experts;    // of one token's k slots
+    uint32_t k, count;         // experts that there are
     const uint16_t *A;         // rows by token, or (by_slot) by sorted slot
     uint32_t lda, by_slot;
     uint32_t N, R;             // columns of the result and terms of a sum (of one tensor), as the tensors have them

@@ -79,6 +79,8 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
     // tiles of 256 where the LDS holds their tables: two of gate and up, one of down
     p.tile = ex.b <= 13 && ex.b_down <= 14 && slots / active > 48 ? 256 : slots / active > 24 ? 64 : slots / active > 8 ? 32 : 16;
     p.max_tiles = static_cast<uint32_t>(active + slots / p.tile);
+    p.one = !backward && tokens == 1 && p.tile == 16 && ex.b <= 13 && ex.b_down <= 14;  // where k_experts_few does both products
+    if (p.one) p.max_tiles = k;
     // few units of work: their reductions are shared until there are two for each CU, of eight slices of 64 at least
     auto split = [&](uint64_t columns, uint64_t slices) {
         const uint64_t units = p.max_tiles * (up_to(columns, 128) / 128);

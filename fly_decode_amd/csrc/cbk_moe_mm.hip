@@ -34,17 +34,54 @@ enum Epi { kSum, kHidden, kHiddenBwd };
 constexpr int waves_n(int BM) { return BM >= 192 ? 2 : 4; }
 constexpr uint32_t slice_bytes(int BM) { return (BM + kColumns) * 128; }
 
-// A tensor's table of 2^b entries, those from U on corrupt, into LDS by all threads.
-__device__ __forceinline__ void stage_table(unsigned char *to, const ExTensor &T, uint32_t tid, uint32_t threads) {
-    const uint32_t n = 1u << T.b;
-    uint16_t *table = reinterpret_cast<uint16_t *>(to);
-    if ((reinterpret_cast<uintptr_t>(T.cb) & 15) == 0) {
-        const uint32_t whole = T.U / 8;
-        for (uint32_t i = tid; i < whole; i += threads) reinterpret_cast<u32x4 *>(table)[i] = reinterpret_cast<const u32x4 *>(T.cb)[i];
-        for (uint32_t i = whole * 8 + tid; i < n; i += threads) table[i] = i < T.U ? T.cb[i] : kCorrupt;
-    } else {
-        for (uint32_t i = tid; i < n; i += threads) table[i] = i < T.U ? T.cb[i] : kCorrupt;
+// A tensor's table of 2^b entries (b <= 14), those from U on corrupt, into LDS by 512 threads: up to 4 chunks of 8 entries
+// each, and the chunk that U falls into by 8 threads, all asked for by load() before store() waits for any.
+struct TableLoad {
+    u32x4 v[4];
+    uint32_t chunks, full, tid, last;
+    uint16_t *to;
+
+    __device__ __forceinline__ void load(unsigned char *table, const ExTensor &T, uint32_t thread) {
+        to = reinterpret_cast<uint16_t *>(table);
+        tid = thread;
+        chunks = ((1u << T.b) + 7) / 8;
+        // (a codebook that is not aligned is read entry by entry, and has no whole chunks here)
+        full = (reinterpret_cast<uintptr_t>(T.cb) & 15) == 0 ? T.U / 8 : 0;
+        const uint32_t corrupt = static_cast<uint32_t>(kCorrupt) * 0x10001u;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            v[i] = (u32x4){corrupt, corrupt, corrupt, corrupt};
+            if (i * 512 + tid < full) v[i] = reinterpret_cast<const u32x4 *>(T.cb)[i * 512 + tid];
+        }
+        last = kCorrupt;
+        if (tid < 8 && 8 * full + tid < T.U) last = T.cb[8 * full + tid];
     }
+    __device__ __forceinline__ void store(const ExTensor &T) const {
+        const bool aligned = (reinterpret_cast<uintptr_t>(T.cb) & 15) == 0;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            const uint32_t c = i * 512 + tid;
+            if (c < chunks && c != full) reinterpret_cast<u32x4 *>(to)[c] = v[i];
+        }
+        if (aligned) {
+            if (tid < 8 && full < chunks) to[8 * full + tid] = static_cast<uint16_t>(last);
+        } else {
+            lds_barrier();
+            for (uint32_t i = tid; i < 8 * chunks; i += 512) to[i] = i < T.U ? T.cb[i] : kCorrupt;
+        }
+    }
+};
+__device__ __forceinline__ void stage_table(unsigned char *table, const ExTensor &T, uint32_t tid) {
+    TableLoad l;
+    l.load(table, T, tid);
+    l.store(T);
+}
+__device__ __forceinline__ void stage_tables(unsigned char *first, const ExTensor &T0, unsigned char *second, const ExTensor &T1, uint32_t tid) {
+    TableLoad l0, l1;
+    l0.load(first, T0, tid);
+    l1.load(second, T1, tid);
+    l0.store(T0);
+    l1.store(T1);
 }
 
 // Twice the four fields (byte offsets into a table) of b bits that start at bit `shift` of d; m2 = 2 (2^b - 1).
@@ -106,7 +143,7 @@ __device__ __forceinline__ void read_columns(bf16x8_t (&x)[N], const uint32_t (&
 // What becomes of a wave's sums of one token (of a tile's token m): FN fragments of 16 columns, of which this lane has
 // columns 4 lg .. 4 lg + 3, from column FN 16 wn of the tile on (the tile has `wn_count` such parts).  Forward pairs
 // have a fragment of gate and then one of up, of the same rows.
-template <int EPI, int FN>
+template <int EPI, int FN, bool ONE = false>
 __device__ __forceinline__ void finish(const ExArgs &p, const f32x4_t (&acc)[FN], const ExTile &tile, uint32_t m, uint32_t share,
                                        uint32_t col_tile, uint32_t wn, uint32_t wn_count, uint32_t lg) {
     const bool there = m < tile.count;
@@ -114,7 +151,7 @@ __device__ __forceinline__ void finish(const ExArgs &p, const f32x4_t (&acc)[FN]
     if constexpr (EPI == kSum) {
         if (!there) return;
         const uint32_t n = (col_tile * wn_count + wn) * (FN * 16) + 4 * lg;
-        const float f = p.scaled ? p.weights[p.slot_of[at]] : 1.f;
+        const float f = p.scaled ? p.weights[ONE ? at : p.slot_of[at]] : 1.f;
         float *out = p.S + share * p.split_stride + at * p.ldS + n;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
@@ -122,7 +159,7 @@ __device__ __forceinline__ void finish(const ExArgs &p, const f32x4_t (&acc)[FN]
     } else {
         const uint32_t f0 = (col_tile * wn_count + wn) * (FN * 8) + 4 * lg;
         float sum = 0.f, w = 0.f;  // <H, D> over this wave's columns; the slot's weight
-        if constexpr (EPI == kHiddenBwd) w = p.weights[p.slot_of[at]];
+        if constexpr (EPI == kHiddenBwd) w = p.weights[ONE ? at : p.slot_of[at]];
 #pragma unroll
         for (int j = 0; j < FN; j += 2) {
             const uint32_t f = f0 + 8 * j;
@@ -221,8 +258,8 @@ __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
     const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(all) * share / p.splits);
     const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(all) * (share + 1) / p.splits);
     if constexpr (!GT) {
-        stage_table(smem, T0, tid, 512);
-        if (PAIR) stage_table(smem + p.table, T1, tid, 512);
+        if constexpr (PAIR) stage_tables(smem, T0, smem + p.table, T1, tid);
+        else stage_table(smem, T0, tid);
     }
 
     // The reduction over slices [s0, s1) of tensor `which` (forward pairs: the wave's own of the two).
@@ -440,7 +477,7 @@ __device__ __forceinline__ void read_windows(u32x3 (&w)[4], const uint32_t (&at)
     w[3] = (u32x3){a3.x, a3.y, b3};
 }
 
-template <int NF, bool PAIR, int EPI>
+template <int NF, bool PAIR, int EPI, bool ONE>
 __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
     static_assert(PAIR == (EPI != kSum), "gate and up, or one tensor");
     constexpr uint32_t NX = 4 * NF;  // loads of a step's tokens
@@ -450,7 +487,12 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
     unsigned char *stages = smem + (PAIR ? 2 : 1) * p.table + wave * (kFewRing * kFewStage);
     float *sums = reinterpret_cast<float *>(smem + (PAIR ? 2 : 1) * p.table + 8 * kFewRing * kFewStage);
 
-    const uint32_t units = *p.ntiles * p.col_tiles;
+    // One token's slots are tiles as they stand, of an expert each (nothing sorts them; unused ones have none); else as
+    // k_sort listed them.
+    auto tile_at = [&](uint32_t t) __attribute__((always_inline)) {
+        return ONE ? ExTile{static_cast<uint32_t>(p.experts[t]), t, 1, 0} : p.tiles[t];
+    };
+    const uint32_t units = (ONE ? p.k : *p.ntiles) * p.col_tiles;
     const uint32_t u0 = static_cast<uint32_t>(static_cast<uint64_t>(units) * blockIdx.x / gridDim.x);
     const uint32_t u1 = static_cast<uint32_t>(static_cast<uint64_t>(units) * (blockIdx.x + 1) / gridDim.x);
     if (u0 == u1) return;
@@ -464,7 +506,7 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
         uint32_t b;
     };
     auto tensor = [&](uint32_t expert, uint32_t j) __attribute__((always_inline)) {
-        const ExTensor &T = p.t[PAIR ? j : 0][expert];
+        const ExTensor &T = p.t[PAIR ? j : 0][ONE && expert >= p.count ? 0 : expert];
         return Tensor{in_scalars(reinterpret_cast<uint64_t>(T.words)), in_scalars(T.bytes), static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(T.b))};
     };
     // first of the 16 rows j of a unit
@@ -477,7 +519,7 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
         uint32_t v[4], b;
     } from[2];
     auto source = [&]() __attribute__((always_inline)) {  // of unit cu
-        const uint32_t expert = p.tiles[cu / p.col_tiles].expert;
+        const uint32_t expert = tile_at(cu / p.col_tiles).expert;
 #pragma unroll
         for (uint32_t j = 0; j < 2; ++j) {
             const Tensor T = tensor(expert, j);
@@ -519,11 +561,11 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
     auto rows_of = [&](uint32_t t) __attribute__((always_inline)) {
         if (rows_at == t) return;
         rows_at = t;
-        const ExTile tile = p.tiles[t];
+        const ExTile tile = tile_at(t);
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
             const uint32_t r = min(i * 16 + li, tile.count - 1);
-            vx[i] = (p.by_slot ? tile.start + r : p.token_of[tile.start + r]);
+            vx[i] = p.by_slot ? tile.start + r : ONE ? 0 : p.token_of[tile.start + r];
         }
     };
     struct Step {
@@ -609,12 +651,15 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
     }
     uint32_t staged = ~0u, place = 0;
     for (uint32_t u = u0; u < u1; ++u) {
-        tile = p.tiles[u / p.col_tiles];
+        tile = tile_at(u / p.col_tiles);
+        // (an unused slot of one token goes through the motions with the first expert's weights, and leaves nothing)
+        const bool used = !ONE || tile.expert < p.count;
+        if (!used) tile.expert = 0;
         windows(u);
         if (staged != tile.expert) {  // (the previous tables' last reads came before the last barrier)
             staged = tile.expert;
-            stage_table(smem, p.t[0][staged], tid, 512);
-            if (PAIR) stage_table(smem + p.table, p.t[1][staged], tid, 512);
+            if constexpr (PAIR) stage_tables(smem, p.t[0][staged], smem + p.table, p.t[1][staged], tid);
+            else stage_table(smem, p.t[0][staged], tid);
             lds_barrier();
         }
 #pragma unroll
@@ -654,14 +699,14 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
             for (int j = 0; j < 2; ++j) *reinterpret_cast<f32x4_t *>(to + ((wave * NF + i) * 2 + j) * 256) = acc[i][j];
         lds_barrier();
         // the waves add a unit's sums in turn
-        if (wave == static_cast<int>(u & 7)) {
+        if (wave == static_cast<int>(u & 7) && used) {
 #pragma unroll
             for (int i = 0; i < NF; ++i) {
                 f32x4_t t[2] = {};
                 for (int w = 0; w < 8; ++w)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) t[j] += *reinterpret_cast<const f32x4_t *>(to + ((w * NF + i) * 2 + j) * 256);
-                finish<EPI, 2>(p, t, tile, i * 16 + li, 0, u % p.col_tiles, 0, 1, lg);
+                finish<EPI, 2, ONE>(p, t, tile, i * 16 + li, 0, u % p.col_tiles, 0, 1, lg);
             }
         }
         if (NF > 1) lds_barrier();
@@ -738,8 +783,8 @@ __global__ __launch_bounds__(512) void k_experts_many(const ExArgs p) {
     const uint32_t all = p.slices * (NN && PAIR ? 2 : 1);  // the reduction's slices, of which this share's:
     const uint32_t c0 = static_cast<uint32_t>(static_cast<uint64_t>(all) * share / p.splits);
     const uint32_t c1 = static_cast<uint32_t>(static_cast<uint64_t>(all) * (share + 1) / p.splits);
-    if constexpr (!(NN && PAIR)) stage_table(smem, T0, tid, 512);
-    if constexpr (!NN && PAIR) stage_table(smem + p.table, T1, tid, 512);
+    if constexpr (!NN && PAIR) stage_tables(smem, T0, smem + p.table, T1, tid);
+    else if constexpr (!PAIR) stage_table(smem, T0, tid);
 
     // The reduction over slices [s0, s1) of tensor `which` (forward pairs: the wave's own of the two).
     auto pass = [&](uint32_t which, uint32_t s0, uint32_t s1, auto active) __attribute__((always_inline)) {
@@ -844,7 +889,7 @@ __global__ __launch_bounds__(512) void k_experts_many(const ExArgs p) {
         keep_order();
         load(w0, s0, 0);
         load(w1, s0, 1);
-        if constexpr (NN && PAIR) stage_table(smem, T, tid, 512);
+        if constexpr (NN && PAIR) stage_table(smem, T, tid);
         lds_barrier();  // the tables
         decode(w0, s0, 0, 0, yes);
         decode(w1, s0, 1, 0, yes);
@@ -965,19 +1010,19 @@ cbk_status run_many(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s
     return launched();
 }
 
-template <int, bool, int>
+template <int, bool, int, bool>
 struct FewTag;
 
-template <int NF, bool PAIR, int EPI>
+template <int NF, bool PAIR, int EPI, bool ONE>
 cbk_status run_few(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s) {
     a.splits = 1;
     a.col_tiles = tiles_of(columns, PAIR ? 16 : 32);
     const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles;
     if (units > (uint64_t(1) << 30)) return CBK_E_UNSUPPORTED;
-    if (!allow_lds_once<FewTag<NF, PAIR, EPI>>(k_experts_few<NF, PAIR, EPI>, kLdsLimit)) return CBK_E_HIP;
+    if (!allow_lds_once<FewTag<NF, PAIR, EPI, ONE>>(k_experts_few<NF, PAIR, EPI, ONE>, kLdsLimit)) return CBK_E_HIP;
     // a workgroup has a CU's LDS
     const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(units, cu_count()));
-    hipLaunchKernelGGL((k_experts_few<NF, PAIR, EPI>), dim3(grid), dim3(512), few_lds((PAIR ? 2 : 1) * a.table, NF), s, a);
+    hipLaunchKernelGGL((k_experts_few<NF, PAIR, EPI, ONE>), dim3(grid), dim3(512), few_lds((PAIR ? 2 : 1) * a.table, NF), s, a);
     return launched();
 }
 
@@ -987,8 +1032,9 @@ cbk_status product(ExArgs &a, const ExPlan &pl, uint32_t columns, uint32_t b, hi
     a.table = std::max(16u, 2u << b);
     if (pl.tile == kManyTokens) return run_many<NN, PAIR, EPI>(a, pl, columns, s);
     if constexpr (!NN) {
+        if (pl.one) return run_few<1, PAIR, EPI, true>(a, pl, columns, s);
         if (pl.tile <= 32 && b <= 14 && few_lds((PAIR ? 2 : 1) * a.table, pl.tile / 16) <= kLdsLimit)
-            return pl.tile == 16 ? run_few<1, PAIR, EPI>(a, pl, columns, s) : run_few<2, PAIR, EPI>(a, pl, columns, s);
+            return pl.tile == 16 ? run_few<1, PAIR, EPI, false>(a, pl, columns, s) : run_few<2, PAIR, EPI, false>(a, pl, columns, s);
     }
     return b > 14 ? run<64, NN, PAIR, EPI, true>(a, pl, columns, s) : run<64, NN, PAIR, EPI, false>(a, pl, columns, s);
 }
