@@ -2,11 +2,18 @@
 //
 // A workgroup of 16 waves has a row.  Every filter keeps a prefix of the row's order (logits falling,
 // then index), so what is kept is what stands before one cut in that order, a 64-bit key of logit and
-// index, and no row is sorted: a histogram of the distance from the largest logit (counts, and sums of
-// exp(x - max) in fixed point, whose atomic additions give the same bits in any order) finds the bin
-// that a cut falls into, and only that bin's entries are sorted, in LDS.  The draw then needs the kept
-// entries' sums in index order: a sum of each 256 entries, the 256 that the target falls into, and in
-// them the entry.
+// index, and no row is sorted.  A histogram over the logits, in bins of a sixteenth of the temperature,
+// finds the bin that a cut falls into; the entries of that bin alone are ranked, in LDS.  Sums whose
+// order could vary (atomic additions) are of fixed-point numbers, so they have the same bits in any order.
+//
+// A row of 10^5 logits is read from memory or the last cache each time, so passes over it are few.  No pass
+// looks for the maximum first: bins and exponentials are relative to the largest of the first 4096 logits.
+//   temperature alone: one pass, a sum of exponentials of each 256 entries;
+//   top_k (up to some 1500): one that counts, and one that collects the entries up to the cut's bin; all
+//     other filters and the draw are then done on that list;
+//   top_p: one that adds up the bins, and one that collects the cut's bin and adds up what stands before it;
+//   min_p without top_k: one for the maximum before those.
+// The draw takes the sums of each 256 entries in index order, then the 256 that the target falls into.
 //
 // The border between two tokens can be anywhere, and a vocabulary has 10^5 of them, so probabilities are
 // formed in fp64: an fp32 sum's 1e-7 would name another token once in some hundred rows.  On this chip
@@ -14,16 +21,21 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cbk_device.h"
 
 namespace cbk {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr uint32_t kBins = 2048;      // of the histogram
-constexpr float kSpan = 32.f;         // what it spans, in units of the temperature; the last bin holds the rest
-constexpr uint32_t kList = 2048;      // entries that are sorted at once
-constexpr uint32_t kSegments = (1u << 20) / 256 + 2;  // of 256 entries
+constexpr uint32_t kBins = 2048;           // of the histogram, 1/16 of the temperature each; the last one holds the rest
+constexpr float kPerUnit = 16.f;
+constexpr float kAbove = 16.f;             // what the first bin starts above the reference, in units of the temperature
+constexpr uint32_t kList = 2048;           // entries of a list,
+constexpr uint32_t kRanked = 1024;         // and those of a bin that are ranked against each other
+constexpr uint32_t kSteps = 4;             // of 256 entries by a wave, in a segment
+constexpr uint32_t kSegments = (1u << 20) / (256 * kSteps) + 2;
 
 struct SampleArgs {
     cbk_sampling p;
@@ -36,19 +48,19 @@ struct SampleArgs {
 };
 
 struct Shared {
+    uint64_t mass[kBins];
+    uint32_t count[kBins];
+    uint64_t list[kList];
+    uint64_t ranked[kRanked];
     union {
-        struct {
-            uint64_t mass[kBins];
-            uint32_t count[kBins];
-            uint64_t list[kList];
-        };
         double segment[kSegments];
+        uint64_t fixed_segment[kSegments];
     };
     uint64_t wave64[kWaves];
     uint32_t wave32[kWaves];
     double wavef[kWaves];
     uint64_t found64[2];
-    uint32_t found32[2];
+    uint32_t found32[3];
 };
 
 // Ascending unsigned numbers for ascending floats (-0 as +0; no NaN).
@@ -60,14 +72,16 @@ __device__ __forceinline__ float from_ascending(uint32_t u) { return __uint_as_f
 // A place in the row's order: smaller keys come first.
 __device__ __forceinline__ uint64_t place_key(float z, uint32_t i) { return (static_cast<uint64_t>(~ascending(z)) << 32) | i; }
 
-// e^x for x <= 0 to some 1e-15 of its value: 2^n times the exponential series at the rest, |r| <= ln 2 / 2, whose
-// first left-out term is r^13 / 13! < 2e-16.  0 below e^-690.
-__device__ __forceinline__ double exp_below(double x) {
-    const double n = rint(x * 1.4426950408889634074);
+// e^x for |x| < 700 to some 1e-14 of its value, 0 below -690: 2^n times the exponential series at the rest,
+// |r| <= ln 2 / 2, whose first left-out term is r^12 / 12! < 7e-15.  n is rounded by adding 1.5 * 2^52, whose sum then
+// holds it in its low bits, and goes into the result's exponent as an integer: conversions and ldexp take as long as four
+// multiplications each.
+__device__ __forceinline__ double exponential(double x) {
+    constexpr double round = 6755399441055744.0;
+    const double t = fma(x, 1.4426950408889634074, round), n = t - round;
     double r = fma(n, -0.69314718055994528623, x);
     r = fma(n, -2.3190468138462995584e-17, r);  // ln 2 less its rounding
-    double s = 1.0 / 479001600.0;
-    s = fma(s, r, 1.0 / 39916800.0);
+    double s = 1.0 / 39916800.0;
     s = fma(s, r, 1.0 / 3628800.0);
     s = fma(s, r, 1.0 / 362880.0);
     s = fma(s, r, 1.0 / 40320.0);
@@ -79,42 +93,101 @@ __device__ __forceinline__ double exp_below(double x) {
     s = fma(s, r, 0.5);
     s = fma(s, r, 1.0);
     s = fma(s, r, 1.0);
-    return x < -690.0 ? 0.0 : ldexp(s, static_cast<int>(n));
+    const uint64_t bits = __builtin_bit_cast(uint64_t, s) + (static_cast<uint64_t>(static_cast<uint32_t>(__builtin_bit_cast(uint64_t, t))) << 52);
+    return x < -690.0 ? 0.0 : __builtin_bit_cast(double, bits);
+}
+// e^x for -0.08 < x < 0.02, the series alone: the first left-out term is below 0.08^9 / 9! < 1e-15 of it.
+__device__ __forceinline__ double exponential_near_0(double x) {
+    double s = 1.0 / 40320.0;
+    s = fma(s, x, 1.0 / 5040.0);
+    s = fma(s, x, 1.0 / 720.0);
+    s = fma(s, x, 1.0 / 120.0);
+    s = fma(s, x, 1.0 / 24.0);
+    s = fma(s, x, 1.0 / 6.0);
+    s = fma(s, x, 0.5);
+    s = fma(s, x, 1.0);
+    return fma(s, x, 1.0);
+}
+// The integer nearest to m * scale, both positive, below 2^51: in the low bits of its sum with 2^52.
+__device__ __forceinline__ uint64_t rounded(double m, double scale) {
+    return __builtin_bit_cast(uint64_t, fma(m, scale, 4503599627370496.0)) & ((uint64_t(1) << 52) - 1);
 }
 
+// A row, in groups of four logits that start on whole multiples of four elements in memory; the first group's `skew` first
+// ones lie before the row.  Groups are read whole, through a resource that ends with the row's last dword (past it nothing
+// is read), and what is not the row's becomes -inf.
 template <typename T>
 struct Row {
-    const T *p;
-    uint32_t V, skew, groups;  // groups of four entries; the first group's `skew` first ones do not exist
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t V, skew, groups;
 
     __device__ __forceinline__ Row(const void *logits, uint64_t ld, uint32_t row, uint32_t n) {
-        p = static_cast<const T *>(logits) + row * ld;
+        const T *p = static_cast<const T *>(logits) + row * ld;
         V = n;
         skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & 3;
         groups = (V + skew + 3) / 4;
+        rs = wave_rsrc(p - skew, ((V + skew) * static_cast<uint32_t>(sizeof(T)) + 3) & ~3u);
     }
-    static __device__ __forceinline__ float value(float v) { return v; }
-    static __device__ __forceinline__ float value(uint16_t v) { return bf16_value(v); }
-    // The index of the group's first entry (possibly before the row) and its four logits, -inf where there is none.
-    __device__ __forceinline__ int32_t load(uint32_t g, float (&z)[4]) const {
-        const int32_t at = static_cast<int32_t>(4 * g) - static_cast<int32_t>(skew);
-        if (at >= 0 && at + 4 <= static_cast<int32_t>(V)) {
-            if constexpr (sizeof(T) == 4) {
-                const f32x4_t v = *reinterpret_cast<const f32x4_t *>(p + at);
-                z[0] = v[0]; z[1] = v[1]; z[2] = v[2]; z[3] = v[3];
-            } else {
-                const u32x2 v = *reinterpret_cast<const u32x2 *>(p + at);
-                z[0] = bf16_value(static_cast<uint16_t>(v.x)); z[1] = bf16_value(static_cast<uint16_t>(v.x >> 16));
-                z[2] = bf16_value(static_cast<uint16_t>(v.y)); z[3] = bf16_value(static_cast<uint16_t>(v.y >> 16));
-            }
+    typedef std::conditional_t<sizeof(T) == 4, u32x4, u32x2> Raw;
+    __device__ __forceinline__ Raw raw(uint32_t g) const {
+        if constexpr (sizeof(T) == 4) return __builtin_amdgcn_raw_buffer_load_b128(rs, static_cast<int>(g * 16), 0, 0);
+        else return __builtin_amdgcn_raw_buffer_load_b64(rs, static_cast<int>(g * 8), 0, 0);
+    }
+    // The index of the group's first entry (possibly before the row) and its four logits.
+    __device__ __forceinline__ int32_t values(uint32_t g, Raw v, float (&z)[4]) const {
+        if constexpr (sizeof(T) == 4) {
+            z[0] = __uint_as_float(v.x); z[1] = __uint_as_float(v.y); z[2] = __uint_as_float(v.z); z[3] = __uint_as_float(v.w);
         } else {
+            z[0] = __uint_as_float(v.x << 16); z[1] = __uint_as_float(v.x & 0xFFFF0000u);
+            z[2] = __uint_as_float(v.y << 16); z[3] = __uint_as_float(v.y & 0xFFFF0000u);
+        }
+        const int32_t at = static_cast<int32_t>(4 * g) - static_cast<int32_t>(skew);
+        if (g == 0 || g + 1 >= groups) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                z[j] = at + j >= 0 && at + j < static_cast<int32_t>(V) ? value(p[at + j]) : -__builtin_inff();
+            for (int j = 0; j < 4; ++j) z[j] = at + j >= 0 && at + j < static_cast<int32_t>(V) ? z[j] : -__builtin_inff();
         }
         return at;
     }
+    __device__ __forceinline__ int32_t load(uint32_t g, float (&z)[4]) const { return values(g, raw(g), z); }
 };
+
+// f(index of the first, four logits, segment, whether it is the wave's last of the segment) for this thread's groups of
+// the row, four pieces ahead of it asked for; past the row's end logits are -inf.  A wave has segments of kSteps times 64
+// neighbouring groups, every 16th of them.  f's code stands once: a pass is short, and what it takes to fetch its
+// instructions counts (unrolled eight times, one row of 32000 took 40 us instead of 28).
+template <typename T, typename F>
+__device__ __forceinline__ void over_row(const Row<T> &r, F f) {
+    constexpr uint32_t N = 4;
+    static_assert(N == kSteps, "a group four pieces on is the same one of the next segment");
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    typename Row<T>::Raw z[N];
+    uint32_t segment = wave, first = wave * (64 * kSteps) + lane;
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) z[i] = r.raw(first + 64 * i);
+    uint32_t step = 0;
+#pragma unroll 1
+    while (segment * (64 * kSteps) < r.groups) {  // a wave stays together
+        const uint32_t g = first + 64 * step;
+        float now[4];
+        const int32_t at = r.values(g, z[0], now);
+#pragma unroll
+        for (uint32_t i = 0; i + 1 < N; ++i) z[i] = z[i + 1];
+        z[N - 1] = r.raw(g + kWaves * (64 * kSteps));
+        f(at, now, segment, step == kSteps - 1);
+        if (++step == kSteps) {
+            step = 0;
+            segment += kWaves;
+            first += kWaves * (64 * kSteps);
+        }
+    }
+}
+
+// The sum of v over the wave, everywhere, in a fixed order.
+__device__ __forceinline__ double wave_total(double v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
 
 template <typename V>
 __device__ __forceinline__ V shuffle_up(V v, int by) {
@@ -153,296 +226,577 @@ __device__ __forceinline__ V sum_before(V v, V *wave, V &total) {
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
-    __shared__ Shared sh;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem);
     const uint32_t row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const Row<T> r(a.logits, a.ld, row, a.V);
     const uint32_t V = a.V;
-    const double nan = __builtin_nan("");
+    const float inf = __builtin_inff();
 
-    // the largest logit, and whether there is a NaN
-    float top = -__builtin_inff();
-    bool odd = false;
-    for (uint32_t g = tid; g < r.groups; g += kThreads) {
-        float z[4];
-        r.load(g, z);
+    // The largest of the threads' v, everywhere; a NaN if any of them has `odd`.
+    auto largest = [&](float v, bool odd) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            odd = odd || z[j] != z[j];
-            top = fmaxf(top, z[j]);
+        for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+        if (__any(odd)) v = __builtin_nanf("");
+        __syncthreads();
+        if (lane == 0) sh.wave32[wave] = __float_as_uint(v);
+        __syncthreads();
+        float most = -inf;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const float t = __uint_as_float(sh.wave32[i]);
+            bad = bad || t != t;
+            most = fmaxf(most, t);
         }
-    }
+        __syncthreads();
+        return bad ? __builtin_nanf("") : most;
+    };
+    auto row_largest = [&]() __attribute__((always_inline)) {
+        float top = -inf;
+        bool odd = false;
+        over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-    if (lane == 0) sh.wavef[wave] = top;
-    if (__any(odd)) {
-        if (lane == 0) sh.wavef[wave] = nan;
-    }
-    __syncthreads();
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        const float t = static_cast<float>(sh.wavef[i]);
-        bad = bad || t != t;
-        top = fmaxf(top, t);
-    }
-    __syncthreads();
-    const float heat = a.p.temperatures ? a.p.temperatures[row] : a.p.temperature;
-    if (bad || top == -__builtin_inff() || heat != heat) {
+            for (int j = 0; j < 4; ++j) {
+                odd = odd || z[j] != z[j];
+                top = fmaxf(top, z[j]);
+            }
+        });
+        return largest(top, odd);
+    };
+    auto nothing = [&]() __attribute__((always_inline)) {  // the row has no token
         if (tid == 0) {
             a.token[row] = -1;
             if (a.logprob) a.logprob[row] = __builtin_nanf("");
         }
-        return;
-    }
-    if (heat <= 0.f) {  // the first of the largest
-        uint32_t first = ~0u;
-        for (uint32_t g = tid; g < r.groups && first == ~0u; g += kThreads) {
-            float z[4];
-            const int32_t at = r.load(g, z);
+    };
+
+    const float heat = a.p.temperatures ? a.p.temperatures[row] : a.p.temperature;
+    const int32_t top_k = a.p.top_ks ? a.p.top_ks[row] : a.p.top_k;
+    const float top_p = a.p.top_ps ? a.p.top_ps[row] : a.p.top_p;
+    const float min_p = fminf(a.p.min_ps ? a.p.min_ps[row] : a.p.min_p, 1.f);
+    const float u = a.uniform[row];
+    const double share = u >= 0.f ? static_cast<double>(u) : 0.0;
+    if (heat != heat) return nothing();
+    if (heat <= 0.f) {  // the first of the largest: the least key
+        uint64_t first = ~uint64_t(0);
+        bool odd = false;
+        over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 3; j >= 0; --j)
-                if (z[j] == top) first = at + j;
-        }
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) first = min(first, static_cast<uint32_t>(__shfl_xor(first, o, 64)));
-        if (lane == 0) sh.wave32[wave] = first;
+            for (int j = 0; j < 4; ++j) {
+                odd = odd || z[j] != z[j];
+                if (z[j] != -inf) first = min(first, place_key(z[j], at + j));
+            }
+        });
+        if (tid == 0) sh.found64[0] = ~uint64_t(0);
+        const float bad = largest(0.f, odd);
+        atomicMin(reinterpret_cast<unsigned long long *>(&sh.found64[0]), static_cast<unsigned long long>(first));
         __syncthreads();
+        first = sh.found64[0];
+        if (bad != bad || first == ~uint64_t(0)) return nothing();
         if (tid == 0) {
-            for (int i = 0; i < kWaves; ++i) first = min(first, sh.wave32[i]);
-            a.token[row] = first;
+            a.token[row] = static_cast<uint32_t>(first);
             if (a.logprob) a.logprob[row] = 0.f;
         }
         return;
     }
 
-    const double inv = 1.0 / static_cast<double>(heat), dtop = top;
-    const bool endless = top == __builtin_inff();
-    // x = (z - max) / temperature
-    auto exponent = [&](float z) { return endless ? (z == top ? 0.0 : -1e300) : (static_cast<double>(z) - dtop) * inv; };
-    auto mass_of = [&](float z) { return z == -__builtin_inff() ? 0.0 : exp_below(exponent(z)); };
-
-    const int32_t top_k = a.p.top_ks ? a.p.top_ks[row] : a.p.top_k;
-    const float top_p = a.p.top_ps ? a.p.top_ps[row] : a.p.top_p;
-    const float min_p = fminf(a.p.min_ps ? a.p.min_ps[row] : a.p.min_p, 1.f);
-    // min_p: logits below `least` are out; rounded up, so that comparing floats is comparing with the border
-    float least = -__builtin_inff();
-    if (min_p > 0.f && !endless) {
-        const double border = dtop + static_cast<double>(heat) * log(static_cast<double>(min_p));
-        least = static_cast<float>(border);
-        if (static_cast<double>(least) < border) least = from_ascending(ascending(least) + 1);
-        least = fminf(least, top);
-    } else if (min_p > 0.f) {
-        least = top;
-    }
-    uint64_t cut = ~uint64_t(0);  // the last key that is kept
     const bool by_count = top_k > 0 && static_cast<uint32_t>(top_k) < V, by_mass = top_p < 1.f;
+    const bool short_list = by_count && static_cast<uint32_t>(top_k) <= kList * 3 / 4;
+    const double inv = 1.0 / static_cast<double>(heat);
+    const double part = fmax(static_cast<double>(top_p), 0.0);
 
-    if (by_count || by_mass) {
-        // the histogram; masses are counted in units of 2^-unit, which leaves their sum below 2^63
-        const int unit = 62 - (32 - __clz(V));
-        const float step = fminf((kBins - 1) / kSpan / heat, 1e30f);
-        auto bin_of = [&](float z) {
-            if (endless) return z == top ? 0u : kBins - 1;
-            return static_cast<uint32_t>(fminf((top - z) * step, static_cast<float>(kBins - 1)));
-        };
-        auto fixed = [&](float z) { return static_cast<uint64_t>(ldexp(mass_of(z), unit)); };
-        for (uint32_t i = tid; i < kBins; i += kThreads) {
-            sh.mass[i] = 0;
-            sh.count[i] = 0;
-        }
-        __syncthreads();
-        for (uint32_t g = tid; g < r.groups; g += kThreads) {
-            float z[4];
-            r.load(g, z);
+    // ---- the reference: the largest of the first entries, or, where it has to be known, of all
+    float ref = -inf, top = -inf;  // top: of the row, once it is known
+    bool known = false;
+    if (!(min_p > 0.f && !short_list)) {
+        float z[4];
+        bool odd = false;
+        r.load(tid, z);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (z[j] >= least && z[j] != -__builtin_inff()) {
-                    const uint32_t b = bin_of(z[j]);
-                    atomicAdd(&sh.count[b], 1u);
-                    atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[b]), static_cast<unsigned long long>(fixed(z[j])));
-                }
+        for (int j = 0; j < 4; ++j) {
+            odd = odd || z[j] != z[j];
+            ref = fmaxf(ref, z[j]);
+        }
+        ref = largest(ref, odd);
+        if (ref != ref) return nothing();
+    }
+    if (!(fabsf(ref) < inf)) {
+        top = ref = row_largest();
+        known = true;
+        if (top != top || top == -inf) return nothing();
+    }
+    float least = -inf;  // what min_p leaves out is below it; rounded up, so that comparing floats is comparing with the border
+    auto border = [&]() __attribute__((always_inline)) {
+        if (min_p > 0.f && top == inf) {
+            least = top;
+        } else if (min_p > 0.f) {
+            const double edge = static_cast<double>(top) + static_cast<double>(heat) * log(static_cast<double>(min_p));
+            least = static_cast<float>(edge);
+            if (static_cast<double>(least) < edge) least = from_ascending(ascending(least) + 1);
+            least = fminf(least, top);
+        }
+    };
+    if (known) border();
+
+    // x relative to a logit; entries of +inf, where there are any, are all that counts
+    auto exponent = [&](float z, float to) __attribute__((always_inline)) {
+        if (to == inf) return z == inf ? 0.0 : -1e300;
+        return (static_cast<double>(z) - static_cast<double>(to)) * inv;
+    };
+    auto mass_of = [&](float z, float to) __attribute__((always_inline)) { return exponential(exponent(z, to)); };  // 0 of -inf
+    // The masses of the four logits that are `kept`, others 0: side by side, with no branch around each (whose chains of
+    // dependent operations would run one after the other), and none at all where the wave has none.
+    auto masses = [&](const float (&z)[4], const bool (&kept)[4], float to, double (&m)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = 0.0;
+        if (!__any(kept[0] || kept[1] || kept[2] || kept[3])) return;
+        double e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = mass_of(z[j], to);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = kept[j] ? e[j] : 0.0;
+    };
+    const float step = fminf(kPerUnit / heat, 1e30f);
+    // where a logit lies in the histogram: below 0 where the reference was too low (its place then is the first bin)
+    auto place_of = [&](float z) __attribute__((always_inline)) {
+        if (ref == inf) return z == inf ? 0.f : static_cast<float>(kBins - 1);
+        return fminf((ref - z) * step + kAbove * kPerUnit, static_cast<float>(kBins - 1));
+    };
+    auto bin_of = [&](float z) __attribute__((always_inline)) { return static_cast<uint32_t>(fmaxf(place_of(z), 0.f)); };
+    auto in = [&](float z) __attribute__((always_inline)) { return z >= least && z != -inf; };
+    // masses relative to the row's largest, in units of 2^-unit, which leaves their sum below 2^63
+    const int unit = min(50, 62 - (32 - __clz(V)));
+    const double scale = ldexp(1.0, unit);
+    auto fixed = [&](float z) __attribute__((always_inline)) { return rounded(mass_of(z, top), scale); };
+    auto key_logit = [&](uint64_t key) __attribute__((always_inline)) { return from_ascending(~static_cast<uint32_t>(key >> 32)); };
+    auto add64 = [&](uint64_t *to, uint64_t v) __attribute__((always_inline)) {
+        atomicAdd(reinterpret_cast<unsigned long long *>(to), static_cast<unsigned long long>(v));
+    };
+
+    uint64_t cut = ~uint64_t(0);  // the last key that is kept
+
+    // Cuts among the n <= kRanked keys in sh.ranked: the `some` first of them, or those before which less than `most` of
+    // mass stands; at least one.  The last one's key in `cut`; returns the mass of what is kept.  All threads.
+    auto cut_ranked = [&](uint32_t n, uint32_t some, uint64_t most) __attribute__((always_inline)) -> uint64_t {
+        if (tid < 2) sh.found64[tid] = 0;
+        uint64_t own = 0, m = 0;
+        if (tid < n) {
+            own = sh.ranked[tid];
+            m = by_mass ? fixed(key_logit(own)) : 0;
         }
         __syncthreads();
-
-        // The entries before bin 2 tid, and their mass.
+        if (tid < n) sh.mass[tid] = m;
+        __syncthreads();
+        if (tid < n) {
+            uint32_t rank = 0;
+            uint64_t before = 0;
+            for (uint32_t i = 0; i < n; ++i) {
+                const bool less = sh.ranked[i] < own;
+                rank += less;
+                before += less ? sh.mass[i] : 0;
+            }
+            if (rank == 0 || (rank < some && before < most)) {
+                atomicMax(reinterpret_cast<unsigned long long *>(&sh.found64[0]), static_cast<unsigned long long>(own));
+                atomicMax(reinterpret_cast<unsigned long long *>(&sh.found64[1]), static_cast<unsigned long long>(before + m));
+            }
+        }
+        __syncthreads();
+        cut = min(cut, sh.found64[0]);
+        const uint64_t mass = sh.found64[1];
+        __syncthreads();
+        return mass;
+    };
+    // The part of bin b that the cut falls into, of 2048, by the counts and masses of its parts in sh.count and sh.mass;
+    // takes what stands before it off `some` and `most`, and adds it to `mass`.
+    auto pick_part = [&](uint32_t &some, uint64_t &most, uint64_t &mass) __attribute__((always_inline)) {
         const uint32_t c0 = sh.count[2 * tid], c1 = sh.count[2 * tid + 1];
         const uint64_t m0 = sh.mass[2 * tid], m1 = sh.mass[2 * tid + 1];
-        uint32_t entries;
-        uint64_t whole;
-        const uint32_t cb = sum_before(c0 + c1, sh.wave32, entries);
-        const uint64_t mb = sum_before(m0 + m1, sh.wave64, whole);
-
-        // The first `some` entries of bin `b`, or those before which less than `most` of mass stands: the key of
-        // the last of them in `cut`; returns their mass.  At least one.  All threads.
-        auto cut_bin = [&](uint32_t b, uint32_t n, uint32_t some, uint64_t most) -> uint64_t {
-            __syncthreads();
-            if (n <= kList) {
-                if (tid == 0) sh.found32[0] = 0;
-                uint32_t size = 64;
-                while (size < n) size *= 2;
-                for (uint32_t i = tid; i < size; i += kThreads) sh.list[i] = ~uint64_t(0);
-                __syncthreads();
-                for (uint32_t g = tid; g < r.groups; g += kThreads) {
-                    float z[4];
-                    const int32_t at = r.load(g, z);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (z[j] >= least && z[j] != -__builtin_inff() && bin_of(z[j]) == b)
-                            sh.list[atomicAdd(&sh.found32[0], 1u)] = place_key(z[j], at + j);
-                }
-                __syncthreads();
-                // bitonic sort
-                for (uint32_t k = 2; k <= size; k *= 2)
-                    for (uint32_t d = k / 2; d > 0; d /= 2) {
-                        for (uint32_t i = tid; i < size / 2; i += kThreads) {
-                            const uint32_t lo = 2 * i - (i & (d - 1)), hi = lo + d;
-                            const uint64_t x = sh.list[lo], y = sh.list[hi];
-                            if ((x > y) == ((lo & k) == 0)) {
-                                sh.list[lo] = y;
-                                sh.list[hi] = x;
-                            }
-                        }
-                        __syncthreads();
-                    }
-                uint64_t m[2] = {0, 0};
-#pragma unroll
-                for (uint32_t j = 0; j < 2; ++j)
-                    if (2 * tid + j < n) m[j] = fixed(from_ascending(~static_cast<uint32_t>(sh.list[2 * tid + j] >> 32)));
-                uint64_t all;
-                uint64_t before = sum_before(m[0] + m[1], sh.wave64, all);
-                if (tid == 0) {
-                    sh.found64[0] = sh.list[0];
-                    sh.found64[1] = m[0];
-                }
-                __syncthreads();
-                // the last that is kept (the entries before it are: sums only grow)
-#pragma unroll
-                for (uint32_t j = 0; j < 2; ++j) {
-                    const uint32_t i = 2 * tid + j;
-                    const bool in = i < n && i < some && before < most;
-                    const uint64_t next = before + m[j];
-                    const bool last = in && !(i + 1 < n && i + 1 < some && next < most);
-                    if (last) {
-                        sh.found64[0] = sh.list[i];
-                        sh.found64[1] = next;
-                    }
-                    before = next;
-                }
-                __syncthreads();
-                cut = sh.found64[0];
-                return sh.found64[1];
-            }
-            // Too many to sort (many equal logits, or a cut far below the largest): the smallest key with enough before
-            // and at it, bit by bit; each of the 64 steps goes over the row.
-            uint64_t key = 0, kept = 0;
-            for (int bit = 63; bit >= 0; --bit) {
-                const uint64_t probe = key | (uint64_t(1) << bit);  // keys below `probe` are counted
-                uint32_t c = 0;
-                uint64_t m = 0;
-                for (uint32_t g = tid; g < r.groups; g += kThreads) {
-                    float z[4];
-                    const int32_t at = r.load(g, z);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (z[j] >= least && z[j] != -__builtin_inff() && bin_of(z[j]) == b && place_key(z[j], at + j) < probe) {
-                            ++c;
-                            m += fixed(z[j]);
-                        }
-                }
-                uint32_t call;
-                uint64_t mall;
-                sum_before(c, sh.wave32, call);
-                sum_before(m, sh.wave64, mall);
-                // the key is at or past `probe` while the entries before `probe` leave room for one more
-                if (call < some && mall < most) {
-                    key = probe;
-                    kept = mall;
-                }
-            }
-            // `key` is the largest key before which there is room: the entry at it, or the last before it, is the last kept
-            uint64_t best = 0, m = 0;
-            for (uint32_t g = tid; g < r.groups; g += kThreads) {
-                float z[4];
-                const int32_t at = r.load(g, z);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (z[j] >= least && z[j] != -__builtin_inff() && bin_of(z[j]) == b && place_key(z[j], at + j) == key) {
-                        best = key;
-                        m = fixed(z[j]);
-                    }
-            }
-            uint64_t at_key;
-            sum_before(m, sh.wave64, at_key);
-            (void)best;
-            cut = key;
-            return kept + at_key;
-        };
-
-        if (by_count && static_cast<uint32_t>(top_k) < entries) {
-            const uint32_t want = top_k;
-            const bool here = cb < want && want <= cb + c0 + c1;  // of one thread alone
-            if (here) {
-                const bool second = want > cb + c0;
-                sh.found32[0] = 2 * tid + second;
-                sh.found32[1] = want - (second ? cb + c0 : cb);
-                sh.found64[0] = second ? mb + m0 : mb;
-            }
-            __syncthreads();
-            const uint32_t b = sh.found32[0], some = sh.found32[1];
-            const uint64_t before = sh.found64[0];
-            const uint32_t n = sh.count[b];
-            whole = before + cut_bin(b, n, some, ~uint64_t(0));
-            __syncthreads();
-        }
-        if (by_mass) {
-            // entries before which less than `want` stands are kept
-            const double share = fmax(static_cast<double>(top_p), 0.0) * static_cast<double>(whole);
-            const uint64_t want = max(uint64_t(1), static_cast<uint64_t>(ceil(share)));
-            if (tid == 0) sh.found32[0] = kBins;
-            __syncthreads();
-            // the last bin before which less than `want` stands, of those that hold anything
-            const bool in0 = c0 > 0 && mb < want, in1 = c1 > 0 && mb + m0 < want;
-            const bool past0 = mb + m0 >= want, past1 = mb + m0 + m1 >= want;
-            if (in0 && past0) {
-                sh.found32[0] = 2 * tid;
-                sh.found64[0] = mb;
-            }
-            if (in1 && past1) {
-                sh.found32[0] = 2 * tid + 1;
-                sh.found64[0] = mb + m0;
-            }
-            __syncthreads();
-            const uint32_t b = sh.found32[0];
-            const uint64_t before = sh.found64[0];
-            if (b < kBins) {  // else rounding leaves nothing past it: all are kept
-                const uint64_t old = cut;
-                cut_bin(b, sh.count[b], ~0u, want - before);
-                cut = cut < old ? cut : old;
-            }
+        uint32_t count_all;
+        uint64_t mass_all;
+        const uint32_t cb = sum_before(c0 + c1, sh.wave32, count_all);
+        const uint64_t mb = sum_before(m0 + m1, sh.wave64, mass_all);
+        if (tid == 0) sh.found32[0] = 0;
+        __syncthreads();
+        // the last part whose first entry is kept
+        const bool k0 = c0 > 0 && (cb == 0 || (cb < some && mb < most));
+        const bool k1 = c1 > 0 && (cb + c0 == 0 || (cb + c0 < some && mb + m0 < most));
+        if (k0 || k1) atomicMax(&sh.found32[0], 2 * tid + (k1 ? 1 : 0));
+        __syncthreads();
+        const uint32_t x = sh.found32[0];
+        if (tid == x / 2) {
+            sh.found32[1] = x & 1 ? cb + c0 : cb;
+            sh.found64[0] = x & 1 ? mb + m0 : mb;
         }
         __syncthreads();
-    }
-
-    // sums of 256 entries each, in index order
-    auto kept_mass = [&](float z, int32_t i) {
-        return z >= least && place_key(z, static_cast<uint32_t>(i)) <= cut ? mass_of(z) : 0.0;
+        some -= min(some, sh.found32[1]);
+        most -= min(most, sh.found64[0]);
+        mass += sh.found64[0];
+        __syncthreads();
+        return x;
     };
-    auto wave_total = [](double v) {
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-        return v;
+    auto part_of = [&](float z, uint32_t b) __attribute__((always_inline)) {
+        return static_cast<uint32_t>(fminf(fmaxf((place_of(z) - static_cast<float>(b)) * kBins, 0.f), static_cast<float>(kBins - 1)));
     };
-    const uint32_t segments = (r.groups + 63) / 64;
-    for (uint32_t s = wave; s < segments; s += kWaves) {
-        float z[4];
-        double m = 0.0;
-        if (s * 64 + lane < r.groups) {
-            const int32_t at = r.load(s * 64 + lane, z);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m += kept_mass(z[j], at + j);
+    auto no_parts = [&]() __attribute__((always_inline)) {
+        for (uint32_t i = tid; i < kBins; i += kThreads) {
+            sh.count[i] = 0;
+            sh.mass[i] = 0;
         }
-        m = wave_total(m);
-        if (lane == 0) sh.segment[s] = m;
+        if (tid == 0) sh.found32[2] = 0;
+        __syncthreads();
+    };
+    auto into_part = [&](float z, uint32_t b) __attribute__((always_inline)) {
+        const uint32_t x = part_of(z, b);
+        atomicAdd(&sh.count[x], 1u);
+        if (by_mass) add64(&sh.mass[x], fixed(z));
+    };
+    auto rank_if = [&](bool yes, uint64_t key) __attribute__((always_inline)) {
+        if (yes) {
+            const uint32_t i = atomicAdd(&sh.found32[2], 1u);
+            if (i < kRanked) sh.ranked[i] = key;
+        }
+    };
+    // The same among the entries of bin b; `segments`: adds up what is kept by segments too, with the entries of the bins
+    // before it; false where it did not.  Up to kList entries are divided up in LDS, more by passes over the row; where even
+    // a part of the bin holds more than kRanked (equal logits), the cut's key is found by its bits.
+    auto cut_bin = [&](uint32_t b, uint32_t some, uint64_t most, bool segments, uint64_t &mass) __attribute__((always_inline)) {
+        __syncthreads();
+        if (tid == 0) sh.found32[2] = 0;
+        __syncthreads();
+        double m = 0.0;
+        over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
+            bool kept[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = bin_of(z[j]);
+                kept[j] = in(z[j]) && x < b;
+                if (in(z[j]) && x == b) {
+                    const uint32_t i = atomicAdd(&sh.found32[2], 1u);
+                    if (i < kList) sh.list[i] = place_key(z[j], at + j);
+                }
+            }
+            if (segments) {
+                double e[4];
+                masses(z, kept, top, e);
+                m += (e[0] + e[1]) + (e[2] + e[3]);
+            }
+            if (segments && last) {
+                m = wave_total(m);
+                if (lane == 0) sh.fixed_segment[segment] = static_cast<uint64_t>(ldexp(m, unit));
+                m = 0.0;
+            }
+        });
+        __syncthreads();
+        const uint32_t n = sh.found32[2];
+        mass = 0;
+        __syncthreads();
+        no_parts();
+        uint64_t key[2];
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) key[j] = n <= kList && 2 * tid + j < n ? sh.list[2 * tid + j] : ~uint64_t(0);
+        if (n <= kList) {
+#pragma unroll
+            for (uint32_t j = 0; j < 2; ++j)
+                if (key[j] != ~uint64_t(0)) into_part(key_logit(key[j]), b);
+        } else {
+            over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in(z[j]) && bin_of(z[j]) == b) into_part(z[j], b);
+            });
+        }
+        __syncthreads();
+        const uint32_t x = pick_part(some, most, mass);
+        if (n <= kList) {
+#pragma unroll
+            for (uint32_t j = 0; j < 2; ++j) rank_if(key[j] != ~uint64_t(0) && part_of(key_logit(key[j]), b) == x, key[j]);
+        } else {
+            over_row(r, [&](int32_t at, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) rank_if(in(z[j]) && bin_of(z[j]) == b && part_of(z[j], b) == x, place_key(z[j], at + j));
+            });
+        }
+        __syncthreads();
+        const uint32_t ranked = sh.found32[2];
+        if (ranked <= kRanked) {
+            mass += cut_ranked(ranked, some, most);
+            if (segments && n <= kList) {
+#pragma unroll
+                for (uint32_t j = 0; j < 2; ++j)
+                    if (key[j] <= cut && key[j] != ~uint64_t(0))
+                        add64(&sh.fixed_segment[(static_cast<uint32_t>(key[j]) + r.skew) / (256 * kSteps)], fixed(key_logit(key[j])));
+                __syncthreads();
+                return true;
+            }
+            return false;
+        }
+        // The largest key before which there is room for one more in the part, bit by bit: 64 passes.
+        uint64_t found = 0, before = 0;
+        for (int bit = 63; bit >= 0; --bit) {
+            const uint64_t probe = found | (uint64_t(1) << bit);
+            uint32_t c = 0;
+            uint64_t own = 0;
+            over_row(r, [&](int32_t at, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in(z[j]) && bin_of(z[j]) == b && part_of(z[j], b) == x && place_key(z[j], at + j) < probe) {
+                        ++c;
+                        if (by_mass) own += fixed(z[j]);
+                    }
+            });
+            uint32_t count_all;
+            uint64_t mass_all;
+            sum_before(c, sh.wave32, count_all);
+            sum_before(own, sh.wave64, mass_all);
+            if (count_all == 0 || (count_all < some && mass_all < most)) {
+                found = probe;
+                before = mass_all;
+            }
+        }
+        // the entry at that key, if there is one, is the last
+        uint64_t own = 0, at_key;
+        over_row(r, [&](int32_t at, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (by_mass && in(z[j]) && place_key(z[j], at + j) == found) own = fixed(z[j]);
+        });
+        sum_before(own, sh.wave64, at_key);
+        cut = min(cut, found);
+        mass += before + at_key;
+        return false;
+    };
+    // Of the histogram's masses (before bin 2 tid: `mb`, its own and the next one's m0 and m1): the bin that the target
+    // falls into, and what stands before it; kBins where rounding leaves nothing past it.
+    auto mass_bin = [&](uint64_t mb, uint64_t m0, uint64_t m1, uint64_t want, uint64_t &earlier) __attribute__((always_inline)) {
+        __syncthreads();
+        if (tid == 0) sh.found32[1] = kBins;
+        __syncthreads();
+        if (mb < want && mb + m0 >= want) {
+            sh.found32[1] = 2 * tid;
+            sh.found64[0] = mb;
+        }
+        if (mb + m0 < want && mb + m0 + m1 >= want) {
+            sh.found32[1] = 2 * tid + 1;
+            sh.found64[0] = mb + m0;
+        }
+        __syncthreads();
+        const uint32_t b = sh.found32[1];
+        earlier = sh.found64[0];
+        __syncthreads();
+        return b;
+    };
+    auto target_of = [&](uint64_t whole) __attribute__((always_inline)) {
+        return max(uint64_t(1), static_cast<uint64_t>(ceil(part * static_cast<double>(whole))));
+    };
+
+    const uint32_t segments = (r.groups + 64 * kSteps - 1) / (64 * kSteps);
+    bool have = false;  // the segments' sums are there, in fixed point
+    if (by_count) {
+        // ---- counts, and the row's largest
+        for (uint32_t i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
+        __syncthreads();
+        float most = -inf;
+        bool odd = false;
+        over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                odd = odd || z[j] != z[j];
+                most = fmaxf(most, z[j]);
+                if (in(z[j])) atomicAdd(&sh.count[bin_of(z[j])], 1u);
+            }
+        });
+        top = largest(most, odd);
+        if (top != top || top == -inf) return nothing();
+        if (top == inf && ref != inf) {  // the bins do not hold: +inf alone counts
+            ref = inf;
+            for (uint32_t i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
+            __syncthreads();
+            over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in(z[j])) atomicAdd(&sh.count[bin_of(z[j])], 1u);
+            });
+            __syncthreads();
+        }
+        const uint32_t c0 = sh.count[2 * tid], c1 = sh.count[2 * tid + 1], want = top_k;
+        uint32_t entries;
+        const uint32_t before = sum_before(c0 + c1, sh.wave32, entries);
+        const uint32_t keep = min(want, entries);
+        if (before < keep && keep <= before + c0 + c1) {  // one thread
+            const bool second = keep > before + c0;
+            sh.found32[0] = 2 * tid + second;
+            sh.found32[1] = before + c0 + (second ? c1 : 0);  // entries up to that bin
+            sh.found32[2] = second ? before + c0 : before;    // and before it
+        }
+        __syncthreads();
+        const uint32_t limit = sh.found32[0], upto = sh.found32[1], earlier = sh.found32[2];
+        __syncthreads();
+        if (upto <= kList && upto - earlier <= kRanked) {
+            // ---- the list: entries up to the cut's bin, those of the bin ranked; then the other filters on it
+            if (tid < 2) sh.found32[tid] = 0;
+            __syncthreads();
+            over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in(z[j]) && bin_of(z[j]) <= limit) {
+                        const uint64_t key = place_key(z[j], at + j);
+                        sh.list[atomicAdd(&sh.found32[0], 1u)] = key;
+                        if (bin_of(z[j]) == limit) sh.ranked[atomicAdd(&sh.found32[1], 1u)] = key;
+                    }
+            });
+            __syncthreads();
+            if (keep < entries) cut_ranked(upto - earlier, keep - earlier, ~uint64_t(0));
+            border();
+            uint64_t key[2], m[2];
+#pragma unroll
+            for (uint32_t j = 0; j < 2; ++j) {
+                key[j] = 2 * tid + j < upto ? sh.list[2 * tid + j] : ~uint64_t(0);
+                m[j] = 0;
+                if (key[j] <= cut && key[j] != ~uint64_t(0) && key_logit(key[j]) >= least) m[j] = fixed(key_logit(key[j]));
+            }
+            if (by_mass) {
+                for (uint32_t i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
+                if (tid == 0) sh.found32[0] = 0;
+                __syncthreads();
+#pragma unroll
+                for (uint32_t j = 0; j < 2; ++j)
+                    if (m[j]) add64(&sh.mass[bin_of(key_logit(key[j]))], m[j]);
+                __syncthreads();
+                const uint64_t m0 = sh.mass[2 * tid], m1 = sh.mass[2 * tid + 1];
+                uint64_t whole, earlier_mass;
+                const uint64_t mb = sum_before(m0 + m1, sh.wave64, whole), want_mass = target_of(whole);
+                const uint32_t b = mass_bin(mb, m0, m1, want_mass, earlier_mass);
+                if (b < kBins) {
+#pragma unroll
+                    for (uint32_t j = 0; j < 2; ++j)
+                        if (m[j] && bin_of(key_logit(key[j])) == b) {
+                            const uint32_t i = atomicAdd(&sh.found32[0], 1u);
+                            if (i < kRanked) sh.ranked[i] = key[j];
+                        }
+                    __syncthreads();
+                    const uint32_t n = sh.found32[0];
+                    if (n <= kRanked) {
+                        cut_ranked(n, ~0u, want_mass - earlier_mass);
+                    } else {
+                        uint64_t mass;
+                        have = cut_bin(b, ~0u, want_mass - earlier_mass, false, mass);
+                    }
+                }
+            }
+            if (!have) {
+                for (uint32_t i = tid; i < segments; i += kThreads) sh.fixed_segment[i] = 0;
+                __syncthreads();
+#pragma unroll
+                for (uint32_t j = 0; j < 2; ++j)
+                    if (m[j] && key[j] <= cut) add64(&sh.fixed_segment[(static_cast<uint32_t>(key[j]) + r.skew) / (256 * kSteps)], m[j]);
+                __syncthreads();
+                have = true;
+            }
+        } else {
+            border();  // (after the cut by count, which does not know of it, unless it was known before)
+            const float floor = least;
+            if (!known) least = -inf;
+            uint64_t mass;
+            if (keep < entries && limit < kBins - 1) cut_bin(limit, keep - earlier, ~uint64_t(0), false, mass);
+            least = floor;
+        }
+        known = true;
+    }
+    if (!have && by_mass) {
+        // ---- the bins' masses.  Relative to their upper edges: within 1/16 of a unit, in fixed point.
+        double mine[2];
+        uint64_t m0, m1, mb, whole;
+        for (;;) {
+            for (uint32_t i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
+            __syncthreads();
+            float most = -inf;
+            bool odd = false;
+            over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    odd = odd || z[j] != z[j];
+                    most = fmaxf(most, z[j]);
+                }
+                uint64_t units[4];
+                float place[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    place[j] = truncf(fmaxf(place_of(z[j]), 0.f));
+                    const float edge = kAbove - place[j] * (1.f / kPerUnit);  // exact
+                    const double x = ref == inf ? 0.0 : exponent(z[j], ref) - static_cast<double>(edge);
+                    units[j] = rounded(exponential_near_0(fmin(x, 0.02)), scale * 0.5);
+                }
+                // the last bin's entries are some e^-112 of the largest: nothing
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in(z[j]) && place[j] < static_cast<float>(kBins - 1) && (cut == ~uint64_t(0) || place_key(z[j], at + j) <= cut))
+                        add64(&sh.mass[static_cast<uint32_t>(place[j])], units[j]);
+            });
+            top = largest(most, odd);
+            if (top != top || top == -inf) return nothing();
+            if (place_of(top) >= 0.f && (top < inf || ref == inf)) break;
+            ref = top;  // it was too low
+        }
+        if (!known) border();
+        known = true;
+        // the bins in units of the row's largest
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) {
+            // (a single one's place is all that +inf leaves)
+            const double edge = ref == inf ? (2 * tid + j == 0 ? 0.0 : -1e300) : static_cast<double>(kAbove) - (2 * tid + j) * (1.0 / kPerUnit) - exponent(top, ref);
+            mine[j] = ldexp(static_cast<double>(sh.mass[2 * tid + j]), 1) * exponential(edge);
+        }
+        m0 = static_cast<uint64_t>(mine[0]);
+        m1 = static_cast<uint64_t>(mine[1]);
+        mb = sum_before(m0 + m1, sh.wave64, whole);
+        uint64_t earlier;
+        const uint64_t want = target_of(whole);
+        const uint32_t b = mass_bin(mb, m0, m1, want, earlier);
+        if (b < kBins) {
+            const uint64_t first_cut = cut;
+            uint64_t mass;
+            have = cut_bin(b, ~0u, want - earlier, first_cut == ~uint64_t(0), mass);
+        }
+    }
+    float base = known ? top : ref;  // what masses are relative to from here on
+    auto kept_masses = [&](const float (&z)[4], int32_t at, double (&m)[4]) __attribute__((always_inline)) {
+        bool kept[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kept[j] = z[j] >= least && (cut == ~uint64_t(0) || place_key(z[j], static_cast<uint32_t>(at + j)) <= cut);
+        masses(z, kept, base, m);
+    };
+    __syncthreads();
+    if (have) {
+        for (uint32_t i = tid; i < segments; i += kThreads) sh.segment[i] = ldexp(static_cast<double>(sh.fixed_segment[i]), -unit);
+    } else {
+        for (;;) {
+            float most = -inf;
+            bool odd = false;
+            double m = 0.0;
+            over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    odd = odd || z[j] != z[j];
+                    most = fmaxf(most, z[j]);
+                }
+                double e[4];
+                kept_masses(z, at, e);
+                m += (e[0] + e[1]) + (e[2] + e[3]);
+                if (last) {
+                    m = wave_total(m);
+                    if (lane == 0) sh.segment[segment] = m;
+                    m = 0.0;
+                }
+            });
+            if (known) break;
+            top = largest(most, odd);
+            if (top != top || top == -inf) return nothing();
+            // (exponentials of what is 600 above the reference would not do)
+            if (base == inf || (top < inf && exponent(top, base) < 600.0)) break;
+            base = top;
+            known = true;
+        }
     }
     __syncthreads();
     // each thread has a run of neighbouring segments
@@ -452,8 +806,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         if (tid * run + i < segments) mine += sh.segment[tid * run + i];
     double total;
     double before = sum_before(mine, sh.wavef, total);
-    const float u = a.uniform[row];
-    const double target = (u >= 0.f ? static_cast<double>(u) : 0.0) * total;
+    const double target = share * total;
     // the first segment whose running sum exceeds the target, or the last that holds anything
     if (tid == 0) {
         sh.found32[0] = ~0u;
@@ -485,42 +838,52 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     }
     __syncthreads();
     if (wave != 0) return;
+    // the segment's steps one after the other, until one holds the target (else the last entry that can be drawn)
     before = sh.wavef[0];
-    float z[4] = {0.f, 0.f, 0.f, 0.f};
-    double m[4] = {0.0, 0.0, 0.0, 0.0};
-    int32_t at = 0;
-    if (s * 64 + lane < r.groups) {
-        at = r.load(s * 64 + lane, z);
+    int64_t token = -1;
+    float drawn = 0.f;
+    for (uint32_t step = 0; step < kSteps; ++step) {
+        const uint32_t g = (s * kSteps + step) * 64 + lane;
+        float z[4] = {0.f, 0.f, 0.f, 0.f};
+        double m[4] = {0.0, 0.0, 0.0, 0.0};
+        int32_t at = 0;
+        at = r.load(g, z);
+        kept_masses(z, at, m);
+        double sum = m[0] + m[1] + m[2] + m[3];
+        const double own = sum;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m[j] = kept_mass(z[j], at + j);
-    }
-    double sum = m[0] + m[1] + m[2] + m[3];
-    const double own = sum;
+        for (int by = 1; by < 64; by *= 2) {
+            const double t = shuffle_up(sum, by);
+            if (lane >= static_cast<uint32_t>(by)) sum += t;
+        }
+        const double next = before + __shfl(sum, 63, 64);
+        sum = before + (sum - own);
+        before = next;
+        int32_t hit = -1, end = -1;  // this lane's first entry past the target, and its last that can be drawn
+        float hz = 0.f, ez = 0.f;
 #pragma unroll
-    for (int by = 1; by < 64; by *= 2) {
-        const double t = shuffle_up(sum, by);
-        if (lane >= static_cast<uint32_t>(by)) sum += t;
-    }
-    sum = before + (sum - own);
-    int32_t hit = -1, end = -1;  // this lane's first entry past the target, and its last that can be drawn
-    float hz = 0.f, ez = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        sum += m[j];
-        if (m[j] > 0.0) {
-            end = at + j;
-            ez = z[j];
-            if (hit < 0 && sum > target) {
-                hit = at + j;
-                hz = z[j];
+        for (int j = 0; j < 4; ++j) {
+            sum += m[j];
+            if (m[j] > 0.0) {
+                end = at + j;
+                ez = z[j];
+                if (hit < 0 && sum > target) {
+                    hit = at + j;
+                    hz = z[j];
+                }
             }
         }
+        const uint64_t hits = __ballot(hit >= 0), ends = __ballot(end >= 0);
+        if (hits || ends) {
+            const int who = hits ? __ffsll(static_cast<unsigned long long>(hits)) - 1 : 63 - __clzll(static_cast<long long>(ends));
+            token = __shfl(hits ? hit : end, who, 64);
+            drawn = __shfl(hits ? hz : ez, who, 64);
+        }
+        if (hits) break;
     }
-    const uint64_t hits = __ballot(hit >= 0), ends = __ballot(end >= 0);
-    const uint32_t who = hits ? __ffsll(static_cast<unsigned long long>(hits)) - 1 : 63 - __clzll(static_cast<long long>(ends | 1));
-    if (lane == who) {
-        a.token[row] = hits ? hit : end;
-        if (a.logprob) a.logprob[row] = static_cast<float>(exponent(hits ? hz : ez) - log(total));
+    if (lane == 0) {
+        a.token[row] = token;
+        if (a.logprob) a.logprob[row] = static_cast<float>(exponent(drawn, base) - log(total));
     }
 }
 
@@ -530,10 +893,13 @@ cbk_status launch_sample(const cbk_sampling &p, const void *logits, int dtype, u
                          const float *uniform, int64_t *token, float *logprob, hipStream_t s) {
     const SampleArgs a{p, logits, ld, static_cast<uint32_t>(V), uniform, token, logprob};
     const dim3 grid(static_cast<uint32_t>(tokens)), block(kThreads);
-    if (dtype == CBK_F32)
-        hipLaunchKernelGGL(k_sample<float>, grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL(k_sample<uint16_t>, grid, block, 0, s, a);
+    if (dtype == CBK_F32) {
+        if (!allow_lds_once<float>(k_sample<float>, sizeof(Shared))) return CBK_E_HIP;
+        hipLaunchKernelGGL(k_sample<float>, grid, block, sizeof(Shared), s, a);
+    } else {
+        if (!allow_lds_once<uint16_t>(k_sample<uint16_t>, sizeof(Shared))) return CBK_E_HIP;
+        hipLaunchKernelGGL(k_sample<uint16_t>, grid, block, sizeof(Shared), s, a);
+    }
     return launched();
 }
 
