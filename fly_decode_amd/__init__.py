@@ -14,6 +14,7 @@ is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -905,15 +906,18 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 def _matrix(x, cols, name):
     """Checks a [tokens][cols] float32 or bfloat16 matrix with unit column stride; returns (pointer, dtype, row stride)."""
     import torch
-    dtypes = {torch.float32: 0, torch.bfloat16: 1}
-    if x.dtype not in dtypes or x.dim() != 2 or x.shape[1] != cols or (cols > 1 and x.shape[0] > 0 and x.stride(1) != 1):
-        raise ValueError(f"{name} must be a [tokens][{cols}] float32 or bfloat16 matrix with unit column stride")
-    rows, ld = x.shape[0], x.stride(0)
-    if rows <= 1:
+    dtype = 0 if x.dtype is torch.float32 else 1 if x.dtype is torch.bfloat16 else None
+    shape = x.shape
+    if dtype is None or len(shape) != 2 or shape[1] != cols:
+        raise ValueError(f"{name} must be a [tokens][{cols}] float32 or bfloat16 matrix")
+    ld, unit = x.stride()
+    if shape[0] <= 1:
         ld = cols
     elif ld < cols:
         raise ValueError(f"the rows of {name} overlap")
-    return x.data_ptr() or None, dtypes[x.dtype], ld
+    if unit != 1 and cols > 1 and shape[0] > 0:
+        raise ValueError(f"{name} must have unit column stride")
+    return x.data_ptr() or None, dtype, ld
 
 
 def _slots(x, shape, dtype, name):
@@ -922,11 +926,13 @@ def _slots(x, shape, dtype, name):
     return x.data_ptr() or None
 
 
+@functools.lru_cache(maxsize=256)
 def _router(experts, k, score, renormalise, scale, groups=1, top_groups=1, group_top=1):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
     if min(k, groups, top_groups, group_top) < 0:
         raise ValueError("k, groups, top_groups and group_top must not be negative")
+    # (the calls only read it)
     return ctypes.byref(_Router(experts, k, _SCORES[score], int(bool(renormalise)), scale, groups, top_groups, group_top))
 
 

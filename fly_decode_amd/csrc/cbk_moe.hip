@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "cbk_exp.h"
 #include "cbk_moe_device.h"
 
 namespace cbk {
@@ -36,6 +37,12 @@ __device__ __forceinline__ uint64_t ascending(double v) {
     return u >> 63 ? ~u : u | (uint64_t(1) << 63);
 }
 
+// 1 / (1 + e^-z), to some 1e-13 of itself
+__device__ __forceinline__ double logistic(double z) {
+    const double e = exponential(-fabs(z)), s = 1.0 / (1.0 + e);  // (of +-infinity: 1, and 0 or 1)
+    return z < 0.0 ? e * s : s;
+}
+
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint64_t dpp_max(uint64_t v) {
     const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
@@ -54,6 +61,10 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
     v = dpp_max<0x143, 0xC>(v);
     const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v)), 63);
     const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v >> 32)), 63);
+    return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+__device__ __forceinline__ uint64_t shuffle_xor(uint64_t v, int o) {
+    const uint32_t lo = __shfl_xor(static_cast<uint32_t>(v), o, 64), hi = __shfl_xor(static_cast<uint32_t>(v >> 32), o, 64);
     return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 __device__ __forceinline__ double wave_sum(double v) {
@@ -105,7 +116,7 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
         double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            s[j] = sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(z[j]))) : exp(static_cast<double>(z[j]) - base);
+            s[j] = sigmoid ? logistic(static_cast<double>(z[j])) : exponential(static_cast<double>(z[j]) - base);
             sum += s[j];
         }
         if (!sigmoid) {
@@ -140,14 +151,17 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
         for (int j = 0; j < NPL; ++j) mine[j * 64 + lane] = key[j];
         asm volatile("" ::: "memory");  // one wave's LDS accesses run in order
         uint64_t marks[NPL];
+        // the best two of a group by `share` neighbouring lanes, a power of two of them, with every share-th of its experts
+        // each; then joined (8 groups of 32: a quarter of a lane's steps through LDS)
+        uint32_t share = 1;
+        while (2 * share * a.r.groups <= 64) share *= 2;
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            const uint32_t g = j * 64 + lane;
+            const uint32_t g = (j * 64 + lane) / share, part = lane & (share - 1);
             uint64_t first = 0, second = 0;
             if (g < a.r.groups)
-                for (uint32_t i = 0; i < size; ++i) {
-                    const uint32_t at = i + lane;  // lanes start at different banks
-                    const uint64_t v = mine[g * size + at % size];
+                for (uint32_t i = part; i < size; i += share) {
+                    const uint64_t v = mine[g * size + i];
                     if (v > first) {
                         second = first;
                         first = v;
@@ -155,11 +169,18 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
                         second = v;
                     }
                 }
+            for (uint32_t o = 1; o < share; o *= 2) {
+                const uint64_t f = shuffle_xor(first, o), t = shuffle_xor(second, o);
+                const uint64_t low = first < f ? first : f;
+                first = first < f ? f : first;
+                second = low > second ? low : second;
+                second = second < t ? t : second;
+            }
             if constexpr (WIDE) {
                 auto value = [](uint64_t u) { return __builtin_bit_cast(double, u >> 63 ? u & ~(uint64_t(1) << 63) : ~u); };
                 if (a.r.group_top == 2 && second) first = ascending(value(first) + value(second));
             }
-            marks[j] = first;
+            marks[j] = part == 0 ? first : 0;
         }
         asm volatile("" ::: "memory");
         // keep the best groups: mark them in LDS
@@ -180,7 +201,7 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
                     found = true;
                     if (lane == static_cast<uint32_t>(__ffsll(static_cast<unsigned long long>(has)) - 1)) {
                         marks[j] = 0;
-                        mine[j * 64 + lane] = 1;
+                        mine[(j * 64 + lane) / share] = 1;
                     }
                 }
             }
@@ -220,11 +241,11 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
     const bool have = chosen >= 0;
     double w = 0.0;
     if (sigmoid) {
-        if (have) w = 1.0 / (1.0 + exp(-static_cast<double>(cz)));
+        if (have) w = logistic(static_cast<double>(cz));
     } else {
         // renormalised: relative to the largest of the chosen, so that something is left to divide by
         const float ref = a.r.renormalise ? wave_top(have ? cz : -__builtin_inff()) : top;
-        if (have) w = exp(static_cast<double>(cz) - static_cast<double>(ref)) / (a.r.renormalise ? 1.0 : denominator);
+        if (have) w = exponential(static_cast<double>(cz) - static_cast<double>(ref)) / (a.r.renormalise ? 1.0 : denominator);
     }
     if (a.r.renormalise) {
         const double sum = wave_sum(w);
