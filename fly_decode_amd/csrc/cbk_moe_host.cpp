@@ -76,8 +76,14 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
     const uint64_t most = std::max<uint64_t>(1, std::min<uint64_t>({kSlots / k, kSlotBytes / (per_slot * k), (uint64_t(1) << 29) / std::max(p.Kp, p.Op)}));
     p.Tc = std::min(tokens, most);
     const uint64_t slots = p.Tc * k, active = std::min<uint64_t>(ex.count, slots);
-    // tiles of 256 where the LDS holds their tables: two of gate and up, one of down
-    p.tile = ex.b <= 13 && ex.b_down <= 14 && slots / active > 48 ? 256 : slots / active > 24 ? 64 : slots / active > 8 ? 32 : 16;
+    // Slots of a token tile, by how many there are for an expert that has any.  32 experts of 2048 x 4096, 4 a token, us with
+    // tiles of 16, 64 and 256 (k_experts_few, k_experts, k_experts_many; the backward pass' gradients by k_experts where
+    // tiles are not of 256): 32 tokens forward 292, 403, 341, backward 478, 563, 590; 64 tokens 336, 409, 345 and 529, 572, 598;
+    // 96 tokens 418, 413, 349 and 676, 577, 597; 192 tokens 615, 439, 361 and 957, 608, 612; 256 tokens 791, 538, 385
+    // and 1221, 765, 645.  Tiles of 256 need the LDS to hold two tables of gate and up, or one of down, beside their blocks.
+    const uint64_t per = slots / active;
+    const bool large = ex.b <= 13 && ex.b_down <= 14;
+    p.tile = per <= 8 ? 16 : large && per > (backward ? 24 : 8) ? 256 : 64;
     p.max_tiles = static_cast<uint32_t>(active + slots / p.tile);
     p.one = !backward && tokens == 1 && p.tile == 16 && ex.b <= 13 && ex.b_down <= 14;  // where k_experts_few does both products
     if (p.one) p.max_tiles = k;
@@ -86,7 +92,7 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
         const uint64_t units = p.max_tiles * (up_to(columns, 128) / 128);
         return static_cast<uint32_t>(std::max<uint64_t>(1, std::min<uint64_t>({512 / units, slices / 8, 8})));
     };
-    p.split_down = p.tile >= 64 ? split(ex.out, p.Fp / 64) : 1;
+    p.split_down = p.tile != 16 ? split(ex.out, p.Fp / 64) : 1;
     p.split_dt = split(ex.rows, p.Op / 64);
     p.split_x = split(ex.cols, 2 * p.Fp / 64);
     uint64_t at = 0;

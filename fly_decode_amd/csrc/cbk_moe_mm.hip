@@ -1,12 +1,12 @@
 // The experts' products of cbk_moe.h for gfx950 (CDNA4): codebook-compressed weights of every expert that tokens were
 // routed to, decoded on the way to the matrix cores.
 //
-// Units of work.  A workgroup takes one token tile (up to BM slots of one expert, as k_sort cut them) and one tile of
-// 128 columns of the result: forward (NN false) 128 rows of a tensor, or 64 rows of gate and of up side by side (PAIR),
-// so that a lane has a hidden column's two sums; gradient (NN true) 128 columns of a tensor, over gate's rows and then
-// up's (PAIR).  It holds the sums of the whole reduction, so the operator's work is its epilogue and nothing is joined;
-// where units are few (splits) a reduction's shares lie side by side in S and are added by who reads them.  How many
-// tiles there are is known on the device alone: the grid covers the most there can be, and workgroups past them end.
+// Units of work.  A workgroup takes one token tile (slots of one expert, as k_sort cut them) and one tile of columns of
+// the result: forward (NN false) rows of a tensor, or half as many of gate and of up side by side (PAIR), so that a lane
+// has a hidden column's two sums; gradient (NN true) columns of a tensor, over gate's rows and then up's (PAIR).  It holds
+// the sums of the whole reduction, so the operator's work is its epilogue and nothing is joined; where units are few
+// (splits) a reduction's shares lie side by side in S and are added by who reads them.  How many tiles there are is known
+// on the device alone: the grid covers the most there can be, and workgroups past them end.
 //
 // Widths.  The index width is read from the tensor's record and the same code takes all of 0 to 16: experts, and the two
 // tensors of a pair, may differ in it, which tensors of some 2^12 distinct patterns do by chance.  Fields are taken in
@@ -14,9 +14,7 @@
 // (Static widths would save some of the shifts, and would need a launch for each width among the experts.)  Tables lie in
 // LDS; those of 2^15 and 2^16 entries do not fit beside the slices and are read through the caches (GT).
 //
-// Slices.  The reduction is walked in slices of 64: while one is multiplied, the tokens' part of the next is copied
-// straight into LDS and the workgroup's 512 lanes decode 16 fields of it each into the same layout as k_fused's
-// (cbk_nn_fused.h).  Two buffers, one barrier a slice.
+// Three kernels, by the number of tokens that an expert has (ex_plan): k_experts_few, k_experts, k_experts_many.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,11 +26,7 @@
 namespace cbk {
 namespace {
 
-constexpr uint32_t kColumns = 128;  // of a tile
 enum Epi { kSum, kHidden, kHiddenBwd };
-
-constexpr int waves_n(int BM) { return BM >= 192 ? 2 : 4; }
-constexpr uint32_t slice_bytes(int BM) { return (BM + kColumns) * 128; }
 
 // A tensor's table of 2^b entries (b <= 14), those from U on corrupt, into LDS by 512 threads: up to 4 chunks of 8 entries
 // each, and the chunk that U falls into by 8 threads, all asked for by load() before store() waits for any.
@@ -199,11 +193,19 @@ __device__ __forceinline__ void finish(const ExArgs &p, const f32x4_t (&acc)[FN]
     }
 }
 
-template <int BM, bool NN, bool PAIR, int EPI, bool GT>
+// ---------------------------------------------------------------------------- up to 64 tokens
+// Tiles of 64 tokens x 128 columns: the gradients' products of few tokens, and every product where a table of 2^14 entries or more
+// rules the others out.  The reduction is walked in slices of 64: while one is multiplied, the tokens' part of the next is
+// copied straight into LDS and the workgroup's 512 lanes decode 16 fields of it each into the same layout as k_fused's
+// (cbk_nn_fused.h).  Two buffers, one barrier a slice.
+constexpr uint32_t kTokens = 64, kColumns = 128;
+constexpr uint32_t kSliceBytes = (kTokens + kColumns) * 128;
+
+template <bool NN, bool PAIR, int EPI, bool GT>
 __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
-    constexpr int WN = waves_n(BM), WM = 8 / WN;
-    constexpr int FM = BM / WM / 16, FN = kColumns / WN / 16;
-    constexpr uint32_t XBYTES = BM * 128, SLICE = slice_bytes(BM);
+    constexpr int WN = 4, WM = 2;
+    constexpr int FM = kTokens / WM / 16, FN = kColumns / WN / 16;
+    constexpr uint32_t XBYTES = kTokens * 128, SLICE = kSliceBytes;
     constexpr uint32_t NL = 4;  // loads of a lane's words
     static_assert(EPI == kSum || (PAIR && !NN), "gate and up side by side");
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -226,14 +228,8 @@ __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
     const uint32_t swz = NN ? 2 * (trow & 3) + 8 * ((trow >> 3) & 1) : trow & 7;
     const uint32_t wrow = trow * (NN ? 256u : 128u);
     // copies of the tokens' part: 8 rows by a wave, rows past the tile's end repeat the last one
-    constexpr int IX = BM / 64;
-    uint32_t vx[IX];
-#pragma unroll
-    for (int i = 0; i < IX; ++i) {
-        const uint32_t r = min(static_cast<uint32_t>((i * 8 + wave) * 8 + (lane >> 3)), tile.count - 1);
-        const uint32_t row = p.by_slot ? r : p.token_of[tile.start + r];
-        vx[i] = row * p.lda * 2 + ((lane & 7) ^ (lane >> 3)) * 16;
-    }
+    const uint32_t xr = min(static_cast<uint32_t>(wave * 8 + (lane >> 3)), tile.count - 1);
+    const uint32_t vx = (p.by_slot ? xr : p.token_of[tile.start + xr]) * p.lda * 2 + ((lane & 7) ^ (lane >> 3)) * 16;
     const auto rx = wave_rsrc(p.A + (p.by_slot ? static_cast<uint64_t>(tile.start) * p.lda : 0), 0x7FFFFFF0u);
     // fragment reads; fragment i of this wave is tokens 16 (i WM + wm) and on
     const uint32_t fa = (wm * 16 + li) * 128 + ((lg ^ (li & 7)) * 16);
@@ -265,7 +261,6 @@ __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
     // The reduction over slices [s0, s1) of tensor `which` (forward pairs: the wave's own of the two).
     auto pass = [&](uint32_t which, uint32_t s0, uint32_t s1, auto active) __attribute__((always_inline)) {
         constexpr int NF = decltype(active)::value;          // fragments of tokens that there are
-        constexpr int NC = BM == 256 ? NF : 1;               // copies of 64 tokens
         const ExTensor &T = which ? T1 : T0;
         const uint32_t b = __builtin_amdgcn_readfirstlane(T.b), m2 = ((1u << b) - 1) << 1;
         const unsigned char *table = smem + which * p.table;
@@ -328,8 +323,7 @@ __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
         };
         auto copy = [&](uint32_t s, uint32_t to) {
             const uint32_t from = (s + (NN && PAIR ? which * p.slices : 0u)) * 128;
-#pragma unroll
-            for (int i = 0; i < NC; ++i) copy_to_lds(rx, ring + to + (i * 8 + wave) * 1024, vx[i], from);
+            copy_to_lds(rx, ring + to + wave * 1024, vx, from);
         };
         struct Frags {
             bf16x8_t a[NF], b[FN];
@@ -422,15 +416,8 @@ __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
         }
     };
     const uint32_t frags = (tile.count + 16 * WM - 1) / (16 * WM);
-    if constexpr (FM == 2) {
-        if (frags == 1) passes(std::integral_constant<int, 1>{});
-        else passes(std::integral_constant<int, 2>{});
-    } else {
-        if (frags == 1) passes(std::integral_constant<int, 1>{});
-        else if (frags == 2) passes(std::integral_constant<int, 2>{});
-        else if (frags == 3) passes(std::integral_constant<int, 3>{});
-        else passes(std::integral_constant<int, 4>{});
-    }
+    if (frags == 1) passes(std::integral_constant<int, 1>{});
+    else passes(std::integral_constant<int, 2>{});
 
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -440,18 +427,19 @@ __global__ __launch_bounds__(512) void k_experts(const ExArgs p) {
 }
 
 // -------------------------------------------------------------------------------- few tokens
-// Forward products of up to 16 NF tokens: bound by reading the weights.  A workgroup goes through a run of units, 32 rows
+// Forward products of up to 16 tokens: bound by reading the weights.  A workgroup goes through a run of units, 32 rows
 // each (16 of gate and 16 of up, or 32 of one tensor) for one token tile; its 8 waves take every eighth step of 128
 // terms, and their sums meet in LDS in a fixed order, one barrier a unit.  A wave works by itself otherwise.  An item is
 // a step of 16 rows: their 128 fields, up to 15 chunks of 16 bytes a row, are copied as they lie straight into one of
 // three places of the wave's own, two items ahead (loads of a lane's own fields, which scatter a wave over 16 rows,
-// took 302 us for 48 tokens of 4 out of 32 experts' gate and up, TODO so).  From there lane l takes 16 fields of row
+// took 302 us for 48 tokens of 4 out of 32 experts' gate and up of 2048 x 4096 each, 197 so: 4.4 TB/s of weights, and
+// the copies alone, without decoding, take 180).  From there lane l takes 16 fields of row
 // l % 16 at term 16 (l / 16) of each 64, decodes them into the layout of the matrix instruction's operand, and the
 // tokens' fragments are read from the caches with the terms in the same order.
-constexpr uint32_t kFewChunks = 15, kFewStage = 16 * kFewChunks * 16, kFewRing = 3, kFewStep = 128;
-// LDS of the sums: of two units for 16 tokens, so that one barrier a unit is enough, of one for more
-constexpr uint32_t few_sums(int NF) { return (NF == 1 ? 2 : 1) * 8 * NF * 2 * 1024; }
-constexpr uint32_t few_lds(uint32_t tables, int NF) { return tables + 8 * kFewRing * kFewStage + few_sums(NF); }
+constexpr uint32_t kFewTokens = 16, kFewChunks = 15, kFewStage = 16 * kFewChunks * 16, kFewRing = 3, kFewStep = 128;
+// LDS of the waves' sums: of two units, so that one barrier a unit is enough
+constexpr uint32_t kFewSums = 8 * 2 * 1024;
+constexpr uint32_t few_lds(uint32_t tables) { return tables + 8 * kFewRing * kFewStage + 2 * kFewSums; }
 
 // The three dwords at each of four LDS addresses.  Written out because the compiler holds reads back until every copy
 // into LDS has landed, also those of items still to come; the block waits for its own reads.
@@ -477,10 +465,10 @@ __device__ __forceinline__ void read_windows(u32x3 (&w)[4], const uint32_t (&at)
     w[3] = (u32x3){a3.x, a3.y, b3};
 }
 
-template <int NF, bool PAIR, int EPI, bool ONE>
+template <bool PAIR, int EPI, bool ONE>
 __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
     static_assert(PAIR == (EPI != kSum), "gate and up, or one tensor");
-    constexpr uint32_t NX = 4 * NF;  // loads of a step's tokens
+    constexpr uint32_t NX = 4;  // loads of a step's tokens
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t li = lane & 15, lg = lane >> 4;
@@ -557,32 +545,26 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
     };
 
     // ---- tokens
-    uint32_t vx[NF], rows_at = ~0u;  // rows of A, and the tile that they are of
+    uint32_t vx = 0, rows_at = ~0u;  // this lane's row of A, and the tile that it is of
     auto rows_of = [&](uint32_t t) __attribute__((always_inline)) {
         if (rows_at == t) return;
         rows_at = t;
         const ExTile tile = tile_at(t);
-#pragma unroll
-        for (int i = 0; i < NF; ++i) {
-            const uint32_t r = min(i * 16 + li, tile.count - 1);
-            vx[i] = p.by_slot ? tile.start + r : ONE ? 0 : p.token_of[tile.start + r];
-        }
+        const uint32_t r = min(li, tile.count - 1);
+        vx = p.by_slot ? tile.start + r : ONE ? 0 : p.token_of[tile.start + r];
     };
     struct Step {
-        bf16x8_t f[NF][4];
+        bf16x8_t f[4];
     };
     // Fragments for step s (the second 64 terms of a last step that has none: the first again, not used).
     auto tokens = [&](Step &x, uint32_t s) __attribute__((always_inline)) {
+        const unsigned char *row = reinterpret_cast<const unsigned char *>(p.A + static_cast<uint64_t>(vx) * p.lda) + lg * 32 + s * (2 * kFewStep);
+        const bool whole = 2 * s + 1 < p.slices;
 #pragma unroll
-        for (int i = 0; i < NF; ++i) {
-            const unsigned char *row = reinterpret_cast<const unsigned char *>(p.A + static_cast<uint64_t>(vx[i]) * p.lda) + lg * 32 + s * (2 * kFewStep);
-            const bool whole = 2 * s + 1 < p.slices;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) x.f[i][h] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(row + (h < 2 ? 16 * h : whole ? 128 + 16 * (h - 2) : 0)));
-        }
+        for (int h = 0; h < 4; ++h) x.f[h] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4 *>(row + (h < 2 ? 16 * h : whole ? 128 + 16 * (h - 2) : 0)));
     };
 
-    f32x4_t acc[NF][2];
+    f32x4_t acc[2];
     // ---- an item: `place` its stage
     struct Window {
         uint32_t at[4], shift[4], b, m2;
@@ -632,8 +614,7 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
             for (int h = 0; h < 2; ++h) {
                 const uint32_t *y = v + 8 * h;
                 const bf16x8_t f = __builtin_bit_cast(bf16x8_t, (u32x4){y[0] | (y[1] << 16), y[2] | (y[3] << 16), y[4] | (y[5] << 16), y[6] | (y[7] << 16)});
-#pragma unroll
-                for (int i = 0; i < NF; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, x.f[i][2 * hh + h], acc[i][j], 0, 0, 0);
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, x.f[2 * hh + h], acc[j], 0, 0, 0);
             }
         }
     };
@@ -663,9 +644,7 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
             lds_barrier();
         }
 #pragma unroll
-        for (int i = 0; i < NF; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < 2; ++j) acc[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
         for (uint32_t s = wave; s < S; s += 8) {
             // The next step's tokens (after the last of all the last again), and the copies two items on; then this item's
             // have landed when no more is in flight than was asked for after them: two copies, and a step's tokens.
@@ -692,36 +671,33 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
             asm volatile("" ::: "memory");
             x = next;
         }
-        float *to = sums + (NF == 1 ? (u & 1) * (8 * 2 * 256) : 0) + lane * 4;
+        float *to = sums + (u & 1) * (kFewSums / 4) + lane * 4;
 #pragma unroll
-        for (int i = 0; i < NF; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) *reinterpret_cast<f32x4_t *>(to + ((wave * NF + i) * 2 + j) * 256) = acc[i][j];
+        for (int j = 0; j < 2; ++j) *reinterpret_cast<f32x4_t *>(to + (wave * 2 + j) * 256) = acc[j];
         lds_barrier();
         // the waves add a unit's sums in turn
         if (wave == static_cast<int>(u & 7) && used) {
+            f32x4_t t[2] = {};
+            for (int w = 0; w < 8; ++w)
 #pragma unroll
-            for (int i = 0; i < NF; ++i) {
-                f32x4_t t[2] = {};
-                for (int w = 0; w < 8; ++w)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) t[j] += *reinterpret_cast<const f32x4_t *>(to + ((w * NF + i) * 2 + j) * 256);
-                finish<EPI, 2, ONE>(p, t, tile, i * 16 + li, 0, u % p.col_tiles, 0, 1, lg);
-            }
+                for (int j = 0; j < 2; ++j) t[j] += *reinterpret_cast<const f32x4_t *>(to + (w * 2 + j) * 256);
+            finish<EPI, 2, ONE>(p, t, tile, li, 0, u % p.col_tiles, 0, 1, lg);
         }
-        if (NF > 1) lds_barrier();
     }
     __builtin_amdgcn_s_waitcnt(0x0070);  // no copy is left in flight
 }
 
 // ------------------------------------------------------------------------------- many tokens
-// A tile of 256 tokens x 256 columns; the reduction in blocks of 64, two buffers of them in LDS.  What bounds it is the
-// LDS: the gathers of a block's 16384 fields take about what its multiplications do.  So nothing else that can stay out
-// of the LDS goes through it: the tokens' fragments come straight from the caches into registers, 32 terms ahead, and
-// only the decoded weights (a wave multiplies 64 tokens with 128 of them) pass through LDS.  While a block is multiplied
-// in halves of 32 terms, a wave decodes the next one in halves of its rows: a row's 64 fields at once by four lanes, whose
-// cache lines are then done with (in slices of 32 terms of all rows, they fell out of the L1 between two slices: 1254 us
-// instead of TODO for 2048 tokens of 4 out of 32 experts of 2048 x 4096).  One barrier a block, before its last multiplications.
+// A tile of 256 tokens x 256 columns; the reduction in blocks of 64, two buffers of tokens and of decoded weights in LDS
+// (a wave multiplies 64 tokens with 128 columns).  While a block is multiplied in halves of 32 terms, the next one's tokens
+// are copied, a wave decodes the next one's weights in halves of its rows (a row's 64 fields at once by four lanes, whose
+// cache lines are then done with), and the words of the one after are asked for.  One barrier a block, before its last
+// multiplications.  Memory answers in order, so words asked for right before their use wait for the tokens too: with words
+// a half ahead in slices of 32 terms of all rows (which fell out of the L1 between two slices), and the tokens' fragments
+// read from the caches by each wave, gate and up of 2048 tokens of 4 out of 32 experts of 2048 x 4096 and back took 1254 us,
+// so 690.  What bounds it is the LDS, busy for 62 % of the time: a gather's 64 addresses meet in banks, ~5 clocks over
+// the 2 it needs.  Without gathers gate and up would take 433 us instead of 447, without scattered words 406, with neither
+// 337; the matrix instructions keep their units busy for 36 %.
 constexpr uint32_t kManyColumns = 256, kManyTokens = 256, kManyBlock = 64;
 constexpr uint32_t kManyBytes = kManyColumns * kManyBlock * 2;  // of a block of weights
 constexpr uint32_t kManyTokenBytes = kManyTokens * kManyBlock * 2;
@@ -982,17 +958,17 @@ __global__ __launch_bounds__(512) void k_experts_many(const ExArgs p) {
 
 uint32_t tiles_of(uint64_t n, uint64_t m) { return static_cast<uint32_t>((n + m - 1) / m); }
 
-template <int, bool, bool, int, bool>
+template <bool, bool, bool, int, bool>
 struct ExTag;
 
-template <int BM, bool NN, bool PAIR, int EPI, bool GT>
+template <bool NN, bool PAIR, int EPI, bool GT>
 cbk_status run(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s) {
     a.col_tiles = tiles_of(columns, EPI == kSum ? kColumns : kColumns / 2);
-    const uint32_t lds = (GT ? 0 : (PAIR ? 2 : 1) * a.table) + 2 * slice_bytes(BM);
-    if (!allow_lds_once<ExTag<BM, NN, PAIR, EPI, GT>>(k_experts<BM, NN, PAIR, EPI, GT>, kLdsLimit)) return CBK_E_HIP;
+    const uint32_t lds = (GT ? 0 : (PAIR ? 2 : 1) * a.table) + 2 * kSliceBytes;
+    if (!allow_lds_once<ExTag<false, NN, PAIR, EPI, GT>>(k_experts<NN, PAIR, EPI, GT>, kLdsLimit)) return CBK_E_HIP;
     const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles * a.splits;
     if (units > (uint64_t(1) << 30)) return CBK_E_UNSUPPORTED;
-    hipLaunchKernelGGL((k_experts<BM, NN, PAIR, EPI, GT>), dim3(static_cast<uint32_t>((units + 7) / 8 * 8)), dim3(512), lds, s, a);
+    hipLaunchKernelGGL((k_experts<NN, PAIR, EPI, GT>), dim3(static_cast<uint32_t>((units + 7) / 8 * 8)), dim3(512), lds, s, a);
     return launched();
 }
 
@@ -1003,26 +979,26 @@ cbk_status run_many(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s
     a.col_tiles = tiles_of(columns, EPI == kSum ? kManyColumns : kManyColumns / 2);
     const uint32_t lds = many_lds(a.table, !NN && PAIR);
     if (lds > kLdsLimit) return CBK_E_UNSUPPORTED;  // the plan rules it out
-    if (!allow_lds_once<ExTag<256, NN, PAIR, EPI, false>>(k_experts_many<NN, PAIR, EPI>, kLdsLimit)) return CBK_E_HIP;
+    if (!allow_lds_once<ExTag<true, NN, PAIR, EPI, false>>(k_experts_many<NN, PAIR, EPI>, kLdsLimit)) return CBK_E_HIP;
     const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles * a.splits;
     if (units > (uint64_t(1) << 30)) return CBK_E_UNSUPPORTED;
     hipLaunchKernelGGL((k_experts_many<NN, PAIR, EPI>), dim3(static_cast<uint32_t>(units)), dim3(512), lds, s, a);
     return launched();
 }
 
-template <int, bool, int, bool>
+template <bool, int, bool>
 struct FewTag;
 
-template <int NF, bool PAIR, int EPI, bool ONE>
+template <bool PAIR, int EPI, bool ONE>
 cbk_status run_few(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s) {
     a.splits = 1;
     a.col_tiles = tiles_of(columns, PAIR ? 16 : 32);
     const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles;
     if (units > (uint64_t(1) << 30)) return CBK_E_UNSUPPORTED;
-    if (!allow_lds_once<FewTag<NF, PAIR, EPI, ONE>>(k_experts_few<NF, PAIR, EPI, ONE>, kLdsLimit)) return CBK_E_HIP;
+    if (!allow_lds_once<FewTag<PAIR, EPI, ONE>>(k_experts_few<PAIR, EPI, ONE>, kLdsLimit)) return CBK_E_HIP;
     // a workgroup has a CU's LDS
     const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(units, cu_count()));
-    hipLaunchKernelGGL((k_experts_few<NF, PAIR, EPI, ONE>), dim3(grid), dim3(512), few_lds((PAIR ? 2 : 1) * a.table, NF), s, a);
+    hipLaunchKernelGGL((k_experts_few<PAIR, EPI, ONE>), dim3(grid), dim3(512), few_lds((PAIR ? 2 : 1) * a.table), s, a);
     return launched();
 }
 
@@ -1032,11 +1008,12 @@ cbk_status product(ExArgs &a, const ExPlan &pl, uint32_t columns, uint32_t b, hi
     a.table = std::max(16u, 2u << b);
     if (pl.tile == kManyTokens) return run_many<NN, PAIR, EPI>(a, pl, columns, s);
     if constexpr (!NN) {
-        if (pl.one) return run_few<1, PAIR, EPI, true>(a, pl, columns, s);
-        if (pl.tile <= 32 && b <= 14 && few_lds((PAIR ? 2 : 1) * a.table, pl.tile / 16) <= kLdsLimit)
-            return pl.tile == 16 ? run_few<1, PAIR, EPI, false>(a, pl, columns, s) : run_few<2, PAIR, EPI, false>(a, pl, columns, s);
+        if constexpr (EPI != kHiddenBwd) {
+            if (pl.one) return run_few<PAIR, EPI, true>(a, pl, columns, s);
+        }
+        if (pl.tile == kFewTokens && b <= 14 && few_lds((PAIR ? 2 : 1) * a.table) <= kLdsLimit) return run_few<PAIR, EPI, false>(a, pl, columns, s);
     }
-    return b > 14 ? run<64, NN, PAIR, EPI, true>(a, pl, columns, s) : run<64, NN, PAIR, EPI, false>(a, pl, columns, s);
+    return b > 14 ? run<NN, PAIR, EPI, true>(a, pl, columns, s) : run<NN, PAIR, EPI, false>(a, pl, columns, s);
 }
 
 }  // namespace

@@ -78,10 +78,9 @@ __device__ __forceinline__ float activation(int act, float z, float *D) {
 // Copies 16 bytes a lane from the resource (at the lane's voff plus the wave's soff) straight into
 // LDS, lane l to dst + 16 l; dst is the same in every lane.  The wave's vmcnt counts it.  The
 // host's pass over this file does not know this chip's wide copies, so it gets an empty body.
-template <int POLICY = 0>
 __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, unsigned char *dst, uint32_t voff, uint32_t soff) {
 #ifdef __HIP_DEVICE_COMPILE__
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (CBK_LDS void *)(dst), 16, static_cast<int>(voff), static_cast<int>(soff), 0, POLICY);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (CBK_LDS void *)(dst), 16, static_cast<int>(voff), static_cast<int>(soff), 0, 0);
 #endif
 }
 
