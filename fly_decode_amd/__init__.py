@@ -930,10 +930,10 @@ def _slots(x, shape, dtype, name):
 def _router(experts, k, score, renormalise, scale, groups=1, top_groups=1, group_top=1):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
-    if min(k, groups, top_groups, group_top) < 0:
-        raise ValueError("k, groups, top_groups and group_top must not be negative")
+    if not all(0 <= n < 1 << 32 for n in (experts, k, groups, top_groups, group_top)):  # (ctypes would wrap them)
+        raise ValueError("k, groups, top_groups and group_top must not be negative, nor so large")
     # (the calls only read it)
-    return ctypes.byref(_Router(experts, k, _SCORES[score], int(bool(renormalise)), scale, groups, top_groups, group_top))
+    return ctypes.byref(_Router(experts, k, _SCORES[score], int(renormalise), scale, groups, top_groups, group_top))
 
 
 def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int | None = None,
@@ -951,7 +951,7 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     zp, dtype, ld = _matrix(logits, E, "logits")
     bp = None if bias is None else _vector(bias, E, torch.float32, "bias")
     _arguments(logits, bias)
-    r = _router(E, k, score, renormalise, scale, groups, groups if top_groups is None else top_groups, group_top)
+    r = _router(E, k, score, bool(renormalise), float(scale), groups, groups if top_groups is None else top_groups, group_top)
     call = _Call(logits, stream)
     experts, weights = call.empty((T, k), torch.int32), call.empty((T, k), torch.float32)
     call.run("cbk_route", None, None, r, zp, dtype, ld, T, bp, experts.data_ptr() or None, weights.data_ptr() or None)
@@ -971,7 +971,7 @@ def route_bwd(logits, experts, dweights, score: str = "softmax", renormalise: bo
     ep = _slots(experts, (T, k), torch.int32, "experts")
     dp = _slots(dweights, (T, k), torch.float32, "dweights")
     _arguments(logits, experts, dweights, out)
-    r = _router(E, k, score, renormalise, scale)
+    r = _router(E, k, score, bool(renormalise), float(scale))
     call = _Call(logits, stream)
     if out is None:
         out = call.empty((T, E), logits.dtype)
@@ -1005,6 +1005,8 @@ class Experts:
         nbytes = int(lib.cbk_experts_bytes(n))
         self._struct = _Experts()
         with torch.cuda.device(self.device):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("Experts cannot be made inside a graph's capture")
             self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
             torch.cuda.current_stream(self.device).synchronize()  # the block may have been another stream work's
             _check(lib.cbk_experts_init(*arrays, n, self.buffer.data_ptr(), nbytes, ctypes.byref(self._struct)), "cbk_experts_init")
@@ -1085,6 +1087,8 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stre
         if isinstance(value, torch.Tensor):
             setattr(p, name + "s", _vector(value, T, kind, name))
             vectors.append(value)
+        elif name == "top_k" and not -(1 << 31) <= value < 1 << 31:
+            raise ValueError("top_k must fit 32 bits")
         else:
             setattr(p, name, value)
     _arguments(logits, uniform, *vectors)

@@ -531,15 +531,28 @@ __global__ __launch_bounds__(256) void k_dweights(const float *__restrict__ part
 }
 
 template <typename T, int NPL>
-void route_as(const RouteArgs &a, bool wide, bool backward, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>((a.tokens + 3) / 4)), block(256);
+void route_as(RouteArgs a, bool wide, bool backward, hipStream_t s) {
     const uint32_t lds = a.r.groups > 1 ? 4 * NPL * 64 * 8 : 0;
-    if (backward)
-        hipLaunchKernelGGL((k_route_bwd<T, NPL>), grid, block, 0, s, a);
-    else if (wide)
-        hipLaunchKernelGGL((k_route<T, NPL, true>), grid, block, lds, s, a);
-    else
-        hipLaunchKernelGGL((k_route<T, NPL, false>), grid, block, lds, s, a);
+    // a launch has fewer than 2^32 threads, 64 a token
+    constexpr uint64_t kMost = uint64_t(1) << 25;
+    for (uint64_t left = a.tokens; left > 0; left -= a.tokens) {
+        a.tokens = std::min(left, kMost);
+        const dim3 grid(static_cast<uint32_t>((a.tokens + 3) / 4)), block(256);
+        if (backward)
+            hipLaunchKernelGGL((k_route_bwd<T, NPL>), grid, block, 0, s, a);
+        else if (wide)
+            hipLaunchKernelGGL((k_route<T, NPL, true>), grid, block, lds, s, a);
+        else
+            hipLaunchKernelGGL((k_route<T, NPL, false>), grid, block, lds, s, a);
+        a.logits = static_cast<const T *>(a.logits) + a.tokens * a.ld;
+        a.experts += a.tokens * a.r.k;
+        if (backward) {
+            a.dweights += a.tokens * a.r.k;
+            a.dlogits = static_cast<T *>(a.dlogits) + a.tokens * a.ldd;
+        } else {
+            a.weights += a.tokens * a.r.k;
+        }
+    }
 }
 template <typename T>
 void route_of(const RouteArgs &a, bool wide, bool backward, hipStream_t s) {

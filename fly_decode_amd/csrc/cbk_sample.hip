@@ -868,16 +868,30 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
 
 cbk_status launch_sample(const cbk_sampling &p, const void *logits, int dtype, uint64_t ld, uint64_t V, uint64_t tokens,
                          const float *uniform, int64_t *token, float *logprob, hipStream_t s) {
-    const SampleArgs a{p, logits, ld, static_cast<uint32_t>(V), uniform, token, logprob};
-    const dim3 grid(static_cast<uint32_t>(tokens)), block(kThreads);
-    if (dtype == CBK_F32) {
-        if (!allow_lds_once<float>(k_sample<float>, sizeof(Shared))) return CBK_E_HIP;
-        hipLaunchKernelGGL(k_sample<float>, grid, block, sizeof(Shared), s, a);
-    } else {
-        if (!allow_lds_once<uint16_t>(k_sample<uint16_t>, sizeof(Shared))) return CBK_E_HIP;
-        hipLaunchKernelGGL(k_sample<uint16_t>, grid, block, sizeof(Shared), s, a);
+    SampleArgs a{p, logits, ld, static_cast<uint32_t>(V), uniform, token, logprob};
+    const bool f32 = dtype == CBK_F32;
+    if (!(f32 ? allow_lds_once<float>(k_sample<float>, sizeof(Shared)) : allow_lds_once<uint16_t>(k_sample<uint16_t>, sizeof(Shared))))
+        return CBK_E_HIP;
+    // a launch has fewer than 2^32 threads
+    constexpr uint64_t kMost = (uint64_t(1) << 31) / kThreads;
+    for (uint64_t left = tokens; left > 0;) {
+        const uint64_t n = std::min(left, kMost);
+        const dim3 grid(static_cast<uint32_t>(n)), block(kThreads);
+        if (f32) hipLaunchKernelGGL(k_sample<float>, grid, block, sizeof(Shared), s, a);
+        else hipLaunchKernelGGL(k_sample<uint16_t>, grid, block, sizeof(Shared), s, a);
+        const cbk_status st = launched();
+        if (st != CBK_OK) return st;
+        left -= n;
+        a.logits = static_cast<const unsigned char *>(a.logits) + n * ld * (f32 ? 4 : 2);
+        a.uniform += n;
+        a.token += n;
+        if (a.logprob) a.logprob += n;
+        if (a.p.temperatures) a.p.temperatures += n;
+        if (a.p.top_ps) a.p.top_ps += n;
+        if (a.p.min_ps) a.p.min_ps += n;
+        if (a.p.top_ks) a.p.top_ks += n;
     }
-    return launched();
+    return CBK_OK;
 }
 
 }  // namespace cbk

@@ -7,7 +7,8 @@
  * caller's stream and workspace, no state kept between calls, outputs must not alias inputs, corrupt
  * indices read as 0x7FC0, equal inputs give equal bits, tokens == 0 is a no-op, gradients of the
  * activations and never of the weights).  What a call does depends on device data alone, nothing is read
- * back to the host, and every call can be captured into a graph.
+ * back to the host, and every call can be captured into a graph.  A call of fewer tokens may need more
+ * workspace than one of more tokens (its reductions are shared out).
  *
  * Notation: T tokens, E experts, k of them for a token.  A token's k places are its slots.
  */
@@ -43,8 +44,8 @@ typedef struct {
  *   chosen, in falling order; equal ones go by the lower index, groups as well as experts;
  *   weights = scale * s, or scale * s / (sum of the chosen s).  The bias only steers the choice.
  * An expert whose logit or bias is -inf is never chosen and is left out of its group's mark; slots that
- * no expert is left for get -1 and a weight of 0 (all of them where a row is all -inf: padding).  A row that holds a NaN, or a +inf logit, or whose
- * biased scores hold a NaN, gets experts 0..k-1 and NaN weights.
+ * no expert is left for get -1 and a weight of 0 (all of them where a row is all -inf: padding).  A row that
+ * holds a NaN, or a +inf logit, or whose biased scores hold a NaN, gets experts 0..k-1 and NaN weights.
  * Scores are compared in 64 bits (without a bias and sums of two, the logits themselves are); weights
  * are rounded to fp32.
  *   logits   device, [tokens][ld] fp32 (4-byte aligned) or BF16 (2-byte aligned), ld >= E, < 2^32.

@@ -148,3 +148,62 @@ def test_sample_draws_as_often_as_its_probabilities(env):
     token, _ = cbk.sample(z.expand(n, 5).contiguous().cuda(), u.cuda(), temperature=0.7)
     share = torch.bincount(token.cpu(), minlength=5) / n
     assert bool(((share - torch.softmax(z / 0.7, 0)).abs() <= 1.5 / n).all())  # each interval's ends
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_sample_flat_rows(env, dtype):
+    """Large vocabularies of nearly equal logits, whose cut lies among tens of thousands of entries of one bin."""
+    torch, cbk = env
+    g = torch.Generator().manual_seed(8)
+    z = 1e-3 * torch.randn(3, 60000, generator=g)
+    z[1] = torch.randint(0, 3, (60000,), generator=g) * 2.0 ** -9
+    z[2, 30000:] += 4.0
+    z, u = z.to(getattr(torch, dtype)), torch.rand(3, generator=g)
+    for kw in ({"top_p": 0.5}, {"top_k": 30000}, {"top_k": 29999, "top_p": 0.7}, {"top_p": 0.999, "min_p": 0.9}, {"temperature": 1e-3, "top_p": 0.3}):
+        check(torch, cbk, z, u, str(kw), **kw)
+
+
+def test_sample_many_rows(env):
+    torch, cbk = env
+    z, u = draws(torch, 700, 300, torch.bfloat16, 9)
+    check(torch, cbk, z, u, temperature=0.9, top_k=20, top_p=0.8)
+    T = (1 << 22) + 7
+    z = torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda")
+    z[-1] = -math.inf
+    token, logprob = cbk.sample(z, torch.zeros(T, device="cuda"), top_k=torch.ones(T, dtype=torch.int32, device="cuda"))
+    assert bool((token[:-1] == 0).all()) and bool((logprob[:-1] == 0).all()) and int(token[-1]) == -1 and bool(logprob[-1].isnan())
+
+
+def test_sample_in_graphs_on_streams_and_without_logprob(env):
+    """Replays with new inputs against eager calls; calls on another stream beside pending work; the C call's NULL."""
+    import ctypes
+    torch, cbk = env
+    T, V = 40, 5000
+    Z, U = torch.empty(T, V, device="cuda"), torch.empty(T, device="cuda")
+    temperatures = torch.linspace(0, 2, T).cuda()
+
+    def run(stream=None):
+        return [*cbk.sample(Z, U, stream=stream), *cbk.sample(Z, U, temperature=temperatures, top_k=90, top_p=0.9, min_p=0.01, stream=stream)]
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = run()
+    big, s = torch.ones(1 << 28, device="cuda"), torch.cuda.Stream()
+    for i in range(4):
+        z, u = draws(torch, T, V, torch.float32, 10 + i)
+        Z.copy_(z)
+        U.copy_(u)
+        g.replay()
+        want = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), i
+        for _ in range(10):
+            big.mul_(1.0)
+        side, here = run(s), run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(side, want, here)), i
+    token = torch.full((T + 2,), 7, dtype=torch.int64, device="cuda")
+    p = cbk._Sampling(1.0, 1.0, 0.0, 0)
+    assert cbk.load_library().cbk_sample(ctypes.byref(p), Z.data_ptr(), 0, V, V, T, U.data_ptr(), token[1:].data_ptr(), None,
+                                         torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(token[1:-1], want[0]) and int(token[0]) == 7 and int(token[-1]) == 7
