@@ -342,10 +342,12 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     };
     auto bin_of = [&](float z) __attribute__((always_inline)) { return static_cast<uint32_t>(fmaxf(place_of(z), 0.f)); };
     auto in = [&](float z) __attribute__((always_inline)) { return z >= least && z != -inf; };
-    // masses relative to the row's largest, in units of 2^-unit, which leaves their sum below 2^63
+    // Fixed point.  The sums of a segment's 1024 masses, and of a list's 2048, relative to the row's largest: in units of
+    // 2^-50.  Sums over a bin, which all of the row may lie in: of masses relative to the bin's edge, in units of 2^-unit,
+    // which leaves them below 2^63.
     const int unit = min(50, 62 - (32 - __clz(V)));
-    const double scale = ldexp(1.0, unit);
-    auto fixed = [&](float z) __attribute__((always_inline)) { return rounded(mass_of(z, top), scale); };
+    const double scale = ldexp(1.0, unit), fine = 1125899906842624.0;
+    auto fixed = [&](float z, double by) __attribute__((always_inline)) { return rounded(mass_of(z, top), by); };
     auto key_logit = [&](uint64_t key) __attribute__((always_inline)) { return from_ascending(~static_cast<uint32_t>(key >> 32)); };
     auto add64 = [&](uint64_t *to, uint64_t v) __attribute__((always_inline)) {
         atomicAdd(reinterpret_cast<unsigned long long *>(to), static_cast<unsigned long long>(v));
@@ -354,13 +356,13 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     uint64_t cut = ~uint64_t(0);  // the last key that is kept
 
     // Cuts among the n <= kRanked keys in sh.ranked: the `some` first of them, or those before which less than `most` of
-    // mass stands; at least one.  The last one's key in `cut`; returns the mass of what is kept.  All threads.
-    auto cut_ranked = [&](uint32_t n, uint32_t some, uint64_t most) __attribute__((always_inline)) -> uint64_t {
-        if (tid < 2) sh.found64[tid] = 0;
+    // mass in units of 1 / by stands; at least one.  The last one's key in `cut`.  All threads.
+    auto cut_ranked = [&](uint32_t n, uint32_t some, uint64_t most, double by) __attribute__((always_inline)) {
+        if (tid == 0) sh.found64[0] = 0;
         uint64_t own = 0, m = 0;
         if (tid < n) {
             own = sh.ranked[tid];
-            m = by_mass ? fixed(key_logit(own)) : 0;
+            m = by_mass ? fixed(key_logit(own), by) : 0;
         }
         __syncthreads();
         if (tid < n) sh.mass[tid] = m;
@@ -373,20 +375,16 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
                 rank += less;
                 before += less ? sh.mass[i] : 0;
             }
-            if (rank == 0 || (rank < some && before < most)) {
+            if (rank == 0 || (rank < some && before < most))
                 atomicMax(reinterpret_cast<unsigned long long *>(&sh.found64[0]), static_cast<unsigned long long>(own));
-                atomicMax(reinterpret_cast<unsigned long long *>(&sh.found64[1]), static_cast<unsigned long long>(before + m));
-            }
         }
         __syncthreads();
         cut = min(cut, sh.found64[0]);
-        const uint64_t mass = sh.found64[1];
         __syncthreads();
-        return mass;
     };
     // The part of bin b that the cut falls into, of 2048, by the counts and masses of its parts in sh.count and sh.mass;
-    // takes what stands before it off `some` and `most`, and adds it to `mass`.
-    auto pick_part = [&](uint32_t &some, uint64_t &most, uint64_t &mass) __attribute__((always_inline)) {
+    // takes what stands before it off `some` and `most`.
+    auto pick_part = [&](uint32_t &some, uint64_t &most) __attribute__((always_inline)) {
         const uint32_t c0 = sh.count[2 * tid], c1 = sh.count[2 * tid + 1];
         const uint64_t m0 = sh.mass[2 * tid], m1 = sh.mass[2 * tid + 1];
         uint32_t count_all;
@@ -408,7 +406,6 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         __syncthreads();
         some -= min(some, sh.found32[1]);
         most -= min(most, sh.found64[0]);
-        mass += sh.found64[0];
         __syncthreads();
         return x;
     };
@@ -423,10 +420,10 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         if (tid == 0) sh.found32[2] = 0;
         __syncthreads();
     };
-    auto into_part = [&](float z, uint32_t b) __attribute__((always_inline)) {
+    auto into_part = [&](float z, uint32_t b, double by) __attribute__((always_inline)) {
         const uint32_t x = part_of(z, b);
         atomicAdd(&sh.count[x], 1u);
-        if (by_mass) add64(&sh.mass[x], fixed(z));
+        if (by_mass) add64(&sh.mass[x], fixed(z, by));
     };
     auto rank_if = [&](bool yes, uint64_t key) __attribute__((always_inline)) {
         if (yes) {
@@ -434,10 +431,19 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
             if (i < kRanked) sh.ranked[i] = key;
         }
     };
-    // The same among the entries of bin b; `segments`: adds up what is kept by segments too, with the entries of the bins
+    // The upper edge of bin b above the row's largest logit, in units of the temperature (a single bin is all that +inf leaves).
+    auto edge_of = [&](uint32_t b) __attribute__((always_inline)) {
+        return ref == inf ? (b == 0 ? 0.0 : -1e300) : static_cast<double>(kAbove) - b * (1.0 / kPerUnit) - exponent(top, ref);
+    };
+    // The same among the entries of bin b, `most` relative to the row's largest; `segments`: adds up what is kept by segments too, with the entries of the bins
     // before it; false where it did not.  Up to kList entries are divided up in LDS, more by passes over the row; where even
     // a part of the bin holds more than kRanked (equal logits), the cut's key is found by its bits.
-    auto cut_bin = [&](uint32_t b, uint32_t some, uint64_t most, bool segments, uint64_t &mass) __attribute__((always_inline)) {
+    auto cut_bin = [&](uint32_t b, uint32_t some, double most_mass, bool segments) __attribute__((always_inline)) {
+        // a power of two by which all of the bin's masses are small enough
+        // (the first bin has no edge that all are below)
+        const int lift = b == 0 ? 0 : static_cast<int>(fmin(fmax(floor(edge_of(b) * -1.4426950408889634), 0.0), 900.0));
+        const double by = ldexp(scale, lift);
+        uint64_t most = most_mass < inf ? max(uint64_t(1), static_cast<uint64_t>(ceil(fmin(most_mass * by, 9e18)))) : ~uint64_t(0);
         __syncthreads();
         if (tid == 0) sh.found32[2] = 0;
         __syncthreads();
@@ -460,13 +466,12 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
             }
             if (segments && last) {
                 m = wave_total(m);
-                if (lane == 0) sh.fixed_segment[segment] = static_cast<uint64_t>(ldexp(m, unit));
+                if (lane == 0) sh.fixed_segment[segment] = static_cast<uint64_t>(m * fine);
                 m = 0.0;
             }
         });
         __syncthreads();
         const uint32_t n = sh.found32[2];
-        mass = 0;
         __syncthreads();
         no_parts();
         uint64_t key[2];
@@ -475,16 +480,16 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         if (n <= kList) {
 #pragma unroll
             for (uint32_t j = 0; j < 2; ++j)
-                if (key[j] != ~uint64_t(0)) into_part(key_logit(key[j]), b);
+                if (key[j] != ~uint64_t(0)) into_part(key_logit(key[j]), b, by);
         } else {
             over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (in(z[j]) && bin_of(z[j]) == b) into_part(z[j], b);
+                    if (in(z[j]) && bin_of(z[j]) == b) into_part(z[j], b, by);
             });
         }
         __syncthreads();
-        const uint32_t x = pick_part(some, most, mass);
+        const uint32_t x = pick_part(some, most);
         if (n <= kList) {
 #pragma unroll
             for (uint32_t j = 0; j < 2; ++j) rank_if(key[j] != ~uint64_t(0) && part_of(key_logit(key[j]), b) == x, key[j]);
@@ -497,19 +502,19 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         __syncthreads();
         const uint32_t ranked = sh.found32[2];
         if (ranked <= kRanked) {
-            mass += cut_ranked(ranked, some, most);
+            cut_ranked(ranked, some, most, by);
             if (segments && n <= kList) {
 #pragma unroll
                 for (uint32_t j = 0; j < 2; ++j)
                     if (key[j] <= cut && key[j] != ~uint64_t(0))
-                        add64(&sh.fixed_segment[(static_cast<uint32_t>(key[j]) + r.skew) / (256 * kSteps)], fixed(key_logit(key[j])));
+                        add64(&sh.fixed_segment[(static_cast<uint32_t>(key[j]) + r.skew) / (256 * kSteps)], fixed(key_logit(key[j]), fine));
                 __syncthreads();
                 return true;
             }
             return false;
         }
         // The largest key before which there is room for one more in the part, bit by bit: 64 passes.
-        uint64_t found = 0, before = 0;
+        uint64_t found = 0;
         for (int bit = 63; bit >= 0; --bit) {
             const uint64_t probe = found | (uint64_t(1) << bit);
             uint32_t c = 0;
@@ -519,52 +524,34 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
                 for (int j = 0; j < 4; ++j)
                     if (in(z[j]) && bin_of(z[j]) == b && part_of(z[j], b) == x && place_key(z[j], at + j) < probe) {
                         ++c;
-                        if (by_mass) own += fixed(z[j]);
+                        if (by_mass) own += fixed(z[j], by);
                     }
             });
             uint32_t count_all;
             uint64_t mass_all;
             sum_before(c, sh.wave32, count_all);
             sum_before(own, sh.wave64, mass_all);
-            if (count_all == 0 || (count_all < some && mass_all < most)) {
-                found = probe;
-                before = mass_all;
-            }
+            if (count_all == 0 || (count_all < some && mass_all < most)) found = probe;
         }
-        // the entry at that key, if there is one, is the last
-        uint64_t own = 0, at_key;
-        over_row(r, [&](int32_t at, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (by_mass && in(z[j]) && place_key(z[j], at + j) == found) own = fixed(z[j]);
-        });
-        sum_before(own, sh.wave64, at_key);
         cut = min(cut, found);
-        mass += before + at_key;
         return false;
     };
     // Of the histogram's masses (before bin 2 tid: `mb`, its own and the next one's m0 and m1): the bin that the target
     // falls into, and what stands before it; kBins where rounding leaves nothing past it.
-    auto mass_bin = [&](uint64_t mb, uint64_t m0, uint64_t m1, uint64_t want, uint64_t &earlier) __attribute__((always_inline)) {
+    auto mass_bin = [&](double mb, double m0, double m1, double want, double &earlier) __attribute__((always_inline)) {
         __syncthreads();
         if (tid == 0) sh.found32[1] = kBins;
         __syncthreads();
-        if (mb < want && mb + m0 >= want) {
-            sh.found32[1] = 2 * tid;
-            sh.found64[0] = mb;
-        }
-        if (mb + m0 < want && mb + m0 + m1 >= want) {
-            sh.found32[1] = 2 * tid + 1;
-            sh.found64[0] = mb + m0;
-        }
+        // (sums of a double's precision: the one in front may seem to reach the target as well)
+        const uint32_t mine = m0 > 0.0 && mb + m0 >= want ? 2 * tid : m1 > 0.0 && mb + m0 + m1 >= want ? 2 * tid + 1 : kBins;
+        if (mine < kBins) atomicMin(&sh.found32[1], mine);
         __syncthreads();
         const uint32_t b = sh.found32[1];
-        earlier = sh.found64[0];
+        if (b < kBins && tid == b / 2) sh.wavef[0] = b & 1 ? mb + m0 : mb;
+        __syncthreads();
+        earlier = sh.wavef[0];
         __syncthreads();
         return b;
-    };
-    auto target_of = [&](uint64_t whole) __attribute__((always_inline)) {
-        return max(uint64_t(1), static_cast<uint64_t>(ceil(part * static_cast<double>(whole))));
     };
 
     const uint32_t segments = (r.groups + 64 * kSteps - 1) / (64 * kSteps);
@@ -623,14 +610,14 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
                     }
             });
             __syncthreads();
-            if (keep < entries) cut_ranked(upto - earlier, keep - earlier, ~uint64_t(0));
+            if (keep < entries) cut_ranked(upto - earlier, keep - earlier, ~uint64_t(0), fine);
             border();
             uint64_t key[2], m[2];
 #pragma unroll
             for (uint32_t j = 0; j < 2; ++j) {
                 key[j] = 2 * tid + j < upto ? sh.list[2 * tid + j] : ~uint64_t(0);
                 m[j] = 0;
-                if (key[j] <= cut && key[j] != ~uint64_t(0) && key_logit(key[j]) >= least) m[j] = fixed(key_logit(key[j]));
+                if (key[j] <= cut && key[j] != ~uint64_t(0) && key_logit(key[j]) >= least) m[j] = fixed(key_logit(key[j]), fine);
             }
             if (by_mass) {
                 for (uint32_t i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
@@ -640,9 +627,10 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
                 for (uint32_t j = 0; j < 2; ++j)
                     if (m[j]) add64(&sh.mass[bin_of(key_logit(key[j]))], m[j]);
                 __syncthreads();
-                const uint64_t m0 = sh.mass[2 * tid], m1 = sh.mass[2 * tid + 1];
-                uint64_t whole, earlier_mass;
-                const uint64_t mb = sum_before(m0 + m1, sh.wave64, whole), want_mass = target_of(whole);
+                // (a double holds 2^53 of these units)
+                const double m0 = static_cast<double>(sh.mass[2 * tid]), m1 = static_cast<double>(sh.mass[2 * tid + 1]);
+                double whole, earlier_mass;
+                const double mb = sum_before(m0 + m1, sh.wavef, whole), want_mass = part * whole;
                 const uint32_t b = mass_bin(mb, m0, m1, want_mass, earlier_mass);
                 if (b < kBins) {
 #pragma unroll
@@ -654,10 +642,9 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
                     __syncthreads();
                     const uint32_t n = sh.found32[0];
                     if (n <= kRanked) {
-                        cut_ranked(n, ~0u, want_mass - earlier_mass);
+                        cut_ranked(n, ~0u, max(uint64_t(1), static_cast<uint64_t>(ceil(want_mass - earlier_mass))), fine);
                     } else {
-                        uint64_t mass;
-                        have = cut_bin(b, ~0u, want_mass - earlier_mass, false, mass);
+                        have = cut_bin(b, ~0u, (want_mass - earlier_mass) / fine, false);
                     }
                 }
             }
@@ -674,8 +661,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
             border();  // (after the cut by count, which does not know of it, unless it was known before)
             const float floor = least;
             if (!known) least = -inf;
-            uint64_t mass;
-            if (keep < entries && limit < kBins - 1) cut_bin(limit, keep - earlier, ~uint64_t(0), false, mass);
+            if (keep < entries && limit < kBins - 1) cut_bin(limit, keep - earlier, static_cast<double>(inf), false);
             least = floor;
         }
         known = true;
@@ -683,7 +669,6 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     if (!have && by_mass) {
         // ---- the bins' masses.  Relative to their upper edges: within 1/16 of a unit, in fixed point.
         double mine[2];
-        uint64_t m0, m1, mb, whole;
         for (;;) {
             for (uint32_t i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
             __syncthreads();
@@ -717,24 +702,13 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         }
         if (!known) border();
         known = true;
-        // the bins in units of the row's largest
+        // relative to the row's largest
 #pragma unroll
-        for (uint32_t j = 0; j < 2; ++j) {
-            // (a single one's place is all that +inf leaves)
-            const double edge = ref == inf ? (2 * tid + j == 0 ? 0.0 : -1e300) : static_cast<double>(kAbove) - (2 * tid + j) * (1.0 / kPerUnit) - exponent(top, ref);
-            mine[j] = ldexp(static_cast<double>(sh.mass[2 * tid + j]), 1) * exponential(edge);
-        }
-        m0 = static_cast<uint64_t>(mine[0]);
-        m1 = static_cast<uint64_t>(mine[1]);
-        mb = sum_before(m0 + m1, sh.wave64, whole);
-        uint64_t earlier;
-        const uint64_t want = target_of(whole);
-        const uint32_t b = mass_bin(mb, m0, m1, want, earlier);
-        if (b < kBins) {
-            const uint64_t first_cut = cut;
-            uint64_t mass;
-            have = cut_bin(b, ~0u, want - earlier, first_cut == ~uint64_t(0), mass);
-        }
+        for (uint32_t j = 0; j < 2; ++j) mine[j] = static_cast<double>(sh.mass[2 * tid + j]) * (2.0 / scale) * exponential(edge_of(2 * tid + j));
+        double whole, earlier;
+        const double before = sum_before(mine[0] + mine[1], sh.wavef, whole), want = part * whole;
+        const uint32_t b = mass_bin(before, mine[0], mine[1], want, earlier);
+        if (b < kBins) have = cut_bin(b, ~0u, want - earlier, cut == ~uint64_t(0));
     }
     float base = known ? top : ref;  // what masses are relative to from here on
     auto kept_masses = [&](const float (&z)[4], int32_t at, double (&m)[4]) __attribute__((always_inline)) {
@@ -745,7 +719,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     };
     __syncthreads();
     if (have) {
-        for (uint32_t i = tid; i < segments; i += kThreads) sh.segment[i] = ldexp(static_cast<double>(sh.fixed_segment[i]), -unit);
+        for (uint32_t i = tid; i < segments; i += kThreads) sh.segment[i] = static_cast<double>(sh.fixed_segment[i]) * (1.0 / fine);
     } else {
         for (;;) {
             float most = -inf;

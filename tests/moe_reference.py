@@ -143,6 +143,23 @@ def experts_bwd(act, wg, wu, wd, x, chosen, weights, dy):
     return (dx, ref.rounded(dx, ex + (k + 10) * U32 * mag)), (dw, edw + ref.TINY)
 
 
+class Sum:
+    """A running sum whose roundings are kept beside it (2 ** -52 of a large first term, added up a million times, would
+    be 0.1 % of terms some 10 ** -13 of it)."""
+
+    def __init__(self):
+        self.high = self.low = 0.0
+
+    def add(self, v):
+        s = self.high + v
+        b = s - self.high
+        self.low += (self.high - (s - b)) + (v - b)
+        self.high = s
+
+    def less(self, limit):
+        return (self.high - limit) + self.low
+
+
 def sample(z, uniform, temperature, top_k=0, top_p=1.0, min_p=0.0):
     """(token, logprob) of one row, as the header words it, with numbers."""
     z = [float(v) for v in z]
@@ -165,20 +182,20 @@ def sample(z, uniform, temperature, top_k=0, top_p=1.0, min_p=0.0):
         order = [i for i in order if x(i) >= border]
     if top_p < 1:
         want = max(top_p, 0.0) * math.fsum(p[i] for i in order)
-        kept, before = [], 0.0
+        kept, before = [], Sum()
         for i in order:
-            if kept and before >= want:
+            if kept and before.less(want) >= 0:
                 break
             kept.append(i)
-            before += p[i]
+            before.add(p[i])
         order = kept
     total = math.fsum(p[i] for i in order)
     u = uniform if uniform >= 0 else 0.0
-    drawn, run = None, 0.0
+    drawn, run = None, Sum()
     for i in sorted(order):
         if p[i] > 0:
-            run += p[i]
+            run.add(p[i])
             drawn = i
-            if run > u * total:
+            if run.less(u * total) > 0:
                 break
     return drawn, x(drawn) - math.log(total)

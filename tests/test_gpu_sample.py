@@ -207,3 +207,16 @@ def test_sample_in_graphs_on_streams_and_without_logprob(env):
     assert cbk.load_library().cbk_sample(ctypes.byref(p), Z.data_ptr(), 0, V, V, T, U.data_ptr(), token[1:].data_ptr(), None,
                                          torch.cuda.current_stream().cuda_stream) == 0
     assert torch.equal(token[1:-1], want[0]) and int(token[0]) == 7 and int(token[-1]) == 7
+
+
+@pytest.mark.parametrize("spread", [0.0, 0.6])
+def test_sample_a_cut_far_below_the_largest(env, spread):
+    """One large logit and a million some e^-30 of it, whose sum 1 - top_p cuts into: what is kept of them shows in the
+    logarithm of the large one's probability."""
+    torch, cbk = env
+    V = 1 << 20
+    g = torch.Generator().manual_seed(11)
+    z = -30.0 + spread * torch.rand(2, V, generator=g)
+    z[:, V - 1] = 0.0
+    u = torch.tensor([0.5, 2.0 ** -26])
+    check(torch, cbk, z, u, top_p=1 - 2.0 ** -24)
