@@ -94,9 +94,6 @@ cbk_status launch_xent_bwd(const cbk_tensor &head, const uint16_t *X, uint64_t l
                            const float *lse, const float *dloss, uint64_t T, int64_t ignore, uint16_t *dX,
                            uint64_t lddx, void *ws, hipStream_t s);
 
-// X [T][K] into P [T][Kp] with zeros past K (cbk_nn.hip).
-cbk_status launch_pad_rows(const uint16_t *X, uint64_t ld, uint64_t T, uint32_t K, uint32_t Kp, uint16_t *P, hipStream_t s);
-
 // Routing (cbk_moe.hip) and drawing (cbk_sample.hip).
 cbk_status launch_route(const cbk_router &r, const void *logits, int dtype, uint64_t ld, uint64_t tokens, const float *bias,
                         int32_t *experts, float *weights, hipStream_t s);

@@ -345,18 +345,46 @@ __global__ __launch_bounds__(256) void k_route_bwd(const RouteArgs a) {
 // One workgroup sorts the slots by expert, stably, and cuts each expert's run into token tiles of equal size, listed by
 // falling quarters of a whole tile (what takes longest is begun first).
 // Each wave counts a run of slots, then places them: the rank of a slot among the wave's 64 of the same expert comes
-// from ballots over the expert's bits.
+// from ballots over the expert's bits.  Eight steps' slots are asked for at once: 8192 slots took 15.8 us with one at a
+// time, 13.4 so.  The other workgroups of the launch copy the rows of X and dY that the products cannot take as they are
+// (launches of their own cost a backward pass of 45 tokens 5 us).
+struct PadArgs {
+    const uint16_t *X;  // [T][ld] into P [T][Kp], columns past K zero; null: nothing to copy
+    uint64_t ld, T;
+    uint32_t K, Kp;
+    uint16_t *P;
+};
 struct SortArgs {
     const int32_t *experts;
     uint32_t slots, k, count, tile, unit;  // tokens of a tile at most, and what its size is rounded up to
     uint32_t *token_of, *slot_of;
     int32_t *place_of;
-    ExTile *tiles;
+    ExTile *tiles;  // null: nothing to sort
     uint32_t *ntiles;
+    PadArgs pad[2];
 };
 constexpr int kSortWaves = 16;
 
+__device__ __forceinline__ void pad_rows(const PadArgs &a) {
+    const uint32_t per = a.Kp / 4, stride = (gridDim.x - 1) * blockDim.x;
+    const uint64_t n = a.T * per;  // (a chunk: T per < 2^28)
+    for (uint32_t i = (blockIdx.x - 1) * blockDim.x + threadIdx.x; i < n; i += stride) {
+        const uint32_t t = i / per, k = (i - t * per) * 4;
+        const uint16_t *x = a.X + t * a.ld + k;
+        uint32_t v[4];
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) v[j] = k + j < a.K ? x[j] : 0u;
+        *reinterpret_cast<u32x2 *>(a.P + static_cast<uint64_t>(i) * 4) = (u32x2){v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
+    }
+}
+
 __global__ __launch_bounds__(64 * kSortWaves) void k_sort(const SortArgs a) {
+    if (blockIdx.x > 0) {
+        for (int i = 0; i < 2; ++i)
+            if (a.pad[i].X) pad_rows(a.pad[i]);
+        return;
+    }
+    if (!a.tiles) return;
     extern __shared__ uint32_t lds[];  // [waves][count]: how many, then where the wave's next one goes
     __shared__ uint32_t wave_sums[5][kSortWaves];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -366,11 +394,22 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_sort(const SortArgs a) {
     const uint32_t steps = (a.slots + 64 * kSortWaves - 1) / (64 * kSortWaves);  // of 64 slots, for a wave
     const uint32_t from = wave * steps * 64;
     uint32_t *mine = lds + wave * n;
-    for (uint32_t i = 0; i < steps; ++i) {
-        const uint32_t s = from + i * 64 + lane;
-        const uint32_t e = s < a.slots ? static_cast<uint32_t>(a.experts[s]) : ~0u;
-        if (e < n) atomicAdd(&mine[e], 1u);
+    constexpr uint32_t N = 8;
+    uint32_t e[N];
+    auto ask = [&](uint32_t i) __attribute__((always_inline)) {
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j) {
+            const uint32_t s = from + (i + j) * 64 + lane;
+            e[j] = i + j < steps && s < a.slots ? static_cast<uint32_t>(a.experts[s]) : ~0u;
+        }
+    };
+    for (uint32_t i = 0; i < steps; i += N) {
+        ask(i);
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j)
+            if (e[j] < n) atomicAdd(&mine[e[j]], 1u);
     }
+    if (steps > N) ask(0);  // (else they are there)
     __syncthreads();
     // expert `tid`: its slots, and its tiles
     uint32_t m = 0;
@@ -430,26 +469,30 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_sort(const SortArgs a) {
     __syncthreads();
     uint32_t bits = 0;
     while ((1u << bits) < n) ++bits;
-    for (uint32_t i = 0; i < steps; ++i) {
-        const uint32_t s = from + i * 64 + lane;
-        const uint32_t e = s < a.slots ? static_cast<uint32_t>(a.experts[s]) : ~0u;
-        const bool in = e < n;
-        uint64_t same = __ballot(in);
-        for (uint32_t b = 0; b < bits; ++b) {
-            const uint64_t has = __ballot((e >> b) & 1);
-            same &= (e >> b) & 1 ? has : ~has;
+    for (uint32_t i = 0; i < steps; i += N) {
+        if (i > 0) ask(i);
+#pragma unroll
+        for (uint32_t j = 0; j < N; ++j) {
+            if (i + j >= steps) break;
+            const uint32_t s = from + (i + j) * 64 + lane;
+            const bool in = e[j] < n;
+            uint64_t same = __ballot(in);
+            for (uint32_t b = 0; b < bits; ++b) {
+                const uint64_t has = __ballot((e[j] >> b) & 1);
+                same &= (e[j] >> b) & 1 ? has : ~has;
+            }
+            const uint32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+            uint32_t at = 0;
+            if (in) at = mine[e[j]] + rank;
+            asm volatile("" ::: "memory");  // one wave's LDS accesses run in order
+            if (in && (same >> lane) == 1) mine[e[j]] = at + 1;  // the last of them
+            asm volatile("" ::: "memory");
+            if (in) {
+                a.slot_of[at] = s;
+                a.token_of[at] = s / a.k;
+            }
+            if (s < a.slots) a.place_of[s] = in ? static_cast<int32_t>(at) : -1;
         }
-        const uint32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-        uint32_t at = 0;
-        if (in) at = mine[e] + rank;
-        asm volatile("" ::: "memory");  // one wave's LDS accesses run in order
-        if (in && (same >> lane) == 1) mine[e] = at + 1;  // the last of them
-        asm volatile("" ::: "memory");
-        if (in) {
-            a.slot_of[at] = s;
-            a.token_of[at] = s / a.k;
-        }
-        if (s < a.slots) a.place_of[s] = in ? static_cast<int32_t>(at) : -1;
     }
 }
 
@@ -465,14 +508,33 @@ struct GatherArgs {
     uint16_t *Y;
     uint64_t ldy;
     uint32_t vec;
+    // a backward pass: the slots' dweights as the sums of `parts` each, by workgroups past the `blocks` of a token
+    uint32_t blocks, parts;
+    const float *dw;
+    float *dweights;
 };
+
+// dweights of a token's slots from their parts over the hidden columns, a wave a slot.
+__device__ __forceinline__ void sum_dweights(const GatherArgs &a, uint64_t t) {
+    const uint32_t lane = threadIdx.x & 63;
+    for (uint32_t j = threadIdx.x >> 6; j < a.k; j += 4) {
+        const int32_t at = a.place_of[t * a.k + j];
+        float v = 0.f;
+        if (at >= 0)
+            for (uint32_t i = lane; i < a.parts; i += 64) v += a.dw[static_cast<uint64_t>(at) * a.parts + i];
+        v = wave_sum(v);
+        if (lane == 0) a.dweights[t * a.k + j] = v;
+    }
+}
 
 // Y[t] = the sum of its slots' results, in the slots' order.  A thread has 4 columns of a token, and asks for eight
 // results at a time (one after the other, the four of one token took 6.2 us).
 __global__ __launch_bounds__(256) void k_gather(const GatherArgs a) {
     const uint32_t c = (blockIdx.x * 256 + threadIdx.x) * 4;
     const uint64_t t = blockIdx.y + static_cast<uint64_t>(blockIdx.z) * gridDim.y;
-    if (c >= a.width || t >= a.tokens) return;
+    if (t >= a.tokens) return;
+    if (blockIdx.x == a.blocks) return sum_dweights(a, t);
+    if (c >= a.width) return;
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
     auto place = [&](uint32_t j) {
         const uint64_t slot = t * a.k + j;
@@ -515,19 +577,6 @@ __global__ __launch_bounds__(256) void k_gather(const GatherArgs a) {
         for (uint32_t r = 0; r < 4; ++r)
             if (c + r < a.width) y[r] = to_bf16(v[r]);
     }
-}
-
-// dweights from their parts over the hidden columns, a wave a slot.
-__global__ __launch_bounds__(256) void k_dweights(const float *__restrict__ parts, uint32_t n, const int32_t *__restrict__ place_of,
-                                                  uint32_t slots, float *__restrict__ dweights) {
-    const uint32_t s = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (s >= slots) return;
-    const int32_t at = place_of[s];
-    float v = 0.f;
-    if (at >= 0)
-        for (uint32_t i = lane; i < n; i += 64) v += parts[static_cast<uint64_t>(at) * n + i];
-    v = wave_sum(v);
-    if (lane == 0) dweights[s] = v;
 }
 
 template <typename T, int NPL>
@@ -608,25 +657,27 @@ bool vec16(const void *p, uint64_t ld) { return (reinterpret_cast<uintptr_t>(p) 
 
 // What the products read of a matrix of tokens: itself where whole 64-wide slices of its rows can be copied 16
 // bytes at a time and the chunk's rows lie within 31 bits of bytes, else a padded copy in the workspace.
-cbk_status token_rows(const uint16_t *X, uint64_t ld, uint64_t T, uint64_t K, uint64_t Kp, uint16_t *P, const uint16_t *&A,
-                      uint32_t &lda, hipStream_t s) {
+const uint16_t *token_rows(const uint16_t *X, uint64_t ld, uint64_t T, uint64_t K, uint64_t Kp, uint16_t *P, PadArgs &pad, uint32_t &lda) {
     if (K == Kp && vec16(X, ld) && T * ld * 2 < 0x7F000000u) {
-        A = X;
         lda = static_cast<uint32_t>(ld);
-        return CBK_OK;
+        return X;
     }
-    A = P;
     lda = static_cast<uint32_t>(Kp);
-    return launch_pad_rows(X, ld, T, static_cast<uint32_t>(K), static_cast<uint32_t>(Kp), P, s);
+    pad = PadArgs{X, ld, T, static_cast<uint32_t>(K), lda, P};
+    return P;
 }
 
-cbk_status gather(const float *S, uint64_t split_stride, uint32_t splits, uint64_t ldS, const int32_t *place_of,
-                  const int32_t *experts, uint32_t count, uint32_t k,
-                  uint64_t T, uint16_t *Y, uint64_t ldy, uint64_t width, hipStream_t s) {
-    GatherArgs g{S, split_stride, splits, static_cast<uint32_t>(ldS), k, static_cast<uint32_t>(width), T, place_of, experts, count, Y, ldy,
-                 (reinterpret_cast<uintptr_t>(Y) & 7) == 0 && ldy % 4 == 0 ? 1u : 0u};
-    const uint32_t rows = static_cast<uint32_t>(std::min<uint64_t>(T, 32768));
-    hipLaunchKernelGGL(k_gather, dim3(static_cast<uint32_t>((width + 1023) / 1024), rows, static_cast<uint32_t>((T + rows - 1) / rows)), dim3(256), 0, s, g);
+cbk_status gather(GatherArgs g, const float *S, uint64_t split_stride, uint32_t splits, uint64_t ldS, uint64_t width, hipStream_t s) {
+    g.S = S;
+    g.split_stride = split_stride;
+    g.splits = splits;
+    g.lds = static_cast<uint32_t>(ldS);
+    g.width = static_cast<uint32_t>(width);
+    g.vec = (reinterpret_cast<uintptr_t>(g.Y) & 7) == 0 && g.ldy % 4 == 0 ? 1u : 0u;
+    g.blocks = static_cast<uint32_t>((width + 1023) / 1024);
+    const uint32_t rows = static_cast<uint32_t>(std::min<uint64_t>(g.tokens, 32768));
+    const dim3 grid(g.blocks + (g.dweights ? 1 : 0), rows, static_cast<uint32_t>((g.tokens + rows - 1) / rows));
+    hipLaunchKernelGGL(k_gather, grid, dim3(256), 0, s, g);
     return launched();
 }
 
@@ -652,11 +703,23 @@ cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, cons
         so.place_of = at<int32_t>(ws, pl.place_of);
         so.tiles = at<ExTile>(ws, pl.tiles);
         so.ntiles = at<uint32_t>(ws, pl.ntiles);
-        if (pl.one) so.place_of = nullptr;
-        if (!allow_lds_once<SortArgs>(k_sort, kLdsLimit / 2)) return CBK_E_HIP;  // 64 KB of counts, and a little
-        if (!pl.one) hipLaunchKernelGGL(k_sort, dim3(1), dim3(64 * kSortWaves), kSortWaves * ex.count * 4, s, so);
-        cbk_status st = launched();
-        if (st != CBK_OK) return st;
+        if (pl.one) {
+            so.place_of = nullptr;
+            so.tiles = nullptr;
+        }
+        uint32_t ldxa, ldya = 0;
+        const uint16_t *Xa = token_rows(X + c * ldx, ldx, n, ex.cols, pl.Kp, at<uint16_t>(ws, pl.xpack), so.pad[0], ldxa);
+        const uint16_t *Ya = dY ? token_rows(dY + c * lddy, lddy, n, ex.out, pl.Op, at<uint16_t>(ws, pl.ypack), so.pad[1], ldya) : nullptr;
+        uint64_t pads = 0;  // groups of four numbers
+        for (const PadArgs &pad : so.pad) pads = std::max(pads, pad.X ? pad.T * (pad.Kp / 4) : 0);
+        cbk_status st = CBK_OK;
+        if (so.tiles || pads > 0) {
+            if (!allow_lds_once<SortArgs>(k_sort, kLdsLimit / 2)) return CBK_E_HIP;  // 64 KB of counts, and a little
+            const uint32_t blocks = static_cast<uint32_t>(1 + std::min<uint64_t>((pads + 64 * kSortWaves - 1) / (64 * kSortWaves), 2048));
+            hipLaunchKernelGGL(k_sort, dim3(blocks), dim3(64 * kSortWaves), kSortWaves * ex.count * 4, s, so);
+            st = launched();
+            if (st != CBK_OK) return st;
+        }
 
         ExArgs a{};
         a.tiles = so.tiles;
@@ -671,10 +734,14 @@ cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, cons
         a.rows = static_cast<uint32_t>(ex.rows);
         a.Fp = static_cast<uint32_t>(pl.Fp);
         const ExTensor *table = static_cast<const ExTensor *>(ex.buffer);
-        const uint16_t *Xa;
-        uint32_t ldxa;
-        st = token_rows(X + c * ldx, ldx, n, ex.cols, pl.Kp, at<uint16_t>(ws, pl.xpack), Xa, ldxa, s);
-        if (st != CBK_OK) return st;
+        GatherArgs by_token{};
+        by_token.k = k;
+        by_token.tokens = n;
+        by_token.place_of = so.place_of;
+        by_token.experts = so.experts;
+        by_token.count = ex.count;
+        by_token.Y = out + c * ldo;
+        by_token.ldy = ldo;
         if (!dY) {
             // H, and its product with down
             ExArgs h = a;
@@ -694,14 +761,10 @@ cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, cons
             d.S = at<float>(ws, pl.s);
             st = ex_down(d, pl, ex, s);
             if (st != CBK_OK) return st;
-            st = gather(d.S, pl.s_stride, pl.split_down, pl.ldO, so.place_of, so.experts, ex.count, k, n, out + c * ldo, ldo, ex.out, s);
+            st = gather(by_token, d.S, pl.s_stride, pl.split_down, pl.ldO, ex.out, s);
             if (st != CBK_OK) return st;
             continue;
         }
-        const uint16_t *Ya;
-        uint32_t ldya;
-        st = token_rows(dY + c * lddy, lddy, n, ex.out, pl.Op, at<uint16_t>(ws, pl.ypack), Ya, ldya, s);
-        if (st != CBK_OK) return st;
         // D = dY . down, then dG and dU, then their product with gate and up
         ExArgs d = a;
         d.t[0] = table + 2 * ex.count;
@@ -729,13 +792,13 @@ cbk_status launch_experts(const cbk_experts &ex, const ExPlan &pl, int act, cons
         x.S = at<float>(ws, pl.s);
         st = ex_dx(x, pl, ex, s);
         if (st != CBK_OK) return st;
-        st = gather(x.S, pl.s_stride, pl.split_x, pl.ldK, so.place_of, so.experts, ex.count, k, n, out + c * ldo, ldo, ex.cols, s);
-        if (st != CBK_OK) return st;
         if (dweights) {
-            hipLaunchKernelGGL(k_dweights, dim3((so.slots + 3) / 4), dim3(256), 0, s, g.dw, pl.dw_parts, so.place_of, so.slots, dweights + c * k);
-            st = launched();
-            if (st != CBK_OK) return st;
+            by_token.parts = pl.dw_parts;
+            by_token.dw = g.dw;
+            by_token.dweights = dweights + c * k;
         }
+        st = gather(by_token, x.S, pl.s_stride, pl.split_x, pl.ldK, ex.cols, s);
+        if (st != CBK_OK) return st;
     }
     return CBK_OK;
 }

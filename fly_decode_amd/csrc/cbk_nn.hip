@@ -1206,11 +1206,6 @@ Weights weights_of(NnOp op, const cbk_tensor *a, const cbk_tensor *b, uint64_t T
 
 }  // namespace
 
-cbk_status launch_pad_rows(const uint16_t *X, uint64_t ld, uint64_t T, uint32_t K, uint32_t Kp, uint16_t *P, hipStream_t s) {
-    hipLaunchKernelGGL(k_pad_rows, dim3(grid_for(T * (Kp / 4), 256)), dim3(256), 0, s, X, ld, T, K, Kp, P);
-    return launched();
-}
-
 cbk_status launch_linear(const cbk_tensor &t, const uint16_t *X, uint64_t ldx, uint64_t T, uint16_t *Y, uint64_t ldy,
                          void *ws, hipStream_t s) {
     Weights w = weights_of(NnOp::linear, &t, nullptr, T, ws, s);
