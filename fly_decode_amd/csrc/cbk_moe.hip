@@ -240,11 +240,12 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
     }
     const bool have = chosen >= 0;
     double w = 0.0;
-    if (sigmoid) {
+    // renormalised: relative to the largest of the chosen, so that something is left to divide by (the sigmoid of what is
+    // below -40 is its exponential, to the last bit)
+    const float ref = a.r.renormalise ? wave_top(have ? cz : -__builtin_inff()) : top;
+    if (sigmoid && !(a.r.renormalise && ref < -40.f)) {
         if (have) w = logistic(static_cast<double>(cz));
     } else {
-        // renormalised: relative to the largest of the chosen, so that something is left to divide by
-        const float ref = a.r.renormalise ? wave_top(have ? cz : -__builtin_inff()) : top;
         if (have) w = exponential(static_cast<double>(cz) - static_cast<double>(ref)) / (a.r.renormalise ? 1.0 : denominator);
     }
     if (a.r.renormalise) {
@@ -295,8 +296,10 @@ __global__ __launch_bounds__(256) void k_route_bwd(const RouteArgs a) {
     if (sigmoid) {
         const float s = e >= 0 ? 1.f / (1.f + expf(-cz)) : 0.f, r = e >= 0 ? 1.f / (1.f + expf(cz)) : 0.f;
         if (a.r.renormalise) {
-            // w = s / sum, w (1 - s) (d - m): formed so that scores far below 1 lose nothing
-            const float best = wave_top(s), rel = best > 0.f ? s / best : 0.f;
+            // w = s / sum, w (1 - s) (d - m): formed so that scores far below 1 lose nothing (below -30 a sigmoid is an
+            // exponential in fp32, and the largest of the chosen divides out)
+            const float most = wave_top(cz), best = wave_top(s);
+            const float rel = most < -30.f ? (e >= 0 && most > -__builtin_inff() ? expf(cz - most) : 0.f) : best > 0.f ? s / best : 0.f;
             const float sum = wave_sum(rel), w = sum > 0.f ? rel / sum : 0.f;
             const float m = wave_sum(e >= 0 ? d * w : 0.f);
             part = e >= 0 ? w * r * (d - m) : 0.f;

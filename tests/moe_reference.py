@@ -44,9 +44,10 @@ def route(z, k, score="softmax", bias=None, groups=1, top_groups=None, group_top
         chosen = sorted(can, key=lambda e: (-rank(e), e))[:k]
         if not chosen:
             continue
-        if renormalise and score == "softmax":
-            ref_z = max(row[e] for e in chosen)
-            w = [math.exp(row[e] - ref_z) for e in chosen]
+        if renormalise:  # relative to the largest of the chosen
+            log_s = (lambda v: v) if score == "softmax" else (lambda v: min(v, 0.0) - math.log1p(math.exp(-abs(v))))
+            top_s = max(log_s(row[e]) for e in chosen)
+            w = [math.exp(log_s(row[e]) - top_s) for e in chosen]
         else:
             w = [s[e] for e in chosen]
         if renormalise and sum(w) > 0:

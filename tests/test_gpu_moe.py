@@ -167,6 +167,29 @@ def test_route_bwd_against_differences(env, score, renormalise):
             assert abs(slope - float(dz[i, j])) < 1e-6 + 2e-6, (i, j)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_route_scores_far_below_one(env, score, dtype):
+    """Logits whose sigmoids are nothing in fp32, and nothing in fp64: renormalised weights and their gradient are not."""
+    torch, cbk = env
+    g = torch.Generator().manual_seed(12)
+    low = torch.tensor([-20.0, -29.5, -30.5, -60.0, -87.0, -95.0, -120.0, -300.0])[:, None]
+    z = (low + 1.5 * torch.randn(8, 20, generator=g)).to(getattr(torch, dtype))
+    dw = torch.randn(8, 4, generator=g)
+    e, w = cbk.route(z.cuda(), 4, score=score)
+    we, ww = moe.route(z, 4, score)
+    assert torch.equal(e.cpu(), we) and bool(((w.cpu().double() - ww).abs() <= 2.0 ** -24 * 1.001 * ww).all())
+    want, bound = moe.route_bwd(z, we, dw, score)
+    dz = cbk.route_bwd(z.cuda(), e, dw.cuda(), score=score)
+    ref.assert_within(dz, want, ref.rounded(want, bound) if dtype == "bfloat16" else bound, "dlogits")
+    far = torch.tensor([[-800.0, -801.0, -900.0, -1e30], [-1e4, -1e4, -2e4, -1e4]])
+    e, w = cbk.route(far.cuda(), 3, score=score)
+    we, ww = moe.route(far, 3, score)
+    # (e^-100 is a subnormal number, of which fp32 has the multiples of 2^-149: rounding is off by up to half of one)
+    assert torch.equal(e.cpu(), we) and bool(((w.cpu().double() - ww).abs() <= 2.0 ** -24 * 1.001 * ww + 2.0 ** -150).all())
+    assert bool(cbk.route_bwd(far.cuda(), e, torch.rand(2, 3).cuda(), score=score).isfinite().all())
+
+
 def routing(torch, T, E, k, seed, unused=True):
     g = torch.Generator().manual_seed(seed)
     chosen = torch.rand(T, E, generator=g).topk(min(k, E), 1)[1]
