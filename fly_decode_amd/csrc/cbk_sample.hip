@@ -8,12 +8,17 @@
 //
 // A row of 10^5 logits is read from memory or the last cache each time, so passes over it are few.  No pass
 // looks for the maximum first: bins and exponentials are relative to the largest of the first 4096 logits.
-//   temperature alone: one pass, a sum of exponentials of each 256 entries;
+//   temperature alone: one pass, a sum of exponentials of each 1024 entries;
 //   top_k (up to some 1500): one that counts, and one that collects the entries up to the cut's bin; all
 //     other filters and the draw are then done on that list;
 //   top_p: one that adds up the bins, and one that collects the cut's bin and adds up what stands before it;
 //   min_p without top_k: one for the maximum before those.
-// The draw takes the sums of each 256 entries in index order, then the 256 that the target falls into.
+// The draw takes the sums of each 1024 entries in index order, then the 1024 that the target falls into.
+//
+// 192 rows of 128000 fp32 logits take 25 us greedy (3.9 TB/s: memory), 58 by temperature alone, 52 with top_k = 50, 124
+// with top_p = 0.9.  Past the first reading the vector units bound it: some 60 instructions an entry for the bins' masses.
+// One row of 32000 takes 23 us, 64 rows of 50257 BF16 logits by temperature 32: a row has one workgroup, which needs no
+// workspace and no second launch, and leaves CUs idle where rows are few.
 //
 // The border between two tokens can be anywhere, and a vocabulary has 10^5 of them, so probabilities are
 // formed in fp64: an fp32 sum's 1e-7 would name another token once in some hundred rows.  On this chip
