@@ -223,7 +223,7 @@ __device__ __forceinline__ void transpose_step(uint32_t (&d)[U64<B>::UD], const 
     asm volatile("" ::: "memory");
 }
 // ------------------------------------------------------------------------------ host side
-[[maybe_unused]] int cu_count() {
+int cu_count() {
     static std::atomic<int> cached[64];
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;

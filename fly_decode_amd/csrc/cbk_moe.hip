@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#pragma clang diagnostic ignored "-Wunused-function"  // cu_count of cbk_device.h
 #include "cbk_exp.h"
 #include "cbk_moe_device.h"
 

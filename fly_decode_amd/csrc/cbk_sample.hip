@@ -28,6 +28,7 @@
 
 #include <type_traits>
 
+#pragma clang diagnostic ignored "-Wunused-function"  // cu_count of cbk_device.h
 #include "cbk_device.h"
 #include "cbk_exp.h"
 
