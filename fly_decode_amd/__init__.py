@@ -25,7 +25,7 @@ __all__ = ["CBK_OK", "CbkError", "bits_for", "words_for", "compressed_bytes", "e
            "ec_decode_group", "ec_gemv_group", "cap_patterns",
            "GemvChain", "linear", "linear_dx", "ffn_gated", "ffn_gated_bwd", "xent", "xent_bwd",
            "linear_workspace_bytes", "ffn_workspace_bytes", "xent_workspace_bytes",
-           "route", "route_bwd", "Experts", "ffn_experts", "ffn_experts_bwd", "experts_workspace_bytes", "sample"]
+           "route", "route_bwd", "Experts", "ffn_experts", "ffn_experts_bwd", "experts_workspace_bytes", "sample", "sample_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # CBK_LIBRARY names another build of the same library (for side-by-side comparisons)
@@ -202,6 +202,8 @@ def load_library():
         rp, ep, i32, u32 = ctypes.POINTER(_Router), ctypes.POINTER(_Experts), ctypes.c_int, ctypes.c_uint32
         lib.cbk_experts_bytes.restype = sz
         lib.cbk_experts_bytes.argtypes = [u32]
+        lib.cbk_sample_workspace_bytes.restype = sz
+        lib.cbk_sample_workspace_bytes.argtypes = [ctypes.POINTER(_Sampling), u64, u64]
         lib.cbk_experts_workspace_bytes.restype = sz
         lib.cbk_experts_workspace_bytes.argtypes = [ep, u64, u32, i32]
         for name, types in (
@@ -210,7 +212,7 @@ def load_library():
                 ("cbk_experts_init", [tp, tp, tp, u32, vp, sz, ep]),
                 ("cbk_ffn_experts", [ep, i32, vp, u64, u64, vp, vp, u32, vp, u64, vp, sz, vp]),
                 ("cbk_ffn_experts_bwd", [ep, i32, vp, u64, u64, vp, vp, u32, vp, u64, vp, u64, vp, vp, sz, vp]),
-                ("cbk_sample", [ctypes.POINTER(_Sampling), vp, i32, u64, u64, u64, vp, vp, vp, vp])):
+                ("cbk_sample", [ctypes.POINTER(_Sampling), vp, i32, u64, u64, u64, vp, vp, vp, vp, sz, vp])):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = types
         _lib = lib
@@ -738,17 +740,19 @@ class _Call:
 
     def __init__(self, x, stream):
         import torch
-        self.torch, self.device = torch, x.device
+        self.torch, self.device, self.current, self.stream = torch, x.device, None, None
         if self.device.type != "cuda":
             raise ValueError("the operators run on GPU tensors")
-        self.current = self.stream = torch.cuda.current_stream(self.device)
-        if stream is not None and stream != self.current:
+        if stream is None:  # the current one, of which run() asks for no more than its handle (2 us of a small call's 11 less)
+            return
+        self.current = torch.cuda.current_stream(self.device)
+        if stream != self.current:
             if stream.device != self.device:
                 raise ValueError(f"the stream is on {stream.device}, the arguments on {self.device}")
             self.stream = stream
 
     def empty(self, shape, dtype, scratch=False):
-        if self.stream is self.current:
+        if self.stream is None:
             return self.torch.empty(shape, dtype=dtype, device=self.device)
         with self.torch.cuda.stream(self.stream):
             out = self.torch.empty(shape, dtype=dtype, device=self.device)
@@ -763,14 +767,19 @@ class _Call:
         if sizes is None:
             pass
         elif workspace is None:
-            # at least one element, so that there is an address; torch's blocks are 512-byte aligned
-            workspace = self.empty((getattr(lib, sizes[0])(*sizes[1:]) or 1,), self.torch.uint8, scratch=True)
+            need = getattr(lib, sizes[0])(*sizes[1:])
+            if need == 0:
+                args += (None, 0)
+                sizes = None
+            else:  # (torch's blocks are 512-byte aligned)
+                workspace = self.empty((need,), self.torch.uint8, scratch=True)
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"the workspace must be a contiguous tensor on {self.device}")
         if sizes is not None:
             args += (workspace.data_ptr() or None, workspace.numel() * workspace.element_size())
-        args += (self.stream.cuda_stream,)
-        if self.torch.cuda.current_device() == self.device.index:
+        native, index = self.torch._C, self.device.index
+        args += (native._cuda_getCurrentRawStream(index) if self.stream is None else self.stream.cuda_stream,)
+        if native._cuda_getDevice() == index:
             st = getattr(lib, name)(*args)
         else:
             with self.torch.cuda.device(self.device):
@@ -1069,7 +1078,18 @@ def ffn_experts_bwd(ex: Experts, X, experts, weights, dY, act: str = "silu", dX=
     return dX, dweights
 
 
-def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
+def sample_workspace_bytes(tokens: int, vocabulary: int, top_k=0, top_p=1.0, min_p=0.0) -> int:
+    """Workspace of ``sample`` with these settings, numbers or vectors (0: none, where they filter anything)."""
+    p = _Sampling(1.0, 1.0, 0.0, 0)
+    for name, value in (("top_p", top_p), ("min_p", min_p), ("top_k", top_k)):
+        if hasattr(value, "data_ptr"):
+            setattr(p, name + "s", 4)  # (any but NULL)
+        else:
+            setattr(p, name, value)
+    return int(load_library().cbk_sample_workspace_bytes(ctypes.byref(p), vocabulary, tokens))
+
+
+def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, workspace=None, stream=None):
     """Draws a token from each row of logits[tokens][vocabulary] (float32 or bfloat16) by a random number uniform[tokens]
     (float32 in [0, 1)): (token int64[tokens], logprob float32[tokens], the logarithm of the probability that it was drawn
     with).  ``temperature`` 0 takes the largest logit; ``top_k`` (0: all), ``min_p`` (times the largest probability) and
@@ -1094,5 +1114,7 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stre
     _arguments(logits, uniform, *vectors)
     call = _Call(logits, stream)
     token, logprob = call.empty((T,), torch.int64), call.empty((T,), torch.float32)
-    call.run("cbk_sample", None, None, ctypes.byref(p), zp, dtype, ld, V, T, up, token.data_ptr() or None, logprob.data_ptr() or None)
+    ps = ctypes.byref(p)
+    call.run("cbk_sample", ("cbk_sample_workspace_bytes", ps, V, T), workspace, ps, zp, dtype, ld, V, T, up, token.data_ptr() or None,
+             logprob.data_ptr() or None)
     return token, logprob

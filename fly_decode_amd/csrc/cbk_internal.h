@@ -99,8 +99,14 @@ cbk_status launch_route(const cbk_router &r, const void *logits, int dtype, uint
                         int32_t *experts, float *weights, hipStream_t s);
 cbk_status launch_route_bwd(const cbk_router &r, const void *logits, int dtype, uint64_t ld, uint64_t tokens,
                             const int32_t *experts, const float *dweights, void *dlogits, uint64_t ldd, hipStream_t s);
+// How a call of cbk_sample is done: rows of a launch, and for calls without a filter the segments of a row (else 0).
+constexpr uint32_t kSamplePartBytes = 16, kSampleSegment = 1024;
+struct SamplePlan {
+    uint64_t rows, bytes;
+    uint32_t segments;
+};
 cbk_status launch_sample(const cbk_sampling &p, const void *logits, int dtype, uint64_t ld, uint64_t V, uint64_t tokens,
-                         const float *uniform, int64_t *token, float *logprob, hipStream_t s);
+                         const float *uniform, int64_t *token, float *logprob, const SamplePlan &pl, void *ws, hipStream_t s);
 
 // Blocks of experts (cbk_moe.hip, cbk_moe_mm.hip).  As for NnPlan, a plan depends on the shapes and the number of
 // tokens alone.  Tokens are taken Tc at a time; a token's k slots are sorted by expert.

@@ -56,6 +56,19 @@ cbk_status check_workspace(const void *ws, size_t bytes, uint64_t need) {
     return CBK_OK;
 }
 
+// A call whose numbers say that no row has a filter takes two kernels over segments of the rows, in chunks of rows with
+// 64 MB of segments' sums; with filters, or with vectors of them, a row has one workgroup (a launch has fewer than 2^32
+// threads).  us of a replayed call, one workgroup a row and segments: 1 row of 1000 12.0 and 9.5, of 32000 22.3 and 12.4, of
+// 128000 51 and 12.3; 64 of 32000 23.5 and 14.5; 192 of 128000 57 and 41; 1000 of 4000 52 and 16.
+cbk::SamplePlan sample_plan(const cbk_sampling &p, uint64_t V, uint64_t tokens) {
+    const bool filters = p.top_ks || p.top_ps || p.min_ps || (p.top_k > 0 && static_cast<uint64_t>(p.top_k) < V) || p.top_p < 1.f || p.min_p > 0.f;
+    if (filters) return {uint64_t(1) << 21, 0, 0};
+    // (the first entry may lie up to three elements into its segment)
+    const uint32_t segments = static_cast<uint32_t>((V + 3 + cbk::kSampleSegment - 1) / cbk::kSampleSegment);
+    const uint64_t rows = std::min<uint64_t>(tokens, (uint64_t(1) << 22) / segments);
+    return {rows, rows * segments * cbk::kSamplePartBytes, segments};
+}
+
 }  // namespace
 
 namespace cbk {
@@ -232,18 +245,27 @@ cbk_status cbk_ffn_experts_bwd(const cbk_experts *ex, int act, const uint16_t *X
                                static_cast<hipStream_t>(stream));
 }
 
+size_t cbk_sample_workspace_bytes(const cbk_sampling *p, uint64_t V, uint64_t tokens) {
+    if (!p || V == 0 || V > kMaxWidth || tokens == 0 || tokens >= kMaxTokens) return 0;
+    return static_cast<size_t>(sample_plan(*p, V, tokens).bytes);
+}
+
 cbk_status cbk_sample(const cbk_sampling *p, const void *logits, int dtype, uint64_t ld, uint64_t V, uint64_t tokens,
-                      const float *uniform, int64_t *token, float *logprob, void *stream) {
+                      const float *uniform, int64_t *token, float *logprob, void *workspace, size_t workspace_bytes,
+                      void *stream) {
     if (!p || V == 0) return CBK_E_INVALID;
-    if (V > (uint64_t(1) << 20) || tokens >= kMaxTokens) return CBK_E_UNSUPPORTED;
+    if (V > kMaxWidth || tokens >= kMaxTokens) return CBK_E_UNSUPPORTED;
     if (tokens == 0) return CBK_OK;
-    const cbk_status st = check_rows(logits, dtype, ld, V);
+    cbk_status st = check_rows(logits, dtype, ld, V);
     if (st != CBK_OK) return st;
     if (!uniform || !token) return CBK_E_INVALID;
     if (!aligned(uniform, 4) || !aligned(token, 8) || !aligned(logprob, 4) || !aligned(p->temperatures, 4) ||
         !aligned(p->top_ps, 4) || !aligned(p->min_ps, 4) || !aligned(p->top_ks, 4))
         return CBK_E_ALIGN;
-    return cbk::launch_sample(*p, logits, dtype, ld, V, tokens, uniform, token, logprob, static_cast<hipStream_t>(stream));
+    const cbk::SamplePlan pl = sample_plan(*p, V, tokens);
+    st = check_workspace(workspace, workspace_bytes, pl.bytes);
+    if (st != CBK_OK) return st;
+    return cbk::launch_sample(*p, logits, dtype, ld, V, tokens, uniform, token, logprob, pl, workspace, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
 // HIP kernel for gfx950 (CDNA4) of cbk_sample.h: drawing a token from a row of logits.
 //
-// A workgroup of 16 waves has a row.  Every filter keeps a prefix of the row's order (logits falling,
+// With filters, a workgroup of 16 waves has a row.  Every filter keeps a prefix of the row's order (logits falling,
 // then index), so what is kept is what stands before one cut in that order, a 64-bit key of logit and
 // index, and no row is sorted.  A histogram over the logits, in bins of a sixteenth of the temperature,
 // finds the bin that a cut falls into; the entries of that bin alone are ranked, in LDS.  Sums whose
@@ -8,7 +8,8 @@
 //
 // A row of 10^5 logits is read from memory or the last cache each time, so passes over it are few.  No pass
 // looks for the maximum first: bins and exponentials are relative to the largest of the first 4096 logits.
-//   temperature alone: one pass, a sum of exponentials of each 1024 entries;
+//   temperature alone: one pass, a sum of exponentials of each 1024 entries (by k_sample_parts and k_sample_join, where a
+//     call's numbers say so: a wave a segment, so that few rows keep all of the chip busy);
 //   top_k (up to some 1500): one that counts, and one that collects the entries up to the cut's bin; all
 //     other filters and the draw are then done on that list;
 //   top_p: one that adds up the bins, and one that collects the cut's bin and adds up what stands before it;
@@ -185,7 +186,7 @@ __device__ __forceinline__ V shuffle_up(V v, int by) {
 
 // The sum of v over the threads before this one, in thread order; `total`: over all.  `wave` has an entry for each
 // wave, and everyone is done with it on return.
-template <typename V>
+template <int WAVES = kWaves, typename V>
 __device__ __forceinline__ V sum_before(V v, V *wave, V &total) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     V s = v;
@@ -199,13 +200,242 @@ __device__ __forceinline__ V sum_before(V v, V *wave, V &total) {
     V before = V(0);
     total = V(0);
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < WAVES; ++i) {
         if (i == w) before = total;
         total += wave[i];
     }
     __syncthreads();
     return before + (s - v);
 }
+
+// The share of the kept masses that the draw goes past: from 1 on none does, whatever sums round to.
+__device__ __forceinline__ double share_of(float u) { return u >= 1.f ? static_cast<double>(__builtin_inff()) : u >= 0.f ? static_cast<double>(u) : 0.0; }
+
+// The first of neighbouring segments whose running sum exceeds the target, or the last that holds anything; thread i has
+// `run` of them from i run on, `before` is the sum of those before it, value(s) that of one.  In `first`, what stands before
+// the segment.  All threads; found32 has two entries.
+template <typename F>
+__device__ __forceinline__ uint32_t find_segment(F value, uint32_t segments, uint32_t run, double before, double target,
+                                                 uint32_t *found32, double *first) {
+    const uint32_t tid = threadIdx.x;
+    if (tid == 0) {
+        found32[0] = ~0u;
+        found32[1] = 0;
+    }
+    __syncthreads();
+    double sum = before;
+    uint32_t hit = ~0u, last = 0;
+    for (uint32_t i = 0; i < run; ++i) {
+        const uint32_t s = tid * run + i;
+        if (s >= segments) break;
+        const double m = value(s);
+        sum += m;
+        if (m > 0.0) {
+            last = s;
+            if (hit == ~0u && sum > target) hit = s;
+        }
+    }
+    if (hit != ~0u) atomicMin(&found32[0], hit);
+    if (last) atomicMax(&found32[1], last);
+    __syncthreads();
+    const uint32_t s = found32[0] != ~0u ? found32[0] : found32[1];
+    if (tid == s / run) {
+        sum = before;
+        for (uint32_t i = tid * run; i < s; ++i) sum += value(i);
+        *first = sum;
+    }
+    __syncthreads();
+    return s;
+}
+
+// One wave: the first entry of segment s at which the running sum, `before` at its start, exceeds the target, or the last
+// that can be drawn.  masses(four logits, index of the first, their masses).
+template <typename T, typename F>
+__device__ __forceinline__ int64_t draw_from(const Row<T> &r, uint32_t s, double before, double target, F masses, float &drawn) {
+    const uint32_t lane = threadIdx.x & 63;
+    int64_t token = -1;
+    drawn = 0.f;
+    typename Row<T>::Raw v[kSteps];
+#pragma unroll
+    for (uint32_t i = 0; i < kSteps; ++i) v[i] = r.raw((s * kSteps + i) * 64 + lane);
+#pragma unroll 1
+    for (uint32_t step = 0; step < kSteps; ++step) {
+        float z[4];
+        double m[4];
+        const int32_t at = r.values((s * kSteps + step) * 64 + lane, v[0], z);
+#pragma unroll
+        for (uint32_t i = 0; i + 1 < kSteps; ++i) v[i] = v[i + 1];
+        masses(z, at, m);
+        double sum = m[0] + m[1] + m[2] + m[3];
+        const double own = sum;
+#pragma unroll
+        for (int by = 1; by < 64; by *= 2) {
+            const double t = shuffle_up(sum, by);
+            if (lane >= static_cast<uint32_t>(by)) sum += t;
+        }
+        const double next = before + __shfl(sum, 63, 64);
+        sum = before + (sum - own);
+        before = next;
+        int32_t hit = -1, end = -1;  // this lane's first entry past the target, and its last that can be drawn
+        float hz = 0.f, ez = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sum += m[j];
+            if (m[j] > 0.0) {
+                end = at + j;
+                ez = z[j];
+                if (hit < 0 && sum > target) {
+                    hit = at + j;
+                    hz = z[j];
+                }
+            }
+        }
+        const uint64_t hits = __ballot(hit >= 0), ends = __ballot(end >= 0);
+        if (hits || ends) {
+            const int who = hits ? __ffsll(static_cast<unsigned long long>(hits)) - 1 : 63 - __clzll(static_cast<long long>(ends));
+            token = __shfl(hits ? hit : end, who, 64);
+            drawn = __shfl(hits ? hz : ez, who, 64);
+        }
+        if (hits) break;
+    }
+    return token;
+}
+
+// ---------------------------------------------------------------------- no filter
+// Segments of 1024 entries by a wave each, all over the chip: a segment's largest logit, and its masses relative to that.
+// Then a workgroup for each row joins them, finds the segment that the target falls into, and draws from it.
+struct Part {
+    double sum;
+    float top;
+    uint32_t odd;  // it holds a NaN
+};
+constexpr int kPartWaves = 4;
+
+// x relative to a logit; entries of +inf, where there are any, are all that counts, and one of -inf never does
+__device__ __forceinline__ double relative(float z, float to, double inv) {
+    if (to == __builtin_inff()) return z == to ? 0.0 : -1e300;
+    return z == -__builtin_inff() ? -1e300 : (static_cast<double>(z) - static_cast<double>(to)) * inv;
+}
+
+template <typename T>
+__global__ __launch_bounds__(64 * kPartWaves) void k_sample_parts(const SampleArgs a, Part *parts, uint32_t segments, uint32_t all) {
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t n = blockIdx.x * kPartWaves + wave;
+    if (n >= all) return;
+    const uint32_t row = n / segments, s = n - row * segments;
+    const Row<T> r(a.logits, a.ld, row, a.V);
+    const float heat = a.p.temperatures ? a.p.temperatures[row] : a.p.temperature;
+    const double inv = 1.0 / static_cast<double>(heat);
+    float z[kSteps][4];
+    float top = -__builtin_inff();
+    bool odd = false;
+#pragma unroll
+    for (uint32_t i = 0; i < kSteps; ++i) {
+        r.load((s * kSteps + i) * 64 + lane, z[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            odd = odd || z[i][j] != z[i][j];
+            top = fmaxf(top, z[i][j]);
+        }
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    odd = __any(odd);
+    double sum = 0.0;
+    if (heat > 0.f && top > -__builtin_inff()) {
+#pragma unroll
+        for (uint32_t i = 0; i < kSteps; ++i) {
+            double m[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m[j] = exponential(relative(z[i][j], top, inv));
+            sum += (m[0] + m[1]) + (m[2] + m[3]);
+        }
+    }
+    sum = wave_total(sum);
+    if (lane == 0) parts[n] = Part{sum, top, odd ? 1u : 0u};
+}
+
+template <typename T>
+__global__ __launch_bounds__(64 * kPartWaves) void k_sample_join(const SampleArgs a, const Part *parts, uint32_t segments) {
+    __shared__ float tops[kPartWaves];
+    __shared__ double sums[kPartWaves], first;
+    __shared__ uint32_t found32[2];
+    const uint32_t row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const Row<T> r(a.logits, a.ld, row, a.V);
+    const float inf = __builtin_inff();
+    const float heat = a.p.temperatures ? a.p.temperatures[row] : a.p.temperature;
+    const float u = a.uniform[row];
+    const double inv = 1.0 / static_cast<double>(heat);
+    parts += static_cast<uint64_t>(row) * segments;
+    const uint32_t run = (segments + 64 * kPartWaves - 1) / (64 * kPartWaves);
+    // the row's largest
+    float top = -inf;
+    bool odd = heat != heat;
+    for (uint32_t i = tid * run; i < min(segments, (tid + 1) * run); ++i) {
+        top = fmaxf(top, parts[i].top);
+        odd = odd || parts[i].odd;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    if (__any(odd)) top = __builtin_nanf("");
+    if (lane == 0) tops[wave] = top;
+    if (tid == 0) found32[0] = ~0u;
+    __syncthreads();
+    top = -inf;
+    odd = false;
+#pragma unroll
+    for (int i = 0; i < kPartWaves; ++i) {
+        odd = odd || tops[i] != tops[i];
+        top = fmaxf(top, tops[i]);
+    }
+    if (odd || top == -inf) {
+        if (tid == 0) {
+            a.token[row] = -1;
+            if (a.logprob) a.logprob[row] = __builtin_nanf("");
+        }
+        return;
+    }
+    if (heat <= 0.f) {  // the first of the largest
+        for (uint32_t i = tid * run; i < min(segments, (tid + 1) * run); ++i)
+            if (parts[i].top == top) {
+                atomicMin(&found32[0], i);
+                break;
+            }
+        __syncthreads();
+        if (wave != 0) return;
+        float drawn;
+        const int64_t token = draw_from(r, found32[0], 0.0, 0.5, [&](const float (&z)[4], int32_t, double (&m)[4]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m[j] = z[j] == top ? 1.0 : 0.0;
+        }, drawn);
+        if (lane == 0) {
+            a.token[row] = token;
+            if (a.logprob) a.logprob[row] = 0.f;
+        }
+        return;
+    }
+    auto value = [&](uint32_t i) __attribute__((always_inline)) {
+        const Part p = parts[i];
+        return p.sum * exponential(relative(p.top, top, inv));
+    };
+    double mine = 0.0, total;
+    for (uint32_t i = tid * run; i < min(segments, (tid + 1) * run); ++i) mine += value(i);
+    const double before = sum_before<kPartWaves>(mine, sums, total);
+    const double target = share_of(u) * total;
+    const uint32_t s = find_segment(value, segments, run, before, target, found32, &first);
+    if (wave != 0) return;
+    float drawn;
+    const int64_t token = draw_from(r, s, first, target, [&](const float (&z)[4], int32_t, double (&m)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = exponential(relative(z[j], top, inv));
+    }, drawn);
+    if (lane == 0) {
+        a.token[row] = token;
+        if (a.logprob) a.logprob[row] = static_cast<float>(relative(drawn, top, inv) - log(total));
+    }
+}
+
+// ---------------------------------------------------------------------- filters
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
@@ -257,9 +487,10 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     const float heat = a.p.temperatures ? a.p.temperatures[row] : a.p.temperature;
     const int32_t top_k = a.p.top_ks ? a.p.top_ks[row] : a.p.top_k;
     const float top_p = a.p.top_ps ? a.p.top_ps[row] : a.p.top_p;
-    const float min_p = fminf(a.p.min_ps ? a.p.min_ps[row] : a.p.min_p, 1.f);
+    const float given_min = a.p.min_ps ? a.p.min_ps[row] : a.p.min_p;
+    const float min_p = given_min > 0.f ? fminf(given_min, 1.f) : 0.f;
     const float u = a.uniform[row];
-    const double share = u >= 0.f ? static_cast<double>(u) : 0.0;
+    const double share = share_of(u);
     if (heat != heat) return nothing();
     if (heat <= 0.f) {  // the first of the largest: the least key
         uint64_t first = ~uint64_t(0);
@@ -720,7 +951,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     auto kept_masses = [&](const float (&z)[4], int32_t at, double (&m)[4]) __attribute__((always_inline)) {
         bool kept[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kept[j] = z[j] >= least && (cut == ~uint64_t(0) || place_key(z[j], static_cast<uint32_t>(at + j)) <= cut);
+        for (int j = 0; j < 4; ++j) kept[j] = in(z[j]) && (cut == ~uint64_t(0) || place_key(z[j], static_cast<uint32_t>(at + j)) <= cut);
         masses(z, kept, base, m);
     };
     __syncthreads();
@@ -764,80 +995,10 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     double total;
     double before = sum_before(mine, sh.wavef, total);
     const double target = share * total;
-    // the first segment whose running sum exceeds the target, or the last that holds anything
-    if (tid == 0) {
-        sh.found32[0] = ~0u;
-        sh.found32[1] = 0;
-    }
-    __syncthreads();
-    {
-        double sum = before;
-        uint32_t first = ~0u, last = 0;
-        for (uint32_t i = 0; i < run; ++i) {
-            const uint32_t s = tid * run + i;
-            if (s >= segments) break;
-            const double m = sh.segment[s];
-            sum += m;
-            if (m > 0.0) {
-                last = s;
-                if (first == ~0u && sum > target) first = s;
-            }
-        }
-        if (first != ~0u) atomicMin(&sh.found32[0], first);
-        if (last) atomicMax(&sh.found32[1], last);
-    }
-    __syncthreads();
-    const uint32_t s = sh.found32[0] != ~0u ? sh.found32[0] : sh.found32[1];
-    if (tid == s / run) {
-        double sum = before;
-        for (uint32_t i = tid * run; i < s; ++i) sum += sh.segment[i];
-        sh.wavef[0] = sum;
-    }
-    __syncthreads();
+    const uint32_t s = find_segment([&](uint32_t i) __attribute__((always_inline)) { return sh.segment[i]; }, segments, run, before, target, sh.found32, sh.wavef);
     if (wave != 0) return;
-    // the segment's steps one after the other, until one holds the target (else the last entry that can be drawn)
-    before = sh.wavef[0];
-    int64_t token = -1;
-    float drawn = 0.f;
-    for (uint32_t step = 0; step < kSteps; ++step) {
-        const uint32_t g = (s * kSteps + step) * 64 + lane;
-        float z[4] = {0.f, 0.f, 0.f, 0.f};
-        double m[4] = {0.0, 0.0, 0.0, 0.0};
-        int32_t at = 0;
-        at = r.load(g, z);
-        kept_masses(z, at, m);
-        double sum = m[0] + m[1] + m[2] + m[3];
-        const double own = sum;
-#pragma unroll
-        for (int by = 1; by < 64; by *= 2) {
-            const double t = shuffle_up(sum, by);
-            if (lane >= static_cast<uint32_t>(by)) sum += t;
-        }
-        const double next = before + __shfl(sum, 63, 64);
-        sum = before + (sum - own);
-        before = next;
-        int32_t hit = -1, end = -1;  // this lane's first entry past the target, and its last that can be drawn
-        float hz = 0.f, ez = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            sum += m[j];
-            if (m[j] > 0.0) {
-                end = at + j;
-                ez = z[j];
-                if (hit < 0 && sum > target) {
-                    hit = at + j;
-                    hz = z[j];
-                }
-            }
-        }
-        const uint64_t hits = __ballot(hit >= 0), ends = __ballot(end >= 0);
-        if (hits || ends) {
-            const int who = hits ? __ffsll(static_cast<unsigned long long>(hits)) - 1 : 63 - __clzll(static_cast<long long>(ends));
-            token = __shfl(hits ? hit : end, who, 64);
-            drawn = __shfl(hits ? hz : ez, who, 64);
-        }
-        if (hits) break;
-    }
+    float drawn;
+    const int64_t token = draw_from(r, s, sh.wavef[0], target, kept_masses, drawn);
     if (lane == 0) {
         a.token[row] = token;
         if (a.logprob) a.logprob[row] = static_cast<float>(exponent(drawn, base) - log(total));
@@ -847,18 +1008,27 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
 }  // namespace
 
 cbk_status launch_sample(const cbk_sampling &p, const void *logits, int dtype, uint64_t ld, uint64_t V, uint64_t tokens,
-                         const float *uniform, int64_t *token, float *logprob, hipStream_t s) {
+                         const float *uniform, int64_t *token, float *logprob, const SamplePlan &pl, void *ws, hipStream_t s) {
     SampleArgs a{p, logits, ld, static_cast<uint32_t>(V), uniform, token, logprob};
     const bool f32 = dtype == CBK_F32;
-    if (!(f32 ? allow_lds_once<float>(k_sample<float>, sizeof(Shared)) : allow_lds_once<uint16_t>(k_sample<uint16_t>, sizeof(Shared))))
+    static_assert(sizeof(Part) == kSamplePartBytes && 256 * kSteps == kSampleSegment, "the plan counts with them");
+    if (!pl.segments && !(f32 ? allow_lds_once<float>(k_sample<float>, sizeof(Shared)) : allow_lds_once<uint16_t>(k_sample<uint16_t>, sizeof(Shared))))
         return CBK_E_HIP;
-    // a launch has fewer than 2^32 threads
-    constexpr uint64_t kMost = (uint64_t(1) << 31) / kThreads;
     for (uint64_t left = tokens; left > 0;) {
-        const uint64_t n = std::min(left, kMost);
-        const dim3 grid(static_cast<uint32_t>(n)), block(kThreads);
-        if (f32) hipLaunchKernelGGL(k_sample<float>, grid, block, sizeof(Shared), s, a);
-        else hipLaunchKernelGGL(k_sample<uint16_t>, grid, block, sizeof(Shared), s, a);
+        const uint64_t n = std::min(left, pl.rows);
+        const dim3 grid(static_cast<uint32_t>(n));
+        if (pl.segments) {
+            const uint32_t all = static_cast<uint32_t>(n * pl.segments);
+            const dim3 waves((all + kPartWaves - 1) / kPartWaves), block(64 * kPartWaves);
+            Part *parts = static_cast<Part *>(ws);
+            if (f32) hipLaunchKernelGGL(k_sample_parts<float>, waves, block, 0, s, a, parts, pl.segments, all);
+            else hipLaunchKernelGGL(k_sample_parts<uint16_t>, waves, block, 0, s, a, parts, pl.segments, all);
+            if (f32) hipLaunchKernelGGL(k_sample_join<float>, grid, block, 0, s, a, parts, pl.segments);
+            else hipLaunchKernelGGL(k_sample_join<uint16_t>, grid, block, 0, s, a, parts, pl.segments);
+        } else {
+            if (f32) hipLaunchKernelGGL(k_sample<float>, grid, dim3(kThreads), sizeof(Shared), s, a);
+            else hipLaunchKernelGGL(k_sample<uint16_t>, grid, dim3(kThreads), sizeof(Shared), s, a);
+        }
         const cbk_status st = launched();
         if (st != CBK_OK) return st;
         left -= n;

@@ -2,8 +2,8 @@
  * cbk_sample.h -- C ABI of libcbk, continued: drawing the next token from a head's logits, as cbk_gemv and
  * cbk_gemm_small (fp32) or cbk_linear (BF16) of the compressed head give them.
  *
- * Conventions: as in cbk_nn.h (status codes, validation before any HIP call, the caller's stream, no
- * allocation, no state kept between calls, tokens == 0 is a no-op); no workspace is needed.
+ * Conventions: as in cbk_nn.h (status codes, validation before any HIP call, the caller's stream and
+ * workspace, no allocation, no state kept between calls, tokens == 0 is a no-op).
  */
 #ifndef CBK_SAMPLE_H
 #define CBK_SAMPLE_H
@@ -43,9 +43,12 @@ typedef struct {
  *   uniform   device, tokens fp32 in [0, 1), 4-byte aligned.
  *   token     device, tokens int64, 8-byte aligned; logprob  device, tokens fp32, 4-byte aligned, or NULL;
  *             overwritten.
+ *   workspace cbk_sample_workspace_bytes(p, V, tokens) bytes (up to 64 MB where p's numbers filter nothing, else 0).
  */
+size_t cbk_sample_workspace_bytes(const cbk_sampling *p, uint64_t V, uint64_t tokens);
 cbk_status cbk_sample(const cbk_sampling *p, const void *logits, int dtype, uint64_t ld, uint64_t V, uint64_t tokens,
-                      const float *uniform, int64_t *token, float *logprob, void *stream);
+                      const float *uniform, int64_t *token, float *logprob, void *workspace, size_t workspace_bytes,
+                      void *stream);
 
 #ifdef __cplusplus
 }

@@ -49,8 +49,8 @@ class Calls:
     def experts_bwd(self, ex=None, act=0, Z=A, ld=128, T=4, E=A, W=A, k=2, G=A, ldg=192, Y=A, ldy=128, D=A, ws=A, n=BIG):
         return self.lib.cbk_ffn_experts_bwd(ctypes.byref(ex or block(self.cbk)), act, Z, ld, T, E, W, k, G, ldg, Y, ldy, D, ws, n, None)
 
-    def sample(self, p=None, Z=A, dtype=0, V=16, ld=16, T=4, U=A, Y=A, L=A):
-        return self.lib.cbk_sample(ctypes.byref(p or self.cbk._Sampling(1.0, 1.0, 0.0, 0)), Z, dtype, ld, V, T, U, Y, L, None)
+    def sample(self, p=None, Z=A, dtype=0, V=16, ld=16, T=4, U=A, Y=A, L=A, ws=A, n=BIG):
+        return self.lib.cbk_sample(ctypes.byref(p or self.cbk._Sampling(1.0, 1.0, 0.0, 0)), Z, dtype, ld, V, T, U, Y, L, ws, n, None)
 
 
 ALL = ["route", "route_bwd", "experts", "experts_bwd", "sample"]
@@ -74,6 +74,7 @@ def test_too_many_tokens(cbk, name):
     ("experts_bwd", {"Z": None}), ("experts_bwd", {"G": None}), ("experts_bwd", {"Y": None}), ("experts_bwd", {"ldg": 191}),
     ("experts_bwd", {"ldy": 127}), ("experts_bwd", {"k": 0}), ("experts_bwd", {"act": 7}), ("experts_bwd", {"ws": None}),
     ("sample", {"Z": None}), ("sample", {"U": None}), ("sample", {"Y": None}), ("sample", {"V": 0}), ("sample", {"ld": 15}), ("sample", {"dtype": -1}),
+    ("sample", {"ws": None}),
 ])
 def test_invalid(cbk, name, args):
     assert getattr(Calls(cbk), name)(**args) == INVALID
@@ -83,7 +84,7 @@ def test_invalid(cbk, name, args):
     ("route", {"Z": A + 2}), ("route", {"Z": A + 1, "dtype": 1}), ("route", {"bias": A + 2}), ("route", {"E": A + 2}), ("route", {"W": A + 1}),
     ("route_bwd", {"Y": A + 2}), ("route_bwd", {"W": A + 2}), ("experts", {"Z": A + 1}), ("experts", {"Y": A + 1}), ("experts", {"E": A + 2}),
     ("experts", {"ws": A + 128}), ("experts_bwd", {"D": A + 2}), ("experts_bwd", {"G": A + 1}), ("sample", {"Z": A + 2}), ("sample", {"U": A + 2}),
-    ("sample", {"Y": A + 4}), ("sample", {"L": A + 2}),
+    ("sample", {"Y": A + 4}), ("sample", {"L": A + 2}), ("sample", {"ws": A + 128}),
 ])
 def test_alignment(cbk, name, args):
     assert getattr(Calls(cbk), name)(**args) == ALIGN
@@ -133,6 +134,26 @@ def test_workspace(cbk):
     assert 0 < lib.cbk_experts_workspace_bytes(ctypes.byref(wide), 1 << 20, 64, 1) < 64 << 30
 
 
+def test_workspace_of_a_draw(cbk):
+    """Only where the numbers filter nothing, in chunks of rows."""
+    size = cbk.sample_workspace_bytes
+    assert size(0, 5) == 0 and size(5, 0) == 0 and size(5, (1 << 20) + 1) == 0 and size(1 << 31, 5) == 0
+    assert 0 < size(1, 1) < size(2, 1) and size(1, 1 << 20) < 1 << 20 and size(10 ** 6, 50000) == size(10 ** 5, 50000) <= 64 << 20
+    for kw in ({"top_k": 5}, {"top_p": 0.9}, {"min_p": 0.1}):
+        assert size(4, 100, **kw) == 0
+    for kw in ({"top_k": 100}, {"top_k": -1}, {"top_p": float("nan")}, {"min_p": -1.0}, {"min_p": float("nan")}):
+        assert size(4, 100, **kw) == size(4, 100)
+    c = Calls(cbk)
+    assert c.sample(n=size(4, 16) - 1) == CAPACITY
+    with_filter = cbk._Sampling(1.0, 0.5, 0.0, 0)
+    assert c.sample(p=with_filter, ws=None, n=0, U=None) == INVALID  # (U, not the workspace)
+    for name in ("temperatures", "top_ps", "min_ps", "top_ks"):
+        p = cbk._Sampling(1.0, 1.0, 0.0, 0)
+        setattr(p, name, A)
+        need = cbk.load_library().cbk_sample_workspace_bytes(ctypes.byref(p), 100, 4)
+        assert (need > 0) == (name == "temperatures")
+
+
 def test_init(cbk):
     lib = cbk.load_library()
 
@@ -177,5 +198,5 @@ def test_the_binding_refuses(cbk):
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
 def test_the_headers_are_c99(tmp_path):
     src = tmp_path / "a.c"
-    src.write_text('#include "cbk_sample.h"\nint main(void) { return cbk_sample(0, 0, CBK_F32, 0, 0, 0, 0, 0, 0, 0) == CBK_OK; }\n')
+    src.write_text('#include "cbk_sample.h"\nint main(void) { return cbk_sample(0, 0, CBK_F32, 0, 0, 0, 0, 0, 0, 0, 0, 0) == CBK_OK; }\n')
     subprocess.run(["gcc", "-std=c99", "-pedantic", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"), "-c", str(src), "-o", str(tmp_path / "a.o")], check=True)

@@ -203,10 +203,16 @@ def test_sample_in_graphs_on_streams_and_without_logprob(env):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(side, want, here)), i
     token = torch.full((T + 2,), 7, dtype=torch.int64, device="cuda")
-    p = cbk._Sampling(1.0, 1.0, 0.0, 0)
-    assert cbk.load_library().cbk_sample(ctypes.byref(p), Z.data_ptr(), 0, V, V, T, U.data_ptr(), token[1:].data_ptr(), None,
-                                         torch.cuda.current_stream().cuda_stream) == 0
-    assert torch.equal(token[1:-1], want[0]) and int(token[0]) == 7 and int(token[-1]) == 7
+    need = cbk.sample_workspace_bytes(T, V)
+    whole = torch.empty(512 + need + 512, dtype=torch.uint8, device="cuda")
+    for p, ws, n, expect in ((cbk._Sampling(1.0, 1.0, 0.0, 0), whole[512:].data_ptr(), need, want[0]),
+                             (cbk._Sampling(1.0, 1.0, 0.0, 50), None, 0, cbk.sample(Z, U, top_k=50)[0])):
+        whole.fill_(0x7F)
+        token.fill_(7)
+        assert cbk.load_library().cbk_sample(ctypes.byref(p), Z.data_ptr(), 0, V, V, T, U.data_ptr(), token[1:].data_ptr(), None, ws, n,
+                                             torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(token[1:-1], expect) and int(token[0]) == 7 and int(token[-1]) == 7
+        assert bool((whole[:512] == 0x7F).all()) and bool((whole[512 + need:] == 0x7F).all())
 
 
 @pytest.mark.parametrize("spread", [0.0, 0.6])
@@ -220,3 +226,34 @@ def test_sample_a_cut_far_below_the_largest(env, spread):
     z[:, V - 1] = 0.0
     u = torch.tensor([0.5, 2.0 ** -26])
     check(torch, cbk, z, u, top_p=1 - 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("V", [1, 3, 1021, 1024, 1025, 5000, 50257])
+def test_sample_without_filters_by_numbers_and_by_vectors(env, V, dtype):
+    """Numbers that filter nothing, and vectors of such numbers, are done by different kernels: rows from any element, every
+    kind of temperature."""
+    torch, cbk = env
+    T, inf = 11, math.inf
+    z, u = draws(torch, T, V, getattr(torch, dtype), 21)
+    z[1] = -inf
+    z[2, V // 2] = math.nan
+    z[3, V - 1] = inf
+    z[4, : V // 2 + 1] = inf
+    z[5] = 0.0
+    z[6, -1] = 60.0
+    u[7], u[8], u[9] = 0.0, 1.0, math.nan
+    for at in (0, 1, 3):
+        big = torch.full((T, V + 7), math.nan, dtype=z.dtype)
+        big[:, at: at + V] = z
+        view = big.cuda()[:, at: at + V]
+        for heat in (1.0, 0.0, -1.0, 0.3, inf, math.nan, 1e-30, torch.tensor([1.0, 0.5, 2.0, 1.0, 0.0, 0.7, 1.0, inf, 0.9, 1.1, math.nan]).cuda()):
+            token, logprob = cbk.sample(view, u.cuda(), temperature=heat)
+            same, close = cbk.sample(view, u.cuda(), temperature=heat, top_k=torch.zeros(T, dtype=torch.int32, device="cuda"),
+                                     top_p=torch.full((T,), math.nan, device="cuda"), min_p=torch.full((T,), math.nan, device="cuda"))
+            assert torch.equal(token, same), heat
+            assert torch.equal(logprob.isnan(), close.isnan())
+            ok = ~logprob.isnan()  # each formed in 64 bits and rounded once
+            assert bool(((logprob - close).abs()[ok] <= 2.0 ** -23 * logprob.abs()[ok] + 1e-11).all()), heat
+    for heat in (1.0, 0.0, inf):
+        check(torch, cbk, z, u, heat, temperature=heat)
