@@ -1079,7 +1079,7 @@ def ffn_experts_bwd(ex: Experts, X, experts, weights, dY, act: str = "silu", dX=
 
 
 def sample_workspace_bytes(tokens: int, vocabulary: int, top_k=0, top_p=1.0, min_p=0.0) -> int:
-    """Workspace of ``sample`` with these settings, numbers or vectors (0: none, where they filter anything)."""
+    """Workspace of ``sample`` with these settings, numbers or vectors (0: none)."""
     p = _Sampling(1.0, 1.0, 0.0, 0)
     for name, value in (("top_p", top_p), ("min_p", min_p), ("top_k", top_k)):
         if hasattr(value, "data_ptr"):

@@ -99,11 +99,14 @@ cbk_status launch_route(const cbk_router &r, const void *logits, int dtype, uint
                         int32_t *experts, float *weights, hipStream_t s);
 cbk_status launch_route_bwd(const cbk_router &r, const void *logits, int dtype, uint64_t ld, uint64_t tokens,
                             const int32_t *experts, const float *dweights, void *dlogits, uint64_t ldd, hipStream_t s);
-// How a call of cbk_sample is done: rows of a launch, and for calls without a filter the segments of a row (else 0).
-constexpr uint32_t kSamplePartBytes = 16, kSampleSegment = 1024;
+// How a call of cbk_sample is done: rows of a launch; a row's segments (0: a workgroup does all of a row); whether there
+// are filters to divide the work of; and where the parts' scratch lies, which begins with the segments' records.
+constexpr uint32_t kSamplePartBytes = 16, kSampleSegment = 1024, kSampleBins = 2048;
 struct SamplePlan {
     uint64_t rows, bytes;
     uint32_t segments;
+    bool divided;
+    uint64_t sums, bins, list, state;
 };
 cbk_status launch_sample(const cbk_sampling &p, const void *logits, int dtype, uint64_t ld, uint64_t V, uint64_t tokens,
                          const float *uniform, int64_t *token, float *logprob, const SamplePlan &pl, void *ws, hipStream_t s);

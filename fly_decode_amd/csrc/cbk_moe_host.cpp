@@ -56,17 +56,29 @@ cbk_status check_workspace(const void *ws, size_t bytes, uint64_t need) {
     return CBK_OK;
 }
 
-// A call whose numbers say that no row has a filter takes two kernels over segments of the rows, in chunks of rows with
-// 64 MB of segments' sums; with filters, or with vectors of them, a row has one workgroup (a launch has fewer than 2^32
-// threads).  us of a replayed call, one workgroup a row and segments: 1 row of 1000 12.0 and 9.5, of 32000 22.3 and 12.4, of
-// 128000 51 and 12.3; 64 of 32000 23.5 and 14.5; 192 of 128000 57 and 41; 1000 of 4000 52 and 16.
+// How a draw is done; us are of replayed calls, rows with one workgroup each against their work divided.
+// Numbers that filter nothing: two kernels, the first over segments of the rows, in chunks of rows with 64 MB of scratch.
+// 1 row of 1000 12.0 and 9.5, of 32000 22.3 and 12.4, of 128000 51 and 12.3; 64 of 32000 23.5 and 14.5; 192 of 128000 57
+// and 41; 1000 of 4000 52 and 16.
+// Filters, or vectors of them: three kernels that share a few long rows' passes, and k_sample, which otherwise does all of a
+// row.  With top_k = 50 and with top_p = 0.9: 1 row of 32000 24, 50 and 28, 42; of 65000 33, 74 and 30, 42; of 128000 48,
+// 124 and 30, 46; 64 of 65000 35, 76 and 37, 52; of 128000 52, 126 and 49, 74; 192 of 128000 55, 128 and 85, 146 (the row's
+// cut is looked for by each of its workgroups).  A launch has fewer than 2^32 threads.
 cbk::SamplePlan sample_plan(const cbk_sampling &p, uint64_t V, uint64_t tokens) {
     const bool filters = p.top_ks || p.top_ps || p.min_ps || (p.top_k > 0 && static_cast<uint64_t>(p.top_k) < V) || p.top_p < 1.f || p.min_p > 0.f;
-    if (filters) return {uint64_t(1) << 21, 0, 0};
+    cbk::SamplePlan pl{uint64_t(1) << 21, 0, 0, false, 0, 0, 0, 0};
+    if (filters && !(V >= 65000 && tokens <= 64)) return pl;
     // (the first entry may lie up to three elements into its segment)
-    const uint32_t segments = static_cast<uint32_t>((V + 3 + cbk::kSampleSegment - 1) / cbk::kSampleSegment);
-    const uint64_t rows = std::min<uint64_t>(tokens, (uint64_t(1) << 22) / segments);
-    return {rows, rows * segments * cbk::kSamplePartBytes, segments};
+    pl.segments = static_cast<uint32_t>((V + 3 + cbk::kSampleSegment - 1) / cbk::kSampleSegment);
+    pl.divided = filters;
+    const uint64_t row = pl.segments * cbk::kSamplePartBytes + (filters ? pl.segments * 8 + cbk::kSampleBins * 16 + cbk::kSamplePartBytes : 0);
+    pl.rows = std::min<uint64_t>(tokens, (uint64_t(1) << 26) / row);
+    pl.sums = pl.rows * pl.segments * cbk::kSamplePartBytes;
+    pl.bins = pl.sums + pl.rows * pl.segments * 8;
+    pl.list = pl.bins + pl.rows * cbk::kSampleBins * 8;
+    pl.state = pl.list + pl.rows * cbk::kSampleBins * 8;
+    pl.bytes = pl.rows * row;
+    return pl;
 }
 
 }  // namespace

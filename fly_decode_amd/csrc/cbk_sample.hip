@@ -1,25 +1,27 @@
-// HIP kernel for gfx950 (CDNA4) of cbk_sample.h: drawing a token from a row of logits.
+// HIP kernels for gfx950 (CDNA4) of cbk_sample.h: drawing a token from a row of logits.
 //
-// With filters, a workgroup of 16 waves has a row.  Every filter keeps a prefix of the row's order (logits falling,
-// then index), so what is kept is what stands before one cut in that order, a 64-bit key of logit and
-// index, and no row is sorted.  A histogram over the logits, in bins of a sixteenth of the temperature,
-// finds the bin that a cut falls into; the entries of that bin alone are ranked, in LDS.  Sums whose
-// order could vary (atomic additions) are of fixed-point numbers, so they have the same bits in any order.
+// Every filter keeps a prefix of the row's order (logits falling, then index), so what is kept is what stands before
+// one cut in that order, a 64-bit key of logit and index, and no row is sorted.  A histogram over the logits, in bins of a
+// sixteenth of the temperature, finds the bin that a cut falls into; the entries of that bin alone are ranked, in LDS.
+// Sums whose order could vary (atomic additions) are of fixed-point numbers, so they have the same bits in any order.
 //
-// A row of 10^5 logits is read from memory or the last cache each time, so passes over it are few.  No pass
+// Without filters (the call's numbers say so) a wave has a segment of 1024 entries, and a workgroup joins a row's
+// (k_sample_parts, k_sample_join): one pass, on all of the chip also for one row.  With filters a workgroup of 16 waves
+// has a row (k_sample), or, where rows are long and few, the end of it, after its passes were shared among workgroups
+// (k_sample_bins, k_sample_collect).  sample_plan has the rule, and both sides' times.
+//
+// A row of 10^5 logits is read from memory or the last cache each time, so k_sample's passes over it are few.  No pass
 // looks for the maximum first: bins and exponentials are relative to the largest of the first 4096 logits.
-//   temperature alone: one pass, a sum of exponentials of each 1024 entries (by k_sample_parts and k_sample_join, where a
-//     call's numbers say so: a wave a segment, so that few rows keep all of the chip busy);
+//   temperature alone: one pass, a sum of exponentials of each 1024 entries;
 //   top_k (up to some 1500): one that counts, and one that collects the entries up to the cut's bin; all
 //     other filters and the draw are then done on that list;
 //   top_p: one that adds up the bins, and one that collects the cut's bin and adds up what stands before it;
 //   min_p without top_k: one for the maximum before those.
 // The draw takes the sums of each 1024 entries in index order, then the 1024 that the target falls into.
 //
-// 192 rows of 128000 fp32 logits take 25 us greedy (3.9 TB/s: memory), 58 by temperature alone, 52 with top_k = 50, 124
+// 192 rows of 128000 fp32 logits take 21 us greedy (4.7 TB/s: memory), 42 by temperature alone, 52 with top_k = 50, 124
 // with top_p = 0.9.  Past the first reading the vector units bound it: some 60 instructions an entry for the bins' masses.
-// One row of 32000 takes 23 us, 64 rows of 50257 BF16 logits by temperature 32: a row has one workgroup, which needs no
-// workspace and no second launch, and leaves CUs idle where rows are few.
+// One row of 128000 takes 12, 12, 30 and 46, what four dependent launches take; one of 32000 with all filters 25.
 //
 // The border between two tokens can be anywhere, and a vocabulary has 10^5 of them, so probabilities are
 // formed in fp64: an fp32 sum's 1e-7 would name another token once in some hundred rows.  On this chip
@@ -27,6 +29,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #pragma clang diagnostic ignored "-Wunused-function"  // cu_count of cbk_device.h
@@ -42,9 +45,22 @@ constexpr float kPerUnit = 16.f;
 constexpr float kAbove = 16.f;             // what the first bin starts above the reference, in units of the temperature
 constexpr uint32_t kList = 2048;           // entries of a list,
 constexpr uint32_t kRanked = 1024;         // and those of a bin that are ranked against each other
+constexpr double kFine = 1125899906842624.0;  // 2^50: units of a segment's and a list's fixed-point masses
 constexpr uint32_t kSteps = 4;             // of 256 entries by a wave, in a segment
 constexpr uint32_t kSegments = (1u << 20) / (256 * kSteps) + 2;
 
+// A segment of 1024 entries: its largest logit, and its masses relative to that.
+struct Part {
+    double sum;
+    float top;
+    uint32_t odd;  // it holds a NaN
+};
+// What the kernels before k_sample found of a row (see "filters, divided").
+struct RowState {
+    uint32_t listed;  // entries that the list was for (it holds kList at most)
+    uint32_t bin;     // of the cut by mass; kBins: none
+    double most;      // of mass before the cut, in that bin
+};
 struct SampleArgs {
     cbk_sampling p;
     const void *logits;
@@ -53,6 +69,12 @@ struct SampleArgs {
     const float *uniform;
     int64_t *token;
     float *logprob;
+    // the workspace: by row, for each of its segments; null where a call has none
+    uint32_t segments;
+    Part *parts;
+    uint64_t *sums;  // kept masses of a segment: fixed point, or a double's bits
+    uint64_t *bins, *list;
+    RowState *state;
 };
 
 struct Shared {
@@ -301,14 +323,177 @@ __device__ __forceinline__ int64_t draw_from(const Row<T> &r, uint32_t s, double
     return token;
 }
 
+// One wave: the first entry of segment s that is `top`.
+template <typename T>
+__device__ __forceinline__ int64_t first_of(const Row<T> &r, uint32_t s, float top, float &drawn) {
+    return draw_from(r, s, 0.0, 0.5, [&](const float (&z)[4], int32_t, double (&m)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = z[j] == top ? 1.0 : 0.0;
+    }, drawn);
+}
+
+// The settings of a row.
+struct Settings {
+    float heat, top_p, min_p;
+    int32_t top_k;
+    bool by_count, by_mass;
+
+    __device__ __forceinline__ Settings(const SampleArgs &a, uint32_t row) {
+        heat = a.p.temperatures ? a.p.temperatures[row] : a.p.temperature;
+        top_k = a.p.top_ks ? a.p.top_ks[row] : a.p.top_k;
+        top_p = a.p.top_ps ? a.p.top_ps[row] : a.p.top_p;
+        const float given = a.p.min_ps ? a.p.min_ps[row] : a.p.min_p;
+        min_p = given > 0.f ? fminf(given, 1.f) : 0.f;
+        by_count = top_k > 0 && static_cast<uint32_t>(top_k) < a.V;
+        by_mass = top_p < 1.f;
+    }
+    // The least logit that min_p keeps: rounded up, so that comparing floats is comparing with the border.
+    __device__ __forceinline__ float border(float top) const {
+        if (!(min_p > 0.f)) return -__builtin_inff();
+        if (top == __builtin_inff()) return top;
+        const double edge = __builtin_fma(static_cast<double>(heat), log(static_cast<double>(min_p)), static_cast<double>(top));
+        float least = static_cast<float>(edge);
+        if (static_cast<double>(least) < edge) least = from_ascending(ascending(least) + 1);
+        return fminf(least, top);
+    }
+};
+
+// What a row's bins and masses are relative to.
+struct Scale {
+    float ref, top, least;  // of the bins; the row's largest, once it is known; what min_p leaves out is below it
+    float step;             // bins a logit
+    double inv;
+
+    // x relative to a logit; entries of +inf, where there are any, are all that counts
+    __device__ __forceinline__ double exponent(float z, float to) const {
+        if (to == __builtin_inff()) return z == to ? 0.0 : -1e300;
+        return (static_cast<double>(z) - static_cast<double>(to)) * inv;
+    }
+    __device__ __forceinline__ bool in(float z) const { return z >= least && z != -__builtin_inff(); }
+    // where a logit lies in the histogram: below 0 where the reference was too low (its place then is the first bin).  (The
+    // kernels have to agree on it, and on the border, so what the compiler may or may not fuse is written out.)
+    __device__ __forceinline__ float place_of(float z) const {
+        if (ref == __builtin_inff()) return z == ref ? 0.f : static_cast<float>(kBins - 1);
+        return fminf(__builtin_fmaf(ref - z, step, kAbove * kPerUnit), static_cast<float>(kBins - 1));
+    }
+    __device__ __forceinline__ uint32_t bin_of(float z) const { return static_cast<uint32_t>(fmaxf(place_of(z), 0.f)); }
+    // The upper edge of bin b above the row's largest logit, in units of the temperature (a single bin is all that +inf
+    // leaves).
+    __device__ __forceinline__ double edge_of(uint32_t b) const {
+        if (ref == __builtin_inff()) return b == 0 ? 0.0 : -1e300;
+        return static_cast<double>(kAbove) - b * (1.0 / kPerUnit) - exponent(top, ref);
+    }
+    // The masses of the four logits that are `kept`, others 0: side by side, with no branch around each (whose chains of
+    // dependent operations would run one after the other), and none at all where the wave has none.
+    __device__ __forceinline__ void masses(const float (&z)[4], const bool (&kept)[4], float to, double (&m)[4]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = 0.0;
+        if (!__any(kept[0] || kept[1] || kept[2] || kept[3])) return;
+        double e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = exponential(exponent(z[j], to));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = kept[j] ? e[j] : 0.0;
+    }
+    // Adds four logits' masses to the histogram, relative to their bins' upper edges (within 1/16 of a unit), those that
+    // are `kept`.  The last bin's entries are some e^-112 of the largest: nothing.
+    template <typename F>
+    __device__ __forceinline__ void add_masses(const float (&z)[4], double units, uint64_t *mass, F kept) const {
+        uint64_t m[4];
+        float place[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            place[j] = truncf(fmaxf(place_of(z[j]), 0.f));
+            const float edge = kAbove - place[j] * (1.f / kPerUnit);  // exact
+            const double x = ref == __builtin_inff() ? 0.0 : exponent(z[j], ref) - static_cast<double>(edge);
+            m[j] = rounded(exponential_near_0(fmin(x, 0.02)), units);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (place[j] < static_cast<float>(kBins - 1) && kept(j))
+                atomicAdd(reinterpret_cast<unsigned long long *>(&mass[static_cast<uint32_t>(place[j])]), static_cast<unsigned long long>(m[j]));
+    }
+};
+// Units of the histogram's masses are 2^-unit, which leaves a row's sum below 2^63.
+__device__ __forceinline__ int unit_of(uint32_t V) { return min(50, 62 - (32 - __clz(V))); }
+
+// The largest of the threads' v, everywhere; a NaN if any of them has `odd`.
+__device__ __forceinline__ float largest_of(float v, bool odd, uint32_t *wave32) {
+    const float inf = __builtin_inff();
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    if (__any(odd)) v = __builtin_nanf("");
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) wave32[threadIdx.x >> 6] = __float_as_uint(v);
+    __syncthreads();
+    float most = -inf;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        const float t = __uint_as_float(wave32[i]);
+        bad = bad || t != t;
+        most = fmaxf(most, t);
+    }
+    __syncthreads();
+    return bad ? __builtin_nanf("") : most;
+}
+// The same of a row's segments.
+__device__ __forceinline__ float joined_top(const Part *parts, uint32_t segments, uint32_t *wave32) {
+    float top = -__builtin_inff();
+    bool odd = false;
+    for (uint32_t i = threadIdx.x; i < segments; i += kThreads) {
+        top = fmaxf(top, parts[i].top);
+        odd = odd || parts[i].odd;
+    }
+    return largest_of(top, odd, wave32);
+}
+
+// Where a cut by count falls: the bin of the last entry that is kept, entries up to that bin and before it, by the threads'
+// counts of bins 2 tid and 2 tid + 1; at most `want` of them are kept.  found32 has three entries.
+struct CountCut {
+    uint32_t keep, entries, limit, upto, earlier;
+};
+__device__ __forceinline__ CountCut count_cut(uint32_t c0, uint32_t c1, uint32_t want, uint32_t *wave32, uint32_t *found32) {
+    const uint32_t tid = threadIdx.x;
+    CountCut c;
+    const uint32_t before = sum_before(c0 + c1, wave32, c.entries);
+    c.keep = min(want, c.entries);
+    if (before < c.keep && c.keep <= before + c0 + c1) {  // one thread
+        const bool second = c.keep > before + c0;
+        found32[0] = 2 * tid + second;
+        found32[1] = before + c0 + (second ? c1 : 0);
+        found32[2] = second ? before + c0 : before;
+    }
+    __syncthreads();
+    c.limit = found32[0];
+    c.upto = found32[1];
+    c.earlier = found32[2];
+    __syncthreads();
+    return c;
+}
+// Of the histogram's masses (before bin 2 tid: `mb`, its own and the next one's m0 and m1): the bin that the target
+// falls into, and what stands before it; kBins where rounding leaves nothing past it.
+__device__ __forceinline__ uint32_t mass_bin(double mb, double m0, double m1, double want, uint32_t *found32, double *found, double &earlier) {
+    const uint32_t tid = threadIdx.x;
+    __syncthreads();
+    if (tid == 0) found32[1] = kBins;
+    __syncthreads();
+    // (sums of a double's precision: the one in front may seem to reach the target as well)
+    const uint32_t mine = m0 > 0.0 && mb + m0 >= want ? 2 * tid : m1 > 0.0 && mb + m0 + m1 >= want ? 2 * tid + 1 : kBins;
+    if (mine < kBins) atomicMin(&found32[1], mine);
+    __syncthreads();
+    const uint32_t b = found32[1];
+    if (b < kBins && tid == b / 2) *found = b & 1 ? mb + m0 : mb;
+    __syncthreads();
+    earlier = *found;
+    __syncthreads();
+    return b;
+}
+__device__ __forceinline__ bool short_cut(const CountCut &c) { return c.upto <= kList && c.upto - c.earlier <= kRanked; }
+
 // ---------------------------------------------------------------------- no filter
 // Segments of 1024 entries by a wave each, all over the chip: a segment's largest logit, and its masses relative to that.
 // Then a workgroup for each row joins them, finds the segment that the target falls into, and draws from it.
-struct Part {
-    double sum;
-    float top;
-    uint32_t odd;  // it holds a NaN
-};
 constexpr int kPartWaves = 4;
 
 // x relative to a logit; entries of +inf, where there are any, are all that counts, and one of -inf never does
@@ -317,8 +502,10 @@ __device__ __forceinline__ double relative(float z, float to, double inv) {
     return z == -__builtin_inff() ? -1e300 : (static_cast<double>(z) - static_cast<double>(to)) * inv;
 }
 
-template <typename T>
-__global__ __launch_bounds__(64 * kPartWaves) void k_sample_parts(const SampleArgs a, Part *parts, uint32_t segments, uint32_t all) {
+// SUMS false: the largest alone, and a row's bins and list are cleared.
+template <typename T, bool SUMS>
+__global__ __launch_bounds__(64 * kPartWaves) void k_sample_parts(const SampleArgs a, uint32_t all) {
+    const uint32_t segments = a.segments;
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t n = blockIdx.x * kPartWaves + wave;
     if (n >= all) return;
@@ -342,7 +529,10 @@ __global__ __launch_bounds__(64 * kPartWaves) void k_sample_parts(const SampleAr
     for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
     odd = __any(odd);
     double sum = 0.0;
-    if (heat > 0.f && top > -__builtin_inff()) {
+    if (!SUMS) {
+        for (uint32_t i = s * 64 + lane; i < kBins; i += segments * 64) a.bins[static_cast<uint64_t>(row) * kBins + i] = 0;
+        if (s == 0 && lane == 0) a.state[row] = RowState{0, kBins, 0.0};
+    } else if (heat > 0.f && top > -__builtin_inff()) {
 #pragma unroll
         for (uint32_t i = 0; i < kSteps; ++i) {
             double m[4];
@@ -351,12 +541,13 @@ __global__ __launch_bounds__(64 * kPartWaves) void k_sample_parts(const SampleAr
             sum += (m[0] + m[1]) + (m[2] + m[3]);
         }
     }
-    sum = wave_total(sum);
-    if (lane == 0) parts[n] = Part{sum, top, odd ? 1u : 0u};
+    if (SUMS) sum = wave_total(sum);
+    if (lane == 0) a.parts[n] = Part{sum, top, odd ? 1u : 0u};
 }
 
 template <typename T>
-__global__ __launch_bounds__(64 * kPartWaves) void k_sample_join(const SampleArgs a, const Part *parts, uint32_t segments) {
+__global__ __launch_bounds__(64 * kPartWaves) void k_sample_join(const SampleArgs a) {
+    const uint32_t segments = a.segments;
     __shared__ float tops[kPartWaves];
     __shared__ double sums[kPartWaves], first;
     __shared__ uint32_t found32[2];
@@ -366,7 +557,7 @@ __global__ __launch_bounds__(64 * kPartWaves) void k_sample_join(const SampleArg
     const float heat = a.p.temperatures ? a.p.temperatures[row] : a.p.temperature;
     const float u = a.uniform[row];
     const double inv = 1.0 / static_cast<double>(heat);
-    parts += static_cast<uint64_t>(row) * segments;
+    const Part *parts = a.parts + static_cast<uint64_t>(row) * segments;
     const uint32_t run = (segments + 64 * kPartWaves - 1) / (64 * kPartWaves);
     // the row's largest
     float top = -inf;
@@ -404,10 +595,7 @@ __global__ __launch_bounds__(64 * kPartWaves) void k_sample_join(const SampleArg
         __syncthreads();
         if (wave != 0) return;
         float drawn;
-        const int64_t token = draw_from(r, found32[0], 0.0, 0.5, [&](const float (&z)[4], int32_t, double (&m)[4]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m[j] = z[j] == top ? 1.0 : 0.0;
-        }, drawn);
+        const int64_t token = first_of(r, found32[0], top, drawn);
         if (lane == 0) {
             a.token[row] = token;
             if (a.logprob) a.logprob[row] = 0.f;
@@ -435,9 +623,141 @@ __global__ __launch_bounds__(64 * kPartWaves) void k_sample_join(const SampleArg
     }
 }
 
-// ---------------------------------------------------------------------- filters
+// ---------------------------------------------------------------------- filters, divided
+// What k_sample does with passes over a row, by workgroups that share its segments: the largest logit (k_sample_parts),
+// then the histogram (k_sample_bins; its counts for a row with top_k, else its masses), then what the cut's bin asks for
+// (k_sample_collect: with top_k a list of the entries up to the bin, else one of the bin's own, and the masses of each
+// segment before it).  k_sample goes on from there.  Atomic additions are of integers, and a list's order does not matter.
+struct BinsShared {
+    uint64_t bins[kBins];
+    uint64_t list[kList];
+    uint32_t wave32[kWaves], found32[3], listed, at;
+    double wavef[kWaves];
+};
+
+// Whether there is anything to be done for a row whose largest logit is `top`.
+__device__ __forceinline__ bool drawn_by_mass(float heat, float top) { return heat > 0.f && top > -__builtin_inff(); }
+
+template <typename T, typename F>
+__device__ __forceinline__ void over_segment(const Row<T> &r, uint32_t s, F f) {
+    const uint32_t lane = threadIdx.x & 63;
+    typename Row<T>::Raw v[kSteps];
+#pragma unroll
+    for (uint32_t i = 0; i < kSteps; ++i) v[i] = r.raw((s * kSteps + i) * 64 + lane);
+#pragma unroll 1
+    for (uint32_t i = 0; i < kSteps; ++i) {
+        float z[4];
+        const int32_t at = r.values((s * kSteps + i) * 64 + lane, v[0], z);
+#pragma unroll
+        for (uint32_t j = 0; j + 1 < kSteps; ++j) v[j] = v[j + 1];
+        f(at, z);
+    }
+}
 
 template <typename T>
+__global__ __launch_bounds__(kThreads) void k_sample_bins(const SampleArgs a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    BinsShared &sh = *reinterpret_cast<BinsShared *>(smem);
+    const uint32_t row = blockIdx.y, tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Settings st(a, row);
+    if (!st.by_count && !st.by_mass) return;
+    const float top = joined_top(a.parts + static_cast<uint64_t>(row) * a.segments, a.segments, sh.wave32);
+    if (!drawn_by_mass(st.heat, top)) return;
+    const Row<T> r(a.logits, a.ld, row, a.V);
+    const Scale sc{top, top, st.border(top), fminf(kPerUnit / st.heat, 1e30f), 1.0 / static_cast<double>(st.heat)};
+    for (uint32_t i = tid; i < kBins; i += kThreads) sh.bins[i] = 0;
+    __syncthreads();
+    const double units = ldexp(0.5, unit_of(a.V));
+    for (uint32_t s = blockIdx.x * kWaves + wave; s < a.segments; s += gridDim.x * kWaves)
+        over_segment(r, s, [&](int32_t, const float (&z)[4]) __attribute__((always_inline)) {
+            if (st.by_count) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (sc.in(z[j])) atomicAdd(reinterpret_cast<unsigned long long *>(&sh.bins[sc.bin_of(z[j])]), 1ull);
+            } else {
+                sc.add_masses(z, units, sh.bins, [&](int j) { return sc.in(z[j]); });
+            }
+        });
+    __syncthreads();
+    for (uint32_t i = tid; i < kBins; i += kThreads)
+        if (sh.bins[i]) atomicAdd(reinterpret_cast<unsigned long long *>(&a.bins[static_cast<uint64_t>(row) * kBins + i]), static_cast<unsigned long long>(sh.bins[i]));
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_sample_collect(const SampleArgs a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    BinsShared &sh = *reinterpret_cast<BinsShared *>(smem);
+    const uint32_t row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Settings st(a, row);
+    const float top = joined_top(a.parts + static_cast<uint64_t>(row) * a.segments, a.segments, sh.wave32);
+    if (!drawn_by_mass(st.heat, top)) return;
+    const Row<T> r(a.logits, a.ld, row, a.V);
+    const Scale sc{top, top, st.border(top), fminf(kPerUnit / st.heat, 1e30f), 1.0 / static_cast<double>(st.heat)};
+    const uint64_t *bins = a.bins + static_cast<uint64_t>(row) * kBins;
+    RowState &state = a.state[row];
+    uint32_t from = 0, upto = 0;  // bins [from, upto) are listed,
+    uint32_t added = 0;           // and [0, added) added up
+    if (st.by_count) {
+        const CountCut c = count_cut(static_cast<uint32_t>(bins[2 * tid]), static_cast<uint32_t>(bins[2 * tid + 1]), st.top_k, sh.wave32, sh.found32);
+        if (!short_cut(c)) return;
+        upto = c.limit + 1;
+    } else if (st.by_mass) {
+        double m[2];
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) m[j] = static_cast<double>(bins[2 * tid + j]) * ldexp(2.0, -unit_of(a.V)) * exponential(sc.edge_of(2 * tid + j));
+        double whole, earlier;
+        const double before = sum_before(m[0] + m[1], sh.wavef, whole), want = fmax(static_cast<double>(st.top_p), 0.0) * whole;
+        const uint32_t b = mass_bin(before, m[0], m[1], want, sh.found32, sh.wavef, earlier);
+        from = b;
+        upto = b < kBins ? b + 1 : b;
+        added = b;
+        if (blockIdx.x == 0 && tid == 0) {
+            state.bin = b;
+            state.most = want - earlier;
+        }
+    } else {
+        from = upto = added = kBins;
+    }
+    if (tid == 0) sh.listed = 0;
+    __syncthreads();
+    for (uint32_t s = blockIdx.x * kWaves + wave; s < a.segments; s += gridDim.x * kWaves) {
+        double m = 0.0;
+        over_segment(r, s, [&](int32_t at, const float (&z)[4]) __attribute__((always_inline)) {
+            bool kept[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = sc.bin_of(z[j]);
+                kept[j] = sc.in(z[j]) && x < added;
+                if (sc.in(z[j]) && x >= from && x < upto) {
+                    const uint32_t i = atomicAdd(&sh.listed, 1u);
+                    if (i < kList) sh.list[i] = place_key(z[j], at + j);
+                }
+            }
+            if (!st.by_count) {
+                double e[4];
+                sc.masses(z, kept, top, e);
+                m += (e[0] + e[1]) + (e[2] + e[3]);
+            }
+        });
+        if (!st.by_count) {
+            m = wave_total(m);
+            if (lane == 0)
+                a.sums[static_cast<uint64_t>(row) * a.segments + s] = st.by_mass ? static_cast<uint64_t>(m * kFine) : __builtin_bit_cast(uint64_t, m);
+        }
+    }
+    __syncthreads();
+    const uint32_t n = sh.listed;
+    if (n == 0) return;
+    if (tid == 0) sh.at = atomicAdd(&state.listed, n);
+    __syncthreads();
+    for (uint32_t i = tid; i < min(n, kList); i += kThreads)
+        if (sh.at + i < kList) a.list[static_cast<uint64_t>(row) * kList + sh.at + i] = sh.list[i];
+}
+
+// ---------------------------------------------------------------------- filters
+
+// `divided`: the kernels above have been over the row.
+template <typename T, bool divided>
 __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem);
@@ -446,25 +766,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     const uint32_t V = a.V;
     const float inf = __builtin_inff();
 
-    // The largest of the threads' v, everywhere; a NaN if any of them has `odd`.
-    auto largest = [&](float v, bool odd) __attribute__((always_inline)) {
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-        if (__any(odd)) v = __builtin_nanf("");
-        __syncthreads();
-        if (lane == 0) sh.wave32[wave] = __float_as_uint(v);
-        __syncthreads();
-        float most = -inf;
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
-            const float t = __uint_as_float(sh.wave32[i]);
-            bad = bad || t != t;
-            most = fmaxf(most, t);
-        }
-        __syncthreads();
-        return bad ? __builtin_nanf("") : most;
-    };
+    auto largest = [&](float v, bool odd) __attribute__((always_inline)) { return largest_of(v, odd, sh.wave32); };
     auto row_largest = [&]() __attribute__((always_inline)) {
         float top = -inf;
         bool odd = false;
@@ -484,15 +786,35 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         }
     };
 
-    const float heat = a.p.temperatures ? a.p.temperatures[row] : a.p.temperature;
-    const int32_t top_k = a.p.top_ks ? a.p.top_ks[row] : a.p.top_k;
-    const float top_p = a.p.top_ps ? a.p.top_ps[row] : a.p.top_p;
-    const float given_min = a.p.min_ps ? a.p.min_ps[row] : a.p.min_p;
-    const float min_p = given_min > 0.f ? fminf(given_min, 1.f) : 0.f;
+    const Settings st(a, row);
+    const float heat = st.heat, min_p = st.min_p;
+    const int32_t top_k = st.top_k;
+    const bool by_count = st.by_count, by_mass = st.by_mass;
     const float u = a.uniform[row];
     const double share = share_of(u);
     if (heat != heat) return nothing();
-    if (heat <= 0.f) {  // the first of the largest: the least key
+    const Part *parts = a.parts + (divided ? static_cast<uint64_t>(row) * a.segments : 0);
+    float row_top = -inf;
+    if (divided) {
+        row_top = joined_top(parts, a.segments, sh.wave32);
+        if (row_top != row_top || row_top == -inf) return nothing();
+    }
+    if (heat <= 0.f && divided) {  // the first of the largest
+        if (tid == 0) sh.found32[0] = ~0u;
+        __syncthreads();
+        for (uint32_t i = tid; i < a.segments; i += kThreads)
+            if (parts[i].top == row_top) atomicMin(&sh.found32[0], i);
+        __syncthreads();
+        if (wave != 0) return;
+        float drawn;
+        const int64_t token = first_of(r, sh.found32[0], row_top, drawn);
+        if (lane == 0) {
+            a.token[row] = token;
+            if (a.logprob) a.logprob[row] = 0.f;
+        }
+        return;
+    }
+    if (heat <= 0.f) {  // the least key
         uint64_t first = ~uint64_t(0);
         bool odd = false;
         over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
@@ -515,15 +837,16 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         return;
     }
 
-    const bool by_count = top_k > 0 && static_cast<uint32_t>(top_k) < V, by_mass = top_p < 1.f;
     const bool short_list = by_count && static_cast<uint32_t>(top_k) <= kList * 3 / 4;
-    const double inv = 1.0 / static_cast<double>(heat);
-    const double part = fmax(static_cast<double>(top_p), 0.0);
+    const double part = fmax(static_cast<double>(st.top_p), 0.0);
 
     // ---- the reference: the largest of the first entries, or, where it has to be known, of all
-    float ref = -inf, top = -inf;  // top: of the row, once it is known
-    bool known = false;
-    if (!(min_p > 0.f && !short_list)) {
+    Scale sc{-inf, -inf, -inf, fminf(kPerUnit / heat, 1e30f), 1.0 / static_cast<double>(heat)};
+    float &ref = sc.ref, &top = sc.top, &least = sc.least;
+    bool known = divided;
+    if (divided) {
+        top = ref = row_top;
+    } else if (!(min_p > 0.f && !short_list)) {
         float z[4];
         bool odd = false;
         r.load(tid, z);
@@ -535,55 +858,23 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         ref = largest(ref, odd);
         if (ref != ref) return nothing();
     }
-    if (!(fabsf(ref) < inf)) {
+    if (!divided && !(fabsf(ref) < inf)) {
         top = ref = row_largest();
         known = true;
         if (top != top || top == -inf) return nothing();
     }
-    float least = -inf;  // what min_p leaves out is below it; rounded up, so that comparing floats is comparing with the border
-    auto border = [&]() __attribute__((always_inline)) {
-        if (min_p > 0.f && top == inf) {
-            least = top;
-        } else if (min_p > 0.f) {
-            const double edge = static_cast<double>(top) + static_cast<double>(heat) * log(static_cast<double>(min_p));
-            least = static_cast<float>(edge);
-            if (static_cast<double>(least) < edge) least = from_ascending(ascending(least) + 1);
-            least = fminf(least, top);
-        }
-    };
+    auto border = [&]() __attribute__((always_inline)) { least = st.border(top); };
     if (known) border();
 
-    // x relative to a logit; entries of +inf, where there are any, are all that counts
-    auto exponent = [&](float z, float to) __attribute__((always_inline)) {
-        if (to == inf) return z == inf ? 0.0 : -1e300;
-        return (static_cast<double>(z) - static_cast<double>(to)) * inv;
-    };
-    auto mass_of = [&](float z, float to) __attribute__((always_inline)) { return exponential(exponent(z, to)); };  // 0 of -inf
-    // The masses of the four logits that are `kept`, others 0: side by side, with no branch around each (whose chains of
-    // dependent operations would run one after the other), and none at all where the wave has none.
-    auto masses = [&](const float (&z)[4], const bool (&kept)[4], float to, double (&m)[4]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m[j] = 0.0;
-        if (!__any(kept[0] || kept[1] || kept[2] || kept[3])) return;
-        double e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) e[j] = mass_of(z[j], to);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m[j] = kept[j] ? e[j] : 0.0;
-    };
-    const float step = fminf(kPerUnit / heat, 1e30f);
-    // where a logit lies in the histogram: below 0 where the reference was too low (its place then is the first bin)
-    auto place_of = [&](float z) __attribute__((always_inline)) {
-        if (ref == inf) return z == inf ? 0.f : static_cast<float>(kBins - 1);
-        return fminf((ref - z) * step + kAbove * kPerUnit, static_cast<float>(kBins - 1));
-    };
-    auto bin_of = [&](float z) __attribute__((always_inline)) { return static_cast<uint32_t>(fmaxf(place_of(z), 0.f)); };
-    auto in = [&](float z) __attribute__((always_inline)) { return z >= least && z != -inf; };
+    auto exponent = [&](float z, float to) __attribute__((always_inline)) { return sc.exponent(z, to); };
+    auto mass_of = [&](float z, float to) __attribute__((always_inline)) { return exponential(sc.exponent(z, to)); };  // 0 of -inf
+    auto place_of = [&](float z) __attribute__((always_inline)) { return sc.place_of(z); };
+    auto bin_of = [&](float z) __attribute__((always_inline)) { return sc.bin_of(z); };
+    auto in = [&](float z) __attribute__((always_inline)) { return sc.in(z); };
     // Fixed point.  The sums of a segment's 1024 masses, and of a list's 2048, relative to the row's largest: in units of
     // 2^-50.  Sums over a bin, which all of the row may lie in: of masses relative to the bin's edge, in units of 2^-unit,
     // which leaves them below 2^63.
-    const int unit = min(50, 62 - (32 - __clz(V)));
-    const double scale = ldexp(1.0, unit), fine = 1125899906842624.0;
+    const double scale = ldexp(1.0, unit_of(V)), fine = kFine;
     auto fixed = [&](float z, double by) __attribute__((always_inline)) { return rounded(mass_of(z, top), by); };
     auto key_logit = [&](uint64_t key) __attribute__((always_inline)) { return from_ascending(~static_cast<uint32_t>(key >> 32)); };
     auto add64 = [&](uint64_t *to, uint64_t v) __attribute__((always_inline)) {
@@ -668,24 +959,26 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
             if (i < kRanked) sh.ranked[i] = key;
         }
     };
-    // The upper edge of bin b above the row's largest logit, in units of the temperature (a single bin is all that +inf leaves).
-    auto edge_of = [&](uint32_t b) __attribute__((always_inline)) {
-        return ref == inf ? (b == 0 ? 0.0 : -1e300) : static_cast<double>(kAbove) - b * (1.0 / kPerUnit) - exponent(top, ref);
-    };
     // The same among the entries of bin b, `most` relative to the row's largest; `segments`: adds up what is kept by segments too, with the entries of the bins
     // before it; false where it did not.  Up to kList entries are divided up in LDS, more by passes over the row; where even
     // a part of the bin holds more than kRanked (equal logits), the cut's key is found by its bits.
-    auto cut_bin = [&](uint32_t b, uint32_t some, double most_mass, bool segments) __attribute__((always_inline)) {
+    auto cut_bin = [&](uint32_t b, uint32_t some, double most_mass, bool segments, bool collected) __attribute__((always_inline)) {
         // a power of two by which all of the bin's masses are small enough
         // (the first bin has no edge that all are below)
-        const int lift = b == 0 ? 0 : static_cast<int>(fmin(fmax(floor(edge_of(b) * -1.4426950408889634), 0.0), 900.0));
+        const int lift = b == 0 ? 0 : static_cast<int>(fmin(fmax(floor(sc.edge_of(b) * -1.4426950408889634), 0.0), 900.0));
         const double by = ldexp(scale, lift);
         uint64_t most = most_mass < inf ? max(uint64_t(1), static_cast<uint64_t>(ceil(fmin(most_mass * by, 9e18)))) : ~uint64_t(0);
         __syncthreads();
-        if (tid == 0) sh.found32[2] = 0;
+        if (tid == 0) sh.found32[2] = collected ? a.state[row].listed : 0;
         __syncthreads();
+        if (collected) {
+            const uint64_t *list = a.list + static_cast<uint64_t>(row) * kList, *sums = a.sums + static_cast<uint64_t>(row) * a.segments;
+            if (sh.found32[2] <= kList)
+                for (uint32_t i = tid; i < sh.found32[2]; i += kThreads) sh.list[i] = list[i];
+            for (uint32_t i = tid; i < a.segments; i += kThreads) sh.fixed_segment[i] = sums[i];
+        }
         double m = 0.0;
-        over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
+        if (!collected) over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
             bool kept[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -698,7 +991,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
             }
             if (segments) {
                 double e[4];
-                masses(z, kept, top, e);
+                sc.masses(z, kept, top, e);
                 m += (e[0] + e[1]) + (e[2] + e[3]);
             }
             if (segments && last) {
@@ -773,71 +1066,50 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         cut = min(cut, found);
         return false;
     };
-    // Of the histogram's masses (before bin 2 tid: `mb`, its own and the next one's m0 and m1): the bin that the target
-    // falls into, and what stands before it; kBins where rounding leaves nothing past it.
-    auto mass_bin = [&](double mb, double m0, double m1, double want, double &earlier) __attribute__((always_inline)) {
-        __syncthreads();
-        if (tid == 0) sh.found32[1] = kBins;
-        __syncthreads();
-        // (sums of a double's precision: the one in front may seem to reach the target as well)
-        const uint32_t mine = m0 > 0.0 && mb + m0 >= want ? 2 * tid : m1 > 0.0 && mb + m0 + m1 >= want ? 2 * tid + 1 : kBins;
-        if (mine < kBins) atomicMin(&sh.found32[1], mine);
-        __syncthreads();
-        const uint32_t b = sh.found32[1];
-        if (b < kBins && tid == b / 2) sh.wavef[0] = b & 1 ? mb + m0 : mb;
-        __syncthreads();
-        earlier = sh.wavef[0];
-        __syncthreads();
-        return b;
-    };
-
     const uint32_t segments = (r.groups + 64 * kSteps - 1) / (64 * kSteps);
     bool have = false;  // the segments' sums are there, in fixed point
     if (by_count) {
         // ---- counts, and the row's largest
-        for (uint32_t i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
+        for (uint32_t i = tid; i < kBins; i += kThreads) sh.count[i] = divided ? static_cast<uint32_t>(a.bins[static_cast<uint64_t>(row) * kBins + i]) : 0;
         __syncthreads();
-        float most = -inf;
-        bool odd = false;
-        over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                odd = odd || z[j] != z[j];
-                most = fmaxf(most, z[j]);
-                if (in(z[j])) atomicAdd(&sh.count[bin_of(z[j])], 1u);
-            }
-        });
-        top = largest(most, odd);
-        if (top != top || top == -inf) return nothing();
-        if (top == inf && ref != inf) {  // the bins do not hold: +inf alone counts
-            ref = inf;
-            for (uint32_t i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
-            __syncthreads();
+        if (!divided) {
+            float most = -inf;
+            bool odd = false;
             over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j) {
+                    odd = odd || z[j] != z[j];
+                    most = fmaxf(most, z[j]);
                     if (in(z[j])) atomicAdd(&sh.count[bin_of(z[j])], 1u);
+                }
             });
-            __syncthreads();
+            top = largest(most, odd);
+            if (top != top || top == -inf) return nothing();
+            if (top == inf && ref != inf) {  // the bins do not hold: +inf alone counts
+                ref = inf;
+                for (uint32_t i = tid; i < kBins; i += kThreads) sh.count[i] = 0;
+                __syncthreads();
+                over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (in(z[j])) atomicAdd(&sh.count[bin_of(z[j])], 1u);
+                });
+                __syncthreads();
+            }
         }
-        const uint32_t c0 = sh.count[2 * tid], c1 = sh.count[2 * tid + 1], want = top_k;
-        uint32_t entries;
-        const uint32_t before = sum_before(c0 + c1, sh.wave32, entries);
-        const uint32_t keep = min(want, entries);
-        if (before < keep && keep <= before + c0 + c1) {  // one thread
-            const bool second = keep > before + c0;
-            sh.found32[0] = 2 * tid + second;
-            sh.found32[1] = before + c0 + (second ? c1 : 0);  // entries up to that bin
-            sh.found32[2] = second ? before + c0 : before;    // and before it
-        }
-        __syncthreads();
-        const uint32_t limit = sh.found32[0], upto = sh.found32[1], earlier = sh.found32[2];
-        __syncthreads();
-        if (upto <= kList && upto - earlier <= kRanked) {
+        const CountCut c = count_cut(sh.count[2 * tid], sh.count[2 * tid + 1], top_k, sh.wave32, sh.found32);
+        const uint32_t keep = c.keep, entries = c.entries, limit = c.limit, upto = c.upto, earlier = c.earlier;
+        if (short_cut(c)) {
             // ---- the list: entries up to the cut's bin, those of the bin ranked; then the other filters on it
             if (tid < 2) sh.found32[tid] = 0;
             __syncthreads();
-            over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
+            if (divided)
+                for (uint32_t i = tid; i < min(upto, a.state[row].listed); i += kThreads) {
+                    const uint64_t key = a.list[static_cast<uint64_t>(row) * kList + i];
+                    sh.list[i] = key;
+                    if (bin_of(key_logit(key)) == limit) sh.ranked[atomicAdd(&sh.found32[1], 1u)] = key;
+                }
+            else over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (in(z[j]) && bin_of(z[j]) <= limit) {
@@ -868,7 +1140,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
                 const double m0 = static_cast<double>(sh.mass[2 * tid]), m1 = static_cast<double>(sh.mass[2 * tid + 1]);
                 double whole, earlier_mass;
                 const double mb = sum_before(m0 + m1, sh.wavef, whole), want_mass = part * whole;
-                const uint32_t b = mass_bin(mb, m0, m1, want_mass, earlier_mass);
+                const uint32_t b = mass_bin(mb, m0, m1, want_mass, sh.found32, sh.wavef, earlier_mass);
                 if (b < kBins) {
 #pragma unroll
                     for (uint32_t j = 0; j < 2; ++j)
@@ -881,7 +1153,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
                     if (n <= kRanked) {
                         cut_ranked(n, ~0u, max(uint64_t(1), static_cast<uint64_t>(ceil(want_mass - earlier_mass))), fine);
                     } else {
-                        have = cut_bin(b, ~0u, (want_mass - earlier_mass) / fine, false);
+                        have = cut_bin(b, ~0u, (want_mass - earlier_mass) / fine, false, false);
                     }
                 }
             }
@@ -898,65 +1170,64 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
             border();  // (after the cut by count, which does not know of it, unless it was known before)
             const float floor = least;
             if (!known) least = -inf;
-            if (keep < entries && limit < kBins - 1) cut_bin(limit, keep - earlier, static_cast<double>(inf), false);
+            if (keep < entries && limit < kBins - 1) cut_bin(limit, keep - earlier, static_cast<double>(inf), false, false);
             least = floor;
         }
         known = true;
     }
     if (!have && by_mass) {
-        // ---- the bins' masses.  Relative to their upper edges: within 1/16 of a unit, in fixed point.
-        double mine[2];
-        for (;;) {
-            for (uint32_t i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
-            __syncthreads();
-            float most = -inf;
-            bool odd = false;
-            over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
+        // ---- the bins' masses
+        uint32_t b;
+        double most_mass = 0.0;
+        const bool collected = divided && !by_count;
+        if (collected) {
+            b = a.state[row].bin;
+            most_mass = a.state[row].most;
+        } else {
+            for (;;) {
+                for (uint32_t i = tid; i < kBins; i += kThreads) sh.mass[i] = 0;
+                __syncthreads();
+                float most = -inf;
+                bool odd = false;
+                over_row(r, [&](int32_t at, const float (&z)[4], uint32_t segment, bool last) __attribute__((always_inline)) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    odd = odd || z[j] != z[j];
-                    most = fmaxf(most, z[j]);
-                }
-                uint64_t units[4];
-                float place[4];
+                    for (int j = 0; j < 4; ++j) {
+                        odd = odd || z[j] != z[j];
+                        most = fmaxf(most, z[j]);
+                    }
+                    sc.add_masses(z, scale * 0.5, sh.mass, [&](int j) __attribute__((always_inline)) {
+                        return in(z[j]) && (cut == ~uint64_t(0) || place_key(z[j], at + j) <= cut);
+                    });
+                });
+                top = largest(most, odd);
+                if (top != top || top == -inf) return nothing();
+                if (place_of(top) >= 0.f && (top < inf || ref == inf)) break;
+                ref = top;  // it was too low
+            }
+            if (!known) border();
+            known = true;
+            double mine[2];  // relative to the row's largest
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    place[j] = truncf(fmaxf(place_of(z[j]), 0.f));
-                    const float edge = kAbove - place[j] * (1.f / kPerUnit);  // exact
-                    const double x = ref == inf ? 0.0 : exponent(z[j], ref) - static_cast<double>(edge);
-                    units[j] = rounded(exponential_near_0(fmin(x, 0.02)), scale * 0.5);
-                }
-                // the last bin's entries are some e^-112 of the largest: nothing
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (in(z[j]) && place[j] < static_cast<float>(kBins - 1) && (cut == ~uint64_t(0) || place_key(z[j], at + j) <= cut))
-                        add64(&sh.mass[static_cast<uint32_t>(place[j])], units[j]);
-            });
-            top = largest(most, odd);
-            if (top != top || top == -inf) return nothing();
-            if (place_of(top) >= 0.f && (top < inf || ref == inf)) break;
-            ref = top;  // it was too low
+            for (uint32_t j = 0; j < 2; ++j) mine[j] = static_cast<double>(sh.mass[2 * tid + j]) * (2.0 / scale) * exponential(sc.edge_of(2 * tid + j));
+            double whole, earlier;
+            const double before = sum_before(mine[0] + mine[1], sh.wavef, whole), want = part * whole;
+            b = mass_bin(before, mine[0], mine[1], want, sh.found32, sh.wavef, earlier);
+            most_mass = want - earlier;
         }
-        if (!known) border();
-        known = true;
-        // relative to the row's largest
-#pragma unroll
-        for (uint32_t j = 0; j < 2; ++j) mine[j] = static_cast<double>(sh.mass[2 * tid + j]) * (2.0 / scale) * exponential(edge_of(2 * tid + j));
-        double whole, earlier;
-        const double before = sum_before(mine[0] + mine[1], sh.wavef, whole), want = part * whole;
-        const uint32_t b = mass_bin(before, mine[0], mine[1], want, earlier);
-        if (b < kBins) have = cut_bin(b, ~0u, want - earlier, cut == ~uint64_t(0));
+        if (b < kBins) have = cut_bin(b, ~0u, most_mass, cut == ~uint64_t(0), collected);
     }
     float base = known ? top : ref;  // what masses are relative to from here on
     auto kept_masses = [&](const float (&z)[4], int32_t at, double (&m)[4]) __attribute__((always_inline)) {
         bool kept[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) kept[j] = in(z[j]) && (cut == ~uint64_t(0) || place_key(z[j], static_cast<uint32_t>(at + j)) <= cut);
-        masses(z, kept, base, m);
+        sc.masses(z, kept, base, m);
     };
     __syncthreads();
     if (have) {
         for (uint32_t i = tid; i < segments; i += kThreads) sh.segment[i] = static_cast<double>(sh.fixed_segment[i]) * (1.0 / fine);
+    } else if (divided && !by_count && !by_mass) {
+        for (uint32_t i = tid; i < segments; i += kThreads) sh.segment[i] = __builtin_bit_cast(double, a.sums[static_cast<uint64_t>(row) * a.segments + i]);
     } else {
         for (;;) {
             float most = -inf;
@@ -1005,31 +1276,60 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     }
 }
 
+template <typename, bool>
+struct SampleTag;
+
+template <typename T>
+cbk_status sample_rows(const SampleArgs &a, uint32_t rows, bool divided, hipStream_t s) {
+    const uint32_t all = rows * a.segments;
+    const dim3 waves((all + kPartWaves - 1) / kPartWaves), block(64 * kPartWaves);
+    if (a.segments && !divided) {
+        hipLaunchKernelGGL((k_sample_parts<T, true>), waves, block, 0, s, a, all);
+        hipLaunchKernelGGL((k_sample_join<T>), dim3(rows), block, 0, s, a);
+        return launched();
+    }
+    if (divided) {
+        if (!allow_lds_once<SampleTag<T, true>>(k_sample<T, true>, sizeof(Shared))) return CBK_E_HIP;
+        // two workgroups a CU: each looks for the row's largest and the cut first, some 5 us
+        const dim3 grid(std::min((a.segments + kWaves - 1) / kWaves, std::max(1u, 512 / rows)), rows);
+        hipLaunchKernelGGL((k_sample_parts<T, false>), waves, block, 0, s, a, all);
+        hipLaunchKernelGGL((k_sample_bins<T>), grid, dim3(kThreads), sizeof(BinsShared), s, a);
+        hipLaunchKernelGGL((k_sample_collect<T>), grid, dim3(kThreads), sizeof(BinsShared), s, a);
+        hipLaunchKernelGGL((k_sample<T, true>), dim3(rows), dim3(kThreads), sizeof(Shared), s, a);
+        return launched();
+    }
+    if (!allow_lds_once<SampleTag<T, false>>(k_sample<T, false>, sizeof(Shared))) return CBK_E_HIP;
+    hipLaunchKernelGGL((k_sample<T, false>), dim3(rows), dim3(kThreads), sizeof(Shared), s, a);
+    return launched();
+}
+
 }  // namespace
 
 cbk_status launch_sample(const cbk_sampling &p, const void *logits, int dtype, uint64_t ld, uint64_t V, uint64_t tokens,
                          const float *uniform, int64_t *token, float *logprob, const SamplePlan &pl, void *ws, hipStream_t s) {
-    SampleArgs a{p, logits, ld, static_cast<uint32_t>(V), uniform, token, logprob};
+    SampleArgs a{};
+    a.p = p;
+    a.logits = logits;
+    a.ld = ld;
+    a.V = static_cast<uint32_t>(V);
+    a.uniform = uniform;
+    a.token = token;
+    a.logprob = logprob;
+    a.segments = pl.segments;
+    if (pl.segments) {
+        const auto at = [&](uint64_t offset) { return static_cast<unsigned char *>(ws) + offset; };
+        a.parts = reinterpret_cast<Part *>(at(0));
+        a.sums = reinterpret_cast<uint64_t *>(at(pl.sums));
+        a.bins = reinterpret_cast<uint64_t *>(at(pl.bins));
+        a.list = reinterpret_cast<uint64_t *>(at(pl.list));
+        a.state = reinterpret_cast<RowState *>(at(pl.state));
+    }
     const bool f32 = dtype == CBK_F32;
-    static_assert(sizeof(Part) == kSamplePartBytes && 256 * kSteps == kSampleSegment, "the plan counts with them");
-    if (!pl.segments && !(f32 ? allow_lds_once<float>(k_sample<float>, sizeof(Shared)) : allow_lds_once<uint16_t>(k_sample<uint16_t>, sizeof(Shared))))
-        return CBK_E_HIP;
+    static_assert(sizeof(Part) == kSamplePartBytes && sizeof(RowState) == kSamplePartBytes && 256 * kSteps == kSampleSegment &&
+                      kBins == kSampleBins && kList == kSampleBins, "the plan counts with them");
     for (uint64_t left = tokens; left > 0;) {
         const uint64_t n = std::min(left, pl.rows);
-        const dim3 grid(static_cast<uint32_t>(n));
-        if (pl.segments) {
-            const uint32_t all = static_cast<uint32_t>(n * pl.segments);
-            const dim3 waves((all + kPartWaves - 1) / kPartWaves), block(64 * kPartWaves);
-            Part *parts = static_cast<Part *>(ws);
-            if (f32) hipLaunchKernelGGL(k_sample_parts<float>, waves, block, 0, s, a, parts, pl.segments, all);
-            else hipLaunchKernelGGL(k_sample_parts<uint16_t>, waves, block, 0, s, a, parts, pl.segments, all);
-            if (f32) hipLaunchKernelGGL(k_sample_join<float>, grid, block, 0, s, a, parts, pl.segments);
-            else hipLaunchKernelGGL(k_sample_join<uint16_t>, grid, block, 0, s, a, parts, pl.segments);
-        } else {
-            if (f32) hipLaunchKernelGGL(k_sample<float>, grid, dim3(kThreads), sizeof(Shared), s, a);
-            else hipLaunchKernelGGL(k_sample<uint16_t>, grid, dim3(kThreads), sizeof(Shared), s, a);
-        }
-        const cbk_status st = launched();
+        const cbk_status st = f32 ? sample_rows<float>(a, static_cast<uint32_t>(n), pl.divided, s) : sample_rows<uint16_t>(a, static_cast<uint32_t>(n), pl.divided, s);
         if (st != CBK_OK) return st;
         left -= n;
         a.logits = static_cast<const unsigned char *>(a.logits) + n * ld * (f32 ? 4 : 2);

@@ -43,7 +43,7 @@ typedef struct {
  *   uniform   device, tokens fp32 in [0, 1), 4-byte aligned.
  *   token     device, tokens int64, 8-byte aligned; logprob  device, tokens fp32, 4-byte aligned, or NULL;
  *             overwritten.
- *   workspace cbk_sample_workspace_bytes(p, V, tokens) bytes (up to 64 MB where p's numbers filter nothing, else 0).
+ *   workspace cbk_sample_workspace_bytes(p, V, tokens) bytes: up to 64 MB, by V and by whether p has filters, 0 for some.
  */
 size_t cbk_sample_workspace_bytes(const cbk_sampling *p, uint64_t V, uint64_t tokens);
 cbk_status cbk_sample(const cbk_sampling *p, const void *logits, int dtype, uint64_t ld, uint64_t V, uint64_t tokens,

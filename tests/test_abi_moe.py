@@ -135,12 +135,14 @@ def test_workspace(cbk):
 
 
 def test_workspace_of_a_draw(cbk):
-    """Only where the numbers filter nothing, in chunks of rows."""
+    """None for short or many rows with filters; without, chunks of rows."""
     size = cbk.sample_workspace_bytes
     assert size(0, 5) == 0 and size(5, 0) == 0 and size(5, (1 << 20) + 1) == 0 and size(1 << 31, 5) == 0
     assert 0 < size(1, 1) < size(2, 1) and size(1, 1 << 20) < 1 << 20 and size(10 ** 6, 50000) == size(10 ** 5, 50000) <= 64 << 20
     for kw in ({"top_k": 5}, {"top_p": 0.9}, {"min_p": 0.1}):
         assert size(4, 100, **kw) == 0
+        assert 32768 < size(1, 100000, **kw) < size(2, 100000, **kw) < size(64, 1 << 20, **kw) < 8 << 20
+        assert size(65, 100000, **kw) == 0
     for kw in ({"top_k": 100}, {"top_k": -1}, {"top_p": float("nan")}, {"min_p": -1.0}, {"min_p": float("nan")}):
         assert size(4, 100, **kw) == size(4, 100)
     c = Calls(cbk)

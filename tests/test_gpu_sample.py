@@ -150,13 +150,14 @@ def test_sample_draws_as_often_as_its_probabilities(env):
     assert bool(((share - torch.softmax(z / 0.7, 0)).abs() <= 1.5 / n).all())  # each interval's ends
 
 
+@pytest.mark.parametrize("V", [60000, 70000])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
-def test_sample_flat_rows(env, dtype):
+def test_sample_flat_rows(env, dtype, V):
     """Large vocabularies of nearly equal logits, whose cut lies among tens of thousands of entries of one bin."""
     torch, cbk = env
     g = torch.Generator().manual_seed(8)
-    z = 1e-3 * torch.randn(3, 60000, generator=g)
-    z[1] = torch.randint(0, 3, (60000,), generator=g) * 2.0 ** -9
+    z = 1e-3 * torch.randn(3, V, generator=g)
+    z[1] = torch.randint(0, 3, (V,), generator=g) * 2.0 ** -9
     z[2, 30000:] += 4.0
     z, u = z.to(getattr(torch, dtype)), torch.rand(3, generator=g)
     for kw in ({"top_p": 0.5}, {"top_k": 30000}, {"top_k": 29999, "top_p": 0.7}, {"top_p": 0.999, "min_p": 0.9}, {"temperature": 1e-3, "top_p": 0.3}):
@@ -205,6 +206,7 @@ def test_sample_in_graphs_on_streams_and_without_logprob(env):
     token = torch.full((T + 2,), 7, dtype=torch.int64, device="cuda")
     need = cbk.sample_workspace_bytes(T, V)
     whole = torch.empty(512 + need + 512, dtype=torch.uint8, device="cuda")
+    assert cbk.sample_workspace_bytes(T, V, top_k=50) == 0
     for p, ws, n, expect in ((cbk._Sampling(1.0, 1.0, 0.0, 0), whole[512:].data_ptr(), need, want[0]),
                              (cbk._Sampling(1.0, 1.0, 0.0, 50), None, 0, cbk.sample(Z, U, top_k=50)[0])):
         whole.fill_(0x7F)
@@ -257,3 +259,68 @@ def test_sample_without_filters_by_numbers_and_by_vectors(env, V, dtype):
             assert bool(((logprob - close).abs()[ok] <= 2.0 ** -23 * logprob.abs()[ok] + 1e-11).all()), heat
     for heat in (1.0, 0.0, inf):
         check(torch, cbk, z, u, heat, temperature=heat)
+
+
+def test_sample_long_rows_with_filters(env):
+    """Rows whose filters' work is divided: replayed with new inputs, on another stream beside pending work, with a workspace
+    whose contents and surroundings do not matter; against the reference."""
+    torch, cbk = env
+    T, V = 61, 70001
+    Z, U = torch.empty(T, V, dtype=torch.bfloat16, device="cuda"), torch.empty(T, device="cuda")
+    g = torch.Generator().manual_seed(31)
+    pick = lambda *values: torch.tensor(values)[torch.randint(0, len(values), (T,), generator=g)]
+    kw = {"temperature": pick(0.0, 0.7, 1.0, 1.5), "top_k": pick(0, 1, 40, 1500, 4000, 9000).int(), "top_p": pick(1.0, 0.3, 0.95), "min_p": pick(0.0, 0.0, 0.05)}
+    device = {n: v.cuda() for n, v in kw.items()}
+    need = cbk.sample_workspace_bytes(T, V, **{n: device[n] for n in ("top_k", "top_p", "min_p")})
+    assert need > 0
+    whole = torch.empty(512 + need + 512, dtype=torch.uint8, device="cuda")
+    graph, big, s = torch.cuda.CUDAGraph(), torch.ones(1 << 28, device="cuda"), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        outs = cbk.sample(Z, U, **device)
+    for i in range(3):
+        z, u = draws(torch, T, V, torch.bfloat16, 32 + i)
+        Z.copy_(z)
+        U.copy_(u)
+        graph.replay()
+        whole.fill_((0xFF, 0x00, 0x7F)[i])
+        want = cbk.sample(Z, U, workspace=whole[512: 512 + need], **device)
+        assert bool((whole[:512] == whole[0]).all()) and bool((whole[512 + need:] == whole[0]).all())
+        for _ in range(10):
+            big.mul_(1.0)
+        side = cbk.sample(Z, U, stream=s, **device)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(outs, want, side)), i
+    with pytest.raises(cbk.CbkError):
+        cbk.sample(Z, U, workspace=whole[512: 512 + need - 1], **device)
+    check(torch, cbk, z[:40], u[:40], **{n: v[:40].tolist() for n, v in kw.items()})
+    # one workgroup a row, where there are more of them
+    twice = [torch.cat([v, v]).cuda() for v in (z, u)]
+    assert cbk.sample_workspace_bytes(2 * T, V, top_k=device["top_k"]) == 0
+    token, logprob = cbk.sample(*twice, **{n: torch.cat([v, v]) for n, v in device.items()})
+    assert torch.equal(token[:T], want[0]) and torch.equal(token[T:], want[0])
+    a, b = logprob[:T], want[1]  # each formed in 64 bits and rounded once
+    assert bool(((a - b).abs() <= 2.0 ** -23 * b.abs() + 1e-11).all())
+
+
+def test_sample_long_rows_of_extremes(env):
+    torch, cbk = env
+    low, inf, V = torch.finfo(torch.float32).min, math.inf, 66001
+    z = 2.5 * torch.randn(12, V, generator=torch.Generator().manual_seed(41))
+    z[0] = -inf
+    z[1] = -inf
+    z[1, V - 1] = 3.0
+    z[2] = low
+    z[3, 10:] = low
+    z[4, 7] = math.nan
+    z[5, 3] = inf
+    z[6, 5:66000:2] = inf
+    z[7] *= 1e4
+    z[8] *= 1e-30
+    z[9, 65536:] = 90.0
+    z[10, 50:] = -inf
+    u = torch.rand(12, generator=torch.Generator().manual_seed(42))
+    u[11] = 1.0
+    for kw in ({"temperature": 0.0, "top_k": 3}, {"top_k": 5}, {"top_p": 0.5}, {"min_p": 0.1}, {"temperature": 1e-20, "top_p": 0.9},
+               {"temperature": inf, "top_p": 0.4}, {"temperature": math.nan, "top_p": 0.4}, {"top_k": 2000, "top_p": 0.99, "min_p": 1e-8},
+               {"top_p": 0.0}, {"top_k": 65999, "top_p": 0.6}, {"min_p": 0.3, "top_p": 0.6}, {"top_k": 1500, "min_p": 0.7}, {"min_p": 5.0}):
+        check(torch, cbk, z, u, str(kw), **kw)
