@@ -520,3 +520,75 @@ def test_a_step_from_the_router_to_the_token_and_back(env, T):
     ref.assert_within(dz, rz, ref.rounded(rz, bz), "dlogits")
     ref.assert_within(dxr, *ref.linear_dx(dz.cpu(), wr), "router's dX")
     assert torch.equal(x.grad, dxe + dxr)
+
+
+def test_rows_past_4_gb(env):
+    """Rows that lie more than 2^32 bytes apart, of inputs and outputs, give what they give side by side."""
+    torch, cbk = env
+    T, ld = 2200, 1 << 20
+    b = Block(torch, cbk, 3, 64, 96, 40, [900])
+    big = [torch.zeros(T, ld, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    x, dy, z = acts(torch, T, 96, 471).cuda(), acts(torch, T, 40, 472, 0.1).cuda(), acts(torch, T, 3, 473).cuda()
+    X, dY, Z, Y, dX, dZ = big[0][:, 8:104], big[0][:, 1000:1040], big[0][:, 2000:2003], big[1][:, 16:56], big[1][:, 101:197], big[1][:, 300:303]
+    X.copy_(x), dY.copy_(dy), Z.copy_(z)
+    e, w = cbk.route(z, 2)
+    same(torch, cbk.route(Z, 2), (e, w))
+    y = cbk.ffn_experts(b.ex, x, e, w)
+    dx, dw = cbk.ffn_experts_bwd(b.ex, x, e, w, dy)
+    cbk.ffn_experts(b.ex, X, e, w, out=Y)
+    dW = cbk.ffn_experts_bwd(b.ex, X, e, w, dY, dX=dX)[1]
+    cbk.route_bwd(Z, e, dw, out=dZ)
+    same(torch, [Y, dX, dW, dZ], [y, dx, dw, cbk.route_bwd(z, e, dw)])
+    big[1][:, 16:56], big[1][:, 101:197], big[1][:, 300:303] = 0, 0, 0
+    assert not bool(big[1].any())
+    # drawing: short rows far apart, and long ones
+    u = torch.rand(T, generator=torch.Generator().manual_seed(474)).cuda()
+    for kw in ({}, {"top_k": 2}):
+        got, want = cbk.sample(Z, u, **kw), cbk.sample(z, u, **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    big[0].normal_(generator=torch.Generator(device="cuda").manual_seed(475))
+    at = torch.tensor([0, 1, 2047, 2048, 2049, T - 1], device="cuda")
+    for kw in ({}, {"top_k": 40}, {"top_p": 0.01}):
+        got, want = cbk.sample(big[0], u, **kw), cbk.sample(big[0][at], u[at], **kw)
+        assert torch.equal(got[0][at], want[0])
+        assert bool(((got[1][at] - want[1]).abs() <= 2.0 ** -23 * want[1].abs() + 1e-11).all())  # (long rows' work may be divided)
+
+
+@pytest.mark.parametrize("T", [1, 12, 40, 70])
+def test_tensors_past_4_gb(env, T):
+    """Experts whose index streams are longer than 2^32 bytes, against the block and the products of one such tensor."""
+    torch, cbk = env
+    rows, cols, out, b = 1 << 20, 2752, 48, 13
+    g = torch.Generator(device="cuda").manual_seed(481)
+    codebook = (0.02 * torch.randn(1 << b, generator=torch.Generator().manual_seed(482))).bfloat16().view(torch.int16).cuda()
+
+    def tensor(r, c):
+        words = torch.empty(cbk.words_for(r * c, b), dtype=torch.int32, device="cuda")
+        words.view(torch.uint8).random_(0, 256, generator=g)
+        return cbk.Compressed(r, c, 1 << b, b, codebook, words)
+
+    gate, up, down = tensor(rows, cols), tensor(rows, cols), tensor(out, rows)
+    assert gate.words.numel() * 4 > 1 << 32
+    ex = cbk.Experts([gate, up], [up, gate], [down, down])
+    x, dy = acts(torch, T, cols, 483).cuda(), acts(torch, T, out, 484, 0.1).cuda()
+    e = (torch.arange(T) % 2)[:, None].int().cuda()
+    w = torch.full((T, 1), 0.5, device="cuda")
+    y = cbk.ffn_experts(ex, x, e, w)
+    dx, dw = cbk.ffn_experts_bwd(ex, x, e, w, dy)
+    wd = cbk.decode_bf16(down).float()
+    for i, (a, c) in enumerate(((gate, up), (up, gate))):
+        part = slice(i, None, 2)
+        if T <= i:
+            continue
+        h = cbk.ffn_gated(a, c, x[part].contiguous())
+        want = 0.5 * (h.float() @ wd.T)
+        # both round H, whose fp32 sums may differ, to BF16, at most a step apart; the weights' signs are random, so that the
+        # differences add up to 8 times the root of the sum of their squares hardly ever; Y is rounded once
+        off = 8 * 2.0 ** -7 * torch.sqrt((0.5 * h.float()) ** 2 @ (wd ** 2).T) + 2.0 ** -8 * want.abs()
+        assert bool(((y[part].float() - want).abs() <= off).all()) and float(want.abs().mean()) > 4 * float(off.mean())
+        dh = (0.5 * (dy[part].float() @ wd)).bfloat16()  # (the experts' is not rounded)
+        dX, dG, dU = cbk.ffn_gated_bwd(a, c, x[part].contiguous(), dh)
+        # dG and dU differ by dH's rounding, their own, and their factors' sums: by two steps at most; a weight is some 0.02
+        size = 0.02 * torch.sqrt((dG.float() ** 2).sum(1) + (dU.float() ** 2).sum(1))[:, None]
+        assert bool(((dx[part].float() - dX.float()).abs() <= 8 * 2.0 ** -6 * size + 2.0 ** -7 * dX.float().abs()).all())
+        assert float(dX.float().abs().mean()) > 0.3 * float(size.mean())
