@@ -45,24 +45,23 @@ __device__ __forceinline__ double logistic(double z) {
 }
 
 template <int CTRL, int ROWS>
-__device__ __forceinline__ uint64_t dpp_max(uint64_t v) {
-    const uint32_t lo = static_cast<uint32_t>(v), hi = static_cast<uint32_t>(v >> 32);
-    const uint32_t ol = __builtin_amdgcn_update_dpp(lo, lo, CTRL, ROWS, 0xF, false);
-    const uint32_t oh = __builtin_amdgcn_update_dpp(hi, hi, CTRL, ROWS, 0xF, false);
-    const uint64_t o = (static_cast<uint64_t>(oh) << 32) | ol;
-    return o > v ? o : v;
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(v), static_cast<int>(v), CTRL, ROWS, 0xF, false)));
 }
 // The largest of the 64 lanes' v, in every lane.
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     v = dpp_max<0x111, 0xF>(v);
     v = dpp_max<0x112, 0xF>(v);
     v = dpp_max<0x114, 0xF>(v);
     v = dpp_max<0x118, 0xF>(v);
     v = dpp_max<0x142, 0xA>(v);
     v = dpp_max<0x143, 0xC>(v);
-    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v)), 63);
-    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v >> 32)), 63);
-    return (static_cast<uint64_t>(hi) << 32) | lo;
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+// (by halves, which takes half the instructions of comparing 64 bits)
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+    const uint32_t mine = static_cast<uint32_t>(v >> 32), hi = wave_max(mine);
+    return (static_cast<uint64_t>(hi) << 32) | wave_max(mine == hi ? static_cast<uint32_t>(v) : 0u);
 }
 __device__ __forceinline__ uint64_t shuffle_xor(uint64_t v, int o) {
     const uint32_t lo = __shfl_xor(static_cast<uint32_t>(v), o, 64), hi = __shfl_xor(static_cast<uint32_t>(v >> 32), o, 64);
@@ -157,11 +156,14 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
         uint64_t marks[NPL];
         // the best two of a group by `share` neighbouring lanes, a power of two of them, with every share-th of its experts
         // each; then joined (8 groups of 32: a quarter of a lane's steps through LDS)
-        uint32_t share = 1;
-        while (2 * share * a.r.groups <= 64) share *= 2;
+        uint32_t shift = 0;
+        while ((a.r.groups << (shift + 1)) <= 64) ++shift;
+        const uint32_t share = 1u << shift;
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            const uint32_t g = (j * 64 + lane) / share, part = lane & (share - 1);
+            marks[j] = 0;
+            if (static_cast<uint32_t>(j * 64) >> shift >= a.r.groups) continue;
+            const uint32_t g = (j * 64 + lane) >> shift, part = lane & (share - 1);
             uint64_t first = 0, second = 0;
             if (g < a.r.groups)
                 for (uint32_t i = part; i < size; i += share) {
@@ -205,16 +207,17 @@ __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
                     found = true;
                     if (lane == static_cast<uint32_t>(__ffsll(static_cast<unsigned long long>(has)) - 1)) {
                         marks[j] = 0;
-                        mine[(j * 64 + lane) / share] = 1;
+                        mine[(j * 64 + lane) >> shift] = 1;
                     }
                 }
             }
         }
         asm volatile("" ::: "memory");
+        const uint32_t inverse = ((1u << 20) + size - 1) / size;  // e / size of e < 1024: e (size - 1) < 2^20
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
             const uint32_t e = j * 64 + lane;
-            if (e < E && mine[e / size] == 0) key[j] = 0;
+            if (e < E && mine[(e * inverse) >> 20] == 0) key[j] = 0;
         }
     }
 
