@@ -351,6 +351,7 @@ struct Settings {
     __device__ __forceinline__ float border(float top) const {
         if (!(min_p > 0.f)) return -__builtin_inff();
         if (top == __builtin_inff()) return top;
+        if (heat == __builtin_inff()) return -__builtin_inff();  // all are as likely (and log(1) times it is a NaN)
         const double edge = __builtin_fma(static_cast<double>(heat), log(static_cast<double>(min_p)), static_cast<double>(top));
         float least = static_cast<float>(edge);
         if (static_cast<double>(least) < edge) least = from_ascending(ascending(least) + 1);
