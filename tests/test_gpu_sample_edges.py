@@ -29,3 +29,19 @@ def test_an_infinite_temperature_keeps_what_is_as_likely(env, dtype, V):
     z[2, : V // 2] = math.inf  # these alone count
     for kw in ({"min_p": 1.0}, {"min_p": 0.5}, {"min_p": 7.0}, {"min_p": 1.0, "top_k": 40}, {"min_p": 1.0, "top_p": 0.3}, {"min_p": 1.0, "top_k": 2500}):
         check(torch, cbk, z, u, str(kw), temperature=math.inf, **kw)
+
+
+@pytest.mark.parametrize("V", [300, 5000, 66001])
+@pytest.mark.parametrize("temperature", [1e-29, 1e-30, 3e-38, 7e-45])
+def test_the_least_temperatures(env, temperature, V):
+    """Logits that lie within some hundred temperatures of each other, down to where both are subnormal numbers."""
+    torch, cbk = env
+    g = torch.Generator().manual_seed(52)
+    z = (2.5 * temperature * torch.randn(6, V, generator=g, dtype=torch.float64)).float()
+    z[1] = 0.0
+    z[2, ::2] = -1.0  # far away, like all that differ by more than their roundings
+    z[3, 5:] = -math.inf
+    u = torch.rand(6, generator=g)
+    for kw in ({"top_p": 0.9}, {"top_p": 0.3}, {"top_k": 20}, {"top_k": 20, "top_p": 0.8}, {"min_p": 0.1}, {"min_p": 0.02, "top_p": 0.95}, {}):
+        check(torch, cbk, z, u, str(kw), temperature=temperature, **kw)
+    check(torch, cbk, z, u, "rows", temperature=[temperature, 1.0] * 3, top_p=[0.9, 0.5, 0.2] * 2)
