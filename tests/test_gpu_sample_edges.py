@@ -45,3 +45,48 @@ def test_the_least_temperatures(env, temperature, V):
     for kw in ({"top_p": 0.9}, {"top_p": 0.3}, {"top_k": 20}, {"top_k": 20, "top_p": 0.8}, {"min_p": 0.1}, {"min_p": 0.02, "top_p": 0.95}, {}):
         check(torch, cbk, z, u, str(kw), temperature=temperature, **kw)
     check(torch, cbk, z, u, "rows", temperature=[temperature, 1.0] * 3, top_p=[0.9, 0.5, 0.2] * 2)
+
+
+def low_start(torch, T, V, mask, seed):
+    """Rows whose first 4096 entries are masked by a finite number; of the others some are allowed."""
+    g = torch.Generator().manual_seed(seed)
+    z = 2.5 * torch.randn(T, V, generator=g)
+    z[:, :4096] = mask
+    z[1::2, 4096:-20] = mask  # 20 allowed entries
+    return z, torch.rand(T, generator=g)
+
+
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -3.4028234663852886e38])
+@pytest.mark.parametrize("T,V", [(4, 40000), (66, 70000)])
+def test_masked_first_entries(env, T, V, mask):
+    torch, cbk = env
+    z, u = low_start(torch, 4, V, mask, 53)
+    for kw in ({"top_k": 50}, {"top_k": 3000}, {"top_k": 50, "top_p": 0.9}, {"top_k": 3000, "top_p": 0.9}, {"top_k": 50, "min_p": 0.05}, {"top_p": 0.9}):
+        check(torch, cbk, z.repeat((T + 3) // 4, 1)[:T] if kw == {"top_k": 50} else z, (u.repeat((T + 3) // 4))[:T] if kw == {"top_k": 50} else u, str(kw), **kw)
+
+
+@pytest.mark.parametrize("kw", [{"top_k": 50}, {"top_k": 3000}, {"top_k": 50, "top_p": 0.9}])
+def test_masked_first_entries_take_a_pass_more(env, kw):
+    """A reference that is too low costs another pass over the row (in which much is added to one bin), not one for each of a
+    key's 64 bits: less than 20 passes, where a row with nothing masked takes two."""
+    torch, cbk = env
+    T, V = 66, 70000
+    z, u = low_start(torch, T, V, -1e9, 54)
+    plain, _ = draws(torch, T, V, torch.float32, 55)
+    z, plain, u = z.cuda(), plain.cuda(), u.cuda()
+
+    def us(x):
+        for _ in range(3):
+            cbk.sample(x, u, **kw)
+        times = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            cbk.sample(x, u, **kw)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 1e3)
+        return min(times)
+
+    ordinary, masked = us(plain), us(z)
+    assert masked < 10 * ordinary, (ordinary, masked)
