@@ -799,6 +799,8 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
     const bool by_count = st.by_count, by_mass = st.by_mass;
     const float u = a.uniform[row];
     const double share = share_of(u);
+    // the first or the last kept entry is drawn, however little it weighs: fixed-point sums would not show it
+    const bool at_end = !(share > 0.0 && share < static_cast<double>(inf));
     if (heat != heat) return nothing();
     const Part *parts = a.parts + (divided ? static_cast<uint64_t>(row) * a.segments : 0);
     float row_top = -inf;
@@ -1181,7 +1183,8 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
             border();  // (after the cut by count, which does not know of it, unless it was known before)
             const float floor = least;
             if (!known) least = -inf;
-            if (keep < entries && limit < kBins - 1) cut_bin(limit, keep - earlier, static_cast<double>(inf), false, false);
+            // (what is left out of the last bin weighs nothing, and shows at the ends alone)
+            if (keep < entries && (limit < kBins - 1 || at_end)) cut_bin(limit, keep - earlier, static_cast<double>(inf), false, false);
             least = floor;
         }
         known = true;
@@ -1235,7 +1238,7 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
         sc.masses(z, kept, base, m);
     };
     __syncthreads();
-    if (have) {
+    if (have && !at_end) {
         for (uint32_t i = tid; i < segments; i += kThreads) sh.segment[i] = static_cast<double>(sh.fixed_segment[i]) * (1.0 / fine);
     } else if (divided && !by_count && !by_mass) {
         for (uint32_t i = tid; i < segments; i += kThreads) sh.segment[i] = __builtin_bit_cast(double, a.sums[static_cast<uint64_t>(row) * a.segments + i]);

@@ -90,3 +90,35 @@ def test_masked_first_entries_take_a_pass_more(env, kw):
 
     ordinary, masked = us(plain), us(z)
     assert masked < 10 * ordinary, (ordinary, masked)
+
+
+def ends(torch, z, top_k, top_p=1.0):
+    """The first and the last kept entry of a row by index, and their logprobs, as the header words them (the reference's
+    running sum may seem to pass the whole one by what rounding leaves)."""
+    order = sorted(range(len(z)), key=lambda i: (-z[i], i))[:top_k]
+    p = [math.exp(z[i] - z[order[0]]) for i in order]
+    n = len(p) if top_p >= 1 else next(n for n in range(1, len(p) + 1) if math.fsum(p[:n]) >= top_p * math.fsum(p))
+    whole = math.log(math.fsum(p[:n]))
+    return [(i, z[i] - z[order[0]] - whole) for i in (min(order[:n]), max(order[:n]))]
+
+
+@pytest.mark.parametrize("T,V", [(3, 3000), (3, 9000), (3, 70000), (66, 70000)])
+@pytest.mark.parametrize("low,spread", [(-200.0, 0.0), (-60.0, 2.5), (-30.0, 1.0)])
+def test_a_uniform_number_at_and_past_its_ends(env, T, V, low, spread):
+    """Twelve entries, and the rest far below them, of which top_k keeps a few: numbers up to 0 draw the first kept entry, those
+    from 1 on the last, also where they weigh nothing beside the others, and never one that is left out."""
+    torch, cbk = env
+    g = torch.Generator().manual_seed(56)
+    z = low + spread * torch.randn(3, V, generator=g)
+    z[:, 1100:1112] = torch.randn(3, 12, generator=g)
+    z[1, ::2] -= 100.0
+    many = lambda v: v.repeat((T + 2) // 3, 1)[:T]
+    for kw in ({"top_k": 20}, {"top_k": 1000}, {"top_k": 2000}, {"top_k": 13, "top_p": 0.9}, {"top_k": 2900}):
+        want = [ends(torch, row, **kw) for row in z.tolist()]
+        for v in (0.0, -1.0, math.nan, 1.0, 3.0):
+            token, logprob = cbk.sample(many(z).cuda(), torch.full((T,), v, device="cuda"), **kw)
+            for t in range(T):
+                i, log = want[t % 3][1 if v >= 1 else 0]
+                assert int(token[t]) == i, (kw, v, t, int(token[t]), i)
+                assert abs(float(logprob[t]) - log) <= 2.0 ** -24 * abs(log) + 1e-11
+        check(torch, cbk, z, torch.tensor([0.5, 0.01, 1.0 - 2.0 ** -24]), str(kw), **kw)
