@@ -100,7 +100,7 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
     // a chunk's rows of X and dY lie within 31 bits of bytes (their padded copies do)
     const uint64_t most = std::max<uint64_t>(1, std::min<uint64_t>({kSlots / k, kSlotBytes / (per_slot * k), (uint64_t(1) << 29) / std::max(p.Kp, p.Op)}));
     p.Tc = std::min(tokens, most);
-    const uint64_t slots = p.Tc * k, active = std::min<uint64_t>(ex.count, slots);
+    uint64_t slots = p.Tc * k, active = std::min<uint64_t>(ex.count, slots);
     // Slots of a token tile, by how many there are for an expert that has any.  32 experts of 2048 x 4096, 4 a token, us with
     // tiles of 16, 64 and 256 (k_experts_few, k_experts, k_experts_many; the backward pass' gradients by k_experts where
     // tiles are not of 256): 32 tokens forward 292, 403, 341, backward 478, 563, 590; 64 tokens 336, 409, 345 and 529, 572, 598;
@@ -109,6 +109,15 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
     const uint64_t per = slots / active;
     const bool large = ex.b <= 13 && ex.b_down <= 14;
     p.tile = per <= 8 ? 16 : large && per > (backward ? 24 : 8) ? 256 : 64;
+    // A launch has fewer than 2^32 threads, 512 for each tile of the result.  Hundreds of experts in use, of 2^19 hidden columns
+    // and more, have more tiles of 16 slots x 64 of them (other products' results take a chunk's bytes long before that, and
+    // tiles of more slots are fewer): such a chunk is cut down, to 7 tokens or more, which have tiles of 16 again.
+    constexpr uint64_t kMostTiles = (uint64_t(1) << 23) - 8;
+    if (p.tile == 16 && (active + slots / 16) * (p.Fp / 64) > kMostTiles) {
+        p.Tc = kMostTiles / (p.Fp / 64) * 16 / 17 / k;
+        slots = p.Tc * k;
+        active = std::min<uint64_t>(ex.count, slots);
+    }
     p.max_tiles = static_cast<uint32_t>(active + slots / p.tile);
     p.one = !backward && tokens == 1 && p.tile == 16 && ex.b <= 13 && ex.b_down <= 14;  // where k_experts_few does both products
     if (p.one) p.max_tiles = k;

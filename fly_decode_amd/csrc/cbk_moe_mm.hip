@@ -957,7 +957,6 @@ __global__ __launch_bounds__(512) void k_experts_many(const ExArgs p) {
     }
 }
 
-constexpr uint64_t kMostUnits = (uint64_t(1) << 23) - 8;  // a launch has fewer than 2^32 threads, 512 a unit
 uint32_t tiles_of(uint64_t n, uint64_t m) { return static_cast<uint32_t>((n + m - 1) / m); }
 
 template <bool, bool, bool, int, bool>
@@ -968,9 +967,8 @@ cbk_status run(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s) {
     a.col_tiles = tiles_of(columns, EPI == kSum ? kColumns : kColumns / 2);
     const uint32_t lds = (GT ? 0 : (PAIR ? 2 : 1) * a.table) + 2 * kSliceBytes;
     if (!allow_lds_once<ExTag<false, NN, PAIR, EPI, GT>>(k_experts<NN, PAIR, EPI, GT>, kLdsLimit)) return CBK_E_HIP;
-    const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles * a.splits;
-    if (units > kMostUnits) return CBK_E_UNSUPPORTED;
-    hipLaunchKernelGGL((k_experts<NN, PAIR, EPI, GT>), dim3(static_cast<uint32_t>((units + 7) / 8 * 8)), dim3(512), lds, s, a);
+    const uint32_t units = pl.max_tiles * a.col_tiles * a.splits;  // (fewer than 2^23: ex_plan)
+    hipLaunchKernelGGL((k_experts<NN, PAIR, EPI, GT>), dim3((units + 7) / 8 * 8), dim3(512), lds, s, a);
     return launched();
 }
 
@@ -982,9 +980,8 @@ cbk_status run_many(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s
     const uint32_t lds = many_lds(a.table, !NN && PAIR);
     if (lds > kLdsLimit) return CBK_E_UNSUPPORTED;  // the plan rules it out
     if (!allow_lds_once<ExTag<true, NN, PAIR, EPI, false>>(k_experts_many<NN, PAIR, EPI>, kLdsLimit)) return CBK_E_HIP;
-    const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles * a.splits;
-    if (units > kMostUnits) return CBK_E_UNSUPPORTED;
-    hipLaunchKernelGGL((k_experts_many<NN, PAIR, EPI>), dim3(static_cast<uint32_t>(units)), dim3(512), lds, s, a);
+    const uint32_t units = pl.max_tiles * a.col_tiles * a.splits;
+    hipLaunchKernelGGL((k_experts_many<NN, PAIR, EPI>), dim3(units), dim3(512), lds, s, a);
     return launched();
 }
 
@@ -995,11 +992,10 @@ template <bool PAIR, int EPI, bool ONE>
 cbk_status run_few(ExArgs &a, const ExPlan &pl, uint32_t columns, hipStream_t s) {
     a.splits = 1;
     a.col_tiles = tiles_of(columns, PAIR ? 16 : 32);
-    const uint64_t units = static_cast<uint64_t>(pl.max_tiles) * a.col_tiles;
-    if (units > kMostUnits) return CBK_E_UNSUPPORTED;
+    const uint32_t units = pl.max_tiles * a.col_tiles;  // (below 2^26)
     if (!allow_lds_once<FewTag<PAIR, EPI, ONE>>(k_experts_few<PAIR, EPI, ONE>, kLdsLimit)) return CBK_E_HIP;
     // a workgroup has a CU's LDS
-    const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(units, cu_count()));
+    const uint32_t grid = std::min<uint32_t>(units, cu_count());
     hipLaunchKernelGGL((k_experts_few<PAIR, EPI, ONE>), dim3(grid), dim3(512), few_lds((PAIR ? 2 : 1) * a.table), s, a);
     return launched();
 }

@@ -108,8 +108,7 @@ cbk_status cbk_experts_init(const cbk_tensor *gate, const cbk_tensor *up, const 
  *   dX       device, [tokens][lddx] BF16, lddx >= cols; overwritten.
  *   dweights device, [tokens][k] fp32, 4-byte aligned; overwritten; NULL where it is not wanted.
  * Both run on the device that `ex` was made on (CBK_E_INVALID where another is current), with
- * cbk_experts_workspace_bytes(ex, tokens, k, backward) bytes of workspace.  CBK_E_UNSUPPORTED where hundreds
- * of experts in use are so wide that a product has 2^23 tiles of some 64 tokens x 128 columns.
+ * cbk_experts_workspace_bytes(ex, tokens, k, backward) bytes of workspace.
  */
 size_t cbk_experts_workspace_bytes(const cbk_experts *ex, uint64_t tokens, uint32_t k, int backward);
 cbk_status cbk_ffn_experts(const cbk_experts *ex, int act, const uint16_t *X, uint64_t ldx, uint64_t tokens,
