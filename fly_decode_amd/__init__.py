@@ -994,7 +994,8 @@ def route_bwd(logits, experts, dweights, score: str = "softmax", renormalise: bo
 class Experts:
     """The experts of a layer: lists of device ``Compressed`` tensors, gate and up [rows][cols] and down [out][rows], of
     one shape each (their codebooks and widths may differ).  Holds a table of them in device memory, made here (not
-    inside a graph's capture), and references to them."""
+    inside a graph's capture), and references to them and their arrays: a ``Compressed`` that gets other ones later does
+    not change the table."""
 
     def __init__(self, gates, ups, downs):
         import torch
@@ -1006,6 +1007,7 @@ class Experts:
         self.device = kinds[0][0].words.device
         if self.device.type != "cuda":
             raise ValueError("the experts' tensors must be on a GPU")
+        self._arrays = [(t.codebook, t.words) for ts in kinds for t in ts]
         for t in (t for ts in kinds for t in ts):
             if t.words.device != self.device or t.codebook.device != self.device:
                 raise ValueError("the experts' tensors are on different devices")
