@@ -87,10 +87,10 @@ __device__ __forceinline__ float wave_top(float v) {
 // order is that of the logits, whose keys are exact; with them (WIDE) scores are formed and compared in fp64, where
 // rounding does not decide between two that an fp32 sum could not tell apart.  Weights take an fp64 exponential for
 // each chosen expert (and each expert, for a softmax that is not renormalised), which nothing waits for.
-// What bounds it is a wave's instructions, not memory: 4096 tokens of 256 experts in 8 groups, 8 chosen, take 12.4 us
-// (0.36 TB/s; 17.4 with a group's best two found by one lane each, and 14.6 with 64-bit maxima and divisions by the
-// groups' sizes), one token of 64 experts 3.8, a launch's time.  A wave a token: with more lanes than 64 a maximum would
-// have to go through LDS.
+// What bounds it is a wave's instructions, not memory: 4096 tokens of 256 experts in 8 groups, 8 chosen, take 12.3 us
+// among other calls, 12.7 to 13.5 in a graph of them, by what they hold (0.36 TB/s; among other calls 17.4 with a group's
+// best two found by one lane each, and 14.6 with 64-bit maxima and divisions by the groups' sizes), one token of 64 experts
+// 3.8, a launch's time.  A wave a token: with more lanes than 64 a maximum would have to go through LDS.
 template <typename T, int NPL, bool WIDE>
 __global__ __launch_bounds__(256) void k_route(const RouteArgs a) {
     extern __shared__ uint64_t keys_lds[];  // groups only: a wave's keys

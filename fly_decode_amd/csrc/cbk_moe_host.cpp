@@ -63,7 +63,8 @@ cbk_status check_workspace(const void *ws, size_t bytes, uint64_t need) {
 // Filters, or vectors of them: three kernels that share a few long rows' passes, and k_sample, which otherwise does all of a
 // row.  With top_k = 50 and with top_p = 0.9: 1 row of 32000 24, 50 and 28, 42; of 65000 33, 74 and 30, 42; of 128000 48,
 // 124 and 30, 46; 64 of 65000 35, 76 and 37, 52; of 128000 52, 126 and 49, 74; 192 of 128000 55, 128 and 85, 146 (the row's
-// cut is looked for by each of its workgroups).  A launch has fewer than 2^32 threads.
+// cut is looked for by each of its workgroups).  The rule goes by the rows' length and number alone, also where the call's
+// numbers say which filters there are.  A launch has fewer than 2^32 threads.
 cbk::SamplePlan sample_plan(const cbk_sampling &p, uint64_t V, uint64_t tokens) {
     const bool filters = p.top_ks || p.top_ps || p.min_ps || (p.top_k > 0 && static_cast<uint64_t>(p.top_k) < V) || p.top_p < 1.f || p.min_p > 0.f;
     cbk::SamplePlan pl{uint64_t(1) << 21, 0, 0, false, 0, 0, 0, 0};
@@ -105,7 +106,9 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
     // tiles of 16, 64 and 256 (k_experts_few, k_experts, k_experts_many; the backward pass' gradients by k_experts where
     // tiles are not of 256): 32 tokens forward 292, 403, 341, backward 478, 563, 590; 64 tokens 336, 409, 345 and 529, 572, 598;
     // 96 tokens 418, 413, 349 and 676, 577, 597; 192 tokens 615, 439, 361 and 957, 608, 612; 256 tokens 791, 538, 385
-    // and 1221, 765, 645.  Tiles of 256 need the LDS to hold two tables of gate and up, or one of down, beside their blocks.
+    // and 1221, 765, 645.  (It was measured on that layer alone, and does not ask how many workgroups a size leaves: narrow layers
+    // of few experts may have fewer of 256 than there are CUs.)  Tiles of 256 need the LDS to hold two tables of gate and up, or
+    // one of down, beside their blocks.
     const uint64_t per = slots / active;
     const bool large = ex.b <= 13 && ex.b_down <= 14;
     p.tile = per <= 8 ? 16 : large && per > (backward ? 24 : 8) ? 256 : 64;

@@ -696,9 +696,9 @@ __global__ __launch_bounds__(512) void k_experts_few(const ExArgs p) {
 // multiplications.  Memory answers in order, so words asked for right before their use wait for the tokens too: with words
 // a half ahead in slices of 32 terms of all rows (which fell out of the L1 between two slices), and the tokens' fragments
 // read from the caches by each wave, gate and up of 2048 tokens of 4 out of 32 experts of 2048 x 4096 and back took 1254 us,
-// so 690.  What bounds it is the LDS, busy for 62 % of the time: a gather's 64 addresses meet in banks, ~5 clocks over
-// the 2 it needs.  Without gathers gate and up would take 433 us instead of 447, without scattered words 406, with neither
-// 337; the matrix instructions keep their units busy for 36 %.
+// so 690 (672 to 785 by how many token tiles the routing leaves, 46 to 50).  What bounds it is the LDS, busy for 62 % of the
+// time: a gather's 64 addresses meet in banks, ~5 clocks over the 2 it needs.  Without gathers gate and up would take 433 us
+// instead of 447, without scattered words 406, with neither 337; the matrix instructions keep their units busy for 36 %.
 constexpr uint32_t kManyColumns = 256, kManyTokens = 256, kManyBlock = 64;
 constexpr uint32_t kManyBytes = kManyColumns * kManyBlock * 2;  // of a block of weights
 constexpr uint32_t kManyTokenBytes = kManyTokens * kManyBlock * 2;

@@ -13,15 +13,16 @@
 // A row of 10^5 logits is read from memory or the last cache each time, so k_sample's passes over it are few.  No pass
 // looks for the maximum first: bins and exponentials are relative to the largest of the first 4096 logits.
 //   temperature alone: one pass, a sum of exponentials of each 1024 entries;
-//   top_k (up to some 1500): one that counts, and one that collects the entries up to the cut's bin; all
-//     other filters and the draw are then done on that list;
+//   top_k (up to some 1500): one that counts (two where the first logits are far below the others), and one that collects the
+//     entries up to the cut's bin; all other filters and the draw are then done on that list;
 //   top_p: one that adds up the bins, and one that collects the cut's bin and adds up what stands before it;
 //   min_p without top_k: one for the maximum before those.
 // The draw takes the sums of each 1024 entries in index order, then the 1024 that the target falls into.
 //
-// 192 rows of 128000 fp32 logits take 21 us greedy (4.7 TB/s: memory), 42 by temperature alone, 52 with top_k = 50, 124
+// 192 rows of 128000 fp32 logits take 21 us greedy (4.7 TB/s: memory), 43 by temperature alone, 52 with top_k = 50, 126
 // with top_p = 0.9.  Past the first reading the vector units bound it: some 60 instructions an entry for the bins' masses.
-// One row of 128000 takes 12, 12, 30 and 46, what four dependent launches take; one of 32000 with all filters 25.
+// One row of 128000 takes 12, 15, 28 and 45, what two and four dependent launches take; one of 32000 24 with top_k = 50, 27 with
+// min_p and top_p too, 45 with top_p = 0.9 alone.
 //
 // The border between two tokens can be anywhere, and a vocabulary has 10^5 of them, so probabilities are
 // formed in fp64: an fp32 sum's 1e-7 would name another token once in some hundred rows.  On this chip
