@@ -1184,8 +1184,17 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
             border();  // (after the cut by count, which does not know of it, unless it was known before)
             const float floor = least;
             if (!known) least = -inf;
-            // (what is left out of the last bin weighs nothing, and shows at the ends alone)
-            if (keep < entries && (limit < kBins - 1 || at_end)) cut_bin(limit, keep - earlier, static_cast<double>(inf), false, false);
+            // What is left out of the last bin weighs nothing, and shows at the ends alone, unless its masses are 0 (as of what is
+            // masked by a large number).
+            auto shows = [&]() __attribute__((always_inline)) {
+                bool any = false;
+                over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) any = any || (in(z[j]) && bin_of(z[j]) == kBins - 1 && mass_of(z[j], top) > 0.0);
+                });
+                return largest(any ? 1.f : 0.f, false) > 0.f;
+            };
+            if (keep < entries && (limit < kBins - 1 || (at_end && shows()))) cut_bin(limit, keep - earlier, static_cast<double>(inf), false, false);
             least = floor;
         }
         known = true;

@@ -122,3 +122,34 @@ def test_a_uniform_number_at_and_past_its_ends(env, T, V, low, spread):
                 assert int(token[t]) == i, (kw, v, t, int(token[t]), i)
                 assert abs(float(logprob[t]) - log) <= 2.0 ** -24 * abs(log) + 1e-11
         check(torch, cbk, z, torch.tensor([0.5, 0.01, 1.0 - 2.0 ** -24]), str(kw), **kw)
+
+
+@pytest.mark.parametrize("T,V", [(3, 40000), (3, 70000), (66, 70000)])
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -3.4028234663852886e38])
+def test_masked_rows_at_the_ends_of_uniform(env, T, V, mask):
+    """Fewer entries are allowed than top_k takes: the first or the last of them is drawn, for a few passes over the row (what is
+    masked weighs nothing, so that no cut among it has to be found)."""
+    torch, cbk = env
+    g = torch.Generator().manual_seed(57)
+    z = torch.full((T, V), mask)
+    allowed = torch.randperm(V, generator=g)[:30]
+    z[:, allowed] = 2.5 * torch.randn(T, 30, generator=g)
+    z, plain = z.cuda(), 2.5 * torch.randn(T, V, generator=g).cuda()
+    inside, ends = (torch.full((T,), v, device="cuda") for v in (0.5, 0.0))
+
+    def us(x, u):
+        times = []
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            cbk.sample(x, u, top_k=50)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 1e3)
+        return min(times)
+
+    for v, want in ((0.0, allowed.min()), (-2.0, allowed.min()), (1.0, allowed.max()), (9.0, allowed.max())):
+        token, logprob = cbk.sample(z, torch.full((T,), v, device="cuda"), top_k=50)
+        assert bool((token == int(want)).all()) and bool(logprob.isfinite().all()), v
+    ordinary, at_end = us(plain, inside), us(z, ends)
+    assert at_end < 10 * ordinary, (ordinary, at_end)
