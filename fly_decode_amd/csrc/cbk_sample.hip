@@ -1184,8 +1184,9 @@ __global__ __launch_bounds__(kThreads) void k_sample(const SampleArgs a) {
             border();  // (after the cut by count, which does not know of it, unless it was known before)
             const float floor = least;
             if (!known) least = -inf;
-            // What is left out of the last bin weighs nothing, and shows at the ends alone, unless its masses are 0 (as of what is
-            // masked by a large number).
+            // What is left out of the last bin weighs nothing, and shows at the ends alone, unless its masses are 0, as of what is
+            // masked by a large number (a cut among whose equal keys takes a pass for each bit: 66 rows of 70000, 30 allowed and
+            // top_k = 50, 1346 us at the ends, 134 without it).
             auto shows = [&]() __attribute__((always_inline)) {
                 bool any = false;
                 over_row(r, [&](int32_t, const float (&z)[4], uint32_t, bool) __attribute__((always_inline)) {
