@@ -112,7 +112,7 @@ ExPlan ex_plan(const cbk_experts &ex, uint64_t tokens, uint32_t k, bool backward
     const uint64_t per = slots / active;
     const bool large = ex.b <= 13 && ex.b_down <= 14;
     p.tile = per <= 8 ? 16 : large && per > (backward ? 24 : 8) ? 256 : 64;
-    // A launch has fewer than 2^32 threads, 512 for each tile of the result.  Hundreds of experts in use, of 2^19 hidden columns
+    // A launch has fewer than 2^32 threads, 512 for each tile of the result.  Hundreds of experts in use, of some 2^19 hidden columns
     // and more, have more tiles of 16 slots x 64 of them (other products' results take a chunk's bytes long before that, and
     // tiles of more slots are fewer): such a chunk is cut down, to 7 tokens or more, which have tiles of 16 again.
     constexpr uint64_t kMostTiles = (uint64_t(1) << 23) - 8;
